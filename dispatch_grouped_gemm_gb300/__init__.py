@@ -24,12 +24,17 @@ __all__ = [
     "HmmError", "HmmShape", "hmm_create", "hmm_destroy", "hmm_set_option",
     "hmm_workspace_size", "hmm_route", "hmm_route_static", "hmm_forward", "hmm_backward",
     "hmm_backward_dx", "hmm_backward_dw", "hmm_forward_shared", "hmm_backward_shared",
+    "hmm_gate_forward", "hmm_gate_backward", "HmmGate", "make_gate", "moe_gate",
+    "hmm_mx4_size", "hmm_mx4_quantize", "hmm_mx4_dequantize", "hmm_mx4_workspace_size",
+    "hmm_forward_mx4", "HmmMx4", "make_mx4", "Mx4Tensor", "mx4_quantize", "mx4_quantize_experts",
+    "moe_ffn_mx4",
     "hmm_status",
     "hmm_error_string", "Context", "moe_ffn", "library_path", "load_library",
     "hmm_profile_read", "hmm_phase_name", "hmm_set_trace",
     "HMM_OPT_VALIDATE", "HMM_OPT_WAIT_BUDGET_NS", "HMM_OPT_INJECT_SKIP_READY", "HMM_OPT_PROFILE",
     "HMM_OPT_PAIR_ROWS", "HMM_OPT_OVERLAP_LAUNCHES", "HMM_OPT_FUSED_COMBINE",
-    "HMM_DTYPE_BF16", "HMM_DTYPE_F32", "HMM_STATUS_EXPERT_ID", "HMM_STATUS_TIMEOUT",
+    "HMM_DTYPE_BF16", "HMM_DTYPE_F32", "HMM_SCORE_SOFTMAX", "HMM_SCORE_SIGMOID",
+    "HMM_MX4_ROWS", "HMM_MX4_COLUMNS", "HMM_MX4_GATE_UP", "HMM_STATUS_EXPERT_ID", "HMM_STATUS_TIMEOUT",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -62,6 +67,11 @@ HMM_OPT_OVERLAP_LAUNCHES = _C["HMM_OPT_OVERLAP_LAUNCHES"]
 HMM_OPT_FUSED_COMBINE = _C["HMM_OPT_FUSED_COMBINE"]
 HMM_DTYPE_BF16 = _C["HMM_DTYPE_BF16"]
 HMM_DTYPE_F32 = _C["HMM_DTYPE_F32"]
+HMM_SCORE_SOFTMAX = _C["HMM_SCORE_SOFTMAX"]
+HMM_SCORE_SIGMOID = _C["HMM_SCORE_SIGMOID"]
+HMM_MX4_ROWS = _C["HMM_MX4_ROWS"]
+HMM_MX4_COLUMNS = _C["HMM_MX4_COLUMNS"]
+HMM_MX4_GATE_UP = _C["HMM_MX4_GATE_UP"]
 HMM_STATUS_EXPERT_ID = _C["HMM_STATUS_EXPERT_ID"]
 HMM_STATUS_TIMEOUT = _C["HMM_STATUS_TIMEOUT"]
 
@@ -70,6 +80,20 @@ class HmmShape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("I", ctypes.c_int64),
                 ("E", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("weights_dtype", ctypes.c_int32), ("shared", ctypes.c_int32)]
+
+
+class HmmGate(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("ld_logits", ctypes.c_int64), ("logits_dtype", ctypes.c_int32),
+                ("weights_dtype", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class HmmMx4(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32)]
 
 
 class HmmError(RuntimeError):
@@ -89,6 +113,8 @@ def library_path() -> str:
 def load_library():
     """Load libhmm.so (raises if it was not built: there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lib_lock:
         if _lib is not None:
             return _lib
@@ -98,7 +124,8 @@ def load_library():
                 "`python -m dispatch_grouped_gemm_gb300.build` (nvcc, sm_103a)")
         lib = ctypes.CDLL(_LIB_PATH)
         vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
-        sp = ctypes.POINTER(HmmShape)
+        sp, gp = ctypes.POINTER(HmmShape), ctypes.POINTER(HmmGate)
+        mp, szp = ctypes.POINTER(HmmMx4), ctypes.POINTER(sz)
         sig = {
             "hmm_create": [ctypes.POINTER(vp), i32],
             "hmm_destroy": [vp],
@@ -114,6 +141,13 @@ def load_library():
             "hmm_backward_shared": [vp, sp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, vp, vp,
                                     vp, vp, sz, vp],
             "hmm_backward_dw": [vp, sp, vp, sz, vp, vp, vp, sz, vp],
+            "hmm_gate_forward": [vp, gp, vp, vp, vp, vp, vp, vp],
+            "hmm_gate_backward": [vp, gp, vp, vp, vp, vp, vp, vp],
+            "hmm_mx4_size": [mp, szp, szp],
+            "hmm_mx4_quantize": [vp, mp, vp, vp, vp, vp],
+            "hmm_mx4_dequantize": [vp, mp, vp, vp, vp, vp],
+            "hmm_mx4_workspace_size": [sp, szp],
+            "hmm_forward_mx4": [vp, sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
             "hmm_status": [vp, vp, ctypes.POINTER(i32)],
             "hmm_profile_read": [vp, i32, ctypes.POINTER(ctypes.c_double),
                                  ctypes.POINTER(ctypes.c_int64)],
@@ -264,6 +298,70 @@ def hmm_backward_dw(ctx, shape, saved, d_up_proj_weight, d_down_proj_weight, wor
     _check(rc, "hmm_backward_dw")
 
 
+def make_gate(T, E, K, *, score=HMM_SCORE_SOFTMAX, ld_logits=None, logits_dtype=HMM_DTYPE_F32,
+              weights_dtype=HMM_DTYPE_F32, renormalize=0, groups=1, topk_groups=1, group_top=1,
+              scale=1.0) -> HmmGate:
+    return HmmGate(int(T), int(E), int(K), int(E if ld_logits is None else ld_logits),
+                   int(logits_dtype), int(weights_dtype), int(score), int(renormalize),
+                   int(groups), int(topk_groups), int(group_top), float(scale))
+
+
+def hmm_gate_forward(ctx, gate, logits, bias, topk_ids, topk_weights, scores=None, stream=None):
+    rc = load_library().hmm_gate_forward(ctx, ctypes.byref(gate), _ptr(logits), _ptr(bias),
+                                         _ptr(topk_ids), _ptr(topk_weights), _ptr(scores),
+                                         _stream(stream))
+    _check(rc, "hmm_gate_forward")
+
+
+def hmm_gate_backward(ctx, gate, logits, topk_ids, d_topk_weights, d_scores, d_logits,
+                      stream=None):
+    rc = load_library().hmm_gate_backward(ctx, ctypes.byref(gate), _ptr(logits), _ptr(topk_ids),
+                                          _ptr(d_topk_weights), _ptr(d_scores), _ptr(d_logits),
+                                          _stream(stream))
+    _check(rc, "hmm_gate_backward")
+
+
+def make_mx4(rows, cols, *, batch=1, ld=None, dtype=HMM_DTYPE_BF16, layout=HMM_MX4_ROWS) -> HmmMx4:
+    return HmmMx4(int(batch), int(rows), int(cols), int(cols if ld is None else ld), int(dtype),
+                  int(layout))
+
+
+def hmm_mx4_size(desc):
+    """(bytes of the codes, bytes of the scales)."""
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load_library().hmm_mx4_size(ctypes.byref(desc), ctypes.byref(c), ctypes.byref(s)),
+           "hmm_mx4_size")
+    return c.value, s.value
+
+
+def hmm_mx4_quantize(ctx, desc, values, codes, scales, stream=None):
+    rc = load_library().hmm_mx4_quantize(ctx, ctypes.byref(desc), _ptr(values), _ptr(codes),
+                                         _ptr(scales), _stream(stream))
+    _check(rc, "hmm_mx4_quantize")
+
+
+def hmm_mx4_dequantize(ctx, desc, codes, scales, values, stream=None):
+    rc = load_library().hmm_mx4_dequantize(ctx, ctypes.byref(desc), _ptr(codes), _ptr(scales),
+                                           _ptr(values), _stream(stream))
+    _check(rc, "hmm_mx4_dequantize")
+
+
+def hmm_mx4_workspace_size(shape: HmmShape) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().hmm_mx4_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
+           "hmm_mx4_workspace_size")
+    return n.value
+
+
+def hmm_forward_mx4(ctx, shape, x, topk_ids, topk_weights, up_codes, up_scales, down_codes,
+                    down_scales, y, workspace, stream=None):
+    rc = load_library().hmm_forward_mx4(ctx, ctypes.byref(shape), _ptr(x), _ptr(topk_ids),
+                                        _ptr(topk_weights), _ptr(up_codes), _ptr(up_scales),
+                                        _ptr(down_codes), _ptr(down_scales), _ptr(y),
+                                        _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check(rc, "hmm_forward_mx4")
+
+
 def hmm_status(ctx, stream=None):
     """Synchronise the stream, read and clear the device status word.
     Returns (return code, HMM_STATUS_* bits) without raising."""
@@ -296,6 +394,7 @@ def hmm_set_trace(ctx, buffer, which: int):
 
 # ------------------------------------------------------------ torch layer
 _WDTYPES = {torch.bfloat16: HMM_DTYPE_BF16, torch.float32: HMM_DTYPE_F32}
+_TORCH_WDTYPES = {code: dtype for dtype, code in _WDTYPES.items()}
 
 
 def _u8(nbytes: int, device) -> torch.Tensor:
@@ -471,3 +570,221 @@ def moe_ffn(x, topk_ids, topk_weights, up_proj_weight, down_proj_weight, *,
         return _MoEFFNShared.apply(x, topk_ids, topk_weights, up_proj_weight, down_proj_weight,
                                    *shared)
     return _MoEFFN.apply(x, topk_ids, topk_weights, up_proj_weight, down_proj_weight)
+
+
+_SCORES = {"softmax": HMM_SCORE_SOFTMAX, "sigmoid": HMM_SCORE_SIGMOID}
+
+
+def _gate_forward(logits, gate, bias, return_scores):
+    c = Context.for_device(logits.device)
+    ids = torch.empty((gate.T, gate.K), dtype=torch.int32, device=logits.device)
+    w = torch.empty((gate.T, gate.K), dtype=_TORCH_WDTYPES[gate.weights_dtype],
+                    device=logits.device)
+    scores = (torch.empty((gate.T, gate.E), dtype=torch.float32, device=logits.device)
+              if return_scores else None)
+    hmm_gate_forward(c.handle, gate, logits, bias, ids, w, scores)
+    return ids, w, scores
+
+
+class _MoEGate(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, gate, bias, return_scores):
+        ids, w, scores = _gate_forward(logits, gate, bias, return_scores)
+        ctx.gate = gate
+        ctx.save_for_backward(logits, ids)
+        ctx.mark_non_differentiable(ids)
+        ctx.set_materialize_grads(False)
+        return ids, w, scores
+
+    @staticmethod
+    def backward(ctx, _, dw, ds):
+        if dw is None and ds is None:
+            return None, None, None, None
+        logits, ids = ctx.saved_tensors
+        dw = None if dw is None else dw.contiguous()
+        ds = None if ds is None else ds.contiguous()
+        dl = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        c = Context.for_device(logits.device)
+        hmm_gate_backward(c.handle, ctx.gate, logits, ids, dw, ds, dl)
+        return dl, None, None, None
+
+
+def moe_gate(logits, k, *, score="softmax", bias=None, groups=1, topk_groups=None, group_top=1,
+             renormalize=False, scale=1.0, weights_dtype=torch.float32, return_scores=False):
+    """Router: logits [T, E] (bfloat16 or float32, unit stride along E) to
+    (topk_ids int32 [T, k], topk_weights [T, k]), the inputs of moe_ffn, and
+    with return_scores the scores p, float32 [T, E].
+
+    p = softmax or sigmoid of the logits; the k best p + bias are selected
+    (bias: float32 [E], selection only; equal keys by ascending expert), with
+    groups > 1 only inside the topk_groups best of `groups` groups of
+    consecutive experts, a group counting by the sum of its group_top best
+    keys; the weights are scale * p of the selected experts, divided by their
+    sum with renormalize.  A logit of -inf closes its expert.  Differentiable
+    in the logits through the weights and the scores."""
+    if logits.dim() != 2:
+        raise ValueError("logits [T, E] expected")
+    if logits.dtype not in _WDTYPES or weights_dtype not in _WDTYPES:
+        raise TypeError("logits and weights_dtype must be bfloat16 or float32")
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    T, E = logits.shape
+    if not logits.is_cuda or (E > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA tensor with unit stride along the experts")
+    if T > 1 and logits.stride(0) < E:
+        logits = logits.contiguous()  # broadcast or overlapping rows
+    if bias is not None:
+        if tuple(bias.shape) != (E,) or bias.device != logits.device or not bias.is_contiguous():
+            raise ValueError(f"bias must be a contiguous [{E}] tensor on the logits' device")
+        if bias.dtype != torch.float32:
+            raise TypeError("bias must be float32")
+    gate = make_gate(T, E, k, score=_SCORES[score], ld_logits=max(E, logits.stride(0)),
+                     logits_dtype=_WDTYPES[logits.dtype], weights_dtype=_WDTYPES[weights_dtype],
+                     renormalize=1 if renormalize else 0, groups=groups,
+                     topk_groups=groups if topk_groups is None else topk_groups,
+                     group_top=group_top, scale=scale)
+    if torch.is_grad_enabled() and logits.requires_grad:
+        ids, w, scores = _MoEGate.apply(logits, gate, bias, return_scores)
+    else:
+        ids, w, scores = _gate_forward(logits, gate, bias, return_scores)
+    return (ids, w, scores) if return_scores else (ids, w)
+
+
+class Mx4Tensor:
+    """A microscaled 4-bit operand, or a stack of them for the experts: uint8
+    `codes` [N, K/2] and `scales` [N tiles, K tiles, 512] (with a leading batch
+    dimension for experts) in the storage that include/hmm.h describes.
+
+    layout HMM_MX4_ROWS stands for values [rows, cols]; HMM_MX4_COLUMNS and
+    HMM_MX4_GATE_UP for expert weights [batch, cols, rows] (cols: the
+    contraction)."""
+
+    __slots__ = ("codes", "scales", "batch", "rows", "cols", "layout")
+
+    def __init__(self, codes, scales, batch, rows, cols, layout):
+        self.codes, self.scales = codes, scales
+        self.batch, self.rows, self.cols, self.layout = batch, rows, cols, layout
+
+    @staticmethod
+    def _shapes(batch, rows, cols, layout):
+        stored = (rows // 2 + 31) // 32 * 64 if layout == HMM_MX4_GATE_UP else rows
+        codes = (stored, (cols + 31) // 32 * 16)
+        scales = ((stored + 127) // 128, (cols + 127) // 128, 512)
+        return (codes, scales) if layout == HMM_MX4_ROWS else ((batch,) + codes, (batch,) + scales)
+
+    @classmethod
+    def _wrap(cls, codes, scales, batch, rows, cols, layout):
+        want = cls._shapes(batch, rows, cols, layout)
+        if (tuple(codes.shape), tuple(scales.shape)) != want:
+            raise ValueError(f"codes and scales must be {want}, got "
+                             f"{(tuple(codes.shape), tuple(scales.shape))}")
+        for t in (codes, scales):
+            if t.dtype != torch.uint8:
+                raise TypeError("codes and scales must be uint8")
+            if not t.is_cuda or not t.is_contiguous() or t.device != codes.device:
+                raise ValueError("codes and scales must be contiguous tensors of one CUDA device")
+        return cls(codes, scales, batch, rows, cols, layout)
+
+    @classmethod
+    def from_rows(cls, codes, scales, cols):
+        """Stored rows (e.g. loaded from a file)."""
+        return cls._wrap(codes, scales, 1, codes.shape[0], cols, HMM_MX4_ROWS)
+
+    @classmethod
+    def experts(cls, codes, scales, *, K, N, gate_up=False):
+        """Stored expert weights [E, K, N], contraction K; gate_up: an
+        up-projection (N = 2I) with gate and up rows in turn."""
+        return cls._wrap(codes, scales, codes.shape[0], N, K,
+                         HMM_MX4_GATE_UP if gate_up else HMM_MX4_COLUMNS)
+
+    @property
+    def shape(self):
+        """Shape of the values."""
+        if self.layout == HMM_MX4_ROWS:
+            return (self.rows, self.cols)
+        return (self.batch, self.cols, self.rows)
+
+    def dequantize(self, dtype=torch.bfloat16):
+        """The values that the codes and scales stand for (exact)."""
+        if dtype not in _WDTYPES:
+            raise TypeError("dtype must be bfloat16 or float32")
+        out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
+        d = make_mx4(self.rows, self.cols, batch=self.batch, dtype=_WDTYPES[dtype],
+                     layout=self.layout)
+        hmm_mx4_dequantize(Context.for_device(out.device).handle, d, self.codes, self.scales, out)
+        return out
+
+
+def _mx4_of(values, batch, rows, cols, ld, layout):
+    cs, ss = Mx4Tensor._shapes(batch, rows, cols, layout)
+    d = make_mx4(rows, cols, batch=batch, ld=ld, dtype=_WDTYPES[values.dtype], layout=layout)
+    hmm_mx4_size(d)  # refuses an unsupported shape before anything is allocated
+    codes = torch.empty(cs, dtype=torch.uint8, device=values.device)
+    scales = torch.empty(ss, dtype=torch.uint8, device=values.device)
+    hmm_mx4_quantize(Context.for_device(values.device).handle, d, values, codes, scales)
+    return Mx4Tensor(codes, scales, batch, rows, cols, layout)
+
+
+def mx4_quantize(x):
+    """Rows [R, C] (bfloat16 or float32, C a multiple of 8, unit stride along
+    C) to microscaled 4-bit form, blocks of 32 along C."""
+    if x.dim() != 2:
+        raise ValueError("x [R, C] expected")
+    if x.dtype not in _WDTYPES:
+        raise TypeError("x must be bfloat16 or float32")
+    R, C = x.shape
+    if not x.is_cuda or (C > 1 and x.stride(1) != 1):
+        raise ValueError("x must be a CUDA tensor with unit stride along its columns")
+    if R > 1 and x.stride(0) < C:
+        x = x.contiguous()  # broadcast or overlapping rows
+    return _mx4_of(x, 1, R, C, x.stride(0) if R > 1 else C, HMM_MX4_ROWS)
+
+
+def mx4_quantize_experts(w, *, gate_up=False):
+    """Expert weights [E, K, N] as moe_ffn takes them (bfloat16 or float32) to
+    microscaled 4-bit form, blocks of 32 along the contraction K.  gate_up:
+    up_proj_weight (N = 2I, gate columns first)."""
+    if w.dim() != 3:
+        raise ValueError("w [E, K, N] expected")
+    if w.dtype not in _WDTYPES:
+        raise TypeError("w must be bfloat16 or float32")
+    if not w.is_cuda or not w.is_contiguous():
+        raise ValueError("w must be a contiguous CUDA tensor")
+    E, K, N = w.shape
+    return _mx4_of(w, E, N, K, K, HMM_MX4_GATE_UP if gate_up else HMM_MX4_COLUMNS)
+
+
+def moe_ffn_mx4(x, topk_ids, topk_weights, up_proj, down_proj):
+    """moe_ffn for inference with microscaled 4-bit expert weights: up_proj and
+    down_proj are Mx4Tensors of mx4_quantize_experts (up_proj with gate_up).
+    x is rounded to 4-bit blocks along H, the fp32 SwiGLU outputs along I; the
+    products accumulate in fp32.  Not differentiable."""
+    if up_proj.layout != HMM_MX4_GATE_UP or down_proj.layout != HMM_MX4_COLUMNS:
+        raise ValueError("up_proj must be experts with gate_up, down_proj experts without")
+    if x.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("x [T, H] and topk_ids [T, K] expected")
+    T, H = x.shape
+    E, I = up_proj.batch, up_proj.rows // 2
+    if up_proj.cols != H or (down_proj.batch, down_proj.cols, down_proj.rows) != (E, I, H):
+        raise ValueError(f"up_proj {up_proj.shape} and down_proj {down_proj.shape} do not match "
+                         f"each other and x {tuple(x.shape)}")
+    if topk_ids.shape[0] != T or topk_weights.shape != topk_ids.shape:
+        raise ValueError("topk_ids / topk_weights must both be [T, K]")
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be bfloat16")
+    if topk_ids.dtype != torch.int32:
+        raise TypeError("topk_ids must be int32")
+    if topk_weights.dtype not in _WDTYPES:
+        raise TypeError("topk_weights must be bfloat16 or float32")
+    for t in (x, topk_ids, topk_weights):
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("all arguments must be contiguous CUDA tensors")
+    if torch.is_grad_enabled() and (x.requires_grad or topk_weights.requires_grad):
+        raise RuntimeError("moe_ffn_mx4 has no backward: call it under torch.no_grad(), or train "
+                           "with moe_ffn")
+    shape = make_shape(T, H, I, E, topk_ids.shape[1], _WDTYPES[topk_weights.dtype])
+    ws = _u8(hmm_mx4_workspace_size(shape), x.device)
+    y = torch.empty_like(x)
+    hmm_forward_mx4(Context.for_device(x.device).handle, shape, x, topk_ids, topk_weights,
+                    up_proj.codes, up_proj.scales, down_proj.codes, down_proj.scales, y, ws)
+    return y

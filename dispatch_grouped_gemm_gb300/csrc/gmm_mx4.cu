@@ -1,0 +1,699 @@
+// gmm_mx4.cu -- the experts' products with microscaled 4-bit operands: token
+// dispatch with quantisation, and GMM1 (SwiGLU and re-quantisation in its
+// epilogue) and GMM2 in one persistent launch.
+//
+//   a = Q(silu(Q(x) . W1g^T) * (Q(x) . W1u^T)),   o = a . W2^T    per expert
+//
+// tcgen05.mma kind::mxf4 multiplies e2m1 codes with one power-of-two scale per
+// 32 elements of the contraction on either side, accumulating in fp32.  The
+// token rows sit on M (128 TMEM lanes), the weight rows on N (256 accumulator
+// columns): a thread of the epilogue then holds whole blocks of 32
+// consecutive outputs of one token, so a block's maximum, its scale and its
+// codes need no exchange between threads.  Both operands are contraction-major
+// with 128-byte rows of 256 elements per K block; their scales come as 512-byte
+// tiles (128 rows x 4 blocks) that tcgen05.cp spreads over the TMEM lanes.
+//
+// TMEM: two accumulators of 256 columns and 24 columns of scales do not fit
+// into 512 columns side by side, so the accumulators share 32 columns: [0, 256)
+// and [224, 480), scales from 480.  The epilogue of a tile reads the shared
+// columns first and releases them; all warps together then also say that the
+// tile before has been read, so that one barrier per tile orders both.
+//
+// The rows of the up-projection are stored as 32 gate rows and the matching 32
+// up rows in turn: accumulator columns 64 c .. 64 c + 31 are the gate and the
+// next 32 the up values of chunk c.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "mx4.cuh"
+#include "ptx.cuh"
+
+namespace hmm {
+
+namespace {
+
+constexpr int XM = 128;              // token rows per tile
+constexpr int XN = 256;              // weight rows per tile
+constexpr int XK = 256;              // contraction per stage: 128 bytes of codes
+constexpr int XA_BYTES = XM * 128;   // 16 KB
+constexpr int XB_BYTES = XN * 128;   // 32 KB
+constexpr int XSA_BYTES = 2 * MX_TILE_BYTES;
+constexpr int XSB_BYTES = 4 * MX_TILE_BYTES;
+constexpr int XSTAGE_BYTES = XA_BYTES + XB_BYTES + XSA_BYTES + XSB_BYTES;  // 51 KB
+constexpr int XSTAGES = 4;
+constexpr int XEPI_WARPS = 8;        // two per TMEM lane quarter
+constexpr int XTHREADS = 32 * (XEPI_WARPS + 3);
+constexpr int XBUF = 32 * 64;        // staged output: 32 rows of 32 bf16
+constexpr int XTI_DEPTH = 3;
+constexpr int XACC1 = XN - 32;       // second accumulator's first column
+constexpr int XSF_COL = XACC1 + XN;  // scales of A: 2 x 4 columns, then of B: 2 x 8
+constexpr int XBARS = 2 * XSTAGES + 3 + 2 * XTI_DEPTH + 1;
+constexpr int XSMEM = 1024 + XSTAGES * XSTAGE_BYTES + XEPI_WARPS * XBUF + 256 +
+                      XTI_DEPTH * 20 + 8 + 4 * (MAX_E + 1);
+static_assert(XSMEM <= 232448, "shared memory per CTA");
+static_assert(XSF_COL + 24 <= 512, "TMEM columns");
+static_assert(XBARS * 8 <= 256, "barriers");
+
+struct XProb {
+  int kp;        // contraction, padded to 32
+  int kt;        // scale tiles along it
+  int n;         // stored weight rows
+  int rt;        // scale tiles along them
+  int n_tiles;
+  const uint8_t* sa;  // scales of the token rows
+  const uint8_t* sw;  // scales of the weights
+};
+
+struct XParams {
+  XProb p[2];
+  const int32_t* poff;
+  const int32_t* counts;
+  int E;
+  int* ticket;
+  int* ready;       // per 128 token rows: epilogue warps of GMM1 that are done
+  int ready_unit;   // ... when all are
+  int signal;       // 0: test-only fault injection, nothing is released
+  uint8_t* a_codes;
+  uint8_t* a_scales;
+  int a_blocks;     // blocks of 32 along I
+  int a_pitch;      // bytes of a row of a
+  int a_kt;
+  __nv_bfloat16* o;
+  int H;
+  unsigned* status;
+  unsigned long long budget_ns;
+};
+
+struct XMaps {
+  CUtensorMap a[2][4];  // token rows: boxes of 16, 32, 64, 128 rows
+  CUtensorMap w[2];
+};
+
+struct XTile {
+  int prob;  // -1: no more tiles
+  int e;
+  int row0;  // first padded token row
+  int rows;  // valid rows, 1 .. 128
+  int n0;    // first weight row
+};
+
+// ---------------------------------------------------------------------- PTX
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+// 512 bytes of scales (32 lanes x 16 bytes) to 4 TMEM columns, the same in
+// each of the four lane quarters.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+// D[tmem] (+)= A * B, e2m1 codes with a ue8m0 scale per 32 elements.
+__device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], "
+      "[%6], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+// Instruction descriptor of kind::mxf4: e2m1 x e2m1, ue8m0 scales, both
+// operands K-major; sf: which half of a 4-byte scale column (0 or 2).
+__device__ __forceinline__ uint32_t idesc_mx4(int n, uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(XM >> 4) << 24) | (sf << 29);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// ---------------------------------------------------------------- scheduling
+// Tickets run over the GMM1 tiles of all experts, then over the GMM2 tiles.
+__device__ __forceinline__ int xblocks(const XParams& P, int e) {
+  return (P.counts[e] + XM - 1) / XM;
+}
+
+// Prefix sums of the experts' token blocks (one warp).
+__device__ void xschedule(const XParams& P, int* pref) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  if (lane == 0) pref[0] = 0;
+  for (int base = 0; base < P.E; base += 32) {
+    const int e = base + lane;
+    int inc = e < P.E ? xblocks(P, e) : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += n;
+    }
+    if (e < P.E) pref[e + 1] = carry + inc;
+    carry += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  __syncwarp();
+}
+
+__device__ bool xlocate(const XParams& P, const int* pref, int t, XTile& ti) {
+  const int blocks = pref[P.E];
+  ti.prob = t >= blocks * P.p[0].n_tiles;
+  if (ti.prob) t -= blocks * P.p[0].n_tiles;
+  const int nt = P.p[ti.prob].n_tiles;
+  if (t >= blocks * nt) {
+    ti.prob = -1;
+    return false;
+  }
+  int lo = 0, hi = P.E - 1;  // largest expert whose first tile is at most t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pref[mid] * nt <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  ti.e = lo;
+  const int nb = pref[lo + 1] - pref[lo];
+  const int r = t - pref[lo] * nt;
+  const int wt = r / nb;  // token blocks innermost: a weight tile is reused from L2
+  const int b = r - wt * nb;
+  ti.row0 = P.poff[lo] + XM * b;
+  ti.rows = min(XM, P.counts[lo] - XM * b);
+  ti.n0 = wt * XN;
+  return true;
+}
+
+// ------------------------------------------------------------------ epilogue
+// GMM1: one chunk (32 gate and 32 up columns) of this thread's row.  Returns
+// the block's scale byte and writes its codes.
+__device__ __forceinline__ uint32_t swiglu_block(const uint32_t (&g)[32], const uint32_t (&u)[32],
+                                                 uint4* codes, bool valid) {
+  float v[32];
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float x = __uint_as_float(g[j]);
+    // silu(g) * u; exp(-g) overflowing to inf gives 0
+    v[j] = __fdividef(x, 1.0f + __expf(-x)) * __uint_as_float(u[j]);
+    m = max_nan(m, fabsf(v[j]));
+  }
+  const uint32_t s = mx_scale_byte(__float_as_uint(m));
+  const float inv = mx_inverse_scale(s);
+  uint32_t q[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = v[8 * j + k] * inv;
+    q[j] = mx_codes8(w);
+  }
+  if (valid) *codes = make_uint4(q[0], q[1], q[2], q[3]);
+  return s;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(XTHREADS, 1)
+    gmm_mx4_kernel(const __grid_constant__ XParams P, const __grid_constant__ XMaps maps) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* bufs = smem + XSTAGES * XSTAGE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(bufs + XEPI_WARPS * XBUF);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + XSTAGES;
+  uint64_t* tfull = bars + 2 * XSTAGES;  // [2]
+  uint64_t* tfree = tfull + 2;           // one phase per tile (see the top)
+  uint64_t* ti_full = tfree + 1;
+  uint64_t* ti_empty = ti_full + XTI_DEPTH;
+  uint64_t* mma_done = ti_empty + XTI_DEPTH;
+  XTile* s_ti = reinterpret_cast<XTile*>(bars + 32);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_ti + XTI_DEPTH);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_pref = reinterpret_cast<int*>(s_tmem + 2);  // [E + 1]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < XSTAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&tfull[0], 1);
+    mbar_init(&tfull[1], 1);
+    mbar_init(tfree, XEPI_WARPS);
+    for (int i = 0; i < XTI_DEPTH; ++i) {
+      mbar_init(&ti_full[i], 1);
+      mbar_init(&ti_empty[i], 2 + XEPI_WARPS);
+    }
+    mbar_init(mma_done, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  grid_dep_wait();
+  const WaitCtl wc{s_abort, P.status, P.budget_ns};
+
+  if (warp == 2 + XEPI_WARPS) {
+    // --------------------------------------------------------- tile scheduler
+    xschedule(P, s_pref);
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t phase = 0;
+      int t = atomicAdd(P.ticket, 1);
+      for (;;) {
+        XTile ti{-1, 0, 0, 0, 0};
+        if (xlocate(P, s_pref, t, ti)) {
+          t = atomicAdd(P.ticket, 1);
+          // every GMM1 tile has a smaller ticket: its CTA is running or done
+          if (ti.prob == 1 && !counter_wait(&P.ready[ti.row0 / XM], P.ready_unit, wc)) break;
+        }
+        if (!mbar_wait(&ti_empty[slot], phase ^ 1u, wc)) break;
+        s_ti[slot] = ti;
+        mbar_arrive(&ti_full[slot]);
+        if (++slot == XTI_DEPTH) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        if (ti.prob < 0) break;
+      }
+    }
+  } else if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------- producer
+      uint32_t stage = 0, sphase = 0, issued = 0;
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (;;) {
+        if (!mbar_wait(&ti_full[slot], phase, wc)) {
+          ok = false;
+          break;
+        }
+        const XTile ti = s_ti[slot];
+        mbar_arrive(&ti_empty[slot]);
+        if (++slot == XTI_DEPTH) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        if (ti.prob < 0) break;
+        const XProb& pr = P.p[ti.prob];
+        // a was written by this launch's epilogues: the scheduler acquired its
+        // counter, order that with the asynchronous copies below
+        if (ti.prob == 1) fence_proxy_async_global();
+        const int box = ti.rows <= 16 ? 0 : (ti.rows <= 32 ? 1 : (ti.rows <= 64 ? 2 : 3));
+        const int nrt = min(2, pr.rt - ti.n0 / 128);
+        const uint8_t* sa = pr.sa + static_cast<int64_t>(ti.row0 / 128) * pr.kt * MX_TILE_BYTES;
+        const uint8_t* sw =
+            pr.sw + (static_cast<int64_t>(ti.e) * pr.rt + ti.n0 / 128) * pr.kt * MX_TILE_BYTES;
+        for (int k = 0; k < pr.kp; k += XK) {
+          if (!mbar_wait(&empty[stage], sphase ^ 1u, wc)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sA = smem + stage * XSTAGE_BYTES;
+          uint8_t* sB = sA + XA_BYTES;
+          uint8_t* sSA = sB + XB_BYTES;
+          uint8_t* sSB = sSA + XSA_BYTES;
+          const int kt0 = k / 128;
+          const uint32_t sb = static_cast<uint32_t>(min(2, pr.kt - kt0)) * MX_TILE_BYTES;
+          mbar_arrive_expect_tx(&full[stage], (16u << box) * 128 + XB_BYTES + sb * (1 + nrt));
+          tma_load_3d(sB, &maps.w[ti.prob], &full[stage], k / 2, ti.n0, ti.e);
+          tma_load_2d(sA, &maps.a[ti.prob][box], &full[stage], k / 2, ti.row0);
+          bulk_load(sSA, sa + kt0 * MX_TILE_BYTES, sb, &full[stage]);
+          for (int r = 0; r < nrt; ++r)
+            bulk_load(sSB + r * 2 * MX_TILE_BYTES,
+                      sw + (static_cast<int64_t>(r) * pr.kt + kt0) * MX_TILE_BYTES, sb,
+                      &full[stage]);
+          ++issued;
+          if (++stage == XSTAGES) {
+            stage = 0;
+            sphase ^= 1u;
+          }
+        }
+        if (!ok) break;
+      }
+      // wait (bounded) for the copies still in flight before leaving
+      if (!ok)
+        for (uint32_t s = 0; s < XSTAGES; ++s)
+          if (issued > s)
+            drain_wait(&full[s], ((issued - 1 - s) / XSTAGES) & 1u, P.budget_ns);
+      grid_dep_launch();  // this CTA is in its last tile
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA issue
+      uint32_t stage = 0, sphase = 0;
+      int slot = 0;
+      uint32_t phase = 0;
+      uint32_t n = 0;  // tiles so far
+      for (;;) {
+        if (!mbar_wait(&ti_full[slot], phase, wc)) break;
+        const XTile ti = s_ti[slot];
+        mbar_arrive(&ti_empty[slot]);
+        if (++slot == XTI_DEPTH) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        if (ti.prob < 0) break;
+        const XProb& pr = P.p[ti.prob];
+        // tile n - 1's shared columns and all of tile n - 2 have been read
+        if (n > 0 && !mbar_wait(tfree, (n - 1) & 1u, wc)) break;
+        tc_fence_after();
+        const uint32_t acc = n & 1u;
+        const uint32_t d = tmem + acc * XACC1;
+        const int cols = min(XN, (pr.n - ti.n0 + 15) / 16 * 16);
+        const int nrt = min(2, pr.rt - ti.n0 / 128);
+        const uint32_t id0 = idesc_mx4(cols, 0), id1 = idesc_mx4(cols, 2);
+        bool ok = true;
+        for (int k = 0; k < pr.kp; k += XK) {
+          if (!mbar_wait(&full[stage], sphase, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(smem + stage * XSTAGE_BYTES);
+          const uint32_t b = a + XA_BYTES;
+          const uint32_t sa = b + XB_BYTES;
+          const uint32_t sb = sa + XSA_BYTES;
+          const int steps = min(4, (pr.kp - k + 63) / 64);
+          const int tiles = (steps + 1) / 2;
+          for (int i = 0; i < tiles; ++i) {
+            tmem_cp_scales(tmem + XSF_COL + 4 * i,
+                           smem_desc(sa + i * MX_TILE_BYTES, 0, 128, LAYOUT_NONE));
+            for (int r = 0; r < nrt; ++r)
+              tmem_cp_scales(tmem + XSF_COL + 8 + 8 * i + 4 * r,
+                             smem_desc(sb + (2 * r + i) * MX_TILE_BYTES, 0, 128, LAYOUT_NONE));
+          }
+          for (int s = 0; s < steps; ++s)
+            umma_mx4(d, smem_desc(a + s * 32, 16, 1024, LAYOUT_SW128),
+                     smem_desc(b + s * 32, 16, 1024, LAYOUT_SW128), (s & 1) ? id1 : id0,
+                     tmem + XSF_COL + 4 * (s >> 1), tmem + XSF_COL + 8 + 8 * (s >> 1),
+                     (k > 0 || s > 0) ? 1u : 0u);
+          umma_commit(&empty[stage]);
+          if (++stage == XSTAGES) {
+            stage = 0;
+            sphase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit(&tfull[acc]);
+        ++n;
+      }
+      // every MMA issued by this thread completes before TMEM is released
+      umma_commit(mma_done);
+      drain_wait(mma_done, 0, P.budget_ns);
+    }
+  } else {
+    // --------------------------------------------------------------- epilogue
+    const int q = warp & 3;          // TMEM lane quarter
+    const int h = (warp - 2) >> 2;   // half of the tile's columns: 128 h ..
+    uint8_t* buf = bufs + (warp - 2) * XBUF;
+    int slot = 0;
+    uint32_t phase = 0;
+    uint32_t n = 0;
+    for (;;) {
+      bool got = false;
+      if (lane == 0) got = mbar_wait(&ti_full[slot], phase, wc);
+      got = __shfl_sync(0xffffffffu, got, 0);
+      if (!got) break;
+      const XTile ti = s_ti[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ti_empty[slot]);
+      if (++slot == XTI_DEPTH) {
+        slot = 0;
+        phase ^= 1u;
+      }
+      if (ti.prob < 0) break;
+      const XProb& pr = P.p[ti.prob];
+      const uint32_t acc = n & 1u;
+      // Accumulator 0 shares its last columns (half 1), accumulator 1 its first
+      // (half 0).  The half that does not read them says only that it has left
+      // the previous tile.  (Not before this tile's accumulator is complete:
+      // the barrier's previous phase is, then, so that no warp counts twice in
+      // one phase.)
+      const bool shares = h == (acc ^ 1);
+      const bool live = 32 * q < ti.rows;
+      if (lane == 0) got = mbar_wait(&tfull[acc], (n >> 1) & 1u, wc);
+      got = __shfl_sync(0xffffffffu, got, 0);
+      if (!got) break;
+      ++n;
+      tc_fence_after();
+      if (!(shares && live) && lane == 0) mbar_arrive(tfree);
+      if (live) {
+        const uint32_t taddr =
+            tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * XACC1 + h * 128;
+        const int row = 32 * q + lane;
+        const bool valid = row < ti.rows;
+        if (ti.prob == 0) {
+          // two chunks of gate and up columns, the one with the shared columns
+          // first: chunk 1 of half 1 (accumulator 0), chunk 0 of half 0
+          const int64_t prow = ti.row0 + row;
+          const int blk0 = ti.n0 / 64 + 2 * h;  // first block of I of this warp
+          uint32_t sc = 0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c = i ^ h;
+            uint32_t g[32], u[32];
+            tmem_ld32(taddr + 64 * c, g);
+            tmem_ld32(taddr + 64 * c + 32, u);
+            tmem_ld_wait();
+            if (i == 0 && shares) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(tfree);
+            }
+            if (blk0 + c < P.a_blocks) {
+              const uint32_t s = swiglu_block(
+                  g, u,
+                  reinterpret_cast<uint4*>(P.a_codes + prow * P.a_pitch + (blk0 + c) * 16), valid);
+              sc |= s << (8 * c);
+            }
+          }
+          // (a missing second block gets scale 0: the last MMA step of GMM2
+          // covers it with zero codes)
+          if (valid && blk0 < P.a_blocks)
+            *reinterpret_cast<uint16_t*>(P.a_scales + mx_scale_offset(prow, blk0, P.a_kt)) =
+                static_cast<uint16_t>(sc);
+        } else {
+          const int c00 = ti.n0 + 128 * h;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const int c = h ? 3 - i : i;
+            uint32_t v[32];
+            tmem_ld32(taddr + 32 * c, v);
+            tmem_ld_wait();
+            if (i == 0 && shares) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(tfree);
+            }
+            const int c0 = c00 + 32 * c;
+            if (c0 < P.H) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  w[k] = pack_bf16(__uint_as_float(v[8 * j + 2 * k]),
+                                   __uint_as_float(v[8 * j + 2 * k + 1]));
+                // 16-byte pieces permuted by the row: no bank conflicts here or below
+                *reinterpret_cast<uint4*>(buf + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+              }
+              __syncwarp();
+              // four lanes per row: 64 contiguous bytes
+#pragma unroll
+              for (int r8 = 0; r8 < 4; ++r8) {
+                const int r = 8 * r8 + (lane >> 2);
+                const int col = c0 + 8 * (lane & 3);
+                if (32 * q + r < ti.rows && col < P.H)
+                  *reinterpret_cast<uint4*>(P.o + static_cast<int64_t>(ti.row0 + 32 * q + r) * P.H +
+                                            col) =
+                      *reinterpret_cast<const uint4*>(buf + r * 64 +
+                                                      16 * ((lane & 3) ^ ((r >> 1) & 3)));
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      if (ti.prob == 0 && P.signal) {
+        fence_proxy_async_global();
+        __syncwarp();
+        if (lane == 0) red_release_add(&P.ready[ti.row0 / XM], 1);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Dispatch: token t's row of x in 4-bit form, once, to the padded rows of its
+// K slots.  One warp per token and MXD_COLS columns; a lane holds 8 elements,
+// four lanes a block, sixteen lanes the four blocks of a scale tile's row.
+namespace {
+constexpr int MXD_UNROLL = 4;
+constexpr int MXD_COLS = 256 * MXD_UNROLL;
+constexpr int MXD_WARPS = 4;
+}  // namespace
+
+__global__ void __launch_bounds__(MXD_WARPS * 32)
+    dispatch_mx4_kernel(const uint4* __restrict__ x, int64_t T, int K, int64_t H, int64_t kp,
+                        int64_t kt, const int32_t* __restrict__ slot2prow,
+                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  const int lane = threadIdx.x & 31;
+  const int64_t parts = (H + MXD_COLS - 1) / MXD_COLS;
+  const int64_t g = static_cast<int64_t>(blockIdx.x) * MXD_WARPS + (threadIdx.x >> 5);
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t t = g / parts;
+  if (t >= T) return;
+  const int64_t c0 = (g - t * parts) * MXD_COLS + 8 * lane;
+  int32_t prow_l = -1;
+  if (lane < K) prow_l = slot2prow[t * K + lane];
+  uint4 v[MXD_UNROLL];
+#pragma unroll
+  for (int i = 0; i < MXD_UNROLL; ++i) {
+    const int64_t c = c0 + 256 * i;
+    v[i] = c < H ? x[(t * H + c) / 8] : make_uint4(0, 0, 0, 0);
+  }
+  uint32_t q[MXD_UNROLL], s[MXD_UNROLL];
+#pragma unroll
+  for (int i = 0; i < MXD_UNROLL; ++i) {
+    const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, max((u[j] << 16) & 0x7FFFFFFFu, u[j] & 0x7FFF0000u));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t b = mx_scale_byte(m);
+    const float inv = mx_inverse_scale(b);
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[2 * j] = __uint_as_float(u[j] << 16) * inv;
+      w[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u) * inv;
+    }
+    q[i] = mx_codes8(w);
+    // the four blocks of this lane's scale tile row as one word
+    uint32_t word = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      word |= __shfl_sync(0xffffffffu, b, (lane & 16) + 4 * j) << (8 * j);
+    s[i] = word;
+  }
+  for (int k = 0; k < K; ++k) {
+    const int32_t prow = __shfl_sync(0xffffffffu, prow_l, k);
+    if (prow < 0) continue;
+#pragma unroll
+    for (int i = 0; i < MXD_UNROLL; ++i) {
+      const int64_t c = c0 + 256 * i;
+      if (c < kp)
+        *reinterpret_cast<uint32_t*>(codes + static_cast<int64_t>(prow) * (kp / 2) + c / 2) = q[i];
+      if ((lane & 15) == 0 && c < kt * 128)
+        *reinterpret_cast<uint32_t*>(scales + mx_scale_offset(prow, c / 32, kt)) = s[i];
+    }
+  }
+}
+
+cudaError_t launch_dispatch_mx4(const Plan& p, const FfnMx4Plan& f, const void* x, MetaPtrs m,
+                                uint8_t* codes, uint8_t* scales, cudaStream_t st, bool pdl) {
+  const int64_t warps = p.T * ((p.H + MXD_COLS - 1) / MXD_COLS);
+  return launch_kernel(dispatch_mx4_kernel,
+                       static_cast<unsigned>((warps + MXD_WARPS - 1) / MXD_WARPS), MXD_WARPS * 32,
+                       0, st, pdl, 1, static_cast<const uint4*>(x), p.T, static_cast<int>(p.K),
+                       p.H, f.hp, f.h_kt, static_cast<const int32_t*>(m.slot2prow), codes, scales);
+}
+
+namespace {
+
+// codes [outer, rows, bytes] as a tensor map with boxes of 128 bytes x box rows
+int map_codes(const GemmEnv& env, CUtensorMap* map, const void* base, int64_t bytes, int64_t rows,
+              int64_t outer, uint32_t box_rows) {
+  const cuuint32_t rank = outer > 0 ? 3 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(bytes),
+                                 static_cast<cuuint64_t>(bytes * rows)};
+  const cuuint32_t box[3] = {128, box_rows, 1}, es[3] = {1, 1, 1};
+  return env.encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims,
+                    strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? HMM_OK
+             : HMM_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, MetaPtrs m,
+                       CtrlPtrs c, uint8_t* ws, const void* up_codes, const void* up_scales,
+                       const void* down_codes, const void* down_scales, bool skip_ready_release) {
+  XMaps maps;
+  XParams P{};
+  int rc = HMM_OK;
+  for (int i = 0; i < 4; ++i) {
+    rc |= map_codes(env, &maps.a[0][i], ws + f.off_x, f.hp / 2, p.R, 0, 16u << i);
+    rc |= map_codes(env, &maps.a[1][i], ws + f.off_a, f.ip / 2, p.R, 0, 16u << i);
+  }
+  rc |= map_codes(env, &maps.w[0], up_codes, f.hp / 2, 2 * f.ip, p.E, XN);
+  rc |= map_codes(env, &maps.w[1], down_codes, f.ip / 2, p.H, p.E, XN);
+  if (rc != HMM_OK) return HMM_ERR_CUDA;
+  auto prob = [](XProb& q, int64_t kp, int64_t n, const uint8_t* sa, const void* sw) {
+    q.kp = static_cast<int>(kp);
+    q.kt = static_cast<int>((kp + 127) / 128);
+    q.n = static_cast<int>(n);
+    q.rt = static_cast<int>((n + 127) / 128);
+    q.n_tiles = static_cast<int>((n + XN - 1) / XN);
+    q.sa = sa;
+    q.sw = static_cast<const uint8_t*>(sw);
+  };
+  prob(P.p[0], f.hp, 2 * f.ip, ws + f.off_xs, up_scales);
+  prob(P.p[1], f.ip, p.H, ws + f.off_as, down_scales);
+  P.poff = m.poff;
+  P.counts = m.counts;
+  P.E = static_cast<int>(p.E);
+  P.ticket = c.tickets;
+  P.ready = c.ready;
+  P.ready_unit = XEPI_WARPS * P.p[0].n_tiles;
+  P.signal = skip_ready_release ? 0 : 1;
+  P.a_codes = ws + f.off_a;
+  P.a_scales = ws + f.off_as;
+  P.a_blocks = static_cast<int>(f.ip / 32);
+  P.a_pitch = static_cast<int>(f.ip / 2);
+  P.a_kt = static_cast<int>(f.i_kt);
+  P.o = reinterpret_cast<__nv_bfloat16*>(ws + f.off_o);
+  P.H = static_cast<int>(p.H);
+  P.status = env.status;
+  P.budget_ns = env.budget_ns;
+  if (cudaFuncSetAttribute(gmm_mx4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, XSMEM) !=
+      cudaSuccess)
+    return HMM_ERR_CUDA;
+  const int64_t tiles = (p.R / XM) * (P.p[0].n_tiles + P.p[1].n_tiles);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(env.num_sms, tiles));
+  return launch_kernel(gmm_mx4_kernel, grid, XTHREADS, XSMEM, env.stream, env.pdl, 1, P, maps) ==
+                 cudaSuccess
+             ? HMM_OK
+             : HMM_ERR_CUDA;
+}
+
+}  // namespace hmm

@@ -217,6 +217,25 @@ CtrlPtrs ctrl_at(const Plan& p, void* base) {
   return c;
 }
 
+FfnMx4Plan ffn_mx4_plan(const Plan& p) {
+  FfnMx4Plan f;
+  f.hp = (p.H + 31) / 32 * 32;
+  f.ip = (p.I + 31) / 32 * 32;
+  f.h_kt = (f.hp + 127) / 128;
+  f.i_kt = (f.ip + 127) / 128;
+  const size_t A = 256, tiles = static_cast<size_t>(p.R / BM) * 512;
+  size_t o = 0;
+  f.off_ctrl = o; o = align_up(o + p.ctrl_bytes, A);
+  f.off_meta = o; o = align_up(o + p.meta_bytes, A);
+  f.off_x = o;    o = align_up(o + static_cast<size_t>(p.R) * (f.hp / 2), A);
+  f.off_xs = o;   o = align_up(o + tiles * f.h_kt, A);
+  f.off_a = o;    o = align_up(o + static_cast<size_t>(p.R) * (f.ip / 2), A);
+  f.off_as = o;   o = align_up(o + tiles * f.i_kt, A);
+  f.off_o = o;    o = align_up(o + static_cast<size_t>(p.R) * p.H * 2, A);
+  f.bytes = o;
+  return f;
+}
+
 // Host-side limits of every entry point [HyperMegaMoE §4.2: shapes, dtypes
 // and layouts are rejected at the boundary, before any device work].
 int check_shape(const hmm_shape* s) {
@@ -242,6 +261,11 @@ using namespace hmm;
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// element alignment (the router reads and writes single elements)
+bool gate_aligned(const void* p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == HMM_DTYPE_F32 ? 3u : 1u)) == 0;
+}
 
 struct DeviceGuard {
   int prev = -1;
@@ -704,6 +728,141 @@ int hmm_backward_dw(hmm_ctx* ctx, const hmm_shape* shape, const void* saved, siz
   return backward_impl(ctx, shape, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, saved,
                        saved_bytes, nullptr, d_up_proj_weight, d_down_proj_weight, nullptr,
                        nullptr, nullptr, workspace, workspace_bytes, stream, BWD_DW);
+}
+
+int hmm_gate_forward(hmm_ctx* ctx, const hmm_gate* gate, const void* logits, const float* bias,
+                     int32_t* topk_ids, void* topk_weights, float* scores, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  const int rc = check_gate(gate);
+  if (rc != HMM_OK) return rc;
+  if (gate->T == 0) return HMM_OK;
+  if (!logits || !topk_ids || !topk_weights) return HMM_ERR_ARG;
+  if (!gate_aligned(logits, gate->logits_dtype) || !gate_aligned(bias, HMM_DTYPE_F32) ||
+      !gate_aligned(topk_ids, HMM_DTYPE_F32) || !gate_aligned(topk_weights, gate->weights_dtype) ||
+      !gate_aligned(scores, HMM_DTYPE_F32))
+    return HMM_ERR_LAYOUT;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return HMM_ERR_CUDA;
+  return cuda_rc(launch_gate_forward(*gate, logits, bias, topk_ids, topk_weights, scores,
+                                     static_cast<cudaStream_t>(stream), ctx->overlap != 0));
+}
+
+int hmm_gate_backward(hmm_ctx* ctx, const hmm_gate* gate, const void* logits,
+                      const int32_t* topk_ids, const void* d_topk_weights, const float* d_scores,
+                      void* d_logits, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  const int rc = check_gate(gate);
+  if (rc != HMM_OK) return rc;
+  if (gate->T == 0) return HMM_OK;
+  if (!logits || !topk_ids || !d_logits) return HMM_ERR_ARG;
+  if (!gate_aligned(logits, gate->logits_dtype) || !gate_aligned(topk_ids, HMM_DTYPE_F32) ||
+      !gate_aligned(d_topk_weights, gate->weights_dtype) ||
+      !gate_aligned(d_scores, HMM_DTYPE_F32) || !gate_aligned(d_logits, gate->logits_dtype))
+    return HMM_ERR_LAYOUT;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return HMM_ERR_CUDA;
+  return cuda_rc(launch_gate_backward(*gate, logits, topk_ids, d_topk_weights, d_scores, d_logits,
+                                      static_cast<cudaStream_t>(stream), ctx->overlap != 0));
+}
+
+int hmm_mx4_size(const hmm_mx4* desc, size_t* codes_bytes, size_t* scales_bytes) {
+  const int rc = check_mx4(desc);
+  if (rc != HMM_OK) return rc;
+  const Mx4Plan p = mx4_plan(*desc);
+  if (codes_bytes) *codes_bytes = p.codes_bytes;
+  if (scales_bytes) *scales_bytes = p.scales_bytes;
+  return HMM_OK;
+}
+
+int hmm_mx4_quantize(hmm_ctx* ctx, const hmm_mx4* desc, const void* values, void* codes,
+                     void* scales, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  const int rc = check_mx4(desc);
+  if (rc != HMM_OK) return rc;
+  if (desc->batch == 0 || desc->rows == 0) return HMM_OK;
+  if (!values || !codes || !scales) return HMM_ERR_ARG;
+  if (!aligned16(values) || !aligned16(codes) || !aligned16(scales)) return HMM_ERR_LAYOUT;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return HMM_ERR_CUDA;
+  return cuda_rc(launch_mx4_quantize(*desc, values, codes, scales,
+                                     static_cast<cudaStream_t>(stream), ctx->overlap != 0));
+}
+
+int hmm_mx4_dequantize(hmm_ctx* ctx, const hmm_mx4* desc, const void* codes, const void* scales,
+                       void* values, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  const int rc = check_mx4(desc);
+  if (rc != HMM_OK) return rc;
+  if (desc->batch == 0 || desc->rows == 0) return HMM_OK;
+  if (!values || !codes || !scales) return HMM_ERR_ARG;
+  if (!aligned16(values) || !aligned16(codes) || !aligned16(scales)) return HMM_ERR_LAYOUT;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return HMM_ERR_CUDA;
+  return cuda_rc(launch_mx4_dequantize(*desc, codes, scales, values,
+                                       static_cast<cudaStream_t>(stream), ctx->overlap != 0));
+}
+
+int hmm_mx4_workspace_size(const hmm_shape* shape, size_t* workspace_bytes) {
+  const int rc = check_shape(shape);
+  if (rc != HMM_OK) return rc;
+  if (shape->shared != 0) return HMM_ERR_ARG;
+  Plan p;
+  make_plan(shape, false, &p);
+  if (workspace_bytes) *workspace_bytes = ffn_mx4_plan(p).bytes;
+  return HMM_OK;
+}
+
+int hmm_forward_mx4(hmm_ctx* ctx, const hmm_shape* shape, const void* x, const int32_t* topk_ids,
+                    const void* topk_weights, const void* up_codes, const void* up_scales,
+                    const void* down_codes, const void* down_scales, void* y, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  int rc = check_shape(shape);
+  if (rc != HMM_OK) return rc;
+  if (shape->shared != 0) return HMM_ERR_ARG;
+  Plan p;
+  make_plan(shape, false, &p);
+  if (p.TK == 0) return HMM_OK;
+  for (const void* ptr : {x, static_cast<const void*>(topk_ids), topk_weights, up_codes,
+                          up_scales, down_codes, down_scales, static_cast<const void*>(y),
+                          static_cast<const void*>(workspace)}) {
+    if (!ptr) return HMM_ERR_ARG;
+    if (!aligned16(ptr)) return HMM_ERR_LAYOUT;
+  }
+  const FfnMx4Plan f = ffn_mx4_plan(p);
+  if (workspace_bytes < f.bytes) return HMM_ERR_CAPACITY;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return HMM_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const bool pdl = ctx->overlap != 0;
+  CtrlPtrs c = ctrl_at(p, ws + f.off_ctrl);
+  MetaPtrs m = meta_at(p, ws + f.off_meta);
+  {
+    PhaseScope ps(ctx, PH_ROUTE, st, route_launches(p));
+    rc = cuda_rc(launch_route(p, topk_ids, m, c, nullptr, nullptr, ctx->status, st, pdl));
+  }
+  if (rc != HMM_OK) return rc;
+  if (ctx->validate) {
+    rc = read_route_error(ctx, st);
+    if (rc != HMM_OK) return rc;
+  }
+  {
+    PhaseScope ps(ctx, PH_DISPATCH_X, st);
+    rc = cuda_rc(launch_dispatch_mx4(p, f, x, m, ws + f.off_x, ws + f.off_xs, st, pdl));
+  }
+  if (rc != HMM_OK) return rc;
+  const bool inject = ctx->inject_skip_ready == 1;
+  if (inject) ctx->inject_skip_ready = 0;
+  {
+    PhaseScope ps(ctx, PH_GEMM_FWD, st);
+    rc = launch_forward_mx4(env_of(ctx, p, st), p, f, m, c, ws, up_codes, up_scales, down_codes,
+                            down_scales, inject);
+  }
+  if (rc != HMM_OK) return rc;
+  PhaseScope ps(ctx, PH_COMBINE_Y, st);
+  return cuda_rc(launch_combine_y(p, ws + f.off_o, topk_weights, shape->weights_dtype, m, y, st,
+                                  pdl));
 }
 
 int hmm_status(hmm_ctx* ctx, void* stream, int* device_error) {

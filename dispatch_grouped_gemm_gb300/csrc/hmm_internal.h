@@ -152,6 +152,39 @@ cudaError_t launch_dispatch_dy(const Plan& p, const void* dy, const void* w, int
 cudaError_t launch_combine_dx(const Plan& p, const void* dx_perm, const float* dwp, MetaPtrs m,
                               void* dx, void* dw, int w_dtype, cudaStream_t st, bool pdl);
 
+// The router (gate.cu).  check_gate: HMM_OK or the error of an unsupported
+// hmm_gate, before any device work.
+int check_gate(const hmm_gate* g);
+cudaError_t launch_gate_forward(const hmm_gate& g, const void* logits, const float* bias,
+                                int32_t* ids, void* weights, float* scores, cudaStream_t st,
+                                bool pdl);
+cudaError_t launch_gate_backward(const hmm_gate& g, const void* logits, const int32_t* ids,
+                                 const void* d_weights, const float* d_scores, void* d_logits,
+                                 cudaStream_t st, bool pdl);
+
+// Microscaled 4-bit operands (mx4.cu, mx4.cuh): derived sizes of a descriptor.
+struct Mx4Plan {
+  bool gate_up;
+  int64_t kp, kt;      // contraction padded to 32; scale tiles along it
+  int64_t stored, rt;  // stored rows; scale tiles along them
+  size_t codes_bytes, scales_bytes;
+};
+int check_mx4(const hmm_mx4* d);
+Mx4Plan mx4_plan(const hmm_mx4& d);
+cudaError_t launch_mx4_quantize(const hmm_mx4& d, const void* values, void* codes, void* scales,
+                                cudaStream_t st, bool pdl);
+cudaError_t launch_mx4_dequantize(const hmm_mx4& d, const void* codes, const void* scales,
+                                  void* values, cudaStream_t st, bool pdl);
+
+// Workspace of hmm_forward_mx4:
+//   [ctrl | meta | x codes | x scales | a codes | a scales | o]
+// with x and a in 4-bit storage over the padded rows.
+struct FfnMx4Plan {
+  int64_t hp, ip, h_kt, i_kt;  // H and I padded to 32, scale tiles along them
+  size_t off_ctrl, off_meta, off_x, off_xs, off_a, off_as, off_o, bytes;
+};
+FfnMx4Plan ffn_mx4_plan(const Plan& p);
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -180,6 +213,13 @@ int launch_forward_gemms(const GemmEnv& env, const Plan& p, MetaPtrs m, CtrlPtrs
                          const void* x_perm, const void* W1, const void* W2, const void* Ws1,
                          const void* Ws2, void* a, float* h32, void* o, bool skip_ready_release,
                          int* cmb, const void* w, int w_dtype, void* fused_y);
+// the experts' products with 4-bit operands (gmm_mx4.cu): x quantised and
+// permuted; GMM1, SwiGLU, re-quantisation and GMM2 from the workspace ws
+cudaError_t launch_dispatch_mx4(const Plan& p, const FfnMx4Plan& f, const void* x, MetaPtrs m,
+                                uint8_t* codes, uint8_t* scales, cudaStream_t st, bool pdl);
+int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, MetaPtrs m,
+                       CtrlPtrs c, uint8_t* ws, const void* up_codes, const void* up_scales,
+                       const void* down_codes, const void* down_scales, bool skip_ready_release);
 // backward data gradients in one persistent launch: act_grad (+SwiGLU grad,
 // d_w partials; dH and w*a written as a bf16 high part plus an e5m2 low part)
 // and input-grad (released per token block), routed and shared experts.

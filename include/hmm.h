@@ -335,6 +335,113 @@ int hmm_backward_dw(hmm_ctx* ctx, const hmm_shape* shape, const void* saved,
                     void* d_down_proj_weight, void* workspace,
                     size_t workspace_bytes, void* stream);
 
+/* Router: scores of E experts per token, selection and routing weights, in
+ * front of hmm_forward (topk_ids and topk_weights are its inputs).
+ *   p            = softmax(logits) or sigmoid(logits), fp32            [T, E]
+ *   key          = p + bias.  Softmax without a bias and with group_top 1 goes
+ *                  by the logit instead: the same order, with no rounding.
+ *   groups > 1:    a group of E / groups consecutive experts counts by the sum
+ *                  of its group_top best keys; only the topk_groups best
+ *                  groups (ties: lower group) are open.
+ *   topk_ids     = the K best keys of the open groups, best first; equal keys
+ *                  by ascending expert.  Always K distinct ids in [0, E).
+ *   topk_weights = scale * p[topk_ids], with renormalize divided by the sum of
+ *                  the K selected p (the bias only selects).
+ * A logit of -inf closes its expert: p = 0, chosen after every other open
+ * expert.  A row with every logit -inf has p = 0 and weights 0 (softmax or
+ * renormalize divide by 1 there) and a zero gradient.  NaN is chosen first and
+ * shows in the weights. */
+#define HMM_SCORE_SOFTMAX 0
+#define HMM_SCORE_SIGMOID 1
+
+typedef struct hmm_gate {
+  int64_t T;              /* tokens (may be 0) */
+  int64_t E;              /* experts, 1 .. 1024 */
+  int64_t K;              /* experts per token, 1 .. 32, at most those of the open groups */
+  int64_t ld_logits;      /* elements from one row of logits to the next, >= E */
+  int32_t logits_dtype;   /* HMM_DTYPE_BF16 or HMM_DTYPE_F32 (logits, d_logits) */
+  int32_t weights_dtype;  /* HMM_DTYPE_BF16 or HMM_DTYPE_F32 (topk_weights and its gradient) */
+  int32_t score;          /* HMM_SCORE_SOFTMAX or HMM_SCORE_SIGMOID */
+  int32_t renormalize;    /* 0 / 1 */
+  int32_t groups;         /* 1 .. 32, divides E */
+  int32_t topk_groups;    /* 1 .. groups */
+  int32_t group_top;      /* 1 .. E / groups */
+  float scale;            /* finite */
+} hmm_gate;
+
+/* bias fp32 [E] or NULL; scores fp32 [T, E] (p, for a balance loss) or NULL.
+ * Rows of logits start ld_logits apart; every other array is dense.  Needs the
+ * natural alignment of the element types only. */
+int hmm_gate_forward(hmm_ctx* ctx, const hmm_gate* gate, const void* logits,
+                     const float* bias, int32_t* topk_ids, void* topk_weights,
+                     float* scores, void* stream);
+
+/* d_logits [T, E] (dense, logits_dtype) from the gradients of topk_weights
+ * [T, K] and of the scores [T, E] fp32 (either may be NULL: zero), the logits
+ * and the topk_ids of the forward.  The selection itself has no gradient. */
+int hmm_gate_backward(hmm_ctx* ctx, const hmm_gate* gate, const void* logits,
+                      const int32_t* topk_ids, const void* d_topk_weights,
+                      const float* d_scores, void* d_logits, void* stream);
+
+/* Microscaled 4-bit operands: 32 consecutive elements of the contraction (cols)
+ * are a block with one power-of-two scale and 4-bit e2m1 codes (0, .5, 1, 1.5,
+ * 2, 3, 4, 6 and the negatives, code + 8).
+ *   scale of a block  2^(s - 127), s - 127 = floor(log2(max |v|)) - 2 clamped to
+ *                     [-127, 127]; s = 0 for a block of zeros; s = 255 (NaN) if
+ *                     the block holds an infinity or a NaN
+ *   element           v / scale to the nearest code, ties to even, at most 6
+ * Storage of one operand with N stored rows and K = cols rounded up to 32:
+ *   codes   [N, K / 2] bytes, the even column of a pair in the low four bits
+ *   scales  [ceil(N / 128), ceil(cols / 128), 512] bytes: row n, block c at byte
+ *           (n % 32) * 16 + (n / 32 % 4) * 4 + c % 4 of tile (n / 128, c / 4);
+ *           bytes of no row or no block are 0
+ * Elements past cols are 0.  The value arrays by layout:
+ *   HMM_MX4_ROWS     values [rows, cols], rows ld elements apart, batch 1;
+ *                    stored row = row
+ *   HMM_MX4_COLUMNS  values [batch, cols, rows] (expert weights as hmm_forward
+ *                    takes them); stored row = row
+ *   HMM_MX4_GATE_UP  the same for an up-projection (rows = 2I): stored row
+ *                    64 j + i is gate column 32 j + i, 64 j + 32 + i the up
+ *                    column of the same index (i < 32); I rounded up to 32 */
+#define HMM_MX4_ROWS 0
+#define HMM_MX4_COLUMNS 1
+#define HMM_MX4_GATE_UP 2
+
+typedef struct hmm_mx4 {
+  int64_t batch;   /* operands (experts); 1 for HMM_MX4_ROWS */
+  int64_t rows;    /* multiple of 8 (HMM_MX4_COLUMNS), of 16 (HMM_MX4_GATE_UP) */
+  int64_t cols;    /* contraction, multiple of 8 */
+  int64_t ld;      /* HMM_MX4_ROWS: elements between rows, multiple of 8, >= cols */
+  int32_t dtype;   /* of the values: HMM_DTYPE_BF16 or HMM_DTYPE_F32 */
+  int32_t layout;  /* HMM_MX4_* */
+} hmm_mx4;
+
+/* Sizes in bytes of the codes and the scales (either pointer may be NULL). */
+int hmm_mx4_size(const hmm_mx4* desc, size_t* codes_bytes, size_t* scales_bytes);
+
+/* Values to codes and scales, and back (bf16 and fp32 hold every finite 4-bit
+ * value exactly, fp32 subnormals included; a NaN block comes back as NaN).
+ * All pointers 16-byte aligned. */
+int hmm_mx4_quantize(hmm_ctx* ctx, const hmm_mx4* desc, const void* values, void* codes,
+                     void* scales, void* stream);
+int hmm_mx4_dequantize(hmm_ctx* ctx, const hmm_mx4* desc, const void* codes, const void* scales,
+                       void* values, void* stream);
+
+/* hmm_forward for inference with 4-bit experts:
+ *   y[t] = sum_k topk_weights[t,k] * Q(silu(Q(x) . W1g) * (Q(x) . W1u)) . W2
+ * with W1 = up_proj (HMM_MX4_GATE_UP, rows 2I, cols H, batch E) and W2 =
+ * down_proj (HMM_MX4_COLUMNS, rows H, cols I, batch E) in 4-bit storage and Q the
+ * rounding above, of x (bf16) and of the fp32 SwiGLU outputs, in blocks of 32
+ * along H and I.  Products accumulate in fp32, an expert's output row is
+ * rounded to bf16 as in hmm_forward.  shape->shared must be 0.  There is no
+ * backward: train with hmm_forward / hmm_backward and bf16 weights. */
+int hmm_mx4_workspace_size(const hmm_shape* shape, size_t* workspace_bytes);
+int hmm_forward_mx4(hmm_ctx* ctx, const hmm_shape* shape, const void* x,
+                    const int32_t* topk_ids, const void* topk_weights,
+                    const void* up_codes, const void* up_scales,
+                    const void* down_codes, const void* down_scales, void* y,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* Read and clear the device status word in `stream` order, then wait for
  * `stream` (only that stream: other streams of the device keep running).
  * Work queued on `stream` before the call has set its bits by then.
