@@ -57,12 +57,9 @@ static_assert(XBARS * 8 <= 256, "barriers");
 
 struct XProb {
   int kp;        // contraction, padded to 32
-  int kt;        // scale tiles along it
   int n;         // stored weight rows
   int rt;        // scale tiles along them
   int n_tiles;
-  const uint8_t* sa;  // scales of the token rows
-  const uint8_t* sw;  // scales of the weights
 };
 
 struct XParams {
@@ -88,6 +85,8 @@ struct XParams {
 struct XMaps {
   CUtensorMap a[2][4];  // token rows: boxes of 16, 32, 64, 128 rows
   CUtensorMap w[2];
+  CUtensorMap sa[2];    // scales of the token rows: one scale tile row, 2 tiles
+  CUtensorMap sw[2];    // scales of the weights: 2 scale tile rows, 2 tiles each
 };
 
 struct XTile {
@@ -99,13 +98,17 @@ struct XTile {
 };
 
 // ---------------------------------------------------------------------- PTX
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
+// True in one lane of a converged warp.  The issuing warps run their loops with
+// all lanes and issue under this predicate: the operands of the asynchronous
+// instructions then stay in uniform registers.  (With a lane == 0 branch around
+// the loops an MMA took 205 and a scale copy 111 cycles to issue, 1490 per K
+// block, for 540 cycles of tensor work.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 // 512 bytes of scales (32 lanes x 16 bytes) to 4 TMEM columns, the same in
 // each of the four lane quarters.
@@ -136,6 +139,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+
+// One answer for the whole warp (a bounded wait may give up in single lanes).
+__device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
 
 // ---------------------------------------------------------------- scheduling
 // Tickets run over the GMM1 tiles of all experts, then over the GMM2 tiles.
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);  // uniform
   grid_dep_wait();
   const WaitCtl wc{s_abort, P.status, P.budget_ns};
 
@@ -292,131 +298,129 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       }
     }
   } else if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------- producer
-      uint32_t stage = 0, sphase = 0, issued = 0;
-      int slot = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (;;) {
-        if (!mbar_wait(&ti_full[slot], phase, wc)) {
-          ok = false;
-          break;
-        }
-        const XTile ti = s_ti[slot];
-        mbar_arrive(&ti_empty[slot]);
-        if (++slot == XTI_DEPTH) {
-          slot = 0;
-          phase ^= 1u;
-        }
-        if (ti.prob < 0) break;
-        const XProb& pr = P.p[ti.prob];
-        // a was written by this launch's epilogues: the scheduler acquired its
-        // counter, order that with the asynchronous copies below
-        if (ti.prob == 1) fence_proxy_async_global();
-        const int box = ti.rows <= 16 ? 0 : (ti.rows <= 32 ? 1 : (ti.rows <= 64 ? 2 : 3));
-        const int nrt = min(2, pr.rt - ti.n0 / 128);
-        const uint8_t* sa = pr.sa + static_cast<int64_t>(ti.row0 / 128) * pr.kt * MX_TILE_BYTES;
-        const uint8_t* sw =
-            pr.sw + (static_cast<int64_t>(ti.e) * pr.rt + ti.n0 / 128) * pr.kt * MX_TILE_BYTES;
-        for (int k = 0; k < pr.kp; k += XK) {
-          if (!mbar_wait(&empty[stage], sphase ^ 1u, wc)) {
-            ok = false;
-            break;
-          }
+    // --------------------------------------------------------------- producer
+    uint32_t stage = 0, sphase = 0, issued = 0;
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (;;) {
+      ok = warp_all(mbar_wait(&ti_full[slot], phase, wc));
+      if (!ok) break;
+      const XTile ti = s_ti[slot];
+      __syncwarp();
+      if (elect_one()) mbar_arrive(&ti_empty[slot]);
+      if (++slot == XTI_DEPTH) {
+        slot = 0;
+        phase ^= 1u;
+      }
+      if (ti.prob < 0) break;
+      const XProb& pr = P.p[ti.prob];
+      // a was written by this launch's epilogues: the scheduler acquired its
+      // counter, order that with the asynchronous copies below
+      if (ti.prob == 1) fence_proxy_async_global();
+      const int box = ti.rows <= 16 ? 0 : (ti.rows <= 32 ? 1 : (ti.rows <= 64 ? 2 : 3));
+      const CUtensorMap* ma = &maps.a[ti.prob][box];
+      const CUtensorMap* mw = &maps.w[ti.prob];
+      const CUtensorMap* msa = &maps.sa[ti.prob];
+      const CUtensorMap* msw = &maps.sw[ti.prob];
+      const uint32_t bytes = (16u << box) * 128 + XB_BYTES + XSA_BYTES + XSB_BYTES;
+      const int srow = ti.row0 / 128, wrow = ti.e * pr.rt + ti.n0 / 128;
+      for (int kb = 0; kb * XK < pr.kp; ++kb) {
+        ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
+        if (!ok) break;
+        if (elect_one()) {
           uint8_t* sA = smem + stage * XSTAGE_BYTES;
-          uint8_t* sB = sA + XA_BYTES;
-          uint8_t* sSA = sB + XB_BYTES;
-          uint8_t* sSB = sSA + XSA_BYTES;
-          const int kt0 = k / 128;
-          const uint32_t sb = static_cast<uint32_t>(min(2, pr.kt - kt0)) * MX_TILE_BYTES;
-          mbar_arrive_expect_tx(&full[stage], (16u << box) * 128 + XB_BYTES + sb * (1 + nrt));
-          tma_load_3d(sB, &maps.w[ti.prob], &full[stage], k / 2, ti.n0, ti.e);
-          tma_load_2d(sA, &maps.a[ti.prob][box], &full[stage], k / 2, ti.row0);
-          bulk_load(sSA, sa + kt0 * MX_TILE_BYTES, sb, &full[stage]);
-          for (int r = 0; r < nrt; ++r)
-            bulk_load(sSB + r * 2 * MX_TILE_BYTES,
-                      sw + (static_cast<int64_t>(r) * pr.kt + kt0) * MX_TILE_BYTES, sb,
-                      &full[stage]);
-          ++issued;
-          if (++stage == XSTAGES) {
-            stage = 0;
-            sphase ^= 1u;
-          }
+          mbar_arrive_expect_tx(&full[stage], bytes);
+          tma_load_3d(sA + XA_BYTES, mw, &full[stage], kb * (XK / 2), ti.n0, ti.e);
+          tma_load_2d(sA, ma, &full[stage], kb * (XK / 2), ti.row0);
+          tma_load_2d(sA + XA_BYTES + XB_BYTES, msa, &full[stage], kb * 256, srow);
+          tma_load_2d(sA + XA_BYTES + XB_BYTES + XSA_BYTES, msw, &full[stage], kb * 256, wrow);
         }
-        if (!ok) break;
+        __syncwarp();
+        ++issued;
+        if (++stage == XSTAGES) {
+          stage = 0;
+          sphase ^= 1u;
+        }
       }
-      // wait (bounded) for the copies still in flight before leaving
-      if (!ok)
-        for (uint32_t s = 0; s < XSTAGES; ++s)
-          if (issued > s)
-            drain_wait(&full[s], ((issued - 1 - s) / XSTAGES) & 1u, P.budget_ns);
-      grid_dep_launch();  // this CTA is in its last tile
+      if (!ok) break;
     }
+    // wait (bounded) for the copies still in flight before leaving
+    if (!ok && lane == 0)
+      for (uint32_t s = 0; s < XSTAGES; ++s)
+        if (issued > s) drain_wait(&full[s], ((issued - 1 - s) / XSTAGES) & 1u, P.budget_ns);
+    grid_dep_launch();  // this CTA is in its last tile
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMA issue
-      uint32_t stage = 0, sphase = 0;
-      int slot = 0;
-      uint32_t phase = 0;
-      uint32_t n = 0;  // tiles so far
-      for (;;) {
-        if (!mbar_wait(&ti_full[slot], phase, wc)) break;
-        const XTile ti = s_ti[slot];
-        mbar_arrive(&ti_empty[slot]);
-        if (++slot == XTI_DEPTH) {
-          slot = 0;
-          phase ^= 1u;
-        }
-        if (ti.prob < 0) break;
-        const XProb& pr = P.p[ti.prob];
-        // tile n - 1's shared columns and all of tile n - 2 have been read
-        if (n > 0 && !mbar_wait(tfree, (n - 1) & 1u, wc)) break;
-        tc_fence_after();
-        const uint32_t acc = n & 1u;
-        const uint32_t d = tmem + acc * XACC1;
-        const int cols = min(XN, (pr.n - ti.n0 + 15) / 16 * 16);
-        const int nrt = min(2, pr.rt - ti.n0 / 128);
-        const uint32_t id0 = idesc_mx4(cols, 0), id1 = idesc_mx4(cols, 2);
-        bool ok = true;
-        for (int k = 0; k < pr.kp; k += XK) {
-          if (!mbar_wait(&full[stage], sphase, wc)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a = smem_u32(smem + stage * XSTAGE_BYTES);
-          const uint32_t b = a + XA_BYTES;
-          const uint32_t sa = b + XB_BYTES;
-          const uint32_t sb = sa + XSA_BYTES;
-          const int steps = min(4, (pr.kp - k + 63) / 64);
-          const int tiles = (steps + 1) / 2;
-          for (int i = 0; i < tiles; ++i) {
-            tmem_cp_scales(tmem + XSF_COL + 4 * i,
-                           smem_desc(sa + i * MX_TILE_BYTES, 0, 128, LAYOUT_NONE));
-            for (int r = 0; r < nrt; ++r)
-              tmem_cp_scales(tmem + XSF_COL + 8 + 8 * i + 4 * r,
-                             smem_desc(sb + (2 * r + i) * MX_TILE_BYTES, 0, 128, LAYOUT_NONE));
-          }
-          for (int s = 0; s < steps; ++s)
-            umma_mx4(d, smem_desc(a + s * 32, 16, 1024, LAYOUT_SW128),
-                     smem_desc(b + s * 32, 16, 1024, LAYOUT_SW128), (s & 1) ? id1 : id0,
-                     tmem + XSF_COL + 4 * (s >> 1), tmem + XSF_COL + 8 + 8 * (s >> 1),
-                     (k > 0 || s > 0) ? 1u : 0u);
-          umma_commit(&empty[stage]);
-          if (++stage == XSTAGES) {
-            stage = 0;
-            sphase ^= 1u;
-          }
-        }
-        if (!ok) break;
-        umma_commit(&tfull[acc]);
-        ++n;
+    // -------------------------------------------------------------- MMA issue
+    uint32_t stage = 0, sphase = 0;
+    int slot = 0;
+    uint32_t phase = 0;
+    uint32_t n = 0;  // tiles so far
+    for (;;) {
+      if (!warp_all(mbar_wait(&ti_full[slot], phase, wc))) break;
+      const XTile ti = s_ti[slot];
+      __syncwarp();
+      if (elect_one()) mbar_arrive(&ti_empty[slot]);
+      if (++slot == XTI_DEPTH) {
+        slot = 0;
+        phase ^= 1u;
       }
-      // every MMA issued by this thread completes before TMEM is released
-      umma_commit(mma_done);
-      drain_wait(mma_done, 0, P.budget_ns);
+      if (ti.prob < 0) break;
+      const XProb& pr = P.p[ti.prob];
+      // tile n - 1's shared columns and all of tile n - 2 have been read
+      if (n > 0 && !warp_all(mbar_wait(tfree, (n - 1) & 1u, wc))) break;
+      tc_fence_after();
+      const uint32_t acc = n & 1u;
+      const uint32_t d = tmem + acc * XACC1;
+      const int cols = min(XN, (pr.n - ti.n0 + 15) / 16 * 16);
+      const bool wide = cols > 128;  // the second scale tile row is in use
+      const uint32_t id0 = idesc_mx4(cols, 0), id1 = idesc_mx4(cols, 2);
+      bool ok = true;
+      for (int k = 0; k < pr.kp; k += XK) {
+        ok = warp_all(mbar_wait(&full[stage], sphase, wc));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t a = smem_u32(smem) + stage * XSTAGE_BYTES;
+          const uint64_t da = smem_desc(a, 16, 1024, LAYOUT_SW128);
+          const uint64_t db = smem_desc(a + XA_BYTES, 16, 1024, LAYOUT_SW128);
+          const uint64_t ds = smem_desc(a + XA_BYTES + XB_BYTES, 0, 128, LAYOUT_NONE);
+          const uint64_t dt = smem_desc(a + XA_BYTES + XB_BYTES + XSA_BYTES, 0, 128, LAYOUT_NONE);
+          const int left = pr.kp - k;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // scales of 128 elements, then the two MMAs of 64 that use them
+            // (descriptor addresses count 16 bytes)
+            if (128 * i < left) {
+              tmem_cp_scales(tmem + XSF_COL + 4 * i, ds + i * 32);
+              tmem_cp_scales(tmem + XSF_COL + 8 + 8 * i, dt + i * 32);
+              if (wide) tmem_cp_scales(tmem + XSF_COL + 12 + 8 * i, dt + (2 + i) * 32);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (64 * j < left)
+              umma_mx4(d, da + 2 * j, db + 2 * j, (j & 1) ? id1 : id0,
+                       tmem + XSF_COL + 4 * (j >> 1), tmem + XSF_COL + 8 + 8 * (j >> 1),
+                       (k > 0 || j > 0) ? 1u : 0u);
+          umma_commit(&empty[stage]);
+        }
+        __syncwarp();
+        if (++stage == XSTAGES) {
+          stage = 0;
+          sphase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) umma_commit(&tfull[acc]);
+      __syncwarp();
+      ++n;
     }
+    // every MMA issued by this warp's elected lane completes before TMEM is released
+    __syncwarp();
+    if (elect_one()) umma_commit(mma_done);
+    __syncwarp();
+    drain_wait(mma_done, 0, P.budget_ns);
   } else {
     // --------------------------------------------------------------- epilogue
     const int q = warp & 3;          // TMEM lane quarter
@@ -643,6 +647,21 @@ int map_codes(const GemmEnv& env, CUtensorMap* map, const void* base, int64_t by
              : HMM_ERR_CUDA;
 }
 
+// a scale array (rows of kt tiles) with boxes of 2 tiles x box_rows rows
+int map_scales(const GemmEnv& env, CUtensorMap* map, const void* base, int64_t kt, int64_t rows,
+               uint32_t box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kt * (MX_TILE_BYTES / 4)),
+                              static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kt * MX_TILE_BYTES)};
+  const cuuint32_t box[2] = {2 * MX_TILE_BYTES / 4, box_rows}, es[2] = {1, 1};
+  return env.encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides,
+                    box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? HMM_OK
+             : HMM_ERR_CUDA;
+}
+
 }  // namespace
 
 int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, MetaPtrs m,
@@ -657,18 +676,19 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
   }
   rc |= map_codes(env, &maps.w[0], up_codes, f.hp / 2, 2 * f.ip, p.E, XN);
   rc |= map_codes(env, &maps.w[1], down_codes, f.ip / 2, p.H, p.E, XN);
+  rc |= map_scales(env, &maps.sa[0], ws + f.off_xs, f.h_kt, p.R / XM, 1);
+  rc |= map_scales(env, &maps.sa[1], ws + f.off_as, f.i_kt, p.R / XM, 1);
+  rc |= map_scales(env, &maps.sw[0], up_scales, f.h_kt, p.E * ((2 * f.ip + 127) / 128), 2);
+  rc |= map_scales(env, &maps.sw[1], down_scales, f.i_kt, p.E * ((p.H + 127) / 128), 2);
   if (rc != HMM_OK) return HMM_ERR_CUDA;
-  auto prob = [](XProb& q, int64_t kp, int64_t n, const uint8_t* sa, const void* sw) {
+  auto prob = [](XProb& q, int64_t kp, int64_t n) {
     q.kp = static_cast<int>(kp);
-    q.kt = static_cast<int>((kp + 127) / 128);
     q.n = static_cast<int>(n);
     q.rt = static_cast<int>((n + 127) / 128);
     q.n_tiles = static_cast<int>((n + XN - 1) / XN);
-    q.sa = sa;
-    q.sw = static_cast<const uint8_t*>(sw);
   };
-  prob(P.p[0], f.hp, 2 * f.ip, ws + f.off_xs, up_scales);
-  prob(P.p[1], f.ip, p.H, ws + f.off_as, down_scales);
+  prob(P.p[0], f.hp, 2 * f.ip);
+  prob(P.p[1], f.ip, p.H);
   P.poff = m.poff;
   P.counts = m.counts;
   P.E = static_cast<int>(p.E);
