@@ -102,6 +102,9 @@ class HmmError(RuntimeError):
         super().__init__(f"{where}: {hmm_error_string(code)} (code {code})")
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
 _lib = None
 _lib_lock = threading.Lock()
 
@@ -180,7 +183,8 @@ def _nbytes(t) -> int:
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without building the objects (3 us)
+        return _raw_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -427,6 +431,9 @@ class Context:
     @classmethod
     def for_device(cls, device) -> "Context":
         idx = device.index if device.index is not None else torch.cuda.current_device()
+        c = cls._cache.get(idx)
+        if c is not None:
+            return c
         with cls._cache_lock:
             c = cls._cache.get(idx)
             if c is None:
@@ -576,13 +583,12 @@ _SCORES = {"softmax": HMM_SCORE_SOFTMAX, "sigmoid": HMM_SCORE_SIGMOID}
 
 
 def _gate_forward(logits, gate, bias, return_scores):
-    c = Context.for_device(logits.device)
-    ids = torch.empty((gate.T, gate.K), dtype=torch.int32, device=logits.device)
-    w = torch.empty((gate.T, gate.K), dtype=_TORCH_WDTYPES[gate.weights_dtype],
-                    device=logits.device)
-    scores = (torch.empty((gate.T, gate.E), dtype=torch.float32, device=logits.device)
+    dev = logits.device
+    ids = torch.empty((gate.T, gate.K), dtype=torch.int32, device=dev)
+    w = torch.empty((gate.T, gate.K), dtype=_TORCH_WDTYPES[gate.weights_dtype], device=dev)
+    scores = (torch.empty((gate.T, gate.E), dtype=torch.float32, device=dev)
               if return_scores else None)
-    hmm_gate_forward(c.handle, gate, logits, bias, ids, w, scores)
+    hmm_gate_forward(Context.for_device(dev).handle, gate, logits, bias, ids, w, scores)
     return ids, w, scores
 
 
@@ -603,9 +609,9 @@ class _MoEGate(torch.autograd.Function):
         logits, ids = ctx.saved_tensors
         dw = None if dw is None else dw.contiguous()
         ds = None if ds is None else ds.contiguous()
-        dl = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        c = Context.for_device(logits.device)
-        hmm_gate_backward(c.handle, ctx.gate, logits, ids, dw, ds, dl)
+        dev = logits.device
+        dl = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        hmm_gate_backward(Context.for_device(dev).handle, ctx.gate, logits, ids, dw, ds, dl)
         return dl, None, None, None
 
 
@@ -624,26 +630,28 @@ def moe_gate(logits, k, *, score="softmax", bias=None, groups=1, topk_groups=Non
     in the logits through the weights and the scores."""
     if logits.dim() != 2:
         raise ValueError("logits [T, E] expected")
-    if logits.dtype not in _WDTYPES or weights_dtype not in _WDTYPES:
+    ldt, wdt = _WDTYPES.get(logits.dtype), _WDTYPES.get(weights_dtype)
+    if ldt is None or wdt is None:
         raise TypeError("logits and weights_dtype must be bfloat16 or float32")
-    if score not in _SCORES:
+    kind = _SCORES.get(score)
+    if kind is None:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
     T, E = logits.shape
     if not logits.is_cuda or (E > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be a CUDA tensor with unit stride along the experts")
-    if T > 1 and logits.stride(0) < E:
-        logits = logits.contiguous()  # broadcast or overlapping rows
+    ld = logits.stride(0)
+    if ld < E:
+        if T > 1:
+            logits = logits.contiguous()  # broadcast or overlapping rows
+        ld = E
     if bias is not None:
-        if tuple(bias.shape) != (E,) or bias.device != logits.device or not bias.is_contiguous():
+        if bias.shape != (E,) or not bias.is_contiguous() or bias.device != logits.device:
             raise ValueError(f"bias must be a contiguous [{E}] tensor on the logits' device")
         if bias.dtype != torch.float32:
             raise TypeError("bias must be float32")
-    gate = make_gate(T, E, k, score=_SCORES[score], ld_logits=max(E, logits.stride(0)),
-                     logits_dtype=_WDTYPES[logits.dtype], weights_dtype=_WDTYPES[weights_dtype],
-                     renormalize=1 if renormalize else 0, groups=groups,
-                     topk_groups=groups if topk_groups is None else topk_groups,
-                     group_top=group_top, scale=scale)
-    if torch.is_grad_enabled() and logits.requires_grad:
+    gate = HmmGate(T, E, k, ld, ldt, wdt, kind, 1 if renormalize else 0, groups,
+                   groups if topk_groups is None else topk_groups, group_top, scale)
+    if logits.requires_grad and torch.is_grad_enabled():
         ids, w, scores = _MoEGate.apply(logits, gate, bias, return_scores)
     else:
         ids, w, scores = _gate_forward(logits, gate, bias, return_scores)
@@ -706,22 +714,23 @@ class Mx4Tensor:
 
     def dequantize(self, dtype=torch.bfloat16):
         """The values that the codes and scales stand for (exact)."""
-        if dtype not in _WDTYPES:
+        code = _WDTYPES.get(dtype)
+        if code is None:
             raise TypeError("dtype must be bfloat16 or float32")
-        out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
-        d = make_mx4(self.rows, self.cols, batch=self.batch, dtype=_WDTYPES[dtype],
-                     layout=self.layout)
-        hmm_mx4_dequantize(Context.for_device(out.device).handle, d, self.codes, self.scales, out)
+        dev = self.codes.device
+        out = torch.empty(self.shape, dtype=dtype, device=dev)
+        d = HmmMx4(self.batch, self.rows, self.cols, self.cols, code, self.layout)
+        hmm_mx4_dequantize(Context.for_device(dev).handle, d, self.codes, self.scales, out)
         return out
 
 
 def _mx4_of(values, batch, rows, cols, ld, layout):
     cs, ss = Mx4Tensor._shapes(batch, rows, cols, layout)
-    d = make_mx4(rows, cols, batch=batch, ld=ld, dtype=_WDTYPES[values.dtype], layout=layout)
-    hmm_mx4_size(d)  # refuses an unsupported shape before anything is allocated
-    codes = torch.empty(cs, dtype=torch.uint8, device=values.device)
-    scales = torch.empty(ss, dtype=torch.uint8, device=values.device)
-    hmm_mx4_quantize(Context.for_device(values.device).handle, d, values, codes, scales)
+    d = HmmMx4(batch, rows, cols, ld, _WDTYPES[values.dtype], layout)
+    dev = values.device
+    codes = torch.empty(cs, dtype=torch.uint8, device=dev)
+    scales = torch.empty(ss, dtype=torch.uint8, device=dev)
+    hmm_mx4_quantize(Context.for_device(dev).handle, d, values, codes, scales)
     return Mx4Tensor(codes, scales, batch, rows, cols, layout)
 
 
@@ -735,9 +744,10 @@ def mx4_quantize(x):
     R, C = x.shape
     if not x.is_cuda or (C > 1 and x.stride(1) != 1):
         raise ValueError("x must be a CUDA tensor with unit stride along its columns")
-    if R > 1 and x.stride(0) < C:
-        x = x.contiguous()  # broadcast or overlapping rows
-    return _mx4_of(x, 1, R, C, x.stride(0) if R > 1 else C, HMM_MX4_ROWS)
+    ld = x.stride(0) if R > 1 else C
+    if ld < C:
+        x, ld = x.contiguous(), C  # broadcast or overlapping rows
+    return _mx4_of(x, 1, R, C, ld, HMM_MX4_ROWS)
 
 
 def mx4_quantize_experts(w, *, gate_up=False):
@@ -764,6 +774,7 @@ def moe_ffn_mx4(x, topk_ids, topk_weights, up_proj, down_proj):
     if x.dim() != 2 or topk_ids.dim() != 2:
         raise ValueError("x [T, H] and topk_ids [T, K] expected")
     T, H = x.shape
+    K = topk_ids.shape[1]
     E, I = up_proj.batch, up_proj.rows // 2
     if up_proj.cols != H or (down_proj.batch, down_proj.cols, down_proj.rows) != (E, I, H):
         raise ValueError(f"up_proj {up_proj.shape} and down_proj {down_proj.shape} do not match "
@@ -774,17 +785,19 @@ def moe_ffn_mx4(x, topk_ids, topk_weights, up_proj, down_proj):
         raise TypeError("x must be bfloat16")
     if topk_ids.dtype != torch.int32:
         raise TypeError("topk_ids must be int32")
-    if topk_weights.dtype not in _WDTYPES:
+    wdt = _WDTYPES.get(topk_weights.dtype)
+    if wdt is None:
         raise TypeError("topk_weights must be bfloat16 or float32")
     for t in (x, topk_ids, topk_weights):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError("all arguments must be contiguous CUDA tensors")
-    if torch.is_grad_enabled() and (x.requires_grad or topk_weights.requires_grad):
+    if (x.requires_grad or topk_weights.requires_grad) and torch.is_grad_enabled():
         raise RuntimeError("moe_ffn_mx4 has no backward: call it under torch.no_grad(), or train "
                            "with moe_ffn")
-    shape = make_shape(T, H, I, E, topk_ids.shape[1], _WDTYPES[topk_weights.dtype])
-    ws = _u8(hmm_mx4_workspace_size(shape), x.device)
-    y = torch.empty_like(x)
-    hmm_forward_mx4(Context.for_device(x.device).handle, shape, x, topk_ids, topk_weights,
+    shape = HmmShape(T, H, I, E, K, wdt, 0)
+    dev = x.device
+    ws = torch.empty(hmm_mx4_workspace_size(shape), dtype=torch.uint8, device=dev)
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    hmm_forward_mx4(Context.for_device(dev).handle, shape, x, topk_ids, topk_weights,
                     up_proj.codes, up_proj.scales, down_proj.codes, down_proj.scales, y, ws)
     return y
