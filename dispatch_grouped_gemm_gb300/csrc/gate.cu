@@ -107,15 +107,16 @@ __device__ __forceinline__ float ld_w(const void* w, int64_t i, int f32) {
              : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
 }
 
-// Order-preserving map of a float to an unsigned integer above 0: -inf is the
-// least, NaN (any) the greatest, -0 equals +0; and back.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0xffffffffu;
-  const uint32_t u = __float_as_uint(v + 0.0f);
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+// Order-preserving map of a float to an integer above CLOSED: -inf is the
+// least, NaN the greatest (the addition returns the one positive NaN, and +0
+// for -0); and back.
+constexpr int CLOSED = static_cast<int>(0x80000000u);
+__device__ __forceinline__ int order_key(float v) {
+  const int u = __float_as_int(v + 0.0f);
+  return u ^ ((u >> 31) & 0x7fffffff);
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
+__device__ __forceinline__ float key_value(int k) {
+  return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
 }
 
 template <int L = 32>
@@ -173,14 +174,13 @@ namespace {
 
 // Worth of group `lane` from the keys of the whole row (any group shape): the
 // group_top best keys by repeated selection.
-__device__ __noinline__ uint32_t group_worth(const uint32_t* keys, int n, int top) {
-  const uint32_t* k = keys + (threadIdx.x & 31) * n;
+__device__ __noinline__ int group_worth(const int* keys, int n, int top) {
+  const int* k = keys + (threadIdx.x & 31) * n;
   float worth = 0.0f;
-  uint32_t last = 0xffffffffu;
+  int last = 0x7fffffff;
   int last_i = -1;
   for (int r = 0; r < top; ++r) {
-    uint32_t bk = 0;
-    int bi = 0;
+    int bk = CLOSED, bi = 0;
     for (int i = 0; i < n; ++i) {
       const bool taken = r > 0 && (k[i] > last || (k[i] == last && i <= last_i));
       if (!taken && k[i] > bk) {
@@ -195,33 +195,33 @@ __device__ __noinline__ uint32_t group_worth(const uint32_t* keys, int n, int to
   return order_key(worth);
 }
 
-// Closes (key 0) the experts of all but the topk_groups best groups.
+// Closes the experts of all but the topk_groups best groups.
 template <int C>
-__device__ __forceinline__ void keep_groups(const GateArgs& a, uint32_t (&key)[C], int lane,
-                                            int base, uint32_t* smem) {
+__device__ __forceinline__ void keep_groups(const GateArgs& a, int (&key)[C], int lane,
+                                            int base, int* smem) {
   if (a.lane_groups) {
     const int L = 32 / a.groups;  // lanes per group
-    uint32_t k1 = key[0], k2 = 0u;
+    int k1 = key[0], k2 = CLOSED;
 #pragma unroll
     for (int j = 1; j < C; ++j) {
       k2 = max(k2, min(k1, key[j]));
       k1 = max(k1, key[j]);
     }
     for (int d = 1; d < L; d <<= 1) {
-      const uint32_t o1 = __shfl_xor_sync(FULL, k1, d), o2 = __shfl_xor_sync(FULL, k2, d);
+      const int o1 = __shfl_xor_sync(FULL, k1, d), o2 = __shfl_xor_sync(FULL, k2, d);
       k2 = max(min(k1, o1), max(k2, o2));
       k1 = max(k1, o1);
     }
-    const uint32_t worth = a.group_top == 1 ? k1 : order_key(key_value(k1) + key_value(k2));
+    const int worth = a.group_top == 1 ? k1 : order_key(key_value(k1) + key_value(k2));
     const int g = lane / L;
     int better = 0;  // groups that come before this one
     for (int x = 1; x < a.groups; ++x) {
-      const uint32_t o = __shfl_xor_sync(FULL, worth, x * L);
+      const int o = __shfl_xor_sync(FULL, worth, x * L);
       better += o > worth || (o == worth && (g ^ x) < g);
     }
     if (better >= a.topk_groups) {
 #pragma unroll
-      for (int j = 0; j < C; ++j) key[j] = 0u;
+      for (int j = 0; j < C; ++j) key[j] = CLOSED;
     }
     return;
   }
@@ -230,18 +230,18 @@ __device__ __forceinline__ void keep_groups(const GateArgs& a, uint32_t (&key)[C
     if (j < a.c && base + j < a.E) smem[base + j] = key[j];
   __syncwarp();
   const int n = a.E / a.groups;
-  uint32_t worth = lane < a.groups ? group_worth(smem, n, a.group_top) : 0u;
+  int worth = lane < a.groups ? group_worth(smem, n, a.group_top) : CLOSED;
   __syncwarp();
   uint32_t open = 0;
   for (int r = 0; r < a.topk_groups; ++r) {
-    const uint32_t best = __reduce_max_sync(FULL, worth);
+    const int best = __reduce_max_sync(FULL, worth);
     const int g = __ffs(__ballot_sync(FULL, worth == best)) - 1;
     open |= 1u << g;
-    if (lane == g) worth = 0u;
+    if (lane == g) worth = CLOSED;
   }
 #pragma unroll
   for (int j = 0; j < C; ++j)
-    if (base + j < a.E && !((open >> ((base + j) / n)) & 1u)) key[j] = 0u;
+    if (base + j < a.E && !((open >> ((base + j) / n)) & 1u)) key[j] = CLOSED;
 }
 
 }  // namespace
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
     gate_forward_kernel(const GateArgs a, const void* __restrict__ logits,
                         const float* __restrict__ bias, int32_t* __restrict__ ids,
                         void* __restrict__ weights, float* __restrict__ scores) {
-  extern __shared__ uint32_t gate_smem[];  // per warp [E] (groups that are no lane runs)
+  extern __shared__ int gate_smem[];  // per warp [E] (groups that are no lane runs)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int base = lane * a.c;
   const bool by_logit = !SIG && bias == nullptr && a.group_top == 1;
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * GATE_WARPS + warp; t < a.T;
        t += static_cast<int64_t>(gridDim.x) * GATE_WARPS) {
     float l[C], p[C];
-    uint32_t key[C];
+    int key[C];
     ld_chunk<C, BF16, VEC>(logits, t * a.ld, base, a.c, a.E, l);
     float m = 0.0f, z = 1.0f;
     if constexpr (SIG) {
@@ -281,12 +281,11 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
       const bool in = VEC || (j < a.c && base + j < a.E);
       float v = by_logit ? l[j] : p[j];
       if (bias && in) v += __ldg(bias + base + j);
-      key[j] = in ? order_key(v) : 0u;
+      key[j] = in ? order_key(v) : CLOSED;
     }
     if (a.groups > 1) keep_groups<C>(a, key, lane, base, gate_smem + warp * a.E);
     // K rounds: the best key of the lanes' best; lane k keeps expert k
-    uint32_t bk = key[0];
-    int bj = 0;
+    int bk = key[0], bj = 0;
 #pragma unroll
     for (int j = 1; j < C; ++j)
       if (key[j] > bk) {
@@ -295,16 +294,15 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
       }
     int my_id = 0;
     for (int k = 0; k < a.K; ++k) {
-      const uint32_t best = __reduce_max_sync(FULL, bk);
+      const int best = __reduce_max_sync(FULL, bk);
       const int win = __ffs(__ballot_sync(FULL, bk == best)) - 1;
       const int e = __shfl_sync(FULL, base + bj, win);
       if (lane == k) my_id = e;
       if (lane == win) {
-        uint32_t nk = 0u;
-        int nj = 0;
+        int nk = CLOSED, nj = 0;
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-          if (j == bj) key[j] = 0u;
+          if (j == bj) key[j] = CLOSED;
           if (key[j] > nk) {
             nk = key[j];
             nj = j;
@@ -335,6 +333,215 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
   }
 }
 
+// Many tokens: LT lanes per token, up to N experts per lane, so that a warp
+// works on 32 / LT tokens at once.  Lane q of a token holds the experts
+// (i LT + q) 4 .. + 3 (16-byte loads); its keys also sit in shared memory,
+// where a round of the selection reaches them by a computed index, and the
+// maxima of its runs of eight in registers.  A round costs about 70
+// instructions for all of the warp's tokens (the one-warp kernel above: 100
+// for one).  Needs E and, with groups, E / groups to be multiples of 4.
+template <int N, int LT, bool BF16, bool SIG>
+__global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 6 : 8)
+    gate_forward_many_kernel(const GateArgs a, const void* __restrict__ logits,
+                             const float* __restrict__ bias, int32_t* __restrict__ ids,
+                             void* __restrict__ weights, float* __restrict__ scores) {
+  constexpr int TW = 32 / LT;     // tokens per warp
+  constexpr int S = N / 8;        // runs of eight per lane
+  extern __shared__ int gate_smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = lane % LT, tok = lane / LT;
+  // per warp: the keys [32 lanes][N], the 16-byte pieces of a lane permuted so
+  // that lanes do not meet in a bank; then per token the groups' worths and,
+  // after them, the chosen experts
+  int* wkeys = gate_smem + warp * (32 * N + TW * 32);
+  int* worths = wkeys + 32 * N + tok * 32;
+  int* chosen = worths;
+  auto piece = [&](int of_lane, int i) {
+    return reinterpret_cast<int4*>(wkeys + of_lane * N) +
+           (N == 32 ? i ^ (of_lane & 7) : (N == 16 ? i ^ ((of_lane >> 1) & 3) : i));
+  };
+  const bool by_logit = !SIG && bias == nullptr && a.group_top == 1;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t t_raw = (static_cast<int64_t>(blockIdx.x) * GATE_WARPS + warp) * TW + tok;
+  const bool live = t_raw < a.T;
+  const int64_t t = live ? t_raw : a.T - 1;  // (every lane takes part in the shuffles)
+  float l[N];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const int e = (i * LT + q) * 4;
+    l[4 * i] = l[4 * i + 1] = l[4 * i + 2] = l[4 * i + 3] = -INFINITY;
+    if (e < a.E) {
+      if constexpr (BF16) {
+        const uint2 v =
+            *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(logits) + t * a.ld + e);
+        l[4 * i] = __uint_as_float(v.x << 16);
+        l[4 * i + 1] = __uint_as_float(v.x & 0xFFFF0000u);
+        l[4 * i + 2] = __uint_as_float(v.y << 16);
+        l[4 * i + 3] = __uint_as_float(v.y & 0xFFFF0000u);
+      } else {
+        const float4 v =
+            *reinterpret_cast<const float4*>(static_cast<const float*>(logits) + t * a.ld + e);
+        l[4 * i] = v.x;
+        l[4 * i + 1] = v.y;
+        l[4 * i + 2] = v.z;
+        l[4 * i + 3] = v.w;
+      }
+    }
+  }
+  float m = 0.0f, z = 1.0f;
+  if constexpr (!SIG) {
+    m = l[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) m = fmaxf(m, l[j]);
+#pragma unroll
+    for (int d = LT / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, d));
+    if (m == -INFINITY) m = 0.0f;
+    if (scores || !by_logit || !a.renorm) {
+      z = 0.0f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) z += expf(l[j] - m);
+      z = lanes_sum<LT>(z);
+      if (z == 0.0f) z = 1.0f;
+    }
+  }
+  int seg[S];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const int e = (i * LT + q) * 4;
+    const bool in = e < a.E;
+    float v[4];
+    int k[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      v[r] = l[4 * i + r];
+      if (SIG)
+        v[r] = sigmoid_rn(v[r]);
+      else if (scores || !by_logit)
+        v[r] = expf(v[r] - m) / z;
+    }
+    if (scores && in && live)
+      *reinterpret_cast<float4*>(scores + t * a.E + e) = make_float4(v[0], v[1], v[2], v[3]);
+    if (bias && in) {
+      const float4 b = __ldg(reinterpret_cast<const float4*>(bias + e));
+      v[0] += b.x;
+      v[1] += b.y;
+      v[2] += b.z;
+      v[3] += b.w;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) k[r] = in ? order_key(by_logit ? l[4 * i + r] : v[r]) : CLOSED;
+    *piece(lane, i) = make_int4(k[0], k[1], k[2], k[3]);
+    const int top = max(max(k[0], k[1]), max(k[2], k[3]));
+    seg[i / 2] = i % 2 ? max(seg[i / 2], top) : top;
+  }
+  __syncwarp();
+  if (a.groups > 1) {
+    const int n = a.E / a.groups;
+    // lane q: the worths of groups q, q + LT, ..
+    for (int g = q; g < a.groups; g += LT) {
+      int k1 = CLOSED, k2 = CLOSED;
+      for (int e = g * n; e < (g + 1) * n; e += 4) {
+        const int4 k = *piece(tok * LT + (e >> 2) % LT, (e >> 2) / LT);
+        const int h1 = max(k.x, k.y), h2 = max(k.z, k.w);
+        const int s2 = max(min(h1, h2), max(min(k.x, k.y), min(k.z, k.w)));
+        const int s1 = max(h1, h2);
+        k2 = max(min(k1, s1), max(k2, s2));
+        k1 = max(k1, s1);
+      }
+      worths[g] = a.group_top == 1 ? k1 : order_key(key_value(k1) + key_value(k2));
+    }
+    __syncwarp();
+    uint32_t open = 0u;
+    for (int g = q; g < a.groups; g += LT) {
+      const int w = worths[g];
+      int better = 0;
+      for (int o = 0; o < a.groups; ++o) better += worths[o] > w || (worths[o] == w && o < g);
+      if (better < a.topk_groups) open |= 1u << g;
+    }
+#pragma unroll
+    for (int d = LT / 2; d > 0; d >>= 1) open |= __shfl_xor_sync(FULL, open, d);
+    __syncwarp();  // (chosen takes the worths' place)
+    // close the others; e / n by a reciprocal, exact for e < 1024
+    const uint32_t inv = ((1u << 20) + n - 1) / n;
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const int e = (i * LT + q) * 4;
+      const bool on = (open >> ((e * inv) >> 20)) & 1u;
+      if (!on && e < a.E) *piece(lane, i) = make_int4(CLOSED, CLOSED, CLOSED, CLOSED);
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int4 x = *piece(lane, 2 * s), y = *piece(lane, 2 * s + 1);
+      seg[s] = max(max(max(x.x, x.y), max(x.z, x.w)), max(max(y.x, y.y), max(y.z, y.w)));
+    }
+  }
+  for (int k = 0; k < a.K; ++k) {
+    int mine = seg[0];
+#pragma unroll
+    for (int s = 1; s < S; ++s) mine = max(mine, seg[s]);
+    int best = mine;
+#pragma unroll
+    for (int d = LT / 2; d > 0; d >>= 1) best = max(best, __shfl_xor_sync(FULL, best, d));
+    // the first of this lane's keys that equals its maximum, and the maximum
+    // of the rest of its run
+    int s0 = S - 1;
+#pragma unroll
+    for (int s = S - 2; s >= 0; --s)
+      if (seg[s] == mine) s0 = s;
+    const int4 x = *piece(lane, 2 * s0), y = *piece(lane, 2 * s0 + 1);
+    const int run[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    int first = 8, rest = CLOSED;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (first == 8 && run[j] == mine)
+        first = j;
+      else
+        rest = max(rest, run[j]);  // (an equal key behind the first stays)
+    }
+    const int at = 8 * s0 + first;
+    const int e = (((at >> 2) * LT) + q) * 4 + (at & 3);
+    int pick = mine == best ? e : 0x7fffffff;
+#pragma unroll
+    for (int d = LT / 2; d > 0; d >>= 1) pick = min(pick, __shfl_xor_sync(FULL, pick, d));
+    if (mine == best && pick == e) {
+      reinterpret_cast<int*>(piece(lane, at >> 2))[at & 3] = CLOSED;
+      chosen[k] = e;
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        if (s == s0) seg[s] = rest;
+    }
+  }
+  __syncwarp();
+  float w[32 / LT];
+  float sum = 0.0f;
+#pragma unroll
+  for (int x = 0; x < 32 / LT; ++x) {
+    const int k = q + x * LT;
+    w[x] = 0.0f;
+    if (k < a.K) {
+      const float lk = ld_logit<BF16>(logits, t * a.ld + chosen[k]);
+      w[x] = SIG ? sigmoid_rn(lk) : expf(lk - m) / z;
+      sum += w[x];
+    }
+  }
+  if (a.renorm) sum = lanes_sum<LT>(sum);
+#pragma unroll
+  for (int x = 0; x < 32 / LT; ++x) {
+    const int k = q + x * LT;
+    if (k < a.K && live) {
+      float v = w[x];
+      if (a.renorm) v = v / (sum == 0.0f ? 1.0f : sum);
+      v *= a.scale;
+      ids[t * a.K + k] = chosen[k];
+      if (a.weights_f32)
+        static_cast<float*>(weights)[t * a.K + k] = v;
+      else
+        static_cast<__nv_bfloat16*>(weights)[t * a.K + k] = __float2bfloat16_rn(v);
+    }
+  }
+}
+
 // With g_k = scale * d_topk_weights[k], n_k = p_k / sum_sel p and D = sum g n:
 //   without renormalize   dp[topk_ids[k]] = g_k
 //   with it               dp[topk_ids[k]] = (g_k - D) / sum_sel p
@@ -351,7 +558,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
     gate_backward_kernel(const GateArgs a, const void* __restrict__ logits,
                          const int32_t* __restrict__ ids, const void* __restrict__ d_weights,
                          const float* __restrict__ d_scores, void* __restrict__ d_logits) {
-  extern __shared__ uint32_t gate_smem[];  // per warp: gradients at the selected experts
+  extern __shared__ int gate_smem[];  // per warp: gradients at the selected experts
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int base = lane * a.c;
   float* sd = reinterpret_cast<float*>(gate_smem) + warp * (32 * C);
@@ -537,9 +744,7 @@ cudaError_t by_length(const hmm_gate& g, bool vec, Args&&... args) {
   if (c <= 1) return by_type<F, 1>(g, vec, args...);
   if (c <= 2) return by_type<F, 2>(g, vec, args...);
   if (c <= 4) return by_type<F, 4>(g, vec, args...);
-  if (c <= 6) return by_type<F, 6>(g, vec, args...);
   if (c <= 8) return by_type<F, 8>(g, vec, args...);
-  if (c <= 12) return by_type<F, 12>(g, vec, args...);
   if (c <= 16) return by_type<F, 16>(g, vec, args...);
   return by_type<F, 32>(g, vec, args...);
 }
@@ -560,6 +765,24 @@ struct RunForward {
                          smem, st, pdl, 1, a, logits, bias, ids, weights, scores);
   }
 };
+
+template <int N, int LT>
+cudaError_t run_many(const hmm_gate& g, const void* logits, const float* bias, int32_t* ids,
+                     void* weights, float* scores, cudaStream_t st, bool pdl) {
+  constexpr int TOKENS = GATE_WARPS * 32 / LT;
+  const bool sig = g.score == HMM_SCORE_SIGMOID;
+  auto kern = g.logits_dtype == HMM_DTYPE_BF16
+                  ? (sig ? gate_forward_many_kernel<N, LT, true, true>
+                         : gate_forward_many_kernel<N, LT, true, false>)
+                  : (sig ? gate_forward_many_kernel<N, LT, false, true>
+                         : gate_forward_many_kernel<N, LT, false, false>);
+  const size_t smem = sizeof(uint32_t) * GATE_WARPS * (32 * N + 32 / LT * 32);
+  return launch_kernel(kern, static_cast<unsigned>((g.T + TOKENS - 1) / TOKENS), GATE_WARPS * 32,
+                       smem, st, pdl, 1, gate_args(g), logits, bias, ids, weights, scores);
+}
+
+// Tokens from which the kernel for many tokens is the faster one.
+constexpr int64_t GATE_MANY = 4096;
 
 struct RunBackward {
   template <int C, bool BF16, bool SIG, bool VEC>
@@ -620,6 +843,20 @@ cudaError_t launch_gate_forward(const hmm_gate& g, const void* logits, const flo
   const GateArgs a = gate_args(g);
   const bool vec = gate_vec(a, g.logits_dtype == HMM_DTYPE_BF16 ? 2 : 4, g.ld_logits, logits) &&
                    (!scores || aligned_to(scores, 16));
+  const int64_t logit_bytes = g.logits_dtype == HMM_DTYPE_BF16 ? 2 : 4;
+  if (g.T >= GATE_MANY && g.E % 4 == 0 && (g.groups == 1 || (g.E / g.groups) % 4 == 0) &&
+      g.group_top <= 2 && g.ld_logits % 4 == 0 && aligned_to(logits, 4 * logit_bytes) &&
+      aligned_to(bias, 16) && aligned_to(scores, 16)) {
+    // 32 to 40 experts per lane (E = 256, T = 65537: 64 per lane 64 us, few warps
+    // fit; 32 51 us; 16 72 us, fewer tokens share a round.  E = 160, T = 131072: 40
+    // per lane 59 us, 24 63 us)
+    if (g.E <= 64) return run_many<16, 4>(g, logits, bias, ids, weights, scores, st, pdl);
+    if (g.E <= 128) return run_many<32, 4>(g, logits, bias, ids, weights, scores, st, pdl);
+    if (g.E <= 160) return run_many<40, 4>(g, logits, bias, ids, weights, scores, st, pdl);
+    if (g.E <= 256) return run_many<32, 8>(g, logits, bias, ids, weights, scores, st, pdl);
+    if (g.E <= 512) return run_many<32, 16>(g, logits, bias, ids, weights, scores, st, pdl);
+    return run_many<32, 32>(g, logits, bias, ids, weights, scores, st, pdl);
+  }
   return by_length<RunForward>(g, vec, logits, bias, ids, weights, scores, st, pdl);
 }
 

@@ -584,26 +584,9 @@ __global__ void __launch_bounds__(MXD_WARPS * 32)
 #pragma unroll
   for (int i = 0; i < MXD_UNROLL; ++i) {
     const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, max((u[j] << 16) & 0x7FFFFFFFu, u[j] & 0x7FFF0000u));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t b = mx_scale_byte(m);
-    const float inv = mx_inverse_scale(b);
-    float w[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w[2 * j] = __uint_as_float(u[j] << 16) * inv;
-      w[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u) * inv;
-    }
-    q[i] = mx_codes8(w);
-    // the four blocks of this lane's scale tile row as one word
-    uint32_t word = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      word |= __shfl_sync(0xffffffffu, b, (lane & 16) + 4 * j) << (8 * j);
-    s[i] = word;
+    const uint32_t b = quad_scale_bf16(u);
+    q[i] = codes8_bf16(u, b);
+    s[i] = tile_word(b, lane);
   }
   for (int k = 0; k < K; ++k) {
     const int32_t prow = __shfl_sync(0xffffffffu, prow_l, k);

@@ -4,101 +4,141 @@
 // half a byte plus a 32nd of a byte written (and the other way round).
 #include "mx4.cuh"
 
+#include <algorithm>
+
 namespace hmm {
 
 namespace {
 
 constexpr int MX_THREADS = 256;
+constexpr int MX_STEPS = 4;  // most steps of a row that a warp loads at once
 
-template <bool F32>
 __device__ __forceinline__ void ld_values8(const void* p, int64_t i, float (&v)[8]) {
-  if constexpr (F32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(u[j] << 16);
-      v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-    }
-  }
+  const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  const float4 a = q[0], b = q[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-template <bool F32>
 __device__ __forceinline__ void st_values8(void* p, int64_t i, const float (&v)[8]) {
-  if constexpr (F32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    uint4 q;
-    uint32_t* u = reinterpret_cast<uint32_t*>(&q);
+  uint4 q;
+  uint32_t* u = reinterpret_cast<uint32_t*>(&q);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-      u[j] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = q;
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    u[j] = *reinterpret_cast<const uint32_t*>(&b);
   }
-}
-
-// The 8 values of one thread and those of its three neighbours are one block.
-__device__ __forceinline__ uint32_t quad_scale(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  return mx_scale_byte(m);
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = q;
 }
 
 }  // namespace
 
-// One thread per 8 elements; rows and columns run over the scale tiles'
-// 128 x 128, so that the padding scales are written as zeros too.
-template <bool F32>
+// One warp per row; blockIdx.y and gridDim.y share out the pieces of a row, U
+// steps of 256 columns each.  A lane holds 8 elements, four lanes a block,
+// sixteen lanes the four blocks of a scale tile's row.  Rows and columns run
+// over whole scale tiles, so that the padding scales are written too.  (Lane
+// groups walking (row, scale tile) pairs in one flat order, without idle lanes
+// at the end of a row, were slower: their index arithmetic costs more.)
+template <bool F32, int U>
 __global__ void __launch_bounds__(MX_THREADS)
     mx4_quantize_rows_kernel(const void* __restrict__ src, int64_t rows, int64_t cols, int64_t ld,
                              int64_t kt, uint8_t* __restrict__ codes,
                              uint8_t* __restrict__ scales) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * MX_THREADS + threadIdx.x;
-  const int64_t g = i % (kt * 16), r = i / (kt * 16);
+  const int lane = threadIdx.x & 31;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (MX_THREADS / 32) + (threadIdx.x >> 5);
+  const bool in = r < rows;
+  const int64_t kp = (cols + 31) / 32 * 32;
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t c = g * 8;
-  float v[8] = {};
-  if (r < rows && c < cols) ld_values8<F32>(src, r * ld + c, v);
-  const uint32_t s = quad_scale(v);
-  const float inv = mx_inverse_scale(s);
+  for (int64_t p = static_cast<int64_t>(blockIdx.y) * (256 * U); p < kt * 128;
+       p += static_cast<int64_t>(gridDim.y) * (256 * U)) {
+    const int64_t c0 = p + 8 * lane;
+    float v[U][F32 ? 8 : 1];
+    uint4 b[U];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] *= inv;
-  const int64_t kp = (cols + 31) / 32 * 32;
-  if (r < rows && c < kp)
-    *reinterpret_cast<uint32_t*>(codes + r * (kp / 2) + c / 2) = mx_codes8(v);
-  if ((g & 3) == 0 && r < (rows + 127) / 128 * 128)
-    scales[mx_scale_offset(r, g >> 2, kt)] = static_cast<uint8_t>(s);
+    for (int i = 0; i < U; ++i) {
+      const int64_t c = c0 + 256 * i;
+      const bool on = in && c < cols;
+      if constexpr (F32) {
+        if (on) {
+          ld_values8(src, r * ld + c, v[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+        }
+      } else {
+        b[i] = on ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + r * ld + c)
+                  : make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t c = c0 + 256 * i;
+      uint32_t s, q;
+      if constexpr (F32) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        s = mx_scale_byte(m);
+        const float inv = mx_inverse_scale(s);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+        q = mx_codes8(v[i]);
+      } else {
+        const uint32_t u[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+        s = quad_scale_bf16(u);
+        q = codes8_bf16(u, s);
+      }
+      const uint32_t word = tile_word(s, lane);
+      if (in && c < kp) *reinterpret_cast<uint32_t*>(codes + r * (kp / 2) + c / 2) = q;
+      if ((lane & 15) == 0 && c < kt * 128)
+        *reinterpret_cast<uint32_t*>(scales + mx_scale_offset(r, c / 32, kt)) = word;
+    }
+  }
 }
 
-template <bool F32>
+// The way back: 16-byte stores, so 8 bf16 or 4 fp32 values per lane and step.
+template <bool F32, int U>
 __global__ void __launch_bounds__(MX_THREADS)
     mx4_dequantize_rows_kernel(const uint8_t* __restrict__ codes,
                                const uint8_t* __restrict__ scales, int64_t rows, int64_t cols,
                                int64_t ld, int64_t kt, void* __restrict__ dst) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * MX_THREADS + threadIdx.x;
-  const int64_t n8 = cols / 8;
-  const int64_t g = i % n8, r = i / n8;
+  constexpr int PER = F32 ? 4 : 8, STEP = 32 * PER;
+  const int lane = threadIdx.x & 31;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (MX_THREADS / 32) + (threadIdx.x >> 5);
+  const int64_t kp = (cols + 31) / 32 * 32;
   grid_dep_wait();
   grid_dep_launch();
   if (r >= rows) return;
-  const int64_t kp = (cols + 31) / 32 * 32;
-  float v[8];
-  mx_values8(*reinterpret_cast<const uint32_t*>(codes + r * (kp / 2) + g * 4),
-             mx_scale(scales[mx_scale_offset(r, g >> 2, kt)]), v);
-  st_values8<F32>(dst, r * ld + g * 8, v);
+  for (int64_t p = static_cast<int64_t>(blockIdx.y) * (STEP * U); p < cols;
+       p += static_cast<int64_t>(gridDim.y) * (STEP * U)) {
+    const int64_t c0 = p + PER * lane;
+    uint32_t q[U], s[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t c = c0 + STEP * i;
+      if (c < cols) {
+        const uint8_t* at = codes + r * (kp / 2) + c / 2;
+        q[i] = F32 ? *reinterpret_cast<const uint16_t*>(at) : *reinterpret_cast<const uint32_t*>(at);
+        s[i] = scales[mx_scale_offset(r, c / 32, kt)];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t c = c0 + STEP * i;
+      if (c < cols) {
+        float v[8];
+        mx_values8(q[i], mx_scale(s[i]), v);
+        if constexpr (F32)
+          *reinterpret_cast<float4*>(static_cast<float*>(dst) + r * ld + c) =
+              make_float4(v[0], v[1], v[2], v[3]);
+        else
+          st_values8(dst, r * ld + c, v);
+      }
+    }
+  }
 }
 
 namespace {
@@ -135,44 +175,75 @@ __global__ void __launch_bounds__(TW_THREADS)
   grid_dep_launch();
   const int64_t c = source_column(d0 + 2 * lane, n, gate_up);
   const int64_t kb = k0 + warp * 32;
-  const int64_t base = e * cols * n;
-  float v[2][32];
+  const int64_t at = (e * cols + kb) * n + c;
+  const int kn = c < 0 ? 0 : static_cast<int>(max(int64_t(0), min(int64_t(32), cols - kb)));
+  uint32_t q[2][4], s[2];
+  if constexpr (F32) {
+    const float* p = static_cast<const float*>(src) + at;
+    float2 v[32];
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    v[0][k] = v[1][k] = 0.0f;
-    if (c >= 0 && kb + k < cols) {
-      const int64_t at = base + (kb + k) * n + c;
-      if constexpr (F32) {
-        const float2 f = *reinterpret_cast<const float2*>(static_cast<const float*>(src) + at);
-        v[0][k] = f.x;
-        v[1][k] = f.y;
-      } else {
-        const uint32_t u =
-            *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(src) + at);
-        v[0][k] = __uint_as_float(u << 16);
-        v[1][k] = __uint_as_float(u & 0xFFFF0000u);
+    for (int k = 0; k < 32; ++k)
+      v[k] = k < kn ? *reinterpret_cast<const float2*>(p + k * n) : make_float2(0.0f, 0.0f);
+    uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      m0 = max(m0, __float_as_uint(v[k].x) & 0x7FFFFFFFu);
+      m1 = max(m1, __float_as_uint(v[k].y) & 0x7FFFFFFFu);
+    }
+    s[0] = mx_scale_byte(m0);
+    s[1] = mx_scale_byte(m1);
+    const float i0 = mx_inverse_scale(s[0]), i1 = mx_inverse_scale(s[1]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float w0[8], w1[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        w0[k] = v[8 * j + k].x * i0;
+        w1[k] = v[8 * j + k].y * i1;
       }
+      q[0][j] = mx_codes8(w0);
+      q[1][j] = mx_codes8(w1);
+    }
+  } else {
+    // both columns of the lane in one word: maxima and scaling two at a time
+    const uint16_t* p = static_cast<const uint16_t*>(src) + at;
+    uint32_t v[32];
+    if (kn == 32) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = *reinterpret_cast<const uint32_t*>(p + k * n);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        v[k] = k < kn ? *reinterpret_cast<const uint32_t*>(p + k * n) : 0u;
+    }
+    uint32_t m[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 32; ++k) m[k & 3] = pair_amax(m[k & 3], v[k]);
+    const uint32_t mm = pair_amax(pair_amax(m[0], m[1]), pair_amax(m[2], m[3]));
+    s[0] = mx_scale_byte(mm << 16);
+    s[1] = mx_scale_byte(mm & 0xFFFF0000u);
+    // (powers of two up to 2^127: their upper halves are the bf16 values)
+    const uint32_t inv = (__float_as_uint(mx_inverse_scale(s[0])) >> 16) |
+                         (__float_as_uint(mx_inverse_scale(s[1])) & 0xFFFF0000u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float w0[8], w1[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t x = pair_mul(v[8 * j + k], inv);
+        w0[k] = pair_lo(x);
+        w1[k] = pair_hi(x);
+      }
+      q[0][j] = mx_codes8(w0);
+      q[1][j] = mx_codes8(w1);
     }
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < 32; ++k) m = max(m, __float_as_uint(v[h][k]) & 0x7FFFFFFFu);
-    const uint32_t s = mx_scale_byte(m);
-    const float inv = mx_inverse_scale(s);
-    uint32_t q[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float w[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = v[h][8 * j + k] * inv;
-      q[j] = mx_codes8(w);
-    }
     const int row = 2 * lane + h;
     *reinterpret_cast<uint4*>(s_codes + row * TW_PITCH + warp * 16) =
-        make_uint4(q[0], q[1], q[2], q[3]);
-    s_scales[row * 4 + warp] = static_cast<uint8_t>(s);
+        make_uint4(q[h][0], q[h][1], q[h][2], q[h][3]);
+    s_scales[row * 4 + warp] = static_cast<uint8_t>(s[h]);
   }
   __syncthreads();
   uint8_t* dst = codes + e * stored * (kp / 2);
@@ -190,6 +261,10 @@ __global__ void __launch_bounds__(TW_THREADS)
   }
 }
 
+// The way back, 256 stored rows x 128 elements of the contraction per block:
+// a warp takes 64 rows (lane l: rows 2 l, 2 l + 1) and the four blocks one after
+// another, so that the warps of a block write neighbouring pieces of the same
+// output rows.
 template <bool F32>
 __global__ void __launch_bounds__(TW_THREADS)
     mx4_dequantize_columns_kernel(const uint8_t* __restrict__ codes,
@@ -197,42 +272,67 @@ __global__ void __launch_bounds__(TW_THREADS)
                                   int64_t cols, int64_t kt, bool gate_up,
                                   void* __restrict__ dst) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t e = blockIdx.z, d0 = static_cast<int64_t>(blockIdx.y) * TW_ROWS;
-  const int64_t kb = static_cast<int64_t>(blockIdx.x) * 128 + warp * 32;
+  const int64_t e = blockIdx.z;
+  const int64_t d = (static_cast<int64_t>(blockIdx.y) * 4 + warp) * TW_ROWS + 2 * lane;
+  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * 128;
   const int64_t kp = (cols + 31) / 32 * 32;
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t d = d0 + 2 * lane;
+  if (d >= stored) return;
   const int64_t c = source_column(d, n, gate_up);
-  if (c < 0 || kb >= cols) return;
+  if (c < 0) return;
   const int64_t rt = (stored + 127) / 128;
-  float v[2][32];
+  const uint8_t* p = codes + (e * stored + d) * (kp / 2) + k0 / 2;
+  uint4 q[2][4];
+  uint32_t s[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint4 q =
-        *reinterpret_cast<const uint4*>(codes + (e * stored + d + h) * (kp / 2) + kb / 2);
-    const float s = mx_scale(
-        scales[e * rt * kt * MX_TILE_BYTES + mx_scale_offset(d + h, kb / 32, kt)]);
-    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      q[h][b] = k0 + 32 * b < kp ? *reinterpret_cast<const uint4*>(p + h * (kp / 2) + 16 * b)
+                                 : make_uint4(0, 0, 0, 0);
+    s[h] = *reinterpret_cast<const uint32_t*>(scales + e * rt * kt * MX_TILE_BYTES +
+                                              mx_scale_offset(d + h, k0 / 32, kt));
+  }
+  const int64_t at = (e * cols + k0) * n + c;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const float s0 = mx_scale((s[0] >> (8 * b)) & 255u), s1 = mx_scale((s[1] >> (8 * b)) & 255u);
+    const uint32_t u0[4] = {q[0][b].x, q[0][b].y, q[0][b].z, q[0][b].w};
+    const uint32_t u1[4] = {q[1][b].x, q[1][b].y, q[1][b].z, q[1][b].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float w[8];
-      mx_values8(u[j], s, w);
+      if (k0 + 32 * b + 8 * j >= cols) break;  // (cols is a multiple of 8)
+      float v0[8], v1[8];
+      mx_values8(u0[j], s0, v0);
+      mx_values8(u1[j], s1, v1);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[h][8 * j + k] = w[k];
+      for (int k = 0; k < 8; ++k) {
+        const int64_t i = at + (32 * b + 8 * j + k) * n;
+        if constexpr (F32) {
+          *reinterpret_cast<float2*>(static_cast<float*>(dst) + i) = make_float2(v0[k], v1[k]);
+        } else {
+          *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(dst) + i) =
+              __floats2bfloat162_rn(v0[k], v1[k]);
+        }
+      }
     }
   }
-#pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    if (kb + k >= cols) break;
-    const int64_t at = e * cols * n + (kb + k) * n + c;
-    if constexpr (F32) {
-      *reinterpret_cast<float2*>(static_cast<float*>(dst) + at) = make_float2(v[0][k], v[1][k]);
-    } else {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[0][k], v[1][k]);
-      *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(dst) + at) = b;
-    }
-  }
+}
+
+// A row of `steps` warp steps goes in pieces of u <= MX_STEPS steps, about the
+// same for every piece (9 steps as 3 + 3 + 3, not 4 + 4 + 1).  Few rows: the
+// pieces of a row go to several warps.
+struct RowsGrid {
+  dim3 grid;
+  int u;
+};
+static RowsGrid rows_grid(int64_t rows, int64_t steps) {
+  constexpr int64_t WARPS = MX_THREADS / 32;
+  const int64_t pieces = (steps + MX_STEPS - 1) / MX_STEPS;
+  const int64_t parts = rows >= 16384 ? 1 : std::min<int64_t>(pieces, 64);
+  return {dim3(static_cast<unsigned>((rows + WARPS - 1) / WARPS), static_cast<unsigned>(parts)),
+          static_cast<int>((steps + pieces - 1) / pieces)};
 }
 
 Mx4Plan mx4_plan(const hmm_mx4& d) {
@@ -258,9 +358,7 @@ int check_mx4(const hmm_mx4* d) {
     if (d->batch != 1) return HMM_ERR_SHAPE;  // rows are one operand
     if (d->ld < d->cols) return HMM_ERR_SHAPE;
     if (d->ld % 8 != 0) return HMM_ERR_LAYOUT;
-    // one thread per 8 elements of whole 128 x 128 tiles
-    if (d->cols > (1 << 24) || d->rows > (int64_t(1) << 38) / ((d->cols + 127) / 128 * 128))
-      return HMM_ERR_SHAPE;
+    if (d->cols > (1 << 24) || d->rows > (int64_t(1) << 32)) return HMM_ERR_SHAPE;
   } else {
     if (d->rows % (d->layout == HMM_MX4_GATE_UP ? 16 : 8) != 0) return HMM_ERR_LAYOUT;
     if (d->batch > 65535 || d->rows > (1 << 21) || d->cols > (1 << 24)) return HMM_ERR_SHAPE;
@@ -275,11 +373,17 @@ cudaError_t launch_mx4_quantize(const hmm_mx4& d, const void* values, void* code
   uint8_t* c = static_cast<uint8_t*>(codes);
   uint8_t* s = static_cast<uint8_t*>(scales);
   if (d.layout == HMM_MX4_ROWS) {
-    const int64_t threads = p.rt * 128 * p.kt * 16;
-    const unsigned grid = static_cast<unsigned>((threads + MX_THREADS - 1) / MX_THREADS);
-    auto kern = f32 ? mx4_quantize_rows_kernel<true> : mx4_quantize_rows_kernel<false>;
-    return launch_kernel(kern, grid, MX_THREADS, 0, st, pdl, 1, values, d.rows, d.cols, d.ld, p.kt,
-                         c, s);
+    const RowsGrid g = rows_grid(p.rt * 128, (p.kt + 1) / 2);
+    auto kern = f32 ? (g.u == 1   ? mx4_quantize_rows_kernel<true, 1>
+                       : g.u == 2 ? mx4_quantize_rows_kernel<true, 2>
+                       : g.u == 3 ? mx4_quantize_rows_kernel<true, 3>
+                                  : mx4_quantize_rows_kernel<true, 4>)
+                    : (g.u == 1   ? mx4_quantize_rows_kernel<false, 1>
+                       : g.u == 2 ? mx4_quantize_rows_kernel<false, 2>
+                       : g.u == 3 ? mx4_quantize_rows_kernel<false, 3>
+                                  : mx4_quantize_rows_kernel<false, 4>);
+    return launch_kernel(kern, g.grid, MX_THREADS, 0, st, pdl, 1, values, d.rows, d.cols, d.ld,
+                         p.kt, c, s);
   }
   const dim3 grid(static_cast<unsigned>(p.kt), static_cast<unsigned>(p.rt * 2),
                   static_cast<unsigned>(d.batch));
@@ -295,14 +399,20 @@ cudaError_t launch_mx4_dequantize(const hmm_mx4& d, const void* codes, const voi
   const uint8_t* c = static_cast<const uint8_t*>(codes);
   const uint8_t* s = static_cast<const uint8_t*>(scales);
   if (d.layout == HMM_MX4_ROWS) {
-    const int64_t threads = d.rows * (d.cols / 8);
-    const unsigned grid = static_cast<unsigned>((threads + MX_THREADS - 1) / MX_THREADS);
-    auto kern = f32 ? mx4_dequantize_rows_kernel<true> : mx4_dequantize_rows_kernel<false>;
-    return launch_kernel(kern, grid, MX_THREADS, 0, st, pdl, 1, c, s, d.rows, d.cols, d.ld, p.kt,
+    const RowsGrid g = rows_grid(d.rows, (d.cols + (f32 ? 127 : 255)) / (f32 ? 128 : 256));
+    auto kern = f32 ? (g.u == 1   ? mx4_dequantize_rows_kernel<true, 1>
+                       : g.u == 2 ? mx4_dequantize_rows_kernel<true, 2>
+                       : g.u == 3 ? mx4_dequantize_rows_kernel<true, 3>
+                                  : mx4_dequantize_rows_kernel<true, 4>)
+                    : (g.u == 1   ? mx4_dequantize_rows_kernel<false, 1>
+                       : g.u == 2 ? mx4_dequantize_rows_kernel<false, 2>
+                       : g.u == 3 ? mx4_dequantize_rows_kernel<false, 3>
+                                  : mx4_dequantize_rows_kernel<false, 4>);
+    return launch_kernel(kern, g.grid, MX_THREADS, 0, st, pdl, 1, c, s, d.rows, d.cols, d.ld, p.kt,
                          values);
   }
   const dim3 grid(static_cast<unsigned>(p.kt),
-                  static_cast<unsigned>((p.stored + TW_ROWS - 1) / TW_ROWS),
+                  static_cast<unsigned>((p.stored + 4 * TW_ROWS - 1) / (4 * TW_ROWS)),
                   static_cast<unsigned>(d.batch));
   auto kern = f32 ? mx4_dequantize_columns_kernel<true> : mx4_dequantize_columns_kernel<false>;
   return launch_kernel(kern, grid, TW_THREADS, 0, st, pdl, 1, c, s, d.rows, p.stored, d.cols, p.kt,

@@ -74,6 +74,52 @@ __device__ __forceinline__ void mx_values8(uint32_t codes, float scale, float (&
   }
 }
 
+// Pairs of bf16 in 32-bit words (the low half first).
+__device__ __forceinline__ float pair_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float pair_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+// Larger magnitude of each half, NaN if either is (m: a result of this).
+__device__ __forceinline__ uint32_t pair_amax(uint32_t m, uint32_t v) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(v & 0x7FFF7FFFu));
+  return r;
+}
+// Each half times a power of two given as a pair (exact where the block's scale
+// makes the product matter: results below 2^-126 round to 0 either way).
+__device__ __forceinline__ uint32_t pair_mul(uint32_t v, uint32_t s) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(s));
+  return r;
+}
+
+// The scale byte of a block whose 32 bf16 values are held by four neighbouring
+// lanes, eight each (u: four pairs).
+__device__ __forceinline__ uint32_t quad_scale_bf16(const uint32_t (&u)[4]) {
+  uint32_t m = pair_amax(pair_amax(u[0] & 0x7FFF7FFFu, u[1]), pair_amax(u[2] & 0x7FFF7FFFu, u[3]));
+  m = pair_amax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = pair_amax(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  return mx_scale_byte(max(m << 16, m & 0xFFFF0000u));
+}
+// Eight bf16 values to codes.
+__device__ __forceinline__ uint32_t codes8_bf16(const uint32_t (&u)[4], uint32_t s) {
+  const float inv = mx_inverse_scale(s);
+  float w[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    w[2 * j] = pair_lo(u[j]) * inv;
+    w[2 * j + 1] = pair_hi(u[j]) * inv;
+  }
+  return mx_codes8(w);
+}
+// The scale bytes of the four blocks that 16 lanes hold, as the word of a scale
+// tile's row (s: this lane's block).
+__device__ __forceinline__ uint32_t tile_word(uint32_t s, int lane) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w |= __shfl_sync(0xffffffffu, s, (lane & 16) + 4 * j) << (8 * j);
+  return w;
+}
+
 // Byte offset of the scale of (row, block) in an operand's scale array with
 // kt = ceil(cols / 128) tiles per 128 rows.
 __host__ __device__ __forceinline__ int64_t mx_scale_offset(int64_t row, int64_t block, int64_t kt) {

@@ -130,6 +130,45 @@ def test_scores_and_bf16_weights(score):
     compare(50, 96, 4, score, torch.bfloat16, scored=True, renorm=True)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K,groups,topk_groups,group_top", [
+    (64, 6, 1, 1, 1), (8, 8, 1, 1, 1), (128, 8, 1, 1, 1), (100, 7, 5, 3, 2), (160, 6, 8, 3, 1),
+    (256, 8, 8, 4, 2), (224, 32, 4, 3, 2), (300, 5, 1, 1, 1), (512, 9, 32, 5, 2), (384, 8, 8, 4, 1),
+    (1024, 16, 16, 2, 2), (30, 3, 1, 1, 1), (96, 6, 4, 2, 3)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_tokens_like_few(score, E, K, groups, topk_groups, group_top, dtype):
+    """A long batch gives row by row what short ones give: same ids, weights
+    and scores up to the order of their sums (1e-6), closed experts, equal
+    keys, infinities and NaN among them."""
+    T = 4103
+    l = logits_of(T, E, dtype, E)
+    l[5], l[6], l[7], l[8, 3], l[9, 2], l[10, :E // 2] = -math.inf, 0.0, -0.0, math.nan, math.inf, 2.0
+    l[torch.rand((T, E), generator=torch.Generator().manual_seed(3)) < 0.05] = -math.inf
+    l = l.to(DEV)
+    bias = (torch.randint(-20, 21, (E,), generator=torch.Generator().manual_seed(4)) * 1e-3).to(DEV)
+    for b in (None, bias):
+        for renorm in (False, True):
+            kw = dict(score=score, bias=b, groups=groups, topk_groups=topk_groups,
+                      group_top=group_top, renormalize=renorm, scale=1.5)
+            a = hmm.moe_gate(l, K, return_scores=True, **kw)
+            parts = [hmm.moe_gate(x, K, return_scores=True, **kw) for x in l.split(1024)]
+            want = [torch.cat(p) for p in zip(*parts)]
+            # sums in another order move p + bias or p + p by a rounding: only
+            # exact keys have to select the same
+            exact = score == "sigmoid" and group_top <= 2 or b is None and group_top == 1
+            same = (a[0] == want[0]).all(1)
+            assert same.all() if exact else same.float().mean() > 0.995
+            for i in (1, 2):
+                x, y = a[i][same], want[i][same]
+                assert torch.equal(torch.isnan(x), torch.isnan(y))
+                assert torch.allclose(x, y, rtol=2e-6, atol=1e-12, equal_nan=True)
+            no_scores = hmm.moe_gate(l, K, **kw)
+            assert torch.equal(no_scores[0], a[0])
+            odd = torch.empty((T, E + 3), dtype=dtype, device=DEV)[:, 3:]
+            odd.copy_(l)
+            assert torch.equal(hmm.moe_gate(odd, K, **kw)[0][same], a[0][same])
+
+
 def test_equal_keys_go_to_the_lowest_index():
     l = torch.zeros((3, 70), device=DEV)
     l[1, 40:] = 1.0
