@@ -48,7 +48,7 @@ constexpr int XBUF = 32 * 64;        // staged output: 32 rows of 32 bf16
 constexpr int XTI_DEPTH = 3;
 constexpr int XACC1 = XN - 32;       // second accumulator's first column
 constexpr int XSF_COL = XACC1 + XN;  // scales of A: 2 x 4 columns, then of B: 2 x 8
-constexpr int XBARS = 2 * XSTAGES + 3 + 2 * XTI_DEPTH + 1;
+constexpr int XBARS = 2 * XSTAGES + 3 + 2 * XTI_DEPTH + 2;
 constexpr int XSMEM = 1024 + XSTAGES * XSTAGE_BYTES + XEPI_WARPS * XBUF + 256 +
                       XTI_DEPTH * 20 + 8 + 4 * (MAX_E + 1);
 static_assert(XSMEM <= 232448, "shared memory per CTA");
@@ -60,14 +60,14 @@ struct XProb {
   int n;         // stored weight rows
   int rt;        // scale tiles along them
   int n_tiles;
+  int tn;        // weight rows per tile: 256, or 128 (few tiles)
 };
 
 struct XParams {
   XProb p[2];
-  const int32_t* poff;
   const int32_t* counts;
   int E;
-  int* ticket;
+  int* ticket;      // tiles taken after every CTA's first
   int* ready;       // per 128 token rows: epilogue warps of GMM1 that are done
   int ready_unit;   // ... when all are
   int signal;       // 0: test-only fault injection, nothing is released
@@ -145,34 +145,44 @@ __device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffff
 
 // ---------------------------------------------------------------- scheduling
 // Tickets run over the GMM1 tiles of all experts, then over the GMM2 tiles.
-__device__ __forceinline__ int xblocks(const XParams& P, int e) {
-  return (P.counts[e] + XM - 1) / XM;
-}
-
-// Prefix sums of the experts' token blocks (one warp).
-__device__ void xschedule(const XParams& P, int* pref) {
+// pref[e]: token blocks of the experts before e, times 128, plus the rows that
+// e's last block lacks (0 .. 127); pref[E]: all token blocks, times 128.  (The
+// padded row space gives every expert whole blocks, so 128 times its blocks is
+// also e's first row.)
+__device__ void xschedule(const XParams& P, uint32_t* pref) {
+  constexpr int U = 8;  // loads in flight per lane
   const int lane = threadIdx.x & 31;
-  int carry = 0;
-  if (lane == 0) pref[0] = 0;
-  for (int base = 0; base < P.E; base += 32) {
-    const int e = base + lane;
-    int inc = e < P.E ? xblocks(P, e) : 0;
+  uint32_t carry = 0;
+  for (int base = 0; base < P.E; base += 32 * U) {
+    uint32_t cnt[U];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += n;
+    for (int u = 0; u < U; ++u) {
+      const int e = base + 32 * u + lane;
+      cnt[u] = e < P.E ? static_cast<uint32_t>(P.counts[e]) : 0u;
     }
-    if (e < P.E) pref[e + 1] = carry + inc;
-    carry += __shfl_sync(0xffffffffu, inc, 31);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int e = base + 32 * u + lane;
+      const uint32_t blocks = (cnt[u] + XM - 1) / XM;
+      uint32_t inc = blocks;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t n = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += n;
+      }
+      if (e < P.E) pref[e] = ((carry + inc - blocks) << 7) | (blocks * XM - cnt[u]);
+      carry += __shfl_sync(0xffffffffu, inc, 31);
+    }
   }
+  if (lane == 0) pref[P.E] = carry << 7;
   __syncwarp();
 }
 
-__device__ bool xlocate(const XParams& P, const int* pref, int t, XTile& ti) {
-  const int blocks = pref[P.E];
+__device__ bool xlocate(const XParams& P, const uint32_t* pref, uint32_t t, XTile& ti) {
+  const uint32_t blocks = pref[P.E] >> 7;
   ti.prob = t >= blocks * P.p[0].n_tiles;
   if (ti.prob) t -= blocks * P.p[0].n_tiles;
-  const int nt = P.p[ti.prob].n_tiles;
+  const uint32_t nt = P.p[ti.prob].n_tiles;
   if (t >= blocks * nt) {
     ti.prob = -1;
     return false;
@@ -180,19 +190,19 @@ __device__ bool xlocate(const XParams& P, const int* pref, int t, XTile& ti) {
   int lo = 0, hi = P.E - 1;  // largest expert whose first tile is at most t
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (pref[mid] * nt <= t)
+    if ((pref[mid] >> 7) * nt <= t)
       lo = mid;
     else
       hi = mid - 1;
   }
   ti.e = lo;
-  const int nb = pref[lo + 1] - pref[lo];
-  const int r = t - pref[lo] * nt;
-  const int wt = r / nb;  // token blocks innermost: a weight tile is reused from L2
-  const int b = r - wt * nb;
-  ti.row0 = P.poff[lo] + XM * b;
-  ti.rows = min(XM, P.counts[lo] - XM * b);
-  ti.n0 = wt * XN;
+  const uint32_t b0 = pref[lo] >> 7, nb = (pref[lo + 1] >> 7) - b0;
+  const uint32_t r = t - b0 * nt;
+  const uint32_t wt = r / nb;  // token blocks innermost: a weight tile is reused from L2
+  const uint32_t b = r - wt * nb;
+  ti.row0 = static_cast<int>((b0 + b) * XM);
+  ti.rows = b + 1 == nb ? XM - static_cast<int>(pref[lo] & 127u) : XM;
+  ti.n0 = static_cast<int>(wt * P.p[ti.prob].tn);
   return true;
 }
 
@@ -240,10 +250,11 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   uint64_t* ti_full = tfree + 1;
   uint64_t* ti_empty = ti_full + XTI_DEPTH;
   uint64_t* mma_done = ti_empty + XTI_DEPTH;
+  uint64_t* want = mma_done + 1;
   XTile* s_ti = reinterpret_cast<XTile*>(bars + 32);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_ti + XTI_DEPTH);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-  int* s_pref = reinterpret_cast<int*>(s_tmem + 2);  // [E + 1]
+  uint32_t* s_pref = s_tmem + 2;  // [E + 1]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -259,12 +270,18 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       mbar_init(&ti_empty[i], 2 + XEPI_WARPS);
     }
     mbar_init(mma_done, 1);
+    mbar_init(want, 1);
     *s_abort = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
+  } else if (warp == 0 && lane < 2) {
+    tma_prefetch_desc(&maps.w[lane]);
+    tma_prefetch_desc(&maps.sw[lane]);
+    tma_prefetch_desc(&maps.sa[lane]);
+    for (int i = 0; i < 4; ++i) tma_prefetch_desc(&maps.a[lane][i]);
   }
   tc_fence_before();
   __syncthreads();
@@ -275,18 +292,19 @@ __global__ void __launch_bounds__(XTHREADS, 1)
 
   if (warp == 2 + XEPI_WARPS) {
     // --------------------------------------------------------- tile scheduler
+    // The first tile is the CTA's own index, the others come by ticket.  A
+    // ticket is drawn only when the producer is about to need it (`want`): the
+    // atomic's latency is hidden, and a CTA does not sit on a second tile while
+    // another has none.  (With tickets drawn as soon as a slot was free, half
+    // of the CTAs took two of a decode step's 128 GMM1 tiles.)
     xschedule(P, s_pref);
     if (lane == 0) {
       int slot = 0;
-      uint32_t phase = 0;
-      int t = atomicAdd(P.ticket, 1);
+      uint32_t phase = 0, want_phase = 0;
+      uint32_t t = blockIdx.x;
       for (;;) {
         XTile ti{-1, 0, 0, 0, 0};
-        if (xlocate(P, s_pref, t, ti)) {
-          t = atomicAdd(P.ticket, 1);
-          // every GMM1 tile has a smaller ticket: its CTA is running or done
-          if (ti.prob == 1 && !counter_wait(&P.ready[ti.row0 / XM], P.ready_unit, wc)) break;
-        }
+        xlocate(P, s_pref, t, ti);
         if (!mbar_wait(&ti_empty[slot], phase ^ 1u, wc)) break;
         s_ti[slot] = ti;
         mbar_arrive(&ti_full[slot]);
@@ -295,11 +313,15 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           phase ^= 1u;
         }
         if (ti.prob < 0) break;
+        if (!mbar_wait(want, want_phase, wc)) break;
+        want_phase ^= 1u;
+        t = gridDim.x + static_cast<uint32_t>(atomicAdd(P.ticket, 1));
       }
     }
   } else if (warp == 0) {
     // --------------------------------------------------------------- producer
     uint32_t stage = 0, sphase = 0, issued = 0;
+    uint32_t bare = 0, bare_bytes = 0;  // the last stages issued without token rows
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -315,40 +337,89 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       }
       if (ti.prob < 0) break;
       const XProb& pr = P.p[ti.prob];
-      // a was written by this launch's epilogues: the scheduler acquired its
-      // counter, order that with the asynchronous copies below
-      if (ti.prob == 1) fence_proxy_async_global();
       const int box = ti.rows <= 16 ? 0 : (ti.rows <= 32 ? 1 : (ti.rows <= 64 ? 2 : 3));
       const CUtensorMap* ma = &maps.a[ti.prob][box];
       const CUtensorMap* mw = &maps.w[ti.prob];
       const CUtensorMap* msa = &maps.sa[ti.prob];
       const CUtensorMap* msw = &maps.sw[ti.prob];
-      const uint32_t bytes = (16u << box) * 128 + XB_BYTES + XSA_BYTES + XSB_BYTES;
+      const uint32_t abytes = (16u << box) * 128 + XSA_BYTES;
       const int srow = ti.row0 / 128, wrow = ti.e * pr.rt + ti.n0 / 128;
-      for (int kb = 0; kb * XK < pr.kp; ++kb) {
-        ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
-        if (!ok) break;
-        if (elect_one()) {
-          uint8_t* sA = smem + stage * XSTAGE_BYTES;
-          mbar_arrive_expect_tx(&full[stage], bytes);
-          tma_load_3d(sA + XA_BYTES, mw, &full[stage], kb * (XK / 2), ti.n0, ti.e);
-          tma_load_2d(sA, ma, &full[stage], kb * (XK / 2), ti.row0);
-          tma_load_2d(sA + XA_BYTES + XB_BYTES, msa, &full[stage], kb * 256, srow);
-          tma_load_2d(sA + XA_BYTES + XB_BYTES + XSA_BYTES, msw, &full[stage], kb * 256, wrow);
-        }
-        __syncwarp();
+      // the two halves of stage s, K block kb (one lane)
+      auto load_weights = [&](uint32_t s, int kb) {
+        uint8_t* sB = smem + s * XSTAGE_BYTES + XA_BYTES;
+        mbar_arrive_expect_tx(&full[s], abytes + pr.tn * 128 + pr.tn / 128 * XSA_BYTES);
+        tma_load_3d(sB, mw, &full[s], kb * (XK / 2), ti.n0, ti.e);
+        tma_load_2d(sB + XB_BYTES + XSA_BYTES, msw, &full[s], kb * 256, wrow);
+      };
+      auto load_tokens = [&](uint32_t s, int kb) {
+        uint8_t* sA = smem + s * XSTAGE_BYTES;
+        tma_load_2d(sA, ma, &full[s], kb * (XK / 2), ti.row0);
+        tma_load_2d(sA + XA_BYTES + XB_BYTES, msa, &full[s], kb * 256, srow);
+      };
+      auto next_stage = [&]() {
         ++issued;
         if (++stage == XSTAGES) {
           stage = 0;
           sphase ^= 1u;
         }
+      };
+      const int nkb = (pr.kp + XK - 1) / XK;
+      const int ask = max(0, nkb - 2 * XSTAGES);  // K block at which the next tile is asked for
+      bool asked = ask == 0;
+      int kb = 0;
+      if (asked && elect_one()) mbar_arrive(want);
+      if (ti.prob == 1) {
+        // a comes from this launch's GMM1 tiles; each has a smaller ticket, so
+        // its CTA is running or done.  While it is not there yet the weights,
+        // which wait for nothing, are streamed into the free stages.
+        const int* ready = &P.ready[ti.row0 / XM];
+        int seen = 0;
+        if (lane == 0)
+          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(ready) : "memory");
+        if (__shfl_sync(0xffffffffu, seen, 0) < P.ready_unit) {
+          const uint32_t first = stage;
+          bare_bytes = abytes;
+          for (; kb < nkb && kb < XSTAGES; ++kb) {
+            ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
+            if (!ok) break;
+            if (elect_one()) load_weights(stage, kb);
+            __syncwarp();
+            ++bare;
+            next_stage();
+          }
+          if (ok) ok = warp_all(lane != 0 || counter_wait(ready, P.ready_unit, wc));
+          if (!ok) break;
+          fence_proxy_async_global();
+          if (elect_one())
+            for (int j = 0; j < kb; ++j) load_tokens((first + j) % XSTAGES, j);
+          __syncwarp();
+          bare = 0;
+        }
+        // order the counter's acquire with the asynchronous copies of a below
+        fence_proxy_async_global();
+      }
+      for (; kb < nkb; ++kb) {
+        ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
+        if (!ok) break;
+        if (elect_one()) {
+          load_weights(stage, kb);
+          load_tokens(stage, kb);
+          if (!asked && kb >= ask) mbar_arrive(want);
+        }
+        __syncwarp();
+        asked |= kb >= ask;
+        next_stage();
       }
       if (!ok) break;
     }
     // wait (bounded) for the copies still in flight before leaving
-    if (!ok && lane == 0)
+    // (the token rows that the last `bare` stages were armed for never come)
+    if (!ok && lane == 0) {
+      for (uint32_t j = 1; j <= bare; ++j)
+        mbar_complete_tx(&full[(issued - j) % XSTAGES], bare_bytes);
       for (uint32_t s = 0; s < XSTAGES; ++s)
         if (issued > s) drain_wait(&full[s], ((issued - 1 - s) / XSTAGES) & 1u, P.budget_ns);
+    }
     grid_dep_launch();  // this CTA is in its last tile
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issue
@@ -372,7 +443,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       tc_fence_after();
       const uint32_t acc = n & 1u;
       const uint32_t d = tmem + acc * XACC1;
-      const int cols = min(XN, (pr.n - ti.n0 + 15) / 16 * 16);
+      const int cols = min(pr.tn, (pr.n - ti.n0 + 15) / 16 * 16);
       const bool wide = cols > 128;  // the second scale tile row is in use
       const uint32_t id0 = idesc_mx4(cols, 0), id1 = idesc_mx4(cols, 2);
       bool ok = true;
@@ -424,7 +495,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   } else {
     // --------------------------------------------------------------- epilogue
     const int q = warp & 3;          // TMEM lane quarter
-    const int h = (warp - 2) >> 2;   // half of the tile's columns: 128 h ..
+    const int h = (warp - 2) >> 2;   // half of the tile's columns
     uint8_t* buf = bufs + (warp - 2) * XBUF;
     int slot = 0;
     uint32_t phase = 0;
@@ -458,45 +529,54 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       tc_fence_after();
       if (!(shares && live) && lane == 0) mbar_arrive(tfree);
       if (live) {
+        const int hw = pr.tn / 2;  // columns of this half
         const uint32_t taddr =
-            tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * XACC1 + h * 128;
+            tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * XACC1 + h * hw;
         const int row = 32 * q + lane;
         const bool valid = row < ti.rows;
         if (ti.prob == 0) {
-          // two chunks of gate and up columns, the one with the shared columns
-          // first: chunk 1 of half 1 (accumulator 0), chunk 0 of half 0
+          // chunks of gate and up columns, the one with the shared columns
+          // first: the last of half 1 (accumulator 0), the first of half 0
           const int64_t prow = ti.row0 + row;
-          const int blk0 = ti.n0 / 64 + 2 * h;  // first block of I of this warp
+          const int nc = hw / 64;                // 2 or 1
+          const int blk0 = (ti.n0 + hw * h) / 64;  // first block of I of this warp
           uint32_t sc = 0;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int c = i ^ h;
-            uint32_t g[32], u[32];
-            tmem_ld32(taddr + 64 * c, g);
-            tmem_ld32(taddr + 64 * c + 32, u);
-            tmem_ld_wait();
-            if (i == 0 && shares) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(tfree);
-            }
-            if (blk0 + c < P.a_blocks) {
-              const uint32_t s = swiglu_block(
-                  g, u,
-                  reinterpret_cast<uint4*>(P.a_codes + prow * P.a_pitch + (blk0 + c) * 16), valid);
-              sc |= s << (8 * c);
+            if (i < nc) {
+              const int c = h ? nc - 1 - i : i;
+              uint32_t g[32], u[32];
+              tmem_ld32(taddr + 64 * c, g);
+              tmem_ld32(taddr + 64 * c + 32, u);
+              tmem_ld_wait();
+              if (i == 0 && shares) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tfree);
+              }
+              if (blk0 + c < P.a_blocks) {
+                const uint32_t s = swiglu_block(
+                    g, u,
+                    reinterpret_cast<uint4*>(P.a_codes + prow * P.a_pitch + (blk0 + c) * 16),
+                    valid);
+                sc |= s << (8 * c);
+              }
             }
           }
-          // (a missing second block gets scale 0: the last MMA step of GMM2
-          // covers it with zero codes)
-          if (valid && blk0 < P.a_blocks)
-            *reinterpret_cast<uint16_t*>(P.a_scales + mx_scale_offset(prow, blk0, P.a_kt)) =
-                static_cast<uint16_t>(sc);
+          // (a block that is missing at the end of a pair gets scale 0: the last
+          // MMA step of GMM2 covers it with zero codes)
+          if (valid) {
+            uint8_t* at = P.a_scales + mx_scale_offset(prow, blk0, P.a_kt);
+            if (nc == 2 && blk0 < P.a_blocks)
+              *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(sc);
+            else if (nc == 1 && (blk0 & ~1) < P.a_blocks)
+              *at = static_cast<uint8_t>(sc);
+          }
         } else {
-          const int c00 = ti.n0 + 128 * h;
+          const int c00 = ti.n0 + hw * h;
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const int c = h ? 3 - i : i;
+          for (int i = 0; i < hw / 32; ++i) {
+            const int c = h ? hw / 32 - 1 - i : i;
             uint32_t v[32];
             tmem_ld32(taddr + 32 * c, v);
             tmem_ld_wait();
@@ -657,22 +737,30 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
     rc |= map_codes(env, &maps.a[0][i], ws + f.off_x, f.hp / 2, p.R, 0, 16u << i);
     rc |= map_codes(env, &maps.a[1][i], ws + f.off_a, f.ip / 2, p.R, 0, 16u << i);
   }
-  rc |= map_codes(env, &maps.w[0], up_codes, f.hp / 2, 2 * f.ip, p.E, XN);
-  rc |= map_codes(env, &maps.w[1], down_codes, f.ip / 2, p.H, p.E, XN);
+  // Few tiles (at most four per SM): half of the columns each share out the SMs
+  // more evenly.  One token, 8 experts, H = 7168, I = 2048 on 152 SMs: XONE_128
+  // with 256 and 448 tiles, XONE_256 with 128 and 224.
+  const int64_t most_blocks = std::min(p.E, p.TK) + p.TK / XM;
+  auto columns = [&](int64_t n) {
+    return most_blocks * ((n + XN - 1) / XN) <= 4 * env.num_sms ? XN / 2 : XN;
+  };
+  const int tn1 = columns(2 * f.ip), tn2 = columns(p.H);
+  rc |= map_codes(env, &maps.w[0], up_codes, f.hp / 2, 2 * f.ip, p.E, tn1);
+  rc |= map_codes(env, &maps.w[1], down_codes, f.ip / 2, p.H, p.E, tn2);
   rc |= map_scales(env, &maps.sa[0], ws + f.off_xs, f.h_kt, p.R / XM, 1);
   rc |= map_scales(env, &maps.sa[1], ws + f.off_as, f.i_kt, p.R / XM, 1);
-  rc |= map_scales(env, &maps.sw[0], up_scales, f.h_kt, p.E * ((2 * f.ip + 127) / 128), 2);
-  rc |= map_scales(env, &maps.sw[1], down_scales, f.i_kt, p.E * ((p.H + 127) / 128), 2);
+  rc |= map_scales(env, &maps.sw[0], up_scales, f.h_kt, p.E * ((2 * f.ip + 127) / 128), tn1 / 128);
+  rc |= map_scales(env, &maps.sw[1], down_scales, f.i_kt, p.E * ((p.H + 127) / 128), tn2 / 128);
   if (rc != HMM_OK) return HMM_ERR_CUDA;
-  auto prob = [](XProb& q, int64_t kp, int64_t n) {
+  auto prob = [](XProb& q, int64_t kp, int64_t n, int tn) {
     q.kp = static_cast<int>(kp);
     q.n = static_cast<int>(n);
     q.rt = static_cast<int>((n + 127) / 128);
-    q.n_tiles = static_cast<int>((n + XN - 1) / XN);
+    q.n_tiles = static_cast<int>((n + tn - 1) / tn);
+    q.tn = tn;
   };
-  prob(P.p[0], f.hp, 2 * f.ip);
-  prob(P.p[1], f.ip, p.H);
-  P.poff = m.poff;
+  prob(P.p[0], f.hp, 2 * f.ip, tn1);
+  prob(P.p[1], f.ip, p.H, tn2);
   P.counts = m.counts;
   P.E = static_cast<int>(p.E);
   P.ticket = c.tickets;
@@ -692,6 +780,7 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
       cudaSuccess)
     return HMM_ERR_CUDA;
   const int64_t tiles = (p.R / XM) * (P.p[0].n_tiles + P.p[1].n_tiles);
+  if (tiles >= (int64_t(1) << 31)) return HMM_ERR_SHAPE;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(env.num_sms, tiles));
   return launch_kernel(gmm_mx4_kernel, grid, XTHREADS, XSMEM, env.stream, env.pdl, 1, P, maps) ==
                  cudaSuccess

@@ -20,7 +20,9 @@
 // its ids into registers before the first step, so the steps do not wait on
 // global loads one after another.  When the chunk histograms are small
 // (nchunks * E <= ROUTE_FUSE_MAX) every rank block redoes the scan from them
-// (two launches); otherwise one block scans between the two (three).
+// (two launches); otherwise one block scans between the two (three).  A single
+// chunk (up to 1024 slots) needs no histogram launch: its rank block has the
+// counts in shared memory (one launch).
 #include "hmm_internal.h"
 
 namespace hmm {
@@ -160,21 +162,28 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(int E, int Ex, int32_t
 // the slots of e in chunks before this one, and the exclusive prefixes over
 // experts of the totals and of the totals padded to BM.  Block 0 publishes
 // counts, offsets and poff; every block takes a share of the padding rows of
-// prow2slot and of the counters to zero.
+// prow2slot and of the counters to zero.  warp_cnt (a single chunk): the warps'
+// counts [RWARPS][E] in shared memory stand for the histograms.
 __device__ void route_scan_in_block(int E, int Ex, int32_t T, int64_t nchunks, int64_t chunk,
                                     const int32_t* __restrict__ chunk_cnt, MetaPtrs m,
                                     int32_t* tickets, int64_t zero_count, int32_t* s_tot,
                                     int32_t* s_bef, int32_t* s_off, int32_t* s_poff,
-                                    int32_t* warp_tot) {
+                                    int32_t* warp_tot, const int32_t* warp_cnt) {
   const int tid = threadIdx.x;
+  if (warp_cnt) __syncthreads();  // every warp's counts are there
   for (int e = tid; e < Ex; e += blockDim.x) {
-    s_tot[e] = e < E ? 0 : T;
+    int32_t c = e < E ? 0 : T;
+    if (warp_cnt && e < E) {
+#pragma unroll
+      for (int w = 0; w < RWARPS; ++w) c += warp_cnt[w * E + e];
+    }
+    s_tot[e] = c;
     s_bef[e] = 0;
   }
   __syncthreads();
   // column sums of the [nchunks, E] histograms, eight loads in flight per thread
   constexpr int U = 8;
-  const int64_t n = nchunks * E;
+  const int64_t n = warp_cnt ? 0 : nchunks * E;
   for (int64_t i0 = tid; i0 < n; i0 += static_cast<int64_t>(U) * blockDim.x) {
     int32_t v[U];
 #pragma unroll
@@ -233,13 +242,16 @@ __device__ void route_scan_in_block(int E, int Ex, int32_t T, int64_t nchunks, i
   for (int64_t i = g0; i < zero_count; i += gs) tickets[i] = 0;
 }
 
-// FUSED: the scan above runs in every block (chunk_base holds the chunk
-// histograms); else chunk_base holds each chunk's first row per expert and
+// SINGLE: one chunk, the scan above runs on the warps' counts and bad ids are
+// reported here.  FUSED: the scan above runs in every block (chunk_base holds
+// the chunk histograms); else chunk_base holds each chunk's first row per expert and
 // counts/offsets/poff come from route_scan_kernel.
-template <bool FUSED>
+template <bool FUSED, bool SINGLE>
 __global__ void __launch_bounds__(RWARPS * 32) route_rank_kernel(
     const int32_t* __restrict__ ids, int64_t TK, int E, int Ex, int32_t T, int64_t nchunks,
-    MetaPtrs m, CtrlPtrs c, int64_t zero_count, int32_t* slot2row, int32_t* row2slot) {
+    MetaPtrs m, CtrlPtrs c, int64_t zero_count, int32_t* slot2row, int32_t* row2slot,
+    unsigned* status) {
+  static_assert(FUSED || !SINGLE, "a single chunk scans in its block");
   // [RWARPS][E]: per-warp counts, then cursors; FUSED: then per expert its
   // total [Ex], earlier-chunk slots [Ex], offset [Ex + 1], padded offset [Ex + 1]
   extern __shared__ int32_t sh[];
@@ -259,6 +271,13 @@ __global__ void __launch_bounds__(RWARPS * 32) route_rank_kernel(
   int v[RSTEPS];
   load_chunk_ids(ids, s0, c1, lane, v);
   for (int e = lane; e < E; e += 32) cnt[e] = 0;
+  if constexpr (SINGLE) {
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < RSTEPS; ++j)
+      bad |= v[j] != -2 && static_cast<unsigned>(v[j]) >= static_cast<unsigned>(E);
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(status, HMM_STATUS_EXPERT_ID);
+  }
   __syncwarp();
   // 1. this warp's slots per expert (one lane per group of equal ids adds)
 #pragma unroll
@@ -274,7 +293,7 @@ __global__ void __launch_bounds__(RWARPS * 32) route_rank_kernel(
   }
   if constexpr (FUSED) {
     route_scan_in_block(E, Ex, T, nchunks, chunk, c.chunk_base, m, c.tickets, zero_count, s_tot,
-                        s_bef, s_off, s_poff, warp_tot);
+                        s_bef, s_off, s_poff, warp_tot, SINGLE ? sh : nullptr);
   }
   __syncthreads();
   // 2. cursor of warp w for expert e: the padded row of its first slot of e
@@ -326,7 +345,12 @@ static bool route_fused(const Plan& p) {
   return p.nchunks > 0 && p.nchunks * p.E <= ROUTE_FUSE_MAX && p.E <= ROUTE_FUSE_MAX_E;
 }
 
-int route_launches(const Plan& p) { return p.nchunks == 0 ? 1 : (route_fused(p) ? 2 : 3); }
+static bool route_single(const Plan& p) { return route_fused(p) && p.nchunks == 1; }
+
+int route_launches(const Plan& p) {
+  if (p.nchunks == 0 || route_single(p)) return 1;
+  return route_fused(p) ? 2 : 3;
+}
 
 cudaError_t launch_route(const Plan& p, const int32_t* ids, MetaPtrs m, CtrlPtrs c,
                          int32_t* slot2row, int32_t* row2slot, unsigned* status,
@@ -335,23 +359,25 @@ cudaError_t launch_route(const Plan& p, const int32_t* ids, MetaPtrs m, CtrlPtrs
   const int32_t T = static_cast<int32_t>(p.T);
   const unsigned blocks = static_cast<unsigned>(p.nchunks);  // one block per chunk
   cudaError_t err = cudaSuccess;
-  if (p.nchunks > 0) {
+  if (p.nchunks > 0 && !route_single(p)) {
     err = launch_kernel(route_count_kernel, blocks, RWARPS * 32, sizeof(int32_t) * E, st, pdl, 1,
                         ids, p.TK, E, p.nchunks, c.chunk_base, status);
     if (err != cudaSuccess) return err;
   }
   if (route_fused(p)) {
     const size_t smem = sizeof(int32_t) * (RWARPS * E + 4 * (Ex + 1));
-    return launch_kernel(route_rank_kernel<true>, blocks, RWARPS * 32, smem, st, pdl, 1, ids,
-                         p.TK, E, Ex, T, p.nchunks, m, c, p.ctrl_zero_count, slot2row, row2slot);
+    auto kern = route_single(p) ? route_rank_kernel<true, true> : route_rank_kernel<true, false>;
+    return launch_kernel(kern, blocks, RWARPS * 32, smem, st, pdl, 1, ids, p.TK, E, Ex, T,
+                         p.nchunks, m, c, p.ctrl_zero_count, slot2row, row2slot, status);
   }
   err = launch_kernel(route_scan_kernel, 1, 1024, 0, st, pdl, 1, E, Ex, T, p.nchunks, m, c,
                       p.ctrl_zero_count);
   if (err != cudaSuccess) return err;
   if (p.nchunks > 0) {
     const size_t smem = sizeof(int32_t) * RWARPS * E;
-    err = launch_kernel(route_rank_kernel<false>, blocks, RWARPS * 32, smem, st, pdl, 1, ids,
-                        p.TK, E, Ex, T, p.nchunks, m, c, p.ctrl_zero_count, slot2row, row2slot);
+    err = launch_kernel(route_rank_kernel<false, false>, blocks, RWARPS * 32, smem, st, pdl, 1,
+                        ids, p.TK, E, Ex, T, p.nchunks, m, c, p.ctrl_zero_count, slot2row,
+                        row2slot, status);
   }
   return err;
 }
