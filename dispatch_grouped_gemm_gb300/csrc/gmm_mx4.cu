@@ -85,6 +85,7 @@ struct XParams {
 struct XMaps {
   CUtensorMap a[2][4];  // token rows: boxes of 16, 32, 64, 128 rows
   CUtensorMap w[2];
+  CUtensorMap o;        // expert outputs: boxes of 32 rows x 32 columns
   CUtensorMap sa[2];    // scales of the token rows: one scale tile row, 2 tiles
   CUtensorMap sw[2];    // scales of the weights: 2 scale tile rows, 2 tiles each
 };
@@ -109,6 +110,15 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
+}
+// Store the box at src to the tensor at {c0, c1}; parts outside it are left out.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int c0,
+                                             int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(m)),
+      "r"(smem_u32(src)), "r"(c0), "r"(c1)
+      : "memory");
 }
 // 512 bytes of scales (32 lanes x 16 bytes) to 4 TMEM columns, the same in
 // each of the four lane quarters.
@@ -546,14 +556,25 @@ __global__ void __launch_bounds__(XTHREADS, 1)
             if (i < nc) {
               const int c = h ? nc - 1 - i : i;
               uint32_t g[32], u[32];
-              tmem_ld32(taddr + 64 * c, g);
-              tmem_ld32(taddr + 64 * c + 32, u);
-              tmem_ld_wait();
               if (i == 0 && shares) {
+                // the 32 shared columns alone: the up half (half 1), the gate half
+                if (h)
+                  tmem_ld32(taddr + 64 * c + 32, u);
+                else
+                  tmem_ld32(taddr + 64 * c, g);
+                tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(tfree);
+                if (h)
+                  tmem_ld32(taddr + 64 * c, g);
+                else
+                  tmem_ld32(taddr + 64 * c + 32, u);
+              } else {
+                tmem_ld32(taddr + 64 * c, g);
+                tmem_ld32(taddr + 64 * c + 32, u);
               }
+              tmem_ld_wait();
               if (blk0 + c < P.a_blocks) {
                 const uint32_t s = swiglu_block(
                     g, u,
@@ -573,7 +594,13 @@ __global__ void __launch_bounds__(XTHREADS, 1)
               *at = static_cast<uint8_t>(sc);
           }
         } else {
+          // 32 columns at a time, the shared ones first, as bf16 through this
+          // warp's buffer (16-byte pieces permuted by the row as the store's
+          // 64-byte swizzle wants them: no bank conflicts).  Whole quarters of
+          // 32 rows leave by one asynchronous tensor store; fewer rows by plain
+          // stores of the valid ones, four lanes per row.
           const int c00 = ti.n0 + hw * h;
+          const bool whole = ti.rows - 32 * q >= 32;
 #pragma unroll 1
           for (int i = 0; i < hw / 32; ++i) {
             const int c = h ? hw / 32 - 1 - i : i;
@@ -586,20 +613,26 @@ __global__ void __launch_bounds__(XTHREADS, 1)
               if (lane == 0) mbar_arrive(tfree);
             }
             const int c0 = c00 + 32 * c;
-            if (c0 < P.H) {
+            if (c0 >= P.H) continue;
+            uint32_t w[16];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t w[4];
+            for (int j = 0; j < 16; ++j)
+              w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            if (lane == 0) bulk_wait_group_read<0>();  // the buffer's last store has read it
+            __syncwarp();
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  w[k] = pack_bf16(__uint_as_float(v[8 * j + 2 * k]),
-                                   __uint_as_float(v[8 * j + 2 * k + 1]));
-                // 16-byte pieces permuted by the row: no bank conflicts here or below
-                *reinterpret_cast<uint4*>(buf + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
-              }
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(buf + lane * 64 + 16 * (j ^ ((lane >> 1) & 3))) =
+                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            if (whole) {
+              fence_proxy_async_smem();
               __syncwarp();
-              // four lanes per row: 64 contiguous bytes
+              if (lane == 0) {
+                tma_store_2d(&maps.o, buf, c0, ti.row0 + 32 * q);
+                bulk_commit_group();
+              }
+            } else {
+              __syncwarp();
 #pragma unroll
               for (int r8 = 0; r8 < 4; ++r8) {
                 const int r = 8 * r8 + (lane >> 2);
@@ -610,7 +643,6 @@ __global__ void __launch_bounds__(XTHREADS, 1)
                       *reinterpret_cast<const uint4*>(buf + r * 64 +
                                                       16 * ((lane & 3) ^ ((r >> 1) & 3)));
               }
-              __syncwarp();
             }
           }
         }
@@ -622,6 +654,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         if (lane == 0) red_release_add(&P.ready[ti.row0 / XM], 1);
       }
     }
+    if (lane == 0) bulk_wait_group<0>();  // the stores of o are performed
   }
   tc_fence_before();
   __syncthreads();
@@ -725,6 +758,19 @@ int map_scales(const GemmEnv& env, CUtensorMap* map, const void* base, int64_t k
              : HMM_ERR_CUDA;
 }
 
+// expert outputs [rows, cols] bf16 with boxes of 32 x 32
+int map_out(const GemmEnv& env, CUtensorMap* map, const void* base, int64_t cols, int64_t rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * 2)};
+  const cuuint32_t box[2] = {32, 32}, es[2] = {1, 1};
+  return env.encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+                    strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? HMM_OK
+             : HMM_ERR_CUDA;
+}
+
 }  // namespace
 
 int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, MetaPtrs m,
@@ -747,6 +793,7 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
   const int tn1 = columns(2 * f.ip), tn2 = columns(p.H);
   rc |= map_codes(env, &maps.w[0], up_codes, f.hp / 2, 2 * f.ip, p.E, tn1);
   rc |= map_codes(env, &maps.w[1], down_codes, f.ip / 2, p.H, p.E, tn2);
+  rc |= map_out(env, &maps.o, ws + f.off_o, p.H, p.R);
   rc |= map_scales(env, &maps.sa[0], ws + f.off_xs, f.h_kt, p.R / XM, 1);
   rc |= map_scales(env, &maps.sa[1], ws + f.off_as, f.i_kt, p.R / XM, 1);
   rc |= map_scales(env, &maps.sw[0], up_scales, f.h_kt, p.E * ((2 * f.ip + 127) / 128), tn1 / 128);
