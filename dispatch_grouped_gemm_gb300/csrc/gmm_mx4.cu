@@ -15,9 +15,12 @@
 //
 // TMEM: two accumulators of 256 columns and 24 columns of scales do not fit
 // into 512 columns side by side, so the accumulators share 32 columns: [0, 256)
-// and [224, 480), scales from 480.  The epilogue of a tile reads the shared
-// columns first and releases them; all warps together then also say that the
-// tile before has been read, so that one barrier per tile orders both.
+// and [224, 480), scales from 480.  A tile that would write shared columns of
+// the tile before waits until its epilogue has read those, which it does first;
+// that costs about 0.6 us per tile.  (Tiles of 192 weight rows, which share
+// nothing, were slower all the same: 106 us for 99 at T = 4096, H = 2048, I =
+// 1408.  The loads from L2 bound the loop, and narrower tiles load more.)  Tiles
+// of 128 rows wait for the accumulator's previous use only.
 //
 // The rows of the up-projection are stored as 32 gate rows and the matching 32
 // up rows in turn: accumulator columns 64 c .. 64 c + 31 are the gate and the
@@ -43,14 +46,15 @@ constexpr int XSB_BYTES = 4 * MX_TILE_BYTES;
 constexpr int XSTAGE_BYTES = XA_BYTES + XB_BYTES + XSA_BYTES + XSB_BYTES;  // 51 KB
 constexpr int XSTAGES = 4;
 constexpr int XEPI_WARPS = 8;        // two per TMEM lane quarter
-constexpr int XTHREADS = 32 * (XEPI_WARPS + 3);
+constexpr int XTOKEN_WARP = 3 + XEPI_WARPS;
+constexpr int XTHREADS = 32 * (XEPI_WARPS + 4);
 constexpr int XBUF = 32 * 64;        // staged output: 32 rows of 32 bf16
 constexpr int XTI_DEPTH = 3;
 constexpr int XACC1 = XN - 32;       // second accumulator's first column
 constexpr int XSF_COL = XACC1 + XN;  // scales of A: 2 x 4 columns, then of B: 2 x 8
-constexpr int XBARS = 2 * XSTAGES + 3 + 2 * XTI_DEPTH + 2;
+constexpr int XBARS = 2 * XSTAGES + 5 + 2 * XTI_DEPTH + 2;
 constexpr int XSMEM = 1024 + XSTAGES * XSTAGE_BYTES + XEPI_WARPS * XBUF + 256 +
-                      XTI_DEPTH * 20 + 8 + 4 * (MAX_E + 1);
+                      XTI_DEPTH * 20 + 16 + 4 * (MAX_E + 1);
 static_assert(XSMEM <= 232448, "shared memory per CTA");
 static_assert(XSF_COL + 24 <= 512, "TMEM columns");
 static_assert(XBARS * 8 <= 256, "barriers");
@@ -256,7 +260,9 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   uint64_t* full = bars;
   uint64_t* empty = bars + XSTAGES;
   uint64_t* tfull = bars + 2 * XSTAGES;  // [2]
-  uint64_t* tfree = tfull + 2;           // one phase per tile (see the top)
+  uint64_t* tempty = tfull + 2;          // [2] the accumulator has been read
+  uint64_t* tfree = tempty + 2;          // one phase per tile: its shared columns have been
+                                         // read, and all of the tile before
   uint64_t* ti_full = tfree + 1;
   uint64_t* ti_empty = ti_full + XTI_DEPTH;
   uint64_t* mma_done = ti_empty + XTI_DEPTH;
@@ -264,20 +270,23 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   XTile* s_ti = reinterpret_cast<XTile*>(bars + 32);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_ti + XTI_DEPTH);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-  uint32_t* s_pref = s_tmem + 2;  // [E + 1]
+  uint32_t* s_issued = s_tmem + 2;  // stages issued by the two producers
+  uint32_t* s_pref = s_tmem + 4;    // [E + 1]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < XSTAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);  // both producers arm it
       mbar_init(&empty[s], 1);
     }
     mbar_init(&tfull[0], 1);
     mbar_init(&tfull[1], 1);
+    mbar_init(&tempty[0], XEPI_WARPS);
+    mbar_init(&tempty[1], XEPI_WARPS);
     mbar_init(tfree, XEPI_WARPS);
     for (int i = 0; i < XTI_DEPTH; ++i) {
       mbar_init(&ti_full[i], 1);
-      mbar_init(&ti_empty[i], 2 + XEPI_WARPS);
+      mbar_init(&ti_empty[i], 3 + XEPI_WARPS);
     }
     mbar_init(mma_done, 1);
     mbar_init(want, 1);
@@ -328,10 +337,15 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         t = gridDim.x + static_cast<uint32_t>(atomicAdd(P.ticket, 1));
       }
     }
-  } else if (warp == 0) {
-    // --------------------------------------------------------------- producer
+  } else if (warp == 0 || warp == XTOKEN_WARP) {
+    // --------------------------------------------------------------- producers
+    // One warp for the weights and their scales, one for the token rows and
+    // theirs: each arms a stage for its own bytes.  (One warp with all four
+    // loads took 0.38 us per K block, whatever the tile's width.)  Weights wait
+    // for nothing: while GMM2's token rows are not there yet, they are streamed
+    // into the free stages.
+    const bool weights = warp == 0;
     uint32_t stage = 0, sphase = 0, issued = 0;
-    uint32_t bare = 0, bare_bytes = 0;  // the last stages issued without token rows
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -347,118 +361,104 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       }
       if (ti.prob < 0) break;
       const XProb& pr = P.p[ti.prob];
-      const int box = ti.rows <= 16 ? 0 : (ti.rows <= 32 ? 1 : (ti.rows <= 64 ? 2 : 3));
-      const CUtensorMap* ma = &maps.a[ti.prob][box];
-      const CUtensorMap* mw = &maps.w[ti.prob];
-      const CUtensorMap* msa = &maps.sa[ti.prob];
-      const CUtensorMap* msw = &maps.sw[ti.prob];
-      const uint32_t abytes = (16u << box) * 128 + XSA_BYTES;
-      const int srow = ti.row0 / 128, wrow = ti.e * pr.rt + ti.n0 / 128;
-      // the two halves of stage s, K block kb (one lane)
-      auto load_weights = [&](uint32_t s, int kb) {
-        uint8_t* sB = smem + s * XSTAGE_BYTES + XA_BYTES;
-        mbar_arrive_expect_tx(&full[s], abytes + pr.tn * 128 + pr.tn / 128 * XSA_BYTES);
-        tma_load_3d(sB, mw, &full[s], kb * (XK / 2), ti.n0, ti.e);
-        tma_load_2d(sB + XB_BYTES + XSA_BYTES, msw, &full[s], kb * 256, wrow);
-      };
-      auto load_tokens = [&](uint32_t s, int kb) {
-        uint8_t* sA = smem + s * XSTAGE_BYTES;
-        tma_load_2d(sA, ma, &full[s], kb * (XK / 2), ti.row0);
-        tma_load_2d(sA + XA_BYTES + XB_BYTES, msa, &full[s], kb * 256, srow);
-      };
-      auto next_stage = [&]() {
-        ++issued;
-        if (++stage == XSTAGES) {
-          stage = 0;
-          sphase ^= 1u;
-        }
-      };
       const int nkb = (pr.kp + XK - 1) / XK;
-      const int ask = max(0, nkb - 2 * XSTAGES);  // K block at which the next tile is asked for
-      bool asked = ask == 0;
-      int kb = 0;
-      if (asked && elect_one()) mbar_arrive(want);
-      if (ti.prob == 1) {
-        // a comes from this launch's GMM1 tiles; each has a smaller ticket, so
-        // its CTA is running or done.  While it is not there yet the weights,
-        // which wait for nothing, are streamed into the free stages.
-        const int* ready = &P.ready[ti.row0 / XM];
-        int seen = 0;
-        if (lane == 0)
-          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(ready) : "memory");
-        if (__shfl_sync(0xffffffffu, seen, 0) < P.ready_unit) {
-          const uint32_t first = stage;
-          bare_bytes = abytes;
-          for (; kb < nkb && kb < XSTAGES; ++kb) {
-            ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
-            if (!ok) break;
-            if (elect_one()) load_weights(stage, kb);
-            __syncwarp();
-            ++bare;
-            next_stage();
+      if (weights) {
+        const CUtensorMap* mw = &maps.w[ti.prob];
+        const CUtensorMap* msw = &maps.sw[ti.prob];
+        const uint32_t bytes = pr.tn * 128 + pr.tn / 128 * XSA_BYTES;
+        const int wrow = ti.e * pr.rt + ti.n0 / 128;
+        const int ask = max(0, nkb - 2 * XSTAGES);  // K block at which the next tile is asked for
+        for (int kb = 0; kb < nkb; ++kb) {
+          ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
+          if (!ok) break;
+          if (elect_one()) {
+            uint8_t* sB = smem + stage * XSTAGE_BYTES + XA_BYTES;
+            mbar_arrive_expect_tx(&full[stage], bytes);
+            tma_load_3d(sB, mw, &full[stage], kb * (XK / 2), ti.n0, ti.e);
+            tma_load_2d(sB + XB_BYTES + XSA_BYTES, msw, &full[stage], kb * 256, wrow);
+            if (kb == ask) mbar_arrive(want);
           }
-          if (ok) ok = warp_all(lane != 0 || counter_wait(ready, P.ready_unit, wc));
+          __syncwarp();
+          ++issued;
+          if (++stage == XSTAGES) {
+            stage = 0;
+            sphase ^= 1u;
+          }
+        }
+      } else {
+        const int box = ti.rows <= 16 ? 0 : (ti.rows <= 32 ? 1 : (ti.rows <= 64 ? 2 : 3));
+        const CUtensorMap* ma = &maps.a[ti.prob][box];
+        const CUtensorMap* msa = &maps.sa[ti.prob];
+        const uint32_t bytes = (16u << box) * 128 + XSA_BYTES;
+        const int srow = ti.row0 / 128;
+        if (ti.prob == 1) {
+          // a comes from this launch's GMM1 tiles; each has a smaller ticket, so
+          // its CTA is running or done.  Order the counter's acquire with the
+          // asynchronous copies of a.
+          ok = warp_all(lane != 0 ||
+                        counter_wait(&P.ready[ti.row0 / XM], P.ready_unit, wc));
           if (!ok) break;
           fence_proxy_async_global();
-          if (elect_one())
-            for (int j = 0; j < kb; ++j) load_tokens((first + j) % XSTAGES, j);
+        }
+        for (int kb = 0; kb < nkb; ++kb) {
+          ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
+          if (!ok) break;
+          if (elect_one()) {
+            uint8_t* sA = smem + stage * XSTAGE_BYTES;
+            mbar_arrive_expect_tx(&full[stage], bytes);
+            tma_load_2d(sA, ma, &full[stage], kb * (XK / 2), ti.row0);
+            tma_load_2d(sA + XA_BYTES + XB_BYTES, msa, &full[stage], kb * 256, srow);
+          }
           __syncwarp();
-          bare = 0;
+          ++issued;
+          if (++stage == XSTAGES) {
+            stage = 0;
+            sphase ^= 1u;
+          }
         }
-        // order the counter's acquire with the asynchronous copies of a below
-        fence_proxy_async_global();
-      }
-      for (; kb < nkb; ++kb) {
-        ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
-        if (!ok) break;
-        if (elect_one()) {
-          load_weights(stage, kb);
-          load_tokens(stage, kb);
-          if (!asked && kb >= ask) mbar_arrive(want);
-        }
-        __syncwarp();
-        asked |= kb >= ask;
-        next_stage();
       }
       if (!ok) break;
     }
-    // wait (bounded) for the copies still in flight before leaving
-    // (the token rows that the last `bare` stages were armed for never come)
-    if (!ok && lane == 0) {
-      for (uint32_t j = 1; j <= bare; ++j)
-        mbar_complete_tx(&full[(issued - j) % XSTAGES], bare_bytes);
-      for (uint32_t s = 0; s < XSTAGES; ++s)
-        if (issued > s) drain_wait(&full[s], ((issued - 1 - s) / XSTAGES) & 1u, P.budget_ns);
-    }
-    grid_dep_launch();  // this CTA is in its last tile
+    if (lane == 0) s_issued[weights ? 0 : 1] = issued;
+    if (weights) grid_dep_launch();  // this CTA is in its last tile
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issue
     uint32_t stage = 0, sphase = 0;
     int slot = 0;
     uint32_t phase = 0;
     uint32_t n = 0;  // tiles so far
+    int last_cols = 0;  // columns of the tile before
     for (;;) {
       if (!warp_all(mbar_wait(&ti_full[slot], phase, wc))) break;
-      const XTile ti = s_ti[slot];
-      __syncwarp();
+      const int prob = __shfl_sync(0xffffffffu, s_ti[slot].prob, 0);
+      const int n0 = __shfl_sync(0xffffffffu, s_ti[slot].n0, 0);
       if (elect_one()) mbar_arrive(&ti_empty[slot]);
       if (++slot == XTI_DEPTH) {
         slot = 0;
         phase ^= 1u;
       }
-      if (ti.prob < 0) break;
-      const XProb& pr = P.p[ti.prob];
-      // tile n - 1's shared columns and all of tile n - 2 have been read
-      if (n > 0 && !warp_all(mbar_wait(tfree, (n - 1) & 1u, wc))) break;
-      tc_fence_after();
+      if (prob < 0) break;
+      const int kp = prob == 0 ? P.p[0].kp : P.p[1].kp;
+      const int rows = prob == 0 ? P.p[0].n : P.p[1].n;
+      const int tn = prob == 0 ? P.p[0].tn : P.p[1].tn;
       const uint32_t acc = n & 1u;
       const uint32_t d = tmem + acc * XACC1;
-      const int cols = min(pr.tn, (pr.n - ti.n0 + 15) / 16 * 16);
+      const int cols = min(tn, (rows - n0 + 15) / 16 * 16);
+      // the accumulator-0 one of this tile and the tile before decides whether
+      // the two meet
+      const bool shared = n > 0 && (acc ? last_cols : cols) > XACC1;
+      last_cols = cols;
+      // the first operands, then the accumulator: the waits' latencies overlap
+      bool ok = warp_all(mbar_wait(&full[stage], sphase, wc));
+      if (!ok) break;
+      ok = warp_all(shared ? mbar_wait(tfree, (n - 1) & 1u, wc)
+                           : mbar_wait(&tempty[acc], ((n >> 1) & 1u) ^ 1u, wc));
+      if (!ok) break;
       const bool wide = cols > 128;  // the second scale tile row is in use
       const uint32_t id0 = idesc_mx4(cols, 0), id1 = idesc_mx4(cols, 2);
-      bool ok = true;
-      for (int k = 0; k < pr.kp; k += XK) {
-        ok = warp_all(mbar_wait(&full[stage], sphase, wc));
+      const uint32_t sfa = tmem + XSF_COL, sfb = tmem + XSF_COL + 8;
+      for (int k = 0; k < kp; k += XK) {
+        if (k > 0) ok = warp_all(mbar_wait(&full[stage], sphase, wc));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -467,23 +467,37 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           const uint64_t db = smem_desc(a + XA_BYTES, 16, 1024, LAYOUT_SW128);
           const uint64_t ds = smem_desc(a + XA_BYTES + XB_BYTES, 0, 128, LAYOUT_NONE);
           const uint64_t dt = smem_desc(a + XA_BYTES + XB_BYTES + XSA_BYTES, 0, 128, LAYOUT_NONE);
-          const int left = pr.kp - k;
+          const int left = kp - k;
+          // scales of 128 elements, the MMAs of 64 elements that use them
+          // (descriptor addresses count 16 bytes)
+          if (left >= XK && wide) {
+            // a whole K block without a branch between the instructions (with
+            // the conditions of the other path: 103 us for 99 at T = 4096)
+            tmem_cp_scales(sfa, ds);
+            tmem_cp_scales(sfb, dt);
+            tmem_cp_scales(sfb + 4, dt + 64);
+            tmem_cp_scales(sfa + 4, ds + 32);
+            tmem_cp_scales(sfb + 8, dt + 32);
+            tmem_cp_scales(sfb + 12, dt + 96);
+            umma_mx4(d, da, db, id0, sfa, sfb, k > 0 ? 1u : 0u);
+            umma_mx4(d, da + 2, db + 2, id1, sfa, sfb, 1u);
+            umma_mx4(d, da + 4, db + 4, id0, sfa + 4, sfb + 8, 1u);
+            umma_mx4(d, da + 6, db + 6, id1, sfa + 4, sfb + 8, 1u);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            // scales of 128 elements, then the two MMAs of 64 that use them
-            // (descriptor addresses count 16 bytes)
-            if (128 * i < left) {
-              tmem_cp_scales(tmem + XSF_COL + 4 * i, ds + i * 32);
-              tmem_cp_scales(tmem + XSF_COL + 8 + 8 * i, dt + i * 32);
-              if (wide) tmem_cp_scales(tmem + XSF_COL + 12 + 8 * i, dt + (2 + i) * 32);
+            for (int i = 0; i < 2; ++i) {
+              if (128 * i < left) {
+                tmem_cp_scales(sfa + 4 * i, ds + i * 32);
+                tmem_cp_scales(sfb + 8 * i, dt + i * 32);
+                if (wide) tmem_cp_scales(sfb + 4 + 8 * i, dt + (2 + i) * 32);
+              }
             }
-          }
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (64 * j < left)
-              umma_mx4(d, da + 2 * j, db + 2 * j, (j & 1) ? id1 : id0,
-                       tmem + XSF_COL + 4 * (j >> 1), tmem + XSF_COL + 8 + 8 * (j >> 1),
-                       (k > 0 || j > 0) ? 1u : 0u);
+            for (int j = 0; j < 4; ++j)
+              if (64 * j < left)
+                umma_mx4(d, da + 2 * j, db + 2 * j, (j & 1) ? id1 : id0, sfa + 4 * (j >> 1),
+                         sfb + 8 * (j >> 1), (k > 0 || j > 0) ? 1u : 0u);
+          }
           umma_commit(&empty[stage]);
         }
         __syncwarp();
@@ -532,29 +546,28 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       // one phase.)
       const bool shares = h == (acc ^ 1);
       const bool live = 32 * q < ti.rows;
+      uint64_t* drained = &tempty[acc];
       if (lane == 0) got = mbar_wait(&tfull[acc], (n >> 1) & 1u, wc);
       got = __shfl_sync(0xffffffffu, got, 0);
       if (!got) break;
       ++n;
       tc_fence_after();
       if (!(shares && live) && lane == 0) mbar_arrive(tfree);
+      if (!live && lane == 0) mbar_arrive(drained);
       if (live) {
-        const int hw = pr.tn / 2;  // columns of this half
-        const uint32_t taddr =
-            tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * XACC1 + h * hw;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * XACC1;
         const int row = 32 * q + lane;
         const bool valid = row < ti.rows;
         if (ti.prob == 0) {
           // chunks of gate and up columns, the one with the shared columns
           // first: the last of half 1 (accumulator 0), the first of half 0
           const int64_t prow = ti.row0 + row;
-          const int nc = hw / 64;                // 2 or 1
-          const int blk0 = (ti.n0 + hw * h) / 64;  // first block of I of this warp
-          uint32_t sc = 0;
+          const int nch = pr.tn / 64, mine = nch / 2;
+          uint8_t* crow = P.a_codes + prow * P.a_pitch;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (i < nc) {
-              const int c = h ? nc - 1 - i : i;
+            if (i < mine) {
+              const int c = h ? nch - 1 - i : i;
               uint32_t g[32], u[32];
               if (i == 0 && shares) {
                 // the 32 shared columns alone: the up half (half 1), the gate half
@@ -575,23 +588,26 @@ __global__ void __launch_bounds__(XTHREADS, 1)
                 tmem_ld32(taddr + 64 * c + 32, u);
               }
               tmem_ld_wait();
-              if (blk0 + c < P.a_blocks) {
-                const uint32_t s = swiglu_block(
-                    g, u,
-                    reinterpret_cast<uint4*>(P.a_codes + prow * P.a_pitch + (blk0 + c) * 16),
-                    valid);
-                sc |= s << (8 * c);
+              if (i + 1 == mine) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(drained);
+              }
+              const int blk = ti.n0 / 64 + c;
+              if (blk < P.a_blocks) {
+                const uint32_t s =
+                    swiglu_block(g, u, reinterpret_cast<uint4*>(crow + blk * 16), valid);
+                if (valid) {
+                  uint8_t* at = P.a_scales + mx_scale_offset(prow, blk, P.a_kt);
+                  // (a last block without a partner: the last MMA step of GMM2
+                  // covers the missing one with zero codes, its scale is 0)
+                  if (blk + 1 == P.a_blocks && !(blk & 1))
+                    *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(s);
+                  else
+                    *at = static_cast<uint8_t>(s);
+                }
               }
             }
-          }
-          // (a block that is missing at the end of a pair gets scale 0: the last
-          // MMA step of GMM2 covers it with zero codes)
-          if (valid) {
-            uint8_t* at = P.a_scales + mx_scale_offset(prow, blk0, P.a_kt);
-            if (nc == 2 && blk0 < P.a_blocks)
-              *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(sc);
-            else if (nc == 1 && (blk0 & ~1) < P.a_blocks)
-              *at = static_cast<uint8_t>(sc);
           }
         } else {
           // 32 columns at a time, the shared ones first, as bf16 through this
@@ -599,11 +615,11 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           // 64-byte swizzle wants them: no bank conflicts).  Whole quarters of
           // 32 rows leave by one asynchronous tensor store; fewer rows by plain
           // stores of the valid ones, four lanes per row.
-          const int c00 = ti.n0 + hw * h;
+          const int nu = pr.tn / 64;  // units of this half
           const bool whole = ti.rows - 32 * q >= 32;
 #pragma unroll 1
-          for (int i = 0; i < hw / 32; ++i) {
-            const int c = h ? hw / 32 - 1 - i : i;
+          for (int i = 0; i < nu; ++i) {
+            const int c = h ? 2 * nu - 1 - i : i;
             uint32_t v[32];
             tmem_ld32(taddr + 32 * c, v);
             tmem_ld_wait();
@@ -612,7 +628,12 @@ __global__ void __launch_bounds__(XTHREADS, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(tfree);
             }
-            const int c0 = c00 + 32 * c;
+            if (i + 1 == nu) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(drained);
+            }
+            const int c0 = ti.n0 + 32 * c;
             if (c0 >= P.H) continue;
             uint32_t w[16];
 #pragma unroll
@@ -657,6 +678,18 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     if (lane == 0) bulk_wait_group<0>();  // the stores of o are performed
   }
   tc_fence_before();
+  __syncthreads();
+  if (*s_abort && threadIdx.x == 0) {
+    // The producers may have left after different numbers of stages: complete
+    // the stages that one of them never armed, and wait (bounded) for the last
+    // copies into every slot before the CTA's memory goes.
+    const uint32_t n0 = s_issued[0], n1 = s_issued[1], n = max(n0, n1);
+    for (uint32_t k = n > XSTAGES ? n - XSTAGES : 0u; k < n; ++k) {
+      uint64_t* bar = &full[k % XSTAGES];
+      if (k >= min(n0, n1)) mbar_arrive(bar);
+      drain_wait(bar, (k / XSTAGES) & 1u, P.budget_ns);
+    }
+  }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -796,8 +829,10 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
   rc |= map_out(env, &maps.o, ws + f.off_o, p.H, p.R);
   rc |= map_scales(env, &maps.sa[0], ws + f.off_xs, f.h_kt, p.R / XM, 1);
   rc |= map_scales(env, &maps.sa[1], ws + f.off_as, f.i_kt, p.R / XM, 1);
-  rc |= map_scales(env, &maps.sw[0], up_scales, f.h_kt, p.E * ((2 * f.ip + 127) / 128), tn1 / 128);
-  rc |= map_scales(env, &maps.sw[1], down_scales, f.i_kt, p.E * ((p.H + 127) / 128), tn2 / 128);
+  rc |= map_scales(env, &maps.sw[0], up_scales, f.h_kt, p.E * ((2 * f.ip + 127) / 128),
+                   tn1 / 128);
+  rc |= map_scales(env, &maps.sw[1], down_scales, f.i_kt, p.E * ((p.H + 127) / 128),
+                   tn2 / 128);
   if (rc != HMM_OK) return HMM_ERR_CUDA;
   auto prob = [](XProb& q, int64_t kp, int64_t n, int tn) {
     q.kp = static_cast<int>(kp);
