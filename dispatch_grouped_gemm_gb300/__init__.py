@@ -14,6 +14,7 @@ the HyperMegaMoE API (§3.1) and its DFunction semantics (§3.2).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -584,11 +585,18 @@ _SCORES = {"softmax": HMM_SCORE_SOFTMAX, "sigmoid": HMM_SCORE_SIGMOID}
 
 def _gate_forward(logits, gate, bias, return_scores):
     dev = logits.device
-    ids = torch.empty((gate.T, gate.K), dtype=torch.int32, device=dev)
-    w = torch.empty((gate.T, gate.K), dtype=_TORCH_WDTYPES[gate.weights_dtype], device=dev)
+    shape = (gate.T, gate.K)
+    ids = torch.empty(shape, dtype=torch.int32, device=dev)
+    w = torch.empty(shape, dtype=_TORCH_WDTYPES[gate.weights_dtype], device=dev)
     scores = (torch.empty((gate.T, gate.E), dtype=torch.float32, device=dev)
               if return_scores else None)
-    hmm_gate_forward(Context.for_device(dev).handle, gate, logits, bias, ids, w, scores)
+    # (the library's function itself: a decode step's router is host time)
+    rc = load_library().hmm_gate_forward(
+        Context.for_device(dev).handle, ctypes.byref(gate), logits.data_ptr(),
+        None if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(),
+        None if scores is None else scores.data_ptr(), _raw_stream(_current_device()))
+    if rc != HMM_OK:
+        raise HmmError(rc, "hmm_gate_forward")
     return ids, w, scores
 
 
@@ -607,11 +615,19 @@ class _MoEGate(torch.autograd.Function):
         if dw is None and ds is None:
             return None, None, None, None
         logits, ids = ctx.saved_tensors
-        dw = None if dw is None else dw.contiguous()
-        ds = None if ds is None else ds.contiguous()
+        if dw is not None and not dw.is_contiguous():
+            dw = dw.contiguous()
+        if ds is not None and not ds.is_contiguous():
+            ds = ds.contiguous()
         dev = logits.device
         dl = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-        hmm_gate_backward(Context.for_device(dev).handle, ctx.gate, logits, ids, dw, ds, dl)
+        rc = load_library().hmm_gate_backward(
+            Context.for_device(dev).handle, ctypes.byref(ctx.gate), logits.data_ptr(),
+            ids.data_ptr(), None if dw is None else dw.data_ptr(),
+            None if ds is None else ds.data_ptr(), dl.data_ptr(),
+            _raw_stream(_current_device()))
+        if rc != HMM_OK:
+            raise HmmError(rc, "hmm_gate_backward")
         return dl, None, None, None
 
 
@@ -720,7 +736,11 @@ class Mx4Tensor:
         dev = self.codes.device
         out = torch.empty(self.shape, dtype=dtype, device=dev)
         d = HmmMx4(self.batch, self.rows, self.cols, self.cols, code, self.layout)
-        hmm_mx4_dequantize(Context.for_device(dev).handle, d, self.codes, self.scales, out)
+        rc = load_library().hmm_mx4_dequantize(
+            Context.for_device(dev).handle, ctypes.byref(d), self.codes.data_ptr(),
+            self.scales.data_ptr(), out.data_ptr(), _raw_stream(_current_device()))
+        if rc != HMM_OK:
+            raise HmmError(rc, "hmm_mx4_dequantize")
         return out
 
 
@@ -730,7 +750,11 @@ def _mx4_of(values, batch, rows, cols, ld, layout):
     dev = values.device
     codes = torch.empty(cs, dtype=torch.uint8, device=dev)
     scales = torch.empty(ss, dtype=torch.uint8, device=dev)
-    hmm_mx4_quantize(Context.for_device(dev).handle, d, values, codes, scales)
+    rc = load_library().hmm_mx4_quantize(
+        Context.for_device(dev).handle, ctypes.byref(d), values.data_ptr(), codes.data_ptr(),
+        scales.data_ptr(), _raw_stream(_current_device()))
+    if rc != HMM_OK:
+        raise HmmError(rc, "hmm_mx4_quantize")
     return Mx4Tensor(codes, scales, batch, rows, cols, layout)
 
 
@@ -764,6 +788,13 @@ def mx4_quantize_experts(w, *, gate_up=False):
     return _mx4_of(w, E, N, K, K, HMM_MX4_GATE_UP if gate_up else HMM_MX4_COLUMNS)
 
 
+@functools.lru_cache(maxsize=64)
+def _mx4_call(T, H, I, E, K, weights_dtype):
+    """(hmm_shape, workspace bytes) of a shape."""
+    shape = HmmShape(T, H, I, E, K, weights_dtype, 0)
+    return shape, hmm_mx4_workspace_size(shape)
+
+
 def moe_ffn_mx4(x, topk_ids, topk_weights, up_proj, down_proj):
     """moe_ffn for inference with microscaled 4-bit expert weights: up_proj and
     down_proj are Mx4Tensors of mx4_quantize_experts (up_proj with gate_up).
@@ -774,12 +805,12 @@ def moe_ffn_mx4(x, topk_ids, topk_weights, up_proj, down_proj):
     if x.dim() != 2 or topk_ids.dim() != 2:
         raise ValueError("x [T, H] and topk_ids [T, K] expected")
     T, H = x.shape
-    K = topk_ids.shape[1]
+    Tk, K = topk_ids.shape
     E, I = up_proj.batch, up_proj.rows // 2
     if up_proj.cols != H or (down_proj.batch, down_proj.cols, down_proj.rows) != (E, I, H):
         raise ValueError(f"up_proj {up_proj.shape} and down_proj {down_proj.shape} do not match "
                          f"each other and x {tuple(x.shape)}")
-    if topk_ids.shape[0] != T or topk_weights.shape != topk_ids.shape:
+    if Tk != T or topk_weights.shape != (T, K):
         raise ValueError("topk_ids / topk_weights must both be [T, K]")
     if x.dtype != torch.bfloat16:
         raise TypeError("x must be bfloat16")
@@ -788,16 +819,21 @@ def moe_ffn_mx4(x, topk_ids, topk_weights, up_proj, down_proj):
     wdt = _WDTYPES.get(topk_weights.dtype)
     if wdt is None:
         raise TypeError("topk_weights must be bfloat16 or float32")
-    for t in (x, topk_ids, topk_weights):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError("all arguments must be contiguous CUDA tensors")
+    if not (x.is_cuda and topk_ids.is_cuda and topk_weights.is_cuda and x.is_contiguous()
+            and topk_ids.is_contiguous() and topk_weights.is_contiguous()):
+        raise ValueError("all arguments must be contiguous CUDA tensors")
     if (x.requires_grad or topk_weights.requires_grad) and torch.is_grad_enabled():
         raise RuntimeError("moe_ffn_mx4 has no backward: call it under torch.no_grad(), or train "
                            "with moe_ffn")
-    shape = HmmShape(T, H, I, E, K, wdt, 0)
     dev = x.device
-    ws = torch.empty(hmm_mx4_workspace_size(shape), dtype=torch.uint8, device=dev)
+    shape, size = _mx4_call(T, H, I, E, K, wdt)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
     y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    hmm_forward_mx4(Context.for_device(dev).handle, shape, x, topk_ids, topk_weights,
-                    up_proj.codes, up_proj.scales, down_proj.codes, down_proj.scales, y, ws)
+    rc = load_library().hmm_forward_mx4(
+        Context.for_device(dev).handle, ctypes.byref(shape), x.data_ptr(), topk_ids.data_ptr(),
+        topk_weights.data_ptr(), up_proj.codes.data_ptr(), up_proj.scales.data_ptr(),
+        down_proj.codes.data_ptr(), down_proj.scales.data_ptr(), y.data_ptr(), ws.data_ptr(), size,
+        _raw_stream(_current_device()))
+    if rc != HMM_OK:
+        raise HmmError(rc, "hmm_forward_mx4")
     return y

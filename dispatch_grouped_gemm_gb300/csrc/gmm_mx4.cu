@@ -87,7 +87,7 @@ struct XParams {
 };
 
 struct XMaps {
-  CUtensorMap a[2][4];  // token rows: boxes of 16, 32, 64, 128 rows
+  CUtensorMap a[2][2];  // token rows: boxes of 32 and 128 rows
   CUtensorMap w[2];
   CUtensorMap o;        // expert outputs: boxes of 32 rows x 32 columns
   CUtensorMap sa[2];    // scales of the token rows: one scale tile row, 2 tiles
@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     tma_prefetch_desc(&maps.w[lane]);
     tma_prefetch_desc(&maps.sw[lane]);
     tma_prefetch_desc(&maps.sa[lane]);
-    for (int i = 0; i < 4; ++i) tma_prefetch_desc(&maps.a[lane][i]);
+    tma_prefetch_desc(&maps.a[lane][0]);
+    tma_prefetch_desc(&maps.a[lane][1]);
   }
   tc_fence_before();
   __syncthreads();
@@ -386,10 +387,10 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           }
         }
       } else {
-        const int box = ti.rows <= 16 ? 0 : (ti.rows <= 32 ? 1 : (ti.rows <= 64 ? 2 : 3));
-        const CUtensorMap* ma = &maps.a[ti.prob][box];
+        const bool few = ti.rows <= 32;
+        const CUtensorMap* ma = &maps.a[ti.prob][few ? 0 : 1];
         const CUtensorMap* msa = &maps.sa[ti.prob];
-        const uint32_t bytes = (16u << box) * 128 + XSA_BYTES;
+        const uint32_t bytes = (few ? 32 : XM) * 128 + XSA_BYTES;
         const int srow = ti.row0 / 128;
         if (ti.prob == 1) {
           // a comes from this launch's GMM1 tiles; each has a smaller ticket, so
@@ -713,13 +714,16 @@ __global__ void __launch_bounds__(MXD_WARPS * 32)
   const int lane = threadIdx.x & 31;
   const int64_t parts = (H + MXD_COLS - 1) / MXD_COLS;
   const int64_t g = static_cast<int64_t>(blockIdx.x) * MXD_WARPS + (threadIdx.x >> 5);
-  grid_dep_wait();
-  grid_dep_launch();
+  // (the next kernel is let in only after the wait, whichever branch is taken)
   const int64_t t = g / parts;
-  if (t >= T) return;
+  if (t >= T) {
+    grid_dep_wait();
+    grid_dep_launch();
+    return;
+  }
   const int64_t c0 = (g - t * parts) * MXD_COLS + 8 * lane;
-  int32_t prow_l = -1;
-  if (lane < K) prow_l = slot2prow[t * K + lane];
+  // x is read and quantised before the wait for the routing kernel: that kernel
+  // lets this one in after its own wait, so whatever wrote x has completed
   uint4 v[MXD_UNROLL];
 #pragma unroll
   for (int i = 0; i < MXD_UNROLL; ++i) {
@@ -734,6 +738,10 @@ __global__ void __launch_bounds__(MXD_WARPS * 32)
     q[i] = codes8_bf16(u, b);
     s[i] = tile_word(b, lane);
   }
+  grid_dep_wait();
+  grid_dep_launch();
+  int32_t prow_l = -1;
+  if (lane < K) prow_l = slot2prow[t * K + lane];
   for (int k = 0; k < K; ++k) {
     const int32_t prow = __shfl_sync(0xffffffffu, prow_l, k);
     if (prow < 0) continue;
@@ -812,9 +820,9 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
   XMaps maps;
   XParams P{};
   int rc = HMM_OK;
-  for (int i = 0; i < 4; ++i) {
-    rc |= map_codes(env, &maps.a[0][i], ws + f.off_x, f.hp / 2, p.R, 0, 16u << i);
-    rc |= map_codes(env, &maps.a[1][i], ws + f.off_a, f.ip / 2, p.R, 0, 16u << i);
+  for (int i = 0; i < 2; ++i) {
+    rc |= map_codes(env, &maps.a[0][i], ws + f.off_x, f.hp / 2, p.R, 0, i ? XM : 32);
+    rc |= map_codes(env, &maps.a[1][i], ws + f.off_a, f.ip / 2, p.R, 0, i ? XM : 32);
   }
   // Few tiles (at most four per SM): half of the columns each share out the SMs
   // more evenly.  One token, 8 experts, H = 7168, I = 2048 on 152 SMs: XONE_128
@@ -858,9 +866,12 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
   P.H = static_cast<int>(p.H);
   P.status = env.status;
   P.budget_ns = env.budget_ns;
-  if (cudaFuncSetAttribute(gmm_mx4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, XSMEM) !=
-      cudaSuccess)
-    return HMM_ERR_CUDA;
+  if (!*env.mx4_set) {  // once per context
+    if (cudaFuncSetAttribute(gmm_mx4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, XSMEM) !=
+        cudaSuccess)
+      return HMM_ERR_CUDA;
+    *env.mx4_set = true;
+  }
   const int64_t tiles = (p.R / XM) * (P.p[0].n_tiles + P.p[1].n_tiles);
   if (tiles >= (int64_t(1) << 31)) return HMM_ERR_SHAPE;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(env.num_sms, tiles));

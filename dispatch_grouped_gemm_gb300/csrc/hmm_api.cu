@@ -53,6 +53,7 @@ struct hmm_ctx {
   int pair_rows = 2;  // 0 single CTAs, 1 CTA pairs, 2 automatic, 3 single CTAs, small blocks
   int overlap = 1;    // programmatic dependent launches
   int fused_combine = 0;  // combine in the GMM2 epilogue
+  bool mx4_set = false;   // see GemmEnv
   uint64_t* trace = nullptr;
   size_t trace_bytes = 0;
   int trace_which = 0;
@@ -297,6 +298,7 @@ GemmEnv env_of(hmm_ctx* ctx, const Plan& p, cudaStream_t st) {
   e.budget_ns = ctx->budget_ns;
   e.stream = st;
   e.pdl = ctx->overlap != 0;
+  e.mx4_set = &ctx->mx4_set;
   return e;
 }
 

@@ -202,6 +202,7 @@ struct GemmEnv {
   uint64_t budget_ns;
   cudaStream_t stream;
   bool pdl;          // programmatic dependent launches (launch_kernel)
+  bool* mx4_set;     // the 4-bit GEMM kernel's shared-memory attribute is set
 };
 
 // forward GMM1(+SwiGLU) and GMM2 in one persistent launch with per-token-block

@@ -196,10 +196,13 @@ __device__ __forceinline__ void acc_group(float (&acc)[8], const void* rows, int
 //   d_topk_weights[t,k] = sum over the act_grad N tiles of the per-row
 //   partial dot products <G_s, a_s> (fixed order).
 //   The grid's y dimension splits each token's row over several warps, each
-// taking every gridDim.y-th group of 32 * UNROLL vectors (1 for large T;
-// several for a few tokens, e.g. decode, so that enough rows are in flight).
-template <bool WEIGHTED, bool F32>
-__global__ void __launch_bounds__(MOVE_THREADS, F32 ? 2 : 4) combine_rows_kernel(
+// taking every gridDim.y-th group of 32 * U vectors (1 for large T; several
+// for a few tokens, e.g. decode, so that enough rows are in flight).  KB: rows
+// loaded before the first of them is added (few tokens: the rows' latencies
+// overlap; one token, K = 8, H = 7168: 8.0 us with 1, 4.4 us with 8).  U and
+// KB change no result: every element's sum stays in k order.
+template <bool WEIGHTED, bool F32, int U, int KB>
+__global__ void __launch_bounds__(MOVE_THREADS, F32 || KB > 1 ? 2 : 4) combine_rows_kernel(
     const void* __restrict__ rows, const void* w, int w_dtype, int64_t T, int64_t K, int64_t H8,
     const int32_t* __restrict__ slot2prow, const int32_t* shared_row0, uint4* __restrict__ out,
     const float* dwp, int64_t dwp_ld, void* dw) {
@@ -226,32 +229,56 @@ __global__ void __launch_bounds__(MOVE_THREADS, F32 ? 2 : 4) combine_rows_kernel
   const int64_t srow = shared_row0 ? *shared_row0 + t : -1;
   // every lane runs every iteration (the shuffles below read other lanes'
   // slots); only the loads and stores are guarded
-  for (int64_t c0 = lane + static_cast<int64_t>(part) * 32 * UNROLL; c0 - lane < H8;
-       c0 += static_cast<int64_t>(parts) * 32 * UNROLL) {
-    float acc[UNROLL][8];
+  for (int64_t c0 = lane + static_cast<int64_t>(part) * 32 * U; c0 - lane < H8;
+       c0 += static_cast<int64_t>(parts) * 32 * U) {
+    float acc[U][8];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[u][j] = 0.0f;
-    for (int k = 0; k < K; ++k) {
-      const int32_t prow = __shfl_sync(0xffffffffu, prow_l, k);
-      const float s = __shfl_sync(0xffffffffu, w_l, k);
-      if (prow < 0) continue;
+    if constexpr (KB > 1) {
+      static_assert(!F32, "bf16 rows");
+      for (int k0 = 0; k0 < K; k0 += KB) {
+        uint4 v[KB][U];
+        float s[KB];
+        bool on[KB];
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int64_t c = c0 + 32 * u;
-        if (c < H8) acc_group<F32>(acc[u], rows, prow, c, H8, s);
+        for (int k = 0; k < KB; ++k) {
+          const int32_t prow = __shfl_sync(0xffffffffu, prow_l, (k0 + k) & 31);
+          s[k] = __shfl_sync(0xffffffffu, w_l, (k0 + k) & 31);
+          on[k] = k0 + k < K && prow >= 0;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (on[k] && c0 + 32 * u < H8)
+              v[k][u] = static_cast<const uint4*>(rows)[prow * H8 + c0 + 32 * u];
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (on[k] && c0 + 32 * u < H8) acc8(acc[u], v[k][u], s[k]);
+      }
+    } else {
+      for (int k = 0; k < K; ++k) {
+        const int32_t prow = __shfl_sync(0xffffffffu, prow_l, k);
+        const float s = __shfl_sync(0xffffffffu, w_l, k);
+        if (prow < 0) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t c = c0 + 32 * u;
+          if (c < H8) acc_group<F32>(acc[u], rows, prow, c, H8, s);
+        }
       }
     }
     if (srow >= 0) {
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int64_t c = c0 + 32 * u;
         if (c < H8) acc_group<F32>(acc[u], rows, srow, c, H8, 1.0f);
       }
     }
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int64_t c = c0 + 32 * u;
       if (c < H8) out[t * H8 + c] = pack8(acc[u]);
     }
@@ -273,10 +300,11 @@ static int64_t dispatch_token_warps(const Plan& p) {
   const int64_t ks = p.K + p.shared, spw = dispatch_spw(p);
   return p.T * ((ks + spw - 1) / spw);
 }
-static int combine_parts(const Plan& p) {
+// (vectors per lane and pass: 1 in the bf16 combine of few tokens)
+static int combine_parts(const Plan& p, int unroll) {
   if (p.T >= FEW_TOKENS) return 1;
-  const int64_t groups = (p.H / 8 + 32 * UNROLL - 1) / (32 * UNROLL);
-  return static_cast<int>(std::min<int64_t>(groups, 8));
+  const int64_t groups = (p.H / 8 + 32 * unroll - 1) / (32 * unroll);
+  return static_cast<int>(std::min<int64_t>(groups, unroll == 1 ? 32 : 8));
 }
 
 cudaError_t launch_dispatch_x(const Plan& p, const void* x, MetaPtrs m, void* x_perm, void* x8,
@@ -306,8 +334,11 @@ cudaError_t launch_dispatch_dy(const Plan& p, const void* dy, const void* w, int
 
 cudaError_t launch_combine_y(const Plan& p, const void* o, const void* w, int w_dtype, MetaPtrs m,
                              void* y, cudaStream_t st, bool pdl) {
-  auto kern = p.shared ? combine_rows_kernel<true, true> : combine_rows_kernel<true, false>;
-  const dim3 grid(move_grid(p.T), combine_parts(p));
+  const bool few = p.T < FEW_TOKENS && !p.shared;
+  auto kern = p.shared ? combine_rows_kernel<true, true, UNROLL, 1>
+              : few    ? combine_rows_kernel<true, false, 1, 8>
+                       : combine_rows_kernel<true, false, UNROLL, 1>;
+  const dim3 grid(move_grid(p.T), combine_parts(p, few ? 1 : UNROLL));
   return launch_kernel(kern, grid, MOVE_THREADS, 0, st, pdl, 1, o, w, w_dtype,
                        p.T, p.K, p.H / 8, static_cast<const int32_t*>(m.slot2prow),
                        static_cast<const int32_t*>(p.shared ? m.poff + p.E : nullptr),
@@ -317,8 +348,9 @@ cudaError_t launch_combine_y(const Plan& p, const void* o, const void* w, int w_
 
 cudaError_t launch_combine_dx(const Plan& p, const void* dx_perm, const float* dwp, MetaPtrs m,
                               void* dx, void* dw, int w_dtype, cudaStream_t st, bool pdl) {
-  auto kern = p.shared ? combine_rows_kernel<false, true> : combine_rows_kernel<false, false>;
-  const dim3 grid(move_grid(p.T), combine_parts(p));
+  auto kern = p.shared ? combine_rows_kernel<false, true, UNROLL, 1>
+                       : combine_rows_kernel<false, false, UNROLL, 1>;
+  const dim3 grid(move_grid(p.T), combine_parts(p, UNROLL));
   return launch_kernel(kern, grid, MOVE_THREADS, 0, st, pdl, 1, dx_perm,
                        static_cast<const void*>(nullptr), w_dtype, p.T, p.K, p.H / 8,
                        static_cast<const int32_t*>(m.slot2prow),

@@ -145,8 +145,9 @@ int hmm_destroy(hmm_ctx* ctx);
 /*   HMM_OPT_OVERLAP_LAUNCHES  0/1: launch every kernel with programmatic
  *                         stream serialization, so that it is scheduled and
  *                         sets itself up while the previous kernel of the
- *                         stream drains; it still reads nothing before that
- *                         kernel has completed.  Default 1.  Results do not
+ *                         stream drains; it still reads nothing that earlier
+ *                         work of the stream writes before that work has
+ *                         completed.  Default 1.  Results do not
  *                         depend on it. */
 #define HMM_OPT_OVERLAP_LAUNCHES 8
 /*   HMM_OPT_FUSED_COMBINE  0/1: fold the forward's Combine into the GMM2
