@@ -41,10 +41,13 @@ constexpr int XN = 256;              // weight rows per tile
 constexpr int XK = 256;              // contraction per stage: 128 bytes of codes
 constexpr int XA_BYTES = XM * 128;   // 16 KB
 constexpr int XB_BYTES = XN * 128;   // 32 KB
-constexpr int XSA_BYTES = 2 * MX_TILE_BYTES;
-constexpr int XSB_BYTES = 4 * MX_TILE_BYTES;
-constexpr int XSTAGE_BYTES = XA_BYTES + XB_BYTES + XSA_BYTES + XSB_BYTES;  // 51 KB
+constexpr int XS_BYTES = 2 * MX_TILE_BYTES;  // scales of 128 rows
+constexpr int XSTAGE_BYTES = XA_BYTES + XB_BYTES + 3 * XS_BYTES;  // 51 KB
 constexpr int XSTAGES = 4;
+constexpr int XRING = XSTAGES * XSTAGE_BYTES;
+// Half-width tiles (few tiles) and few token rows make smaller stages, and more
+// of them: what counts there is how many bytes of weights are in flight.
+constexpr int XMAX_STAGES = 9;
 constexpr int XEPI_WARPS = 8;        // two per TMEM lane quarter
 constexpr int XTOKEN_WARP = 3 + XEPI_WARPS;
 constexpr int XTHREADS = 32 * (XEPI_WARPS + 4);
@@ -52,8 +55,8 @@ constexpr int XBUF = 32 * 64;        // staged output: 32 rows of 32 bf16
 constexpr int XTI_DEPTH = 3;
 constexpr int XACC1 = XN - 32;       // second accumulator's first column
 constexpr int XSF_COL = XACC1 + XN;  // scales of A: 2 x 4 columns, then of B: 2 x 8
-constexpr int XBARS = 2 * XSTAGES + 5 + 2 * XTI_DEPTH + 2;
-constexpr int XSMEM = 1024 + XSTAGES * XSTAGE_BYTES + XEPI_WARPS * XBUF + 256 +
+constexpr int XBARS = 2 * XMAX_STAGES + 5 + 2 * XTI_DEPTH + 2;
+constexpr int XSMEM = 1024 + XRING + XEPI_WARPS * XBUF + 256 +
                       XTI_DEPTH * 20 + 16 + 4 * (MAX_E + 1);
 static_assert(XSMEM <= 232448, "shared memory per CTA");
 static_assert(XSF_COL + 24 <= 512, "TMEM columns");
@@ -71,6 +74,9 @@ struct XParams {
   XProb p[2];
   const int32_t* counts;
   int E;
+  int stages;       // pipeline stages of `stage` bytes: token rows, weights, their scales
+  int stage;
+  int a_bytes, b_bytes;  // room for the codes of the token rows and of the weights
   int* ticket;      // tiles taken after every CTA's first
   int* ready;       // per 128 token rows: epilogue warps of GMM1 that are done
   int ready_unit;   // ... when all are
@@ -172,7 +178,7 @@ __device__ void xschedule(const XParams& P, uint32_t* pref) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int e = base + 32 * u + lane;
-      cnt[u] = e < P.E ? static_cast<uint32_t>(P.counts[e]) : 0u;
+      cnt[u] = e < P.E ? static_cast<uint32_t>(__ldcg(P.counts + e)) : 0u;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -255,11 +261,11 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* bufs = smem + XSTAGES * XSTAGE_BYTES;
+  uint8_t* bufs = smem + XRING;
   uint64_t* bars = reinterpret_cast<uint64_t*>(bufs + XEPI_WARPS * XBUF);
   uint64_t* full = bars;
-  uint64_t* empty = bars + XSTAGES;
-  uint64_t* tfull = bars + 2 * XSTAGES;  // [2]
+  uint64_t* empty = bars + XMAX_STAGES;
+  uint64_t* tfull = bars + 2 * XMAX_STAGES;  // [2]
   uint64_t* tempty = tfull + 2;          // [2] the accumulator has been read
   uint64_t* tfree = tempty + 2;          // one phase per tile: its shared columns have been
                                          // read, and all of the tile before
@@ -275,7 +281,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < XSTAGES; ++s) {
+    for (int s = 0; s < P.stages; ++s) {
       mbar_init(&full[s], 2);  // both producers arm it
       mbar_init(&empty[s], 1);
     }
@@ -307,7 +313,10 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);  // uniform
-  grid_dep_wait();
+  // The previous kernel (the dispatch of x) lets this one in after its own wait
+  // for the routing, so the routing's results are there (read past L1, which
+  // could hold older ones) and the weights can start; only the token rows of
+  // GMM1 wait for the dispatch itself.
   const WaitCtl wc{s_abort, P.status, P.budget_ns};
 
   if (warp == 2 + XEPI_WARPS) {
@@ -346,6 +355,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     // for nothing: while GMM2's token rows are not there yet, they are streamed
     // into the free stages.
     const bool weights = warp == 0;
+    const uint32_t nst = P.stages;
+    if (!weights) grid_dep_wait();
     uint32_t stage = 0, sphase = 0, issued = 0;
     int slot = 0;
     uint32_t phase = 0;
@@ -366,22 +377,22 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       if (weights) {
         const CUtensorMap* mw = &maps.w[ti.prob];
         const CUtensorMap* msw = &maps.sw[ti.prob];
-        const uint32_t bytes = pr.tn * 128 + pr.tn / 128 * XSA_BYTES;
+        const uint32_t bytes = pr.tn * 128 + pr.tn / 128 * XS_BYTES;
         const int wrow = ti.e * pr.rt + ti.n0 / 128;
-        const int ask = max(0, nkb - 2 * XSTAGES);  // K block at which the next tile is asked for
+        const int ask = max(0, nkb - 8);  // K block at which the next tile is asked for
         for (int kb = 0; kb < nkb; ++kb) {
           ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
           if (!ok) break;
           if (elect_one()) {
-            uint8_t* sB = smem + stage * XSTAGE_BYTES + XA_BYTES;
+            uint8_t* sB = smem + stage * P.stage + P.a_bytes;
             mbar_arrive_expect_tx(&full[stage], bytes);
             tma_load_3d(sB, mw, &full[stage], kb * (XK / 2), ti.n0, ti.e);
-            tma_load_2d(sB + XB_BYTES + XSA_BYTES, msw, &full[stage], kb * 256, wrow);
+            tma_load_2d(sB + P.b_bytes + XS_BYTES, msw, &full[stage], kb * 256, wrow);
             if (kb == ask) mbar_arrive(want);
           }
           __syncwarp();
           ++issued;
-          if (++stage == XSTAGES) {
+          if (++stage == nst) {
             stage = 0;
             sphase ^= 1u;
           }
@@ -390,7 +401,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         const bool few = ti.rows <= 32;
         const CUtensorMap* ma = &maps.a[ti.prob][few ? 0 : 1];
         const CUtensorMap* msa = &maps.sa[ti.prob];
-        const uint32_t bytes = (few ? 32 : XM) * 128 + XSA_BYTES;
+        const uint32_t bytes = (few ? 32 : XM) * 128 + XS_BYTES;
         const int srow = ti.row0 / 128;
         if (ti.prob == 1) {
           // a comes from this launch's GMM1 tiles; each has a smaller ticket, so
@@ -405,14 +416,14 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
           if (!ok) break;
           if (elect_one()) {
-            uint8_t* sA = smem + stage * XSTAGE_BYTES;
+            uint8_t* sA = smem + stage * P.stage;
             mbar_arrive_expect_tx(&full[stage], bytes);
             tma_load_2d(sA, ma, &full[stage], kb * (XK / 2), ti.row0);
-            tma_load_2d(sA + XA_BYTES + XB_BYTES, msa, &full[stage], kb * 256, srow);
+            tma_load_2d(sA + P.a_bytes + P.b_bytes, msa, &full[stage], kb * 256, srow);
           }
           __syncwarp();
           ++issued;
-          if (++stage == XSTAGES) {
+          if (++stage == nst) {
             stage = 0;
             sphase ^= 1u;
           }
@@ -429,6 +440,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     uint32_t phase = 0;
     uint32_t n = 0;  // tiles so far
     int last_cols = 0;  // columns of the tile before
+    const uint32_t nst = P.stages;
     for (;;) {
       if (!warp_all(mbar_wait(&ti_full[slot], phase, wc))) break;
       const int prob = __shfl_sync(0xffffffffu, s_ti[slot].prob, 0);
@@ -452,8 +464,10 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       // the first operands, then the accumulator: the waits' latencies overlap
       bool ok = warp_all(mbar_wait(&full[stage], sphase, wc));
       if (!ok) break;
-      ok = warp_all(shared ? mbar_wait(tfree, (n - 1) & 1u, wc)
-                           : mbar_wait(&tempty[acc], ((n >> 1) & 1u) ^ 1u, wc));
+      // (always the accumulator's last use: with it tfree has completed the phase
+      // of tile n - 2, so that the parity below can only mean tile n - 1's)
+      ok = warp_all(mbar_wait(&tempty[acc], ((n >> 1) & 1u) ^ 1u, wc));
+      if (ok && shared) ok = warp_all(mbar_wait(tfree, (n - 1) & 1u, wc));
       if (!ok) break;
       const bool wide = cols > 128;  // the second scale tile row is in use
       const uint32_t id0 = idesc_mx4(cols, 0), id1 = idesc_mx4(cols, 2);
@@ -463,11 +477,12 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t a = smem_u32(smem) + stage * XSTAGE_BYTES;
+          const uint32_t a = smem_u32(smem) + stage * P.stage;
+          const uint32_t b = a + P.a_bytes, sc = b + P.b_bytes;
           const uint64_t da = smem_desc(a, 16, 1024, LAYOUT_SW128);
-          const uint64_t db = smem_desc(a + XA_BYTES, 16, 1024, LAYOUT_SW128);
-          const uint64_t ds = smem_desc(a + XA_BYTES + XB_BYTES, 0, 128, LAYOUT_NONE);
-          const uint64_t dt = smem_desc(a + XA_BYTES + XB_BYTES + XSA_BYTES, 0, 128, LAYOUT_NONE);
+          const uint64_t db = smem_desc(b, 16, 1024, LAYOUT_SW128);
+          const uint64_t ds = smem_desc(sc, 0, 128, LAYOUT_NONE);
+          const uint64_t dt = smem_desc(sc + XS_BYTES, 0, 128, LAYOUT_NONE);
           const int left = kp - k;
           // scales of 128 elements, the MMAs of 64 elements that use them
           // (descriptor addresses count 16 bytes)
@@ -502,7 +517,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           umma_commit(&empty[stage]);
         }
         __syncwarp();
-        if (++stage == XSTAGES) {
+        if (++stage == nst) {
           stage = 0;
           sphase ^= 1u;
         }
@@ -588,7 +603,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
                 tmem_ld32(taddr + 64 * c, g);
                 tmem_ld32(taddr + 64 * c + 32, u);
               }
-              tmem_ld_wait();
+              tmem_ld_wait_for(g);
+              tmem_ld_wait_for(u);
               if (i + 1 == mine) {
                 tc_fence_before();
                 __syncwarp();
@@ -623,7 +639,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
             const int c = h ? 2 * nu - 1 - i : i;
             uint32_t v[32];
             tmem_ld32(taddr + 32 * c, v);
-            tmem_ld_wait();
+            tmem_ld_wait_for(v);
             if (i == 0 && shares) {
               tc_fence_before();
               __syncwarp();
@@ -685,10 +701,11 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     // the stages that one of them never armed, and wait (bounded) for the last
     // copies into every slot before the CTA's memory goes.
     const uint32_t n0 = s_issued[0], n1 = s_issued[1], n = max(n0, n1);
-    for (uint32_t k = n > XSTAGES ? n - XSTAGES : 0u; k < n; ++k) {
-      uint64_t* bar = &full[k % XSTAGES];
+    const uint32_t nst = P.stages;
+    for (uint32_t k = n > nst ? n - nst : 0u; k < n; ++k) {
+      uint64_t* bar = &full[k % nst];
       if (k >= min(n0, n1)) mbar_arrive(bar);
-      drain_wait(bar, (k / XSTAGES) & 1u, P.budget_ns);
+      drain_wait(bar, (k / nst) & 1u, P.budget_ns);
     }
   }
   __syncthreads();
@@ -722,13 +739,14 @@ __global__ void __launch_bounds__(MXD_WARPS * 32)
     return;
   }
   const int64_t c0 = (g - t * parts) * MXD_COLS + 8 * lane;
-  // x is read and quantised before the wait for the routing kernel: that kernel
-  // lets this one in after its own wait, so whatever wrote x has completed
+  // x is read (past L1) and quantised before the wait for the routing kernel:
+  // that kernel lets this one in after its own wait, so whatever wrote x has
+  // completed
   uint4 v[MXD_UNROLL];
 #pragma unroll
   for (int i = 0; i < MXD_UNROLL; ++i) {
     const int64_t c = c0 + 256 * i;
-    v[i] = c < H ? x[(t * H + c) / 8] : make_uint4(0, 0, 0, 0);
+    v[i] = c < H ? __ldcg(x + (t * H + c) / 8) : make_uint4(0, 0, 0, 0);
   }
   uint32_t q[MXD_UNROLL], s[MXD_UNROLL];
 #pragma unroll
@@ -853,6 +871,12 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
   prob(P.p[1], f.ip, p.H, tn2);
   P.counts = m.counts;
   P.E = static_cast<int>(p.E);
+  // (an MMA reads 128 token rows; with room for 32 the others are whatever
+  // follows in the stage, and their accumulator rows are not used)
+  P.a_bytes = p.TK <= 32 ? 32 * 128 : XA_BYTES;
+  P.b_bytes = std::max(tn1, tn2) * 128;
+  P.stage = P.a_bytes + P.b_bytes + XS_BYTES + std::max(tn1, tn2) / 128 * XS_BYTES;
+  P.stages = std::min(XRING / P.stage, XMAX_STAGES);
   P.ticket = c.tickets;
   P.ready = c.ready;
   P.ready_unit = XEPI_WARPS * P.p[0].n_tiles;

@@ -69,12 +69,32 @@ def test_one_expert_many_times():
     """The same expert several times for one token (rows are separate slots)."""
     ids = torch.tensor([[2, 2, 2], [0, 2, 0], [1, 1, 1]])
     check(*make(3, 96, 64, 3, 3, ids=ids))
+    check(*make(20, 320, 96, 3, 8, ids=torch.ones((20, 8), dtype=torch.long)))
 
 
 @pytest.mark.parametrize("T,H,I,E,K", [(4096, 2048, 1408, 64, 6), (128, 1024, 512, 256, 8),
                                        (9000, 512, 256, 4, 2)])
 def test_larger(T, H, I, E, K):
     check(*make(T, H, I, E, K, seed=3), tokens=np.random.default_rng(0).integers(0, T, 24))
+
+
+@pytest.mark.parametrize("T,H,I,E,K", [(3637, 2064, 976, 24, 3), (2600, 6040, 696, 8, 2),
+                                       (4000, 752, 1936, 32, 2), (1500, 4112, 520, 12, 4),
+                                       (5000, 272, 136, 64, 4)])
+def test_long_batch_like_short_ones(T, H, I, E, K):
+    """A token's result does not depend on the other tokens, its place in a
+    block or the tiles' width: a long batch gives bit for bit what batches of
+    100 tokens give, call after call without a wait in between.  (Widths whose
+    last tile is narrow mix tiles that share accumulator columns with tiles
+    that do not.)"""
+    x, ids, w, W1, W2 = (t.to(DEV) for t in make(T, H, I, E, K, seed=T))
+    up, down = hmm.mx4_quantize_experts(W1, gate_up=True), hmm.mx4_quantize_experts(W2)
+    want = torch.cat([hmm.moe_ffn_mx4(a.contiguous(), b.contiguous(), c.contiguous(), up, down)
+                      for a, b, c in zip(x.split(100), ids.split(100), w.split(100))])
+    torch.cuda.synchronize()
+    got = [hmm.moe_ffn_mx4(x, ids, w, up, down) for _ in range(12)]
+    for y in got:
+        assert torch.equal(y, want)
 
 
 def test_repeatable_and_other_stream():
