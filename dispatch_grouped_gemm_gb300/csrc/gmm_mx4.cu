@@ -45,9 +45,6 @@ constexpr int XS_BYTES = 2 * MX_TILE_BYTES;  // scales of 128 rows
 constexpr int XSTAGE_BYTES = XA_BYTES + XB_BYTES + 3 * XS_BYTES;  // 51 KB
 constexpr int XSTAGES = 4;
 constexpr int XRING = XSTAGES * XSTAGE_BYTES;
-// Half-width tiles (few tiles) and few token rows make smaller stages, and more
-// of them: what counts there is how many bytes of weights are in flight.
-constexpr int XMAX_STAGES = 9;
 constexpr int XEPI_WARPS = 8;        // two per TMEM lane quarter
 constexpr int XTOKEN_WARP = 3 + XEPI_WARPS;
 constexpr int XTHREADS = 32 * (XEPI_WARPS + 4);
@@ -55,9 +52,9 @@ constexpr int XBUF = 32 * 64;        // staged output: 32 rows of 32 bf16
 constexpr int XTI_DEPTH = 3;
 constexpr int XACC1 = XN - 32;       // second accumulator's first column
 constexpr int XSF_COL = XACC1 + XN;  // scales of A: 2 x 4 columns, then of B: 2 x 8
-constexpr int XBARS = 2 * XMAX_STAGES + 5 + 2 * XTI_DEPTH + 2;
+constexpr int XBARS = 2 * XSTAGES + 5 + 2 * XTI_DEPTH + 2;
 constexpr int XSMEM = 1024 + XRING + XEPI_WARPS * XBUF + 256 +
-                      XTI_DEPTH * 20 + 16 + 4 * (MAX_E + 1);
+                      XTI_DEPTH * 24 + 16 + 4 * (MAX_E + 1);
 static_assert(XSMEM <= 232448, "shared memory per CTA");
 static_assert(XSF_COL + 24 <= 512, "TMEM columns");
 static_assert(XBARS * 8 <= 256, "barriers");
@@ -66,20 +63,14 @@ struct XProb {
   int kp;        // contraction, padded to 32
   int n;         // stored weight rows
   int rt;        // scale tiles along them
-  int n_tiles;
-  int tn;        // weight rows per tile: 256, or 128 (few tiles)
 };
 
 struct XParams {
   XProb p[2];
   const int32_t* counts;
   int E;
-  int stages;       // pipeline stages of `stage` bytes: token rows, weights, their scales
-  int stage;
-  int a_bytes, b_bytes;  // room for the codes of the token rows and of the weights
   int* ticket;      // tiles taken after every CTA's first
   int* ready;       // per 128 token rows: epilogue warps of GMM1 that are done
-  int ready_unit;   // ... when all are
   int signal;       // 0: test-only fault injection, nothing is released
   uint8_t* a_codes;
   uint8_t* a_scales;
@@ -92,12 +83,25 @@ struct XParams {
   unsigned long long budget_ns;
 };
 
+// Weight rows per tile: 256, or 128 where a problem has at most one tile of 256
+// per CTA, so that the work spreads over more SMs (a graph of 21 calls, one set
+// of experts for all tokens, 128 and 256 wide: T = 1, H = 1024, I = 512 16.1 and
+// 17.5 us; T = 47, H = 3792, I = 536 23.2 and 26.5 us; above the limit T = 700, H
+// = I = 1024 33.1 and 29.5 us).  The token blocks are known on the device only,
+// so every CTA decides there.
+__device__ __forceinline__ uint32_t xtiles(const XProb& p, uint32_t tn) {
+  return (static_cast<uint32_t>(p.n) + tn - 1) / tn;
+}
+__device__ __forceinline__ uint32_t xwidth(const XProb& p, uint32_t blocks) {
+  return blocks * xtiles(p, XN) <= gridDim.x ? XN / 2 : XN;
+}
+
 struct XMaps {
   CUtensorMap a[2][2];  // token rows: boxes of 32 and 128 rows
-  CUtensorMap w[2];
+  CUtensorMap w[2][2];  // weights: boxes of 128 and 256 rows
   CUtensorMap o;        // expert outputs: boxes of 32 rows x 32 columns
   CUtensorMap sa[2];    // scales of the token rows: one scale tile row, 2 tiles
-  CUtensorMap sw[2];    // scales of the weights: 2 scale tile rows, 2 tiles each
+  CUtensorMap sw[2][2]; // scales of the weights: 1 and 2 scale tile rows, 2 tiles each
 };
 
 struct XTile {
@@ -106,6 +110,7 @@ struct XTile {
   int row0;  // first padded token row
   int rows;  // valid rows, 1 .. 128
   int n0;    // first weight row
+  int tn;    // weight rows: 128 or 256
 };
 
 // ---------------------------------------------------------------------- PTX
@@ -200,9 +205,15 @@ __device__ void xschedule(const XParams& P, uint32_t* pref) {
 
 __device__ bool xlocate(const XParams& P, const uint32_t* pref, uint32_t t, XTile& ti) {
   const uint32_t blocks = pref[P.E] >> 7;
-  ti.prob = t >= blocks * P.p[0].n_tiles;
-  if (ti.prob) t -= blocks * P.p[0].n_tiles;
-  const uint32_t nt = P.p[ti.prob].n_tiles;
+  ti.prob = 0;
+  ti.tn = xwidth(P.p[0], blocks);
+  uint32_t nt = xtiles(P.p[0], ti.tn);
+  if (t >= blocks * nt) {
+    t -= blocks * nt;
+    ti.prob = 1;
+    ti.tn = xwidth(P.p[1], blocks);
+    nt = xtiles(P.p[1], ti.tn);
+  }
   if (t >= blocks * nt) {
     ti.prob = -1;
     return false;
@@ -222,7 +233,7 @@ __device__ bool xlocate(const XParams& P, const uint32_t* pref, uint32_t t, XTil
   const uint32_t b = r - wt * nb;
   ti.row0 = static_cast<int>((b0 + b) * XM);
   ti.rows = b + 1 == nb ? XM - static_cast<int>(pref[lo] & 127u) : XM;
-  ti.n0 = static_cast<int>(wt * P.p[ti.prob].tn);
+  ti.n0 = static_cast<int>(wt * ti.tn);
   return true;
 }
 
@@ -264,8 +275,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   uint8_t* bufs = smem + XRING;
   uint64_t* bars = reinterpret_cast<uint64_t*>(bufs + XEPI_WARPS * XBUF);
   uint64_t* full = bars;
-  uint64_t* empty = bars + XMAX_STAGES;
-  uint64_t* tfull = bars + 2 * XMAX_STAGES;  // [2]
+  uint64_t* empty = bars + XSTAGES;
+  uint64_t* tfull = bars + 2 * XSTAGES;  // [2]
   uint64_t* tempty = tfull + 2;          // [2] the accumulator has been read
   uint64_t* tfree = tempty + 2;          // one phase per tile: its shared columns have been
                                          // read, and all of the tile before
@@ -281,7 +292,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < P.stages; ++s) {
+    for (int s = 0; s < XSTAGES; ++s) {
       mbar_init(&full[s], 2);  // both producers arm it
       mbar_init(&empty[s], 1);
     }
@@ -303,8 +314,10 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
   } else if (warp == 0 && lane < 2) {
-    tma_prefetch_desc(&maps.w[lane]);
-    tma_prefetch_desc(&maps.sw[lane]);
+    for (int i = 0; i < 2; ++i) {
+      tma_prefetch_desc(&maps.w[lane][i]);
+      tma_prefetch_desc(&maps.sw[lane][i]);
+    }
     tma_prefetch_desc(&maps.sa[lane]);
     tma_prefetch_desc(&maps.a[lane][0]);
     tma_prefetch_desc(&maps.a[lane][1]);
@@ -332,7 +345,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       uint32_t phase = 0, want_phase = 0;
       uint32_t t = blockIdx.x;
       for (;;) {
-        XTile ti{-1, 0, 0, 0, 0};
+        XTile ti{-1, 0, 0, 0, 0, 0};
         xlocate(P, s_pref, t, ti);
         if (!mbar_wait(&ti_empty[slot], phase ^ 1u, wc)) break;
         s_ti[slot] = ti;
@@ -355,7 +368,6 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     // for nothing: while GMM2's token rows are not there yet, they are streamed
     // into the free stages.
     const bool weights = warp == 0;
-    const uint32_t nst = P.stages;
     if (!weights) grid_dep_wait();
     uint32_t stage = 0, sphase = 0, issued = 0;
     int slot = 0;
@@ -375,24 +387,24 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       const XProb& pr = P.p[ti.prob];
       const int nkb = (pr.kp + XK - 1) / XK;
       if (weights) {
-        const CUtensorMap* mw = &maps.w[ti.prob];
-        const CUtensorMap* msw = &maps.sw[ti.prob];
-        const uint32_t bytes = pr.tn * 128 + pr.tn / 128 * XS_BYTES;
+        const CUtensorMap* mw = &maps.w[ti.prob][ti.tn / 128 - 1];
+        const CUtensorMap* msw = &maps.sw[ti.prob][ti.tn / 128 - 1];
+        const uint32_t bytes = ti.tn * 128 + ti.tn / 128 * XS_BYTES;
         const int wrow = ti.e * pr.rt + ti.n0 / 128;
         const int ask = max(0, nkb - 8);  // K block at which the next tile is asked for
         for (int kb = 0; kb < nkb; ++kb) {
           ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
           if (!ok) break;
           if (elect_one()) {
-            uint8_t* sB = smem + stage * P.stage + P.a_bytes;
+            uint8_t* sB = smem + stage * XSTAGE_BYTES + XA_BYTES;
             mbar_arrive_expect_tx(&full[stage], bytes);
             tma_load_3d(sB, mw, &full[stage], kb * (XK / 2), ti.n0, ti.e);
-            tma_load_2d(sB + P.b_bytes + XS_BYTES, msw, &full[stage], kb * 256, wrow);
+            tma_load_2d(sB + XB_BYTES + XS_BYTES, msw, &full[stage], kb * 256, wrow);
             if (kb == ask) mbar_arrive(want);
           }
           __syncwarp();
           ++issued;
-          if (++stage == nst) {
+          if (++stage == XSTAGES) {
             stage = 0;
             sphase ^= 1u;
           }
@@ -407,8 +419,10 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           // a comes from this launch's GMM1 tiles; each has a smaller ticket, so
           // its CTA is running or done.  Order the counter's acquire with the
           // asynchronous copies of a.
-          ok = warp_all(lane != 0 ||
-                        counter_wait(&P.ready[ti.row0 / XM], P.ready_unit, wc));
+          // (all of GMM1's tiles of these rows, every epilogue warp once)
+          const uint32_t blocks = s_pref[P.E] >> 7;
+          const int done = XEPI_WARPS * xtiles(P.p[0], xwidth(P.p[0], blocks));
+          ok = warp_all(lane != 0 || counter_wait(&P.ready[ti.row0 / XM], done, wc));
           if (!ok) break;
           fence_proxy_async_global();
         }
@@ -416,14 +430,14 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
           if (!ok) break;
           if (elect_one()) {
-            uint8_t* sA = smem + stage * P.stage;
+            uint8_t* sA = smem + stage * XSTAGE_BYTES;
             mbar_arrive_expect_tx(&full[stage], bytes);
             tma_load_2d(sA, ma, &full[stage], kb * (XK / 2), ti.row0);
-            tma_load_2d(sA + P.a_bytes + P.b_bytes, msa, &full[stage], kb * 256, srow);
+            tma_load_2d(sA + XA_BYTES + XB_BYTES, msa, &full[stage], kb * 256, srow);
           }
           __syncwarp();
           ++issued;
-          if (++stage == nst) {
+          if (++stage == XSTAGES) {
             stage = 0;
             sphase ^= 1u;
           }
@@ -440,11 +454,11 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     uint32_t phase = 0;
     uint32_t n = 0;  // tiles so far
     int last_cols = 0;  // columns of the tile before
-    const uint32_t nst = P.stages;
     for (;;) {
       if (!warp_all(mbar_wait(&ti_full[slot], phase, wc))) break;
       const int prob = __shfl_sync(0xffffffffu, s_ti[slot].prob, 0);
       const int n0 = __shfl_sync(0xffffffffu, s_ti[slot].n0, 0);
+      const int tn = __shfl_sync(0xffffffffu, s_ti[slot].tn, 0);
       if (elect_one()) mbar_arrive(&ti_empty[slot]);
       if (++slot == XTI_DEPTH) {
         slot = 0;
@@ -453,7 +467,6 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       if (prob < 0) break;
       const int kp = prob == 0 ? P.p[0].kp : P.p[1].kp;
       const int rows = prob == 0 ? P.p[0].n : P.p[1].n;
-      const int tn = prob == 0 ? P.p[0].tn : P.p[1].tn;
       const uint32_t acc = n & 1u;
       const uint32_t d = tmem + acc * XACC1;
       const int cols = min(tn, (rows - n0 + 15) / 16 * 16);
@@ -477,8 +490,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t a = smem_u32(smem) + stage * P.stage;
-          const uint32_t b = a + P.a_bytes, sc = b + P.b_bytes;
+          const uint32_t a = smem_u32(smem) + stage * XSTAGE_BYTES;
+          const uint32_t b = a + XA_BYTES, sc = b + XB_BYTES;
           const uint64_t da = smem_desc(a, 16, 1024, LAYOUT_SW128);
           const uint64_t db = smem_desc(b, 16, 1024, LAYOUT_SW128);
           const uint64_t ds = smem_desc(sc, 0, 128, LAYOUT_NONE);
@@ -517,7 +530,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           umma_commit(&empty[stage]);
         }
         __syncwarp();
-        if (++stage == nst) {
+        if (++stage == XSTAGES) {
           stage = 0;
           sphase ^= 1u;
         }
@@ -553,7 +566,6 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         phase ^= 1u;
       }
       if (ti.prob < 0) break;
-      const XProb& pr = P.p[ti.prob];
       const uint32_t acc = n & 1u;
       // Accumulator 0 shares its last columns (half 1), accumulator 1 its first
       // (half 0).  The half that does not read them says only that it has left
@@ -578,7 +590,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           // chunks of gate and up columns, the one with the shared columns
           // first: the last of half 1 (accumulator 0), the first of half 0
           const int64_t prow = ti.row0 + row;
-          const int nch = pr.tn / 64, mine = nch / 2;
+          const int nch = ti.tn / 64, mine = nch / 2;
           uint8_t* crow = P.a_codes + prow * P.a_pitch;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -632,7 +644,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           // 64-byte swizzle wants them: no bank conflicts).  Whole quarters of
           // 32 rows leave by one asynchronous tensor store; fewer rows by plain
           // stores of the valid ones, four lanes per row.
-          const int nu = pr.tn / 64;  // units of this half
+          const int nu = ti.tn / 64;  // units of this half
           const bool whole = ti.rows - 32 * q >= 32;
 #pragma unroll 1
           for (int i = 0; i < nu; ++i) {
@@ -701,11 +713,10 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     // the stages that one of them never armed, and wait (bounded) for the last
     // copies into every slot before the CTA's memory goes.
     const uint32_t n0 = s_issued[0], n1 = s_issued[1], n = max(n0, n1);
-    const uint32_t nst = P.stages;
-    for (uint32_t k = n > nst ? n - nst : 0u; k < n; ++k) {
-      uint64_t* bar = &full[k % nst];
+    for (uint32_t k = n > XSTAGES ? n - XSTAGES : 0u; k < n; ++k) {
+      uint64_t* bar = &full[k % XSTAGES];
       if (k >= min(n0, n1)) mbar_arrive(bar);
-      drain_wait(bar, (k / nst) & 1u, P.budget_ns);
+      drain_wait(bar, (k / XSTAGES) & 1u, P.budget_ns);
     }
   }
   __syncthreads();
@@ -727,21 +738,23 @@ constexpr int MXD_WARPS = 4;
 __global__ void __launch_bounds__(MXD_WARPS * 32)
     dispatch_mx4_kernel(const uint4* __restrict__ x, int64_t T, int K, int64_t H, int64_t kp,
                         int64_t kt, const int32_t* __restrict__ slot2prow,
-                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, bool early) {
   const int lane = threadIdx.x & 31;
   const int64_t parts = (H + MXD_COLS - 1) / MXD_COLS;
   const int64_t g = static_cast<int64_t>(blockIdx.x) * MXD_WARPS + (threadIdx.x >> 5);
-  // (the next kernel is let in only after the wait, whichever branch is taken)
   const int64_t t = g / parts;
-  if (t >= T) {
+  // early (few tokens): x is read (past L1) and quantised before the wait for the
+  // routing kernel: that kernel lets this one in after its own wait, so whatever
+  // wrote x has completed.  With many tokens the rows' places are better fetched
+  // beside x (T = 16384: 142 us, early 155 us).
+  if (!early || t >= T) {
     grid_dep_wait();
     grid_dep_launch();
-    return;
   }
+  if (t >= T) return;
   const int64_t c0 = (g - t * parts) * MXD_COLS + 8 * lane;
-  // x is read (past L1) and quantised before the wait for the routing kernel:
-  // that kernel lets this one in after its own wait, so whatever wrote x has
-  // completed
+  int32_t prow_l = -1;
+  if (!early && lane < K) prow_l = slot2prow[t * K + lane];
   uint4 v[MXD_UNROLL];
 #pragma unroll
   for (int i = 0; i < MXD_UNROLL; ++i) {
@@ -756,10 +769,11 @@ __global__ void __launch_bounds__(MXD_WARPS * 32)
     q[i] = codes8_bf16(u, b);
     s[i] = tile_word(b, lane);
   }
-  grid_dep_wait();
-  grid_dep_launch();
-  int32_t prow_l = -1;
-  if (lane < K) prow_l = slot2prow[t * K + lane];
+  if (early) {
+    grid_dep_wait();
+    grid_dep_launch();
+    if (lane < K) prow_l = slot2prow[t * K + lane];
+  }
   for (int k = 0; k < K; ++k) {
     const int32_t prow = __shfl_sync(0xffffffffu, prow_l, k);
     if (prow < 0) continue;
@@ -780,7 +794,8 @@ cudaError_t launch_dispatch_mx4(const Plan& p, const FfnMx4Plan& f, const void* 
   return launch_kernel(dispatch_mx4_kernel,
                        static_cast<unsigned>((warps + MXD_WARPS - 1) / MXD_WARPS), MXD_WARPS * 32,
                        0, st, pdl, 1, static_cast<const uint4*>(x), p.T, static_cast<int>(p.K),
-                       p.H, f.hp, f.h_kt, static_cast<const int32_t*>(m.slot2prow), codes, scales);
+                       p.H, f.hp, f.h_kt, static_cast<const int32_t*>(m.slot2prow), codes, scales,
+                       p.T < 1024);
 }
 
 namespace {
@@ -842,44 +857,30 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
     rc |= map_codes(env, &maps.a[0][i], ws + f.off_x, f.hp / 2, p.R, 0, i ? XM : 32);
     rc |= map_codes(env, &maps.a[1][i], ws + f.off_a, f.ip / 2, p.R, 0, i ? XM : 32);
   }
-  // Few tiles (at most four per SM): half of the columns each share out the SMs
-  // more evenly.  One token, 8 experts, H = 7168, I = 2048 on 152 SMs: XONE_128
-  // with 256 and 448 tiles, XONE_256 with 128 and 224.
-  const int64_t most_blocks = std::min(p.E, p.TK) + p.TK / XM;
-  auto columns = [&](int64_t n) {
-    return most_blocks * ((n + XN - 1) / XN) <= 4 * env.num_sms ? XN / 2 : XN;
-  };
-  const int tn1 = columns(2 * f.ip), tn2 = columns(p.H);
-  rc |= map_codes(env, &maps.w[0], up_codes, f.hp / 2, 2 * f.ip, p.E, tn1);
-  rc |= map_codes(env, &maps.w[1], down_codes, f.ip / 2, p.H, p.E, tn2);
+  for (int i = 0; i < 2; ++i) {
+    const int tn = 128 * (i + 1);
+    rc |= map_codes(env, &maps.w[0][i], up_codes, f.hp / 2, 2 * f.ip, p.E, tn);
+    rc |= map_codes(env, &maps.w[1][i], down_codes, f.ip / 2, p.H, p.E, tn);
+    rc |= map_scales(env, &maps.sw[0][i], up_scales, f.h_kt, p.E * ((2 * f.ip + 127) / 128),
+                     tn / 128);
+    rc |= map_scales(env, &maps.sw[1][i], down_scales, f.i_kt, p.E * ((p.H + 127) / 128),
+                     tn / 128);
+  }
   rc |= map_out(env, &maps.o, ws + f.off_o, p.H, p.R);
   rc |= map_scales(env, &maps.sa[0], ws + f.off_xs, f.h_kt, p.R / XM, 1);
   rc |= map_scales(env, &maps.sa[1], ws + f.off_as, f.i_kt, p.R / XM, 1);
-  rc |= map_scales(env, &maps.sw[0], up_scales, f.h_kt, p.E * ((2 * f.ip + 127) / 128),
-                   tn1 / 128);
-  rc |= map_scales(env, &maps.sw[1], down_scales, f.i_kt, p.E * ((p.H + 127) / 128),
-                   tn2 / 128);
   if (rc != HMM_OK) return HMM_ERR_CUDA;
-  auto prob = [](XProb& q, int64_t kp, int64_t n, int tn) {
+  auto prob = [](XProb& q, int64_t kp, int64_t n) {
     q.kp = static_cast<int>(kp);
     q.n = static_cast<int>(n);
     q.rt = static_cast<int>((n + 127) / 128);
-    q.n_tiles = static_cast<int>((n + tn - 1) / tn);
-    q.tn = tn;
   };
-  prob(P.p[0], f.hp, 2 * f.ip, tn1);
-  prob(P.p[1], f.ip, p.H, tn2);
+  prob(P.p[0], f.hp, 2 * f.ip);
+  prob(P.p[1], f.ip, p.H);
   P.counts = m.counts;
   P.E = static_cast<int>(p.E);
-  // (an MMA reads 128 token rows; with room for 32 the others are whatever
-  // follows in the stage, and their accumulator rows are not used)
-  P.a_bytes = p.TK <= 32 ? 32 * 128 : XA_BYTES;
-  P.b_bytes = std::max(tn1, tn2) * 128;
-  P.stage = P.a_bytes + P.b_bytes + XS_BYTES + std::max(tn1, tn2) / 128 * XS_BYTES;
-  P.stages = std::min(XRING / P.stage, XMAX_STAGES);
   P.ticket = c.tickets;
   P.ready = c.ready;
-  P.ready_unit = XEPI_WARPS * P.p[0].n_tiles;
   P.signal = skip_ready_release ? 0 : 1;
   P.a_codes = ws + f.off_a;
   P.a_scales = ws + f.off_as;
@@ -896,7 +897,7 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
       return HMM_ERR_CUDA;
     *env.mx4_set = true;
   }
-  const int64_t tiles = (p.R / XM) * (P.p[0].n_tiles + P.p[1].n_tiles);
+  const int64_t tiles = (p.R / XM) * ((2 * f.ip + 127) / 128 + (p.H + 127) / 128);
   if (tiles >= (int64_t(1) << 31)) return HMM_ERR_SHAPE;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(env.num_sms, tiles));
   return launch_kernel(gmm_mx4_kernel, grid, XTHREADS, XSMEM, env.stream, env.pdl, 1, P, maps) ==
