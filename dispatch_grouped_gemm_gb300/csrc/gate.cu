@@ -333,6 +333,36 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
   }
 }
 
+namespace {
+
+// Lane q's experts (i LT + q) 4 .. + 3 of a row starting at element `row`, LT
+// lanes per token; -inf past E.
+template <int N, int LT, bool BF16>
+__device__ __forceinline__ void ld_token(const void* p, int64_t row, int q, int E, float (&l)[N]) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const int e = (i * LT + q) * 4;
+    l[4 * i] = l[4 * i + 1] = l[4 * i + 2] = l[4 * i + 3] = -INFINITY;
+    if (e < E) {
+      if constexpr (BF16) {
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + row + e);
+        l[4 * i] = __uint_as_float(v.x << 16);
+        l[4 * i + 1] = __uint_as_float(v.x & 0xFFFF0000u);
+        l[4 * i + 2] = __uint_as_float(v.y << 16);
+        l[4 * i + 3] = __uint_as_float(v.y & 0xFFFF0000u);
+      } else {
+        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + row + e);
+        l[4 * i] = v.x;
+        l[4 * i + 1] = v.y;
+        l[4 * i + 2] = v.z;
+        l[4 * i + 3] = v.w;
+      }
+    }
+  }
+}
+
+}  // namespace
+
 // Many tokens: LT lanes per token, up to N experts per lane, so that a warp
 // works on 32 / LT tokens at once.  Lane q of a token holds the experts
 // (i LT + q) 4 .. + 3 (16-byte loads); its keys also sit in shared memory,
@@ -367,28 +397,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 6 : 8)
   const bool live = t_raw < a.T;
   const int64_t t = live ? t_raw : a.T - 1;  // (every lane takes part in the shuffles)
   float l[N];
-#pragma unroll
-  for (int i = 0; i < N / 4; ++i) {
-    const int e = (i * LT + q) * 4;
-    l[4 * i] = l[4 * i + 1] = l[4 * i + 2] = l[4 * i + 3] = -INFINITY;
-    if (e < a.E) {
-      if constexpr (BF16) {
-        const uint2 v =
-            *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(logits) + t * a.ld + e);
-        l[4 * i] = __uint_as_float(v.x << 16);
-        l[4 * i + 1] = __uint_as_float(v.x & 0xFFFF0000u);
-        l[4 * i + 2] = __uint_as_float(v.y << 16);
-        l[4 * i + 3] = __uint_as_float(v.y & 0xFFFF0000u);
-      } else {
-        const float4 v =
-            *reinterpret_cast<const float4*>(static_cast<const float*>(logits) + t * a.ld + e);
-        l[4 * i] = v.x;
-        l[4 * i + 1] = v.y;
-        l[4 * i + 2] = v.z;
-        l[4 * i + 3] = v.w;
-      }
-    }
-  }
+  ld_token<N, LT, BF16>(logits, t * a.ld, q, a.E, l);
   float m = 0.0f, z = 1.0f;
   if constexpr (!SIG) {
     m = l[0];
@@ -623,6 +632,119 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
   }
 }
 
+// The same for many tokens: LT lanes per token, N experts per lane, in the
+// layout of gate_forward_many_kernel; bound by memory from there on.
+template <int N, int LT, bool BF16, bool SIG>
+__global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 4 : 5)
+    gate_backward_many_kernel(const GateArgs a, const void* __restrict__ logits,
+                              const int32_t* __restrict__ ids,
+                              const void* __restrict__ d_weights,
+                              const float* __restrict__ d_scores, void* __restrict__ d_logits) {
+  constexpr int TW = 32 / LT, KL = 32 / LT;  // tokens per warp; selected experts per lane
+  extern __shared__ int gate_smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = lane % LT, tok = lane / LT;
+  // gradients at the selected experts, in the order of the token's experts
+  float* sd = reinterpret_cast<float*>(gate_smem) + (warp * TW + tok) * (N * LT);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    reinterpret_cast<float4*>(sd)[i * LT + q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t t_raw = (static_cast<int64_t>(blockIdx.x) * GATE_WARPS + warp) * TW + tok;
+  const bool live = t_raw < a.T;
+  const int64_t t = live ? t_raw : a.T - 1;  // (every lane takes part in the shuffles)
+  float p[N];
+  ld_token<N, LT, BF16>(logits, t * a.ld, q, a.E, p);
+  float m = 0.0f, z = 1.0f;
+  if constexpr (!SIG) {
+    m = p[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) m = fmaxf(m, p[j]);
+#pragma unroll
+    for (int d = LT / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, d));
+    if (m == -INFINITY) m = 0.0f;
+    z = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      p[j] = expf(p[j] - m);
+      z += p[j];
+    }
+    z = lanes_sum<LT>(z);
+    z = z == 0.0f ? 1.0f : 1.0f / z;
+  }
+  // the selected experts, KL per lane
+  int id[KL];
+  float g[KL], ps[KL], tot = 0.0f, gn = 0.0f;
+#pragma unroll
+  for (int x = 0; x < KL; ++x) {
+    const int k = q + x * LT;
+    id[x] = -1;
+    g[x] = ps[x] = 0.0f;
+    if (k < a.K && d_weights) {
+      id[x] = ids[t * a.K + k];
+      if (static_cast<unsigned>(id[x]) >= static_cast<unsigned>(a.E)) id[x] = -1;
+      g[x] = a.scale * ld_w(d_weights, t * a.K + k, a.weights_f32);
+      if (id[x] >= 0) {
+        const float lk = ld_logit<BF16>(logits, t * a.ld + id[x]);
+        ps[x] = SIG ? sigmoid_rn(lk) : expf(lk - m) * z;
+      }
+    }
+    tot += ps[x];
+    gn += g[x] * ps[x];
+  }
+  float sum = gn;  // softmax: sum dp p
+  if (a.renorm) {
+    tot = lanes_sum<LT>(tot);
+    if (tot == 0.0f) tot = 1.0f;
+    gn = lanes_sum<LT>(gn) / tot;
+    sum = 0.0f;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int x = 0; x < KL; ++x)
+    if (id[x] >= 0) sd[id[x]] = a.renorm ? (g[x] - gn) / tot : g[x];
+  __syncwarp();
+  float4 ds[N / 4];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const int e = (i * LT + q) * 4;
+    ds[i] = d_scores && e < a.E ? *reinterpret_cast<const float4*>(d_scores + t * a.E + e)
+                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if constexpr (!SIG) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) p[4 * i + r] *= z;
+      sum += ds[i].x * p[4 * i] + ds[i].y * p[4 * i + 1] + ds[i].z * p[4 * i + 2] +
+             ds[i].w * p[4 * i + 3];
+    }
+  }
+  if constexpr (!SIG) sum = lanes_sum<LT>(sum);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const int e = (i * LT + q) * 4;
+    if (e >= a.E || !live) continue;
+    const float4 s = reinterpret_cast<const float4*>(sd)[i * LT + q];
+    const float sv[4] = {s.x, s.y, s.z, s.w};
+    const float dv[4] = {ds[i].x, ds[i].y, ds[i].z, ds[i].w};
+    float d[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float v = p[4 * i + r];
+      d[r] = SIG ? (sv[r] + dv[r]) * sigmoid_rn(v) * sigmoid_rn(-v)
+                 : v * (sv[r] + (dv[r] - sum));
+    }
+    if constexpr (BF16) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(d[0], d[1]);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(d[2], d[3]);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(d_logits) + t * a.E + e) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    } else {
+      *reinterpret_cast<float4*>(static_cast<float*>(d_logits) + t * a.E + e) =
+          make_float4(d[0], d[1], d[2], d[3]);
+    }
+  }
+}
+
 // Only the selected experts have a gradient (sigmoid or renormalised weights,
 // no d_scores): L lanes per token, K <= L, read the K selected logits, write
 // the row's zeros and then the K values.  VEC: rows are whole 16-byte vectors.
@@ -781,7 +903,23 @@ cudaError_t run_many(const hmm_gate& g, const void* logits, const float* bias, i
                        smem, st, pdl, 1, gate_args(g), logits, bias, ids, weights, scores);
 }
 
-// Tokens from which the kernel for many tokens is the faster one.
+template <int N, int LT>
+cudaError_t run_backward_many(const hmm_gate& g, const void* logits, const int32_t* ids,
+                              const void* d_weights, const float* d_scores, void* d_logits,
+                              cudaStream_t st, bool pdl) {
+  constexpr int TOKENS = GATE_WARPS * 32 / LT;
+  const bool sig = g.score == HMM_SCORE_SIGMOID;
+  auto kern = g.logits_dtype == HMM_DTYPE_BF16
+                  ? (sig ? gate_backward_many_kernel<N, LT, true, true>
+                         : gate_backward_many_kernel<N, LT, true, false>)
+                  : (sig ? gate_backward_many_kernel<N, LT, false, true>
+                         : gate_backward_many_kernel<N, LT, false, false>);
+  const size_t smem = sizeof(float) * GATE_WARPS * 32 * N;
+  return launch_kernel(kern, static_cast<unsigned>((g.T + TOKENS - 1) / TOKENS), GATE_WARPS * 32,
+                       smem, st, pdl, 1, gate_args(g), logits, ids, d_weights, d_scores, d_logits);
+}
+
+// Tokens from which the kernels for many tokens are the faster ones.
 constexpr int64_t GATE_MANY = 4096;
 
 struct RunBackward {
@@ -870,6 +1008,21 @@ cudaError_t launch_gate_backward(const hmm_gate& g, const void* logits, const in
   }
   const GateArgs a = gate_args(g);
   const int bytes = g.logits_dtype == HMM_DTYPE_BF16 ? 2 : 4;
+  if (g.T >= GATE_MANY && g.E % 4 == 0 && g.ld_logits % 4 == 0 &&
+      aligned_to(logits, 4 * bytes) && aligned_to(d_logits, 4 * bytes) &&
+      aligned_to(d_scores, 16)) {
+    if (g.E <= 64)
+      return run_backward_many<16, 4>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
+    if (g.E <= 128)
+      return run_backward_many<32, 4>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
+    if (g.E <= 160)
+      return run_backward_many<40, 4>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
+    if (g.E <= 256)
+      return run_backward_many<32, 8>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
+    if (g.E <= 512)
+      return run_backward_many<32, 16>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
+    return run_backward_many<32, 32>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
+  }
   const bool vec = gate_vec(a, bytes, g.ld_logits, logits) && gate_vec(a, bytes, g.E, d_logits);
   return by_length<RunBackward>(g, vec, logits, ids, d_weights, d_scores, d_logits, st, pdl);
 }

@@ -169,6 +169,42 @@ def test_many_tokens_like_few(score, E, K, groups, topk_groups, group_top, dtype
             assert torch.equal(hmm.moe_gate(odd, K, **kw)[0][same], a[0][same])
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K", [(64, 6), (8, 8), (128, 8), (100, 7), (160, 6), (256, 32), (300, 5),
+                                 (512, 9), (1024, 16), (31, 3)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_tokens_gradient_like_few(score, E, K, dtype):
+    """The gradient of a long batch against that of short ones, with and without
+    gradients of the scores and of the weights: sums in another order, 2e-5 of
+    the largest gradient of a row; bf16 outputs one rounding."""
+    T = 4099
+    g = torch.Generator().manual_seed(E)
+    l = logits_of(T, E, dtype, E)
+    l[5], l[7] = -math.inf, 0.0
+    l[torch.rand((T, E), generator=g) < 0.05] = -math.inf
+    l = l.to(DEV)
+    dw, ds = torch.randn((T, K), generator=g).to(DEV), 0.1 * torch.randn((T, E), generator=g).to(DEV)
+
+    def grad(x, dw, ds, renorm):
+        x = x.detach().requires_grad_()
+        _, w, p = hmm.moe_gate(x, K, score=score, renormalize=renorm, scale=1.5,
+                               return_scores=True)
+        outs = [o for o, d in ((w, dw), (p, ds)) if d is not None]
+        return torch.autograd.grad(outs, x, [d for d in (dw, ds) if d is not None])[0]
+
+    for renorm in (False, True):
+        for a, b in ((dw, ds), (dw, None), (None, ds)):
+            got = grad(l, a, b, renorm).float()
+            # (short ones in fp32, so that only one side is rounded)
+            want = torch.cat([grad(x, None if a is None else a[i:i + 1024],
+                                   None if b is None else b[i:i + 1024], renorm)
+                              for i, x in zip(range(0, T, 1024), l.float().split(1024))])
+            lim = 2e-5 * want.abs().amax(1, keepdim=True) + 1e-12
+            if dtype == torch.bfloat16:
+                lim = lim + 2.0 ** -8 * want.abs()
+            assert ((got - want).abs() <= lim).all()
+
+
 def test_equal_keys_go_to_the_lowest_index():
     l = torch.zeros((3, 70), device=DEV)
     l[1, 40:] = 1.0
