@@ -369,7 +369,7 @@ __device__ __forceinline__ void ld_token(const void* p, int64_t row, int q, int 
 // where a round of the selection reaches them by a computed index, and the
 // maxima of its runs of eight in registers.  A round costs about 70
 // instructions for all of the warp's tokens (the one-warp kernel above: 100
-// for one).  Needs E and, with groups, E / groups to be multiples of 4.
+// for one).  Needs E to be a multiple of 4.
 template <int N, int LT, bool BF16, bool SIG>
 __global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 6 : 8)
     gate_forward_many_kernel(const GateArgs a, const void* __restrict__ logits,
@@ -450,13 +450,22 @@ __global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 6 : 8)
     // lane q: the worths of groups q, q + LT, ..
     for (int g = q; g < a.groups; g += LT) {
       int k1 = CLOSED, k2 = CLOSED;
-      for (int e = g * n; e < (g + 1) * n; e += 4) {
-        const int4 k = *piece(tok * LT + (e >> 2) % LT, (e >> 2) / LT);
-        const int h1 = max(k.x, k.y), h2 = max(k.z, k.w);
-        const int s2 = max(min(h1, h2), max(min(k.x, k.y), min(k.z, k.w)));
-        const int s1 = max(h1, h2);
-        k2 = max(min(k1, s1), max(k2, s2));
-        k1 = max(k1, s1);
+      if (n % 4) {  // groups that end inside a vector
+        for (int e = g * n; e < (g + 1) * n; ++e) {
+          const int k = reinterpret_cast<const int*>(
+              piece(tok * LT + (e >> 2) % LT, (e >> 2) / LT))[e & 3];
+          k2 = max(k2, min(k1, k));
+          k1 = max(k1, k);
+        }
+      } else {
+        for (int e = g * n; e < (g + 1) * n; e += 4) {
+          const int4 k = *piece(tok * LT + (e >> 2) % LT, (e >> 2) / LT);
+          const int h1 = max(k.x, k.y), h2 = max(k.z, k.w);
+          const int s2 = max(min(h1, h2), max(min(k.x, k.y), min(k.z, k.w)));
+          const int s1 = max(h1, h2);
+          k2 = max(min(k1, s1), max(k2, s2));
+          k1 = max(k1, s1);
+        }
       }
       worths[g] = a.group_top == 1 ? k1 : order_key(key_value(k1) + key_value(k2));
     }
@@ -476,8 +485,15 @@ __global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 6 : 8)
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
       const int e = (i * LT + q) * 4;
-      const bool on = (open >> ((e * inv) >> 20)) & 1u;
-      if (!on && e < a.E) *piece(lane, i) = make_int4(CLOSED, CLOSED, CLOSED, CLOSED);
+      if (n % 4 == 0) {
+        const bool on = (open >> ((e * inv) >> 20)) & 1u;
+        if (!on && e < a.E) *piece(lane, i) = make_int4(CLOSED, CLOSED, CLOSED, CLOSED);
+      } else if (e < a.E) {
+        int* k = reinterpret_cast<int*>(piece(lane, i));
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (!((open >> (((e + r) * inv) >> 20)) & 1u)) k[r] = CLOSED;
+      }
     }
 #pragma unroll
     for (int s = 0; s < S; ++s) {
@@ -919,7 +935,10 @@ cudaError_t run_backward_many(const hmm_gate& g, const void* logits, const int32
                        smem, st, pdl, 1, gate_args(g), logits, ids, d_weights, d_scores, d_logits);
 }
 
-// Tokens from which the kernels for many tokens are the faster ones.
+// Tokens from which the kernels for many tokens are the faster ones (forward,
+// one and the other kernel: E = 64, T = 4000 8.2 and 8.2 us, T = 8000 10.2 and
+// 8.2; E = 256 grouped 12.3 and 14.3, 16.4 and 16.4; E = 160 10.2 and 12.3, 14.3
+// and 12.3).
 constexpr int64_t GATE_MANY = 4096;
 
 struct RunBackward {
@@ -982,9 +1001,9 @@ cudaError_t launch_gate_forward(const hmm_gate& g, const void* logits, const flo
   const bool vec = gate_vec(a, g.logits_dtype == HMM_DTYPE_BF16 ? 2 : 4, g.ld_logits, logits) &&
                    (!scores || aligned_to(scores, 16));
   const int64_t logit_bytes = g.logits_dtype == HMM_DTYPE_BF16 ? 2 : 4;
-  if (g.T >= GATE_MANY && g.E % 4 == 0 && (g.groups == 1 || (g.E / g.groups) % 4 == 0) &&
-      g.group_top <= 2 && g.ld_logits % 4 == 0 && aligned_to(logits, 4 * logit_bytes) &&
-      aligned_to(bias, 16) && aligned_to(scores, 16)) {
+  if (g.T >= GATE_MANY && g.E % 4 == 0 && (g.groups == 1 || g.group_top <= 2) &&
+      g.ld_logits % 4 == 0 && aligned_to(logits, 4 * logit_bytes) && aligned_to(bias, 16) &&
+      aligned_to(scores, 16)) {
     // 32 to 40 experts per lane (E = 256, T = 65537: 64 per lane 64 us, few warps
     // fit; 32 51 us; 16 72 us, fewer tokens share a round.  E = 160, T = 131072: 40
     // per lane 59 us, 24 63 us)

@@ -115,7 +115,8 @@ int hmm_destroy(hmm_ctx* ctx);
  *   HMM_OPT_WAIT_BUDGET_NS  budget of every bounded device wait, in ns
  *                         (default 2e9; range 1e6 .. 6e10).
  *   HMM_OPT_INJECT_SKIP_READY  test-only fault injection on the host side: when
- *                         1, the next hmm_forward launches its GMM1 tiles
+ *                         1, the next hmm_forward (or hmm_forward_mx4)
+ *                         launches its GMM1 tiles
  *                         without releasing the GMM2 ready counters, so every
  *                         GMM2 tile's bounded wait runs out and the call
  *                         reports HMM_STATUS_TIMEOUT; when 2, the next

@@ -134,7 +134,8 @@ def test_scores_and_bf16_weights(score):
 @pytest.mark.parametrize("E,K,groups,topk_groups,group_top", [
     (64, 6, 1, 1, 1), (8, 8, 1, 1, 1), (128, 8, 1, 1, 1), (100, 7, 5, 3, 2), (160, 6, 8, 3, 1),
     (256, 8, 8, 4, 2), (224, 32, 4, 3, 2), (300, 5, 1, 1, 1), (512, 9, 32, 5, 2), (384, 8, 8, 4, 1),
-    (1024, 16, 16, 2, 2), (30, 3, 1, 1, 1), (96, 6, 4, 2, 3)])
+    (1024, 16, 16, 2, 2), (30, 3, 1, 1, 1), (96, 6, 4, 2, 3), (300, 8, 4, 2, 2), (60, 5, 10, 4, 1),
+    (120, 4, 1, 1, 3)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_many_tokens_like_few(score, E, K, groups, topk_groups, group_top, dtype):
     """A long batch gives row by row what short ones give: same ids, weights
