@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
 
 // Dispatch: token t's row of x in 4-bit form, once, to the padded rows of its
 // K slots.  One warp per token and MXD_COLS columns; a lane holds 8 elements,
-// four lanes a block, sixteen lanes the four blocks of a scale tile's row.
+// four lanes a block, the first of which writes the scale.
 namespace {
 constexpr int MXD_UNROLL = 4;
 constexpr int MXD_COLS = 256 * MXD_UNROLL;
@@ -767,23 +767,25 @@ __global__ void __launch_bounds__(MXD_WARPS * 32)
     const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     const uint32_t b = quad_scale_bf16(u);
     q[i] = codes8_bf16(u, b);
-    s[i] = tile_word(b, lane);
+    s[i] = b;
   }
   if (early) {
     grid_dep_wait();
     grid_dep_launch();
     if (lane < K) prow_l = slot2prow[t * K + lane];
   }
+  // (a step of 256 columns: 128 bytes of codes, two scale tiles)
   for (int k = 0; k < K; ++k) {
     const int32_t prow = __shfl_sync(0xffffffffu, prow_l, k);
     if (prow < 0) continue;
+    uint32_t* crow = reinterpret_cast<uint32_t*>(codes + prow * (kp / 2) + c0 / 2);
+    uint8_t* srow = scales + mx_scale_offset(prow, c0 / 32, kt);
 #pragma unroll
     for (int i = 0; i < MXD_UNROLL; ++i) {
       const int64_t c = c0 + 256 * i;
-      if (c < kp)
-        *reinterpret_cast<uint32_t*>(codes + static_cast<int64_t>(prow) * (kp / 2) + c / 2) = q[i];
-      if ((lane & 15) == 0 && c < kt * 128)
-        *reinterpret_cast<uint32_t*>(scales + mx_scale_offset(prow, c / 32, kt)) = s[i];
+      if (c < kp) crow[32 * i] = q[i];
+      if ((lane & 3) == 0 && c < kt * 128)
+        srow[2 * MX_TILE_BYTES * i] = static_cast<uint8_t>(s[i]);
     }
   }
 }

@@ -34,9 +34,9 @@ __device__ __forceinline__ void st_values8(void* p, int64_t i, const float (&v)[
 }  // namespace
 
 // One warp per row; blockIdx.y and gridDim.y share out the pieces of a row, U
-// steps of 256 columns each.  A lane holds 8 elements, four lanes a block,
-// sixteen lanes the four blocks of a scale tile's row.  Rows and columns run
-// over whole scale tiles, so that the padding scales are written too.  (Lane
+// steps of 256 columns each.  A lane holds 8 elements, four lanes a block, the
+// first of which writes the scale.  Rows and columns run over whole scale tiles,
+// so that the padding scales are written too.  (Lane
 // groups walking (row, scale tile) pairs in one flat order, without idle lanes
 // at the end of a row, were slower: their index arithmetic costs more.)
 template <bool F32, int U>
@@ -53,6 +53,9 @@ __global__ void __launch_bounds__(MX_THREADS)
   for (int64_t p = static_cast<int64_t>(blockIdx.y) * (256 * U); p < kt * 128;
        p += static_cast<int64_t>(gridDim.y) * (256 * U)) {
     const int64_t c0 = p + 8 * lane;
+    // (a step of 256 columns: 128 bytes of codes, two scale tiles)
+    uint32_t* crow = reinterpret_cast<uint32_t*>(codes + r * (kp / 2) + c0 / 2);
+    uint8_t* srow = scales + mx_scale_offset(r, c0 / 32, kt);
     float v[U][F32 ? 8 : 1];
     uint4 b[U];
 #pragma unroll
@@ -91,10 +94,9 @@ __global__ void __launch_bounds__(MX_THREADS)
         s = quad_scale_bf16(u);
         q = codes8_bf16(u, s);
       }
-      const uint32_t word = tile_word(s, lane);
-      if (in && c < kp) *reinterpret_cast<uint32_t*>(codes + r * (kp / 2) + c / 2) = q;
-      if ((lane & 15) == 0 && c < kt * 128)
-        *reinterpret_cast<uint32_t*>(scales + mx_scale_offset(r, c / 32, kt)) = word;
+      if (in && c < kp) crow[32 * i] = q;
+      if ((lane & 3) == 0 && c < kt * 128)
+        srow[2 * MX_TILE_BYTES * i] = static_cast<uint8_t>(s);
     }
   }
 }
@@ -115,14 +117,15 @@ __global__ void __launch_bounds__(MX_THREADS)
   for (int64_t p = static_cast<int64_t>(blockIdx.y) * (STEP * U); p < cols;
        p += static_cast<int64_t>(gridDim.y) * (STEP * U)) {
     const int64_t c0 = p + PER * lane;
+    const uint8_t* crow = codes + r * (kp / 2) + c0 / 2;
+    const uint8_t* srow = scales + mx_scale_offset(r, c0 / 32, kt);
     uint32_t q[U], s[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t c = c0 + STEP * i;
-      if (c < cols) {
-        const uint8_t* at = codes + r * (kp / 2) + c / 2;
+      if (c0 + STEP * i < cols) {
+        const uint8_t* at = crow + STEP / 2 * i;
         q[i] = F32 ? *reinterpret_cast<const uint16_t*>(at) : *reinterpret_cast<const uint32_t*>(at);
-        s[i] = scales[mx_scale_offset(r, c / 32, kt)];
+        s[i] = srow[STEP / 128 * MX_TILE_BYTES * i];
       }
     }
 #pragma unroll

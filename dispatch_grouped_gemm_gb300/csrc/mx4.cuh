@@ -99,25 +99,19 @@ __device__ __forceinline__ uint32_t quad_scale_bf16(const uint32_t (&u)[4]) {
   m = pair_amax(m, __shfl_xor_sync(0xffffffffu, m, 2));
   return mx_scale_byte(max(m << 16, m & 0xFFFF0000u));
 }
-// Eight bf16 values to codes.
+// Eight bf16 values to codes (s: their block's scale byte).
 __device__ __forceinline__ uint32_t codes8_bf16(const uint32_t (&u)[4], uint32_t s) {
-  const float inv = mx_inverse_scale(s);
+  // (a power of two up to 2^127: its upper half is the bf16 value)
+  const uint32_t i = __float_as_uint(mx_inverse_scale(s));
+  const uint32_t inv = (i >> 16) | i;
   float w[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    w[2 * j] = pair_lo(u[j]) * inv;
-    w[2 * j + 1] = pair_hi(u[j]) * inv;
+    const uint32_t v = pair_mul(u[j], inv);
+    w[2 * j] = pair_lo(v);
+    w[2 * j + 1] = pair_hi(v);
   }
   return mx_codes8(w);
-}
-// The scale bytes of the four blocks that 16 lanes hold, as the word of a scale
-// tile's row (s: this lane's block).
-__device__ __forceinline__ uint32_t tile_word(uint32_t s, int lane) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w |= __shfl_sync(0xffffffffu, s, (lane & 16) + 4 * j) << (8 * j);
-  return w;
 }
 
 // Byte offset of the scale of (row, block) in an operand's scale array with
