@@ -10,6 +10,10 @@ is missing, every call raises.
 the autograd entry point (forward saves what the backward needs, backward
 returns one gradient per public argument and None for topk_ids), following
 the HyperMegaMoE API (§3.1) and its DFunction semantics (§3.2).
+
+``moe_gate`` is the router in front of it (differentiable in the logits);
+``mx4_quantize_experts`` and ``moe_ffn_mx4`` serve the same layer with
+microscaled 4-bit expert weights.
 """
 from __future__ import annotations
 
