@@ -45,6 +45,14 @@ constexpr int XS_BYTES = 2 * MX_TILE_BYTES;  // scales of 128 rows
 constexpr int XSTAGE_BYTES = XA_BYTES + XB_BYTES + 3 * XS_BYTES;  // 51 KB
 constexpr int XSTAGES = 4;
 constexpr int XRING = XSTAGES * XSTAGE_BYTES;
+// CTA pairs: each CTA stages its 128 token rows, half of the weight rows, and the
+// scales of all of them
+constexpr int XP_B_BYTES = XB_BYTES / 2;
+constexpr int XP_STAGE_BYTES = XA_BYTES + XP_B_BYTES + 3 * XS_BYTES;  // 35 KB
+constexpr int XP_STAGES = XRING / XP_STAGE_BYTES;                     // 5
+constexpr int XP_W_BYTES = XP_B_BYTES + 2 * XS_BYTES;  // loads of one CTA and stage
+constexpr int XP_T_BYTES = XA_BYTES + XS_BYTES;
+static_assert(XP_STAGES >= XSTAGES, "ring");
 constexpr int XEPI_WARPS = 8;        // two per TMEM lane quarter
 constexpr int XTOKEN_WARP = 3 + XEPI_WARPS;
 constexpr int XTHREADS = 32 * (XEPI_WARPS + 4);
@@ -52,9 +60,9 @@ constexpr int XBUF = 32 * 64;        // staged output: 32 rows of 32 bf16
 constexpr int XTI_DEPTH = 3;
 constexpr int XACC1 = XN - 32;       // second accumulator's first column
 constexpr int XSF_COL = XACC1 + XN;  // scales of A: 2 x 4 columns, then of B: 2 x 8
-constexpr int XBARS = 2 * XSTAGES + 5 + 2 * XTI_DEPTH + 2;
+constexpr int XBARS = 2 * XP_STAGES + 5 + 2 * XTI_DEPTH + 2;
 constexpr int XSMEM = 1024 + XRING + XEPI_WARPS * XBUF + 256 +
-                      XTI_DEPTH * 24 + 16 + 4 * (MAX_E + 1);
+                      XTI_DEPTH * 24 + 32 + 4 * (MAX_E + 1);
 static_assert(XSMEM <= 232448, "shared memory per CTA");
 static_assert(XSF_COL + 24 <= 512, "TMEM columns");
 static_assert(XBARS * 8 <= 256, "barriers");
@@ -67,6 +75,7 @@ struct XProb {
 
 struct XParams {
   XProb p[2];
+  const int32_t* poff;
   const int32_t* counts;
   int E;
   int* ticket;      // tiles taken after every CTA's first
@@ -108,7 +117,7 @@ struct XTile {
   int prob;  // -1: no more tiles
   int e;
   int row0;  // first padded token row
-  int rows;  // valid rows, 1 .. 128
+  int rows;  // valid rows, 1 .. 128 (pairs: 1 .. 256, the odd CTA has those from 128)
   int n0;    // first weight row
   int tn;    // weight rows: 128 or 256
 };
@@ -152,11 +161,43 @@ __device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t adesc, uint64_t bd
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
       : "memory");
 }
+// The same for a CTA pair: scales of either CTA from its own shared memory to
+// its own TMEM; D of both CTAs, A by CTA, B half from each.
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+__device__ __forceinline__ void umma_mx4_pair(uint32_t d, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], "
+      "[%6], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
+  if constexpr (PAIR)
+    tmem_cp_scales_pair(taddr, desc);
+  else
+    tmem_cp_scales(taddr, desc);
+}
+template <bool PAIR>
+__device__ __forceinline__ void umma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                     uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (PAIR)
+    umma_mx4_pair(d, adesc, bdesc, idesc, sfa, sfb, accumulate);
+  else
+    umma_mx4(d, adesc, bdesc, idesc, sfa, sfb, accumulate);
+}
 // Instruction descriptor of kind::mxf4: e2m1 x e2m1, ue8m0 scales, both
 // operands K-major; sf: which half of a 4-byte scale column (0 or 2).
+template <bool PAIR>
 __device__ __forceinline__ uint32_t idesc_mx4(int n, uint32_t sf) {
   return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
-         (static_cast<uint32_t>(XM >> 4) << 24) | (sf << 29);
+         (static_cast<uint32_t>((PAIR ? 2 * XM : XM) >> 4) << 24) | (sf << 29);
 }
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -173,7 +214,9 @@ __device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffff
 // pref[e]: token blocks of the experts before e, times 128, plus the rows that
 // e's last block lacks (0 .. 127); pref[E]: all token blocks, times 128.  (The
 // padded row space gives every expert whole blocks, so 128 times its blocks is
-// also e's first row.)
+// also e's first row.)  Pairs: the same with pairs of blocks, whose first rows come
+// from poff.
+template <bool PAIR>
 __device__ void xschedule(const XParams& P, uint32_t* pref) {
   constexpr int U = 8;  // loads in flight per lane
   const int lane = threadIdx.x & 31;
@@ -188,14 +231,15 @@ __device__ void xschedule(const XParams& P, uint32_t* pref) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int e = base + 32 * u + lane;
-      const uint32_t blocks = (cnt[u] + XM - 1) / XM;
+      const uint32_t lack = (XM - cnt[u] % XM) % XM;
+      const uint32_t blocks = PAIR ? (cnt[u] + 2 * XM - 1) / (2 * XM) : (cnt[u] + XM - 1) / XM;
       uint32_t inc = blocks;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const uint32_t n = __shfl_up_sync(0xffffffffu, inc, d);
         if (lane >= d) inc += n;
       }
-      if (e < P.E) pref[e] = ((carry + inc - blocks) << 7) | (blocks * XM - cnt[u]);
+      if (e < P.E) pref[e] = ((carry + inc - blocks) << 7) | lack;
       carry += __shfl_sync(0xffffffffu, inc, 31);
     }
   }
@@ -203,15 +247,16 @@ __device__ void xschedule(const XParams& P, uint32_t* pref) {
   __syncwarp();
 }
 
+template <bool PAIR>
 __device__ bool xlocate(const XParams& P, const uint32_t* pref, uint32_t t, XTile& ti) {
   const uint32_t blocks = pref[P.E] >> 7;
   ti.prob = 0;
-  ti.tn = xwidth(P.p[0], blocks);
+  ti.tn = PAIR ? XN : xwidth(P.p[0], blocks);
   uint32_t nt = xtiles(P.p[0], ti.tn);
   if (t >= blocks * nt) {
     t -= blocks * nt;
     ti.prob = 1;
-    ti.tn = xwidth(P.p[1], blocks);
+    ti.tn = PAIR ? XN : xwidth(P.p[1], blocks);
     nt = xtiles(P.p[1], ti.tn);
   }
   if (t >= blocks * nt) {
@@ -231,8 +276,13 @@ __device__ bool xlocate(const XParams& P, const uint32_t* pref, uint32_t t, XTil
   const uint32_t r = t - b0 * nt;
   const uint32_t wt = r / nb;  // token blocks innermost: a weight tile is reused from L2
   const uint32_t b = r - wt * nb;
-  ti.row0 = static_cast<int>((b0 + b) * XM);
-  ti.rows = b + 1 == nb ? XM - static_cast<int>(pref[lo] & 127u) : XM;
+  if constexpr (PAIR) {
+    ti.row0 = __ldcg(P.poff + lo) + static_cast<int>(b) * 2 * XM;
+    ti.rows = min(2 * XM, __ldcg(P.counts + lo) - static_cast<int>(b) * 2 * XM);
+  } else {
+    ti.row0 = static_cast<int>((b0 + b) * XM);
+    ti.rows = b + 1 == nb ? XM - static_cast<int>(pref[lo] & 127u) : XM;
+  }
   ti.n0 = static_cast<int>(wt * ti.tn);
   return true;
 }
@@ -267,16 +317,30 @@ __device__ __forceinline__ uint32_t swiglu_block(const uint32_t (&g)[32], const 
 
 }  // namespace
 
+// PAIR: clusters of two CTAs run 256 token rows x 256 weight rows with 2-SM MMAs:
+// each CTA holds its 128 token rows and half of the weight rows, so that a stage
+// is 35 KB for the same work per SM, and five fit.  The even CTA schedules, arms
+// the stages for both CTAs' loads and issues.  Single CTAs and pairs, us of this
+// kernel with evenly spread tokens: H = 7168, I = 2048, E = 32, K = 8: T = 16384
+// 1823 and 1638 (skewed 1873 and 1690), T = 4096 523 and 484; H = 2048, I = 1408,
+// K = 6: E = 64, T = 16384 371 and 349, T = 8192 203 and 200, T = 6144 (4.5 blocks
+// an expert) 162 and 173, T = 4096 121 and 125; E = 6, T = 2048 55.5 and 53.2, T =
+// 1024 (too few tiles) 35.6 and 36.4; H = 1024, I = 512, E = 8, K = 2, T = 16384
+// (contractions of 4 and 2 stages) 44.8 and 46.5.
+template <bool PAIR>
 __global__ void __launch_bounds__(XTHREADS, 1)
     gmm_mx4_kernel(const __grid_constant__ XParams P, const __grid_constant__ XMaps maps) {
+  constexpr int NST = PAIR ? XP_STAGES : XSTAGES;
+  constexpr int SBYTES = PAIR ? XP_STAGE_BYTES : XSTAGE_BYTES;
+  constexpr int BBYTES = PAIR ? XP_B_BYTES : XB_BYTES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* bufs = smem + XRING;
   uint64_t* bars = reinterpret_cast<uint64_t*>(bufs + XEPI_WARPS * XBUF);
   uint64_t* full = bars;
-  uint64_t* empty = bars + XSTAGES;
-  uint64_t* tfull = bars + 2 * XSTAGES;  // [2]
+  uint64_t* empty = bars + NST;
+  uint64_t* tfull = bars + 2 * NST;      // [2]
   uint64_t* tempty = tfull + 2;          // [2] the accumulator has been read
   uint64_t* tfree = tempty + 2;          // one phase per tile: its shared columns have been
                                          // read, and all of the tile before
@@ -288,31 +352,42 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_ti + XTI_DEPTH);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   uint32_t* s_issued = s_tmem + 2;  // stages issued by the two producers
-  uint32_t* s_pref = s_tmem + 4;    // [E + 1]
+  uint32_t* s_peer = s_tmem + 4;    // even CTA of a pair: the odd one's counts and abort flag
+  uint32_t* s_pref = s_tmem + 8;    // [E + 1]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  constexpr int EPIS = PAIR ? 2 * XEPI_WARPS : XEPI_WARPS;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < XSTAGES; ++s) {
+    for (int s = 0; s < NST; ++s) {
       mbar_init(&full[s], 2);  // both producers arm it
       mbar_init(&empty[s], 1);
     }
     mbar_init(&tfull[0], 1);
     mbar_init(&tfull[1], 1);
-    mbar_init(&tempty[0], XEPI_WARPS);
-    mbar_init(&tempty[1], XEPI_WARPS);
-    mbar_init(tfree, XEPI_WARPS);
+    mbar_init(&tempty[0], EPIS);
+    mbar_init(&tempty[1], EPIS);
+    mbar_init(tfree, EPIS);
     for (int i = 0; i < XTI_DEPTH; ++i) {
       mbar_init(&ti_full[i], 1);
-      mbar_init(&ti_empty[i], 3 + XEPI_WARPS);
+      // producers, MMA issuer, epilogue warps (+ the odd CTA's producers and epilogue)
+      mbar_init(&ti_empty[i], 3 + EPIS + (PAIR ? 2 : 0));
     }
     mbar_init(mma_done, 1);
     mbar_init(want, 1);
     *s_abort = 0;
     fence_mbar_init();
   }
+  if constexpr (PAIR) cluster_sync_all();  // barriers initialised before any remote arrive
   if (warp == 1) {
-    tmem_alloc(s_tmem, 512);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(s_tmem, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(s_tmem, 512);
+      tmem_relinquish();
+    }
   } else if (warp == 0 && lane < 2) {
     for (int i = 0; i < 2; ++i) {
       tma_prefetch_desc(&maps.w[lane][i]);
@@ -331,6 +406,14 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   // could hold older ones) and the weights can start; only the token rows of
   // GMM1 wait for the dispatch itself.
   const WaitCtl wc{s_abort, P.status, P.budget_ns};
+  // arrivals on the even CTA's barriers
+  auto arrive = [&](uint64_t* bar) {
+    if (!PAIR || leader)
+      mbar_arrive(bar);
+    else
+      mbar_arrive_peer(mapa_shared(smem_u32(bar), 0));
+  };
+  const uint32_t step = PAIR ? ncluster_x() : gridDim.x;
 
   if (warp == 2 + XEPI_WARPS) {
     // --------------------------------------------------------- tile scheduler
@@ -339,16 +422,24 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     // atomic's latency is hidden, and a CTA does not sit on a second tile while
     // another has none.  (With tickets drawn as soon as a slot was free, half
     // of the CTAs took two of a decode step's 128 GMM1 tiles.)
-    xschedule(P, s_pref);
-    if (lane == 0) {
+    if (leader) xschedule<PAIR>(P, s_pref);
+    if (lane == 0 && leader) {
       int slot = 0;
       uint32_t phase = 0, want_phase = 0;
-      uint32_t t = blockIdx.x;
+      uint32_t t = PAIR ? cluster_id_x() : blockIdx.x;
       for (;;) {
         XTile ti{-1, 0, 0, 0, 0, 0};
-        xlocate(P, s_pref, t, ti);
-        if (!mbar_wait(&ti_empty[slot], phase ^ 1u, wc)) break;
+        xlocate<PAIR>(P, s_pref, t, ti);
+        if (!mbar_wait<PAIR>(&ti_empty[slot], phase ^ 1u, wc)) break;
         s_ti[slot] = ti;
+        if constexpr (PAIR) {
+          const uint32_t dst = mapa_shared(smem_u32(&s_ti[slot]), 1);
+          const int* src = reinterpret_cast<const int*>(&ti);
+#pragma unroll
+          for (int j = 0; j < static_cast<int>(sizeof(XTile) / 4); ++j)
+            st_shared_cluster(dst + 4 * j, src[j]);
+          mbar_arrive_cluster(mapa_shared(smem_u32(&ti_full[slot]), 1));
+        }
         mbar_arrive(&ti_full[slot]);
         if (++slot == XTI_DEPTH) {
           slot = 0;
@@ -357,16 +448,15 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         if (ti.prob < 0) break;
         if (!mbar_wait(want, want_phase, wc)) break;
         want_phase ^= 1u;
-        t = gridDim.x + static_cast<uint32_t>(atomicAdd(P.ticket, 1));
+        t = step + static_cast<uint32_t>(atomicAdd(P.ticket, 1));
       }
     }
   } else if (warp == 0 || warp == XTOKEN_WARP) {
     // --------------------------------------------------------------- producers
     // One warp for the weights and their scales, one for the token rows and
-    // theirs: each arms a stage for its own bytes.  (One warp with all four
-    // loads took 0.38 us per K block, whatever the tile's width.)  Weights wait
-    // for nothing: while GMM2's token rows are not there yet, they are streamed
-    // into the free stages.
+    // theirs: each arms a stage for its own bytes.  Weights wait for nothing:
+    // while GMM2's token rows are not there yet, they are streamed into the free
+    // stages.
     const bool weights = warp == 0;
     if (!weights) grid_dep_wait();
     uint32_t stage = 0, sphase = 0, issued = 0;
@@ -374,11 +464,11 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (;;) {
-      ok = warp_all(mbar_wait(&ti_full[slot], phase, wc));
+      ok = warp_all(mbar_wait<PAIR>(&ti_full[slot], phase, wc));
       if (!ok) break;
       const XTile ti = s_ti[slot];
       __syncwarp();
-      if (elect_one()) mbar_arrive(&ti_empty[slot]);
+      if (elect_one()) arrive(&ti_empty[slot]);
       if (++slot == XTI_DEPTH) {
         slot = 0;
         phase ^= 1u;
@@ -386,43 +476,57 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       if (ti.prob < 0) break;
       const XProb& pr = P.p[ti.prob];
       const int nkb = (pr.kp + XK - 1) / XK;
+      auto next_stage = [&]() {
+        __syncwarp();
+        ++issued;
+        if (++stage == NST) {
+          stage = 0;
+          sphase ^= 1u;
+        }
+      };
       if (weights) {
-        const CUtensorMap* mw = &maps.w[ti.prob][ti.tn / 128 - 1];
+        // (a pair's tile takes the first half of its weight rows from the even
+        // CTA, the second from the odd one)
+        const int cols = min(ti.tn, (pr.n - ti.n0 + 31) / 32 * 32);
+        const int first = ti.n0 + static_cast<int>(rank) * cols / 2;
+        const CUtensorMap* mw = &maps.w[ti.prob][PAIR ? 0 : ti.tn / 128 - 1];
         const CUtensorMap* msw = &maps.sw[ti.prob][ti.tn / 128 - 1];
-        const uint32_t bytes = ti.tn * 128 + ti.tn / 128 * XS_BYTES;
+        const uint32_t bytes = PAIR ? 2 * XP_W_BYTES : ti.tn * 128 + ti.tn / 128 * XS_BYTES;
         const int wrow = ti.e * pr.rt + ti.n0 / 128;
         const int ask = max(0, nkb - 8);  // K block at which the next tile is asked for
         for (int kb = 0; kb < nkb; ++kb) {
           ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
           if (!ok) break;
           if (elect_one()) {
-            uint8_t* sB = smem + stage * XSTAGE_BYTES + XA_BYTES;
-            mbar_arrive_expect_tx(&full[stage], bytes);
-            tma_load_3d(sB, mw, &full[stage], kb * (XK / 2), ti.n0, ti.e);
-            tma_load_2d(sB + XB_BYTES + XS_BYTES, msw, &full[stage], kb * 256, wrow);
-            if (kb == ask) mbar_arrive(want);
+            uint8_t* sB = smem + stage * SBYTES + XA_BYTES;
+            if constexpr (PAIR) {
+              const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+              if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+              tma_load_3d_pair(sB, mw, bar, kb * (XK / 2), first, ti.e);
+              tma_load_2d_pair(sB + BBYTES + XS_BYTES, msw, bar, kb * 256, wrow);
+            } else {
+              mbar_arrive_expect_tx(&full[stage], bytes);
+              tma_load_3d(sB, mw, &full[stage], kb * (XK / 2), ti.n0, ti.e);
+              tma_load_2d(sB + BBYTES + XS_BYTES, msw, &full[stage], kb * 256, wrow);
+            }
+            if (kb == ask && leader) mbar_arrive(want);
           }
-          __syncwarp();
-          ++issued;
-          if (++stage == XSTAGES) {
-            stage = 0;
-            sphase ^= 1u;
-          }
+          next_stage();
         }
       } else {
-        const bool few = ti.rows <= 32;
+        const int row0 = ti.row0 + XM * static_cast<int>(rank);
+        const bool few = !PAIR && ti.rows <= 32;
         const CUtensorMap* ma = &maps.a[ti.prob][few ? 0 : 1];
         const CUtensorMap* msa = &maps.sa[ti.prob];
-        const uint32_t bytes = (few ? 32 : XM) * 128 + XS_BYTES;
-        const int srow = ti.row0 / 128;
-        if (ti.prob == 1) {
+        const uint32_t bytes = PAIR ? 2 * XP_T_BYTES : (few ? 32 : XM) * 128 + XS_BYTES;
+        if (ti.prob == 1 && ti.rows > XM * static_cast<int>(rank)) {
           // a comes from this launch's GMM1 tiles; each has a smaller ticket, so
           // its CTA is running or done.  Order the counter's acquire with the
           // asynchronous copies of a.
           // (all of GMM1's tiles of these rows, every epilogue warp once)
-          const uint32_t blocks = s_pref[P.E] >> 7;
-          const int done = XEPI_WARPS * xtiles(P.p[0], xwidth(P.p[0], blocks));
-          ok = warp_all(lane != 0 || counter_wait(&P.ready[ti.row0 / XM], done, wc));
+          const int done =
+              XEPI_WARPS * xtiles(P.p[0], PAIR ? XN : xwidth(P.p[0], s_pref[P.E] >> 7));
+          ok = warp_all(lane != 0 || counter_wait(&P.ready[row0 / XM], done, wc));
           if (!ok) break;
           fence_proxy_async_global();
         }
@@ -430,24 +534,26 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
           if (!ok) break;
           if (elect_one()) {
-            uint8_t* sA = smem + stage * XSTAGE_BYTES;
-            mbar_arrive_expect_tx(&full[stage], bytes);
-            tma_load_2d(sA, ma, &full[stage], kb * (XK / 2), ti.row0);
-            tma_load_2d(sA + XA_BYTES + XB_BYTES, msa, &full[stage], kb * 256, srow);
+            uint8_t* sA = smem + stage * SBYTES;
+            if constexpr (PAIR) {
+              const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+              if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+              tma_load_2d_pair(sA, ma, bar, kb * (XK / 2), row0);
+              tma_load_2d_pair(sA + XA_BYTES + BBYTES, msa, bar, kb * 256, row0 / XM);
+            } else {
+              mbar_arrive_expect_tx(&full[stage], bytes);
+              tma_load_2d(sA, ma, &full[stage], kb * (XK / 2), row0);
+              tma_load_2d(sA + XA_BYTES + BBYTES, msa, &full[stage], kb * 256, row0 / XM);
+            }
           }
-          __syncwarp();
-          ++issued;
-          if (++stage == XSTAGES) {
-            stage = 0;
-            sphase ^= 1u;
-          }
+          next_stage();
         }
       }
       if (!ok) break;
     }
     if (lane == 0) s_issued[weights ? 0 : 1] = issued;
     if (weights) grid_dep_launch();  // this CTA is in its last tile
-  } else if (warp == 1) {
+  } else if (warp == 1 && (!PAIR || leader)) {
     // -------------------------------------------------------------- MMA issue
     uint32_t stage = 0, sphase = 0;
     int slot = 0;
@@ -455,7 +561,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     uint32_t n = 0;  // tiles so far
     int last_cols = 0;  // columns of the tile before
     for (;;) {
-      if (!warp_all(mbar_wait(&ti_full[slot], phase, wc))) break;
+      if (!warp_all(mbar_wait<PAIR>(&ti_full[slot], phase, wc))) break;
       const int prob = __shfl_sync(0xffffffffu, s_ti[slot].prob, 0);
       const int n0 = __shfl_sync(0xffffffffu, s_ti[slot].n0, 0);
       const int tn = __shfl_sync(0xffffffffu, s_ti[slot].tn, 0);
@@ -469,7 +575,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       const int rows = prob == 0 ? P.p[0].n : P.p[1].n;
       const uint32_t acc = n & 1u;
       const uint32_t d = tmem + acc * XACC1;
-      const int cols = min(tn, (rows - n0 + 15) / 16 * 16);
+      const int cols = min(tn, (rows - n0 + 31) / 32 * 32);
       // the accumulator-0 one of this tile and the tile before decides whether
       // the two meet
       const bool shared = n > 0 && (acc ? last_cols : cols) > XACC1;
@@ -479,19 +585,19 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       if (!ok) break;
       // (always the accumulator's last use: with it tfree has completed the phase
       // of tile n - 2, so that the parity below can only mean tile n - 1's)
-      ok = warp_all(mbar_wait(&tempty[acc], ((n >> 1) & 1u) ^ 1u, wc));
-      if (ok && shared) ok = warp_all(mbar_wait(tfree, (n - 1) & 1u, wc));
+      ok = warp_all(mbar_wait<PAIR>(&tempty[acc], ((n >> 1) & 1u) ^ 1u, wc));
+      if (ok && shared) ok = warp_all(mbar_wait<PAIR>(tfree, (n - 1) & 1u, wc));
       if (!ok) break;
       const bool wide = cols > 128;  // the second scale tile row is in use
-      const uint32_t id0 = idesc_mx4(cols, 0), id1 = idesc_mx4(cols, 2);
+      const uint32_t id0 = idesc_mx4<PAIR>(cols, 0), id1 = idesc_mx4<PAIR>(cols, 2);
       const uint32_t sfa = tmem + XSF_COL, sfb = tmem + XSF_COL + 8;
       for (int k = 0; k < kp; k += XK) {
         if (k > 0) ok = warp_all(mbar_wait(&full[stage], sphase, wc));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t a = smem_u32(smem) + stage * XSTAGE_BYTES;
-          const uint32_t b = a + XA_BYTES, sc = b + XB_BYTES;
+          const uint32_t a = smem_u32(smem) + stage * SBYTES;
+          const uint32_t b = a + XA_BYTES, sc = b + BBYTES;
           const uint64_t da = smem_desc(a, 16, 1024, LAYOUT_SW128);
           const uint64_t db = smem_desc(b, 16, 1024, LAYOUT_SW128);
           const uint64_t ds = smem_desc(sc, 0, 128, LAYOUT_NONE);
@@ -502,50 +608,63 @@ __global__ void __launch_bounds__(XTHREADS, 1)
           if (left >= XK && wide) {
             // a whole K block without a branch between the instructions (with
             // the conditions of the other path: 103 us for 99 at T = 4096)
-            tmem_cp_scales(sfa, ds);
-            tmem_cp_scales(sfb, dt);
-            tmem_cp_scales(sfb + 4, dt + 64);
-            tmem_cp_scales(sfa + 4, ds + 32);
-            tmem_cp_scales(sfb + 8, dt + 32);
-            tmem_cp_scales(sfb + 12, dt + 96);
-            umma_mx4(d, da, db, id0, sfa, sfb, k > 0 ? 1u : 0u);
-            umma_mx4(d, da + 2, db + 2, id1, sfa, sfb, 1u);
-            umma_mx4(d, da + 4, db + 4, id0, sfa + 4, sfb + 8, 1u);
-            umma_mx4(d, da + 6, db + 6, id1, sfa + 4, sfb + 8, 1u);
+            cp_scales<PAIR>(sfa, ds);
+            cp_scales<PAIR>(sfb, dt);
+            cp_scales<PAIR>(sfb + 4, dt + 64);
+            cp_scales<PAIR>(sfa + 4, ds + 32);
+            cp_scales<PAIR>(sfb + 8, dt + 32);
+            cp_scales<PAIR>(sfb + 12, dt + 96);
+            umma<PAIR>(d, da, db, id0, sfa, sfb, k > 0 ? 1u : 0u);
+            umma<PAIR>(d, da + 2, db + 2, id1, sfa, sfb, 1u);
+            umma<PAIR>(d, da + 4, db + 4, id0, sfa + 4, sfb + 8, 1u);
+            umma<PAIR>(d, da + 6, db + 6, id1, sfa + 4, sfb + 8, 1u);
           } else {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               if (128 * i < left) {
-                tmem_cp_scales(sfa + 4 * i, ds + i * 32);
-                tmem_cp_scales(sfb + 8 * i, dt + i * 32);
-                if (wide) tmem_cp_scales(sfb + 4 + 8 * i, dt + (2 + i) * 32);
+                cp_scales<PAIR>(sfa + 4 * i, ds + i * 32);
+                cp_scales<PAIR>(sfb + 8 * i, dt + i * 32);
+                if (wide) cp_scales<PAIR>(sfb + 4 + 8 * i, dt + (2 + i) * 32);
               }
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (64 * j < left)
-                umma_mx4(d, da + 2 * j, db + 2 * j, (j & 1) ? id1 : id0, sfa + 4 * (j >> 1),
+                umma<PAIR>(d, da + 2 * j, db + 2 * j, (j & 1) ? id1 : id0, sfa + 4 * (j >> 1),
                          sfb + 8 * (j >> 1), (k > 0 || j > 0) ? 1u : 0u);
           }
-          umma_commit(&empty[stage]);
+          if constexpr (PAIR)
+            umma_commit_pair(&empty[stage], 0x3);
+          else
+            umma_commit(&empty[stage]);
         }
         __syncwarp();
-        if (++stage == XSTAGES) {
+        if (++stage == NST) {
           stage = 0;
           sphase ^= 1u;
         }
       }
       if (!ok) break;
-      if (elect_one()) umma_commit(&tfull[acc]);
+      if (elect_one()) {
+        if constexpr (PAIR)
+          umma_commit_pair(&tfull[acc], 0x3);
+        else
+          umma_commit(&tfull[acc]);
+      }
       __syncwarp();
       ++n;
     }
     // every MMA issued by this warp's elected lane completes before TMEM is released
     __syncwarp();
-    if (elect_one()) umma_commit(mma_done);
+    if (elect_one()) {
+      if constexpr (PAIR)
+        umma_commit_pair(mma_done, 0x1);
+      else
+        umma_commit(mma_done);
+    }
     __syncwarp();
     drain_wait(mma_done, 0, P.budget_ns);
-  } else {
+  } else if (warp >= 2 && warp < 2 + XEPI_WARPS) {
     // --------------------------------------------------------------- epilogue
     const int q = warp & 3;          // TMEM lane quarter
     const int h = (warp - 2) >> 2;   // half of the tile's columns
@@ -555,12 +674,16 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     uint32_t n = 0;
     for (;;) {
       bool got = false;
-      if (lane == 0) got = mbar_wait(&ti_full[slot], phase, wc);
+      if (lane == 0) got = mbar_wait<PAIR>(&ti_full[slot], phase, wc);
       got = __shfl_sync(0xffffffffu, got, 0);
       if (!got) break;
-      const XTile ti = s_ti[slot];
+      XTile ti = s_ti[slot];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ti_empty[slot]);
+      if (lane == 0) arrive(&ti_empty[slot]);
+      if constexpr (PAIR) {  // this CTA's rows (none for the odd CTA of a last block)
+        ti.row0 += XM * static_cast<int>(rank);
+        ti.rows = min(XM, ti.rows - XM * static_cast<int>(rank));
+      }
       if (++slot == XTI_DEPTH) {
         slot = 0;
         phase ^= 1u;
@@ -580,8 +703,8 @@ __global__ void __launch_bounds__(XTHREADS, 1)
       if (!got) break;
       ++n;
       tc_fence_after();
-      if (!(shares && live) && lane == 0) mbar_arrive(tfree);
-      if (!live && lane == 0) mbar_arrive(drained);
+      if (!(shares && live) && lane == 0) arrive(tfree);
+      if (!live && lane == 0) arrive(drained);
       if (live) {
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * XACC1;
         const int row = 32 * q + lane;
@@ -606,7 +729,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
                 tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(tfree);
+                if (lane == 0) arrive(tfree);
                 if (h)
                   tmem_ld32(taddr + 64 * c, g);
                 else
@@ -620,7 +743,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
               if (i + 1 == mine) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(drained);
+                if (lane == 0) arrive(drained);
               }
               const int blk = ti.n0 / 64 + c;
               if (blk < P.a_blocks) {
@@ -655,12 +778,12 @@ __global__ void __launch_bounds__(XTHREADS, 1)
             if (i == 0 && shares) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(tfree);
+              if (lane == 0) arrive(tfree);
             }
             if (i + 1 == nu) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(drained);
+              if (lane == 0) arrive(drained);
             }
             const int c0 = ti.n0 + 32 * c;
             if (c0 >= P.H) continue;
@@ -698,7 +821,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         }
       }
       tc_fence_before();
-      if (ti.prob == 0 && P.signal) {
+      if (ti.prob == 0 && P.signal && (!PAIR || ti.rows > 0)) {
         fence_proxy_async_global();
         __syncwarp();
         if (lane == 0) red_release_add(&P.ready[ti.row0 / XM], 1);
@@ -708,21 +831,54 @@ __global__ void __launch_bounds__(XTHREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (*s_abort && threadIdx.x == 0) {
-    // The producers may have left after different numbers of stages: complete
-    // the stages that one of them never armed, and wait (bounded) for the last
-    // copies into every slot before the CTA's memory goes.
-    const uint32_t n0 = s_issued[0], n1 = s_issued[1], n = max(n0, n1);
-    for (uint32_t k = n > XSTAGES ? n - XSTAGES : 0u; k < n; ++k) {
-      uint64_t* bar = &full[k % XSTAGES];
-      if (k >= min(n0, n1)) mbar_arrive(bar);
-      drain_wait(bar, (k / XSTAGES) & 1u, P.budget_ns);
+  // The producers may have left after different numbers of stages: complete what
+  // one of them never armed or loaded, and wait (bounded) for the last copies into
+  // every slot before the memory goes.
+  if constexpr (PAIR) {
+    if (!leader && threadIdx.x == 0) {
+      const uint32_t dst = mapa_shared(smem_u32(s_peer), 0);
+      st_shared_cluster(dst, static_cast<int>(s_issued[0]));
+      st_shared_cluster(dst + 4, static_cast<int>(s_issued[1]));
+      st_shared_cluster(dst + 8, *s_abort);
     }
+    cluster_sync_all();
+    if (leader && threadIdx.x == 0 && (*s_abort || s_peer[2])) {
+      uint32_t n = 0;
+      for (int i = 0; i < 2; ++i) n = max(n, max(s_issued[i], s_peer[i]));
+      for (uint32_t k = n > NST ? n - NST : 0u; k < n; ++k) {
+        uint64_t* bar = &full[k % NST];
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t bytes = i == 0 ? XP_W_BYTES : XP_T_BYTES;  // of one CTA
+          if (k >= s_issued[i]) {  // never armed: for what the odd CTA loads, if it does
+            if (k < s_peer[i])
+              mbar_arrive_expect_tx(bar, bytes);
+            else
+              mbar_arrive(bar);
+          } else if (k >= s_peer[i]) {
+            mbar_complete_tx(bar, bytes);  // armed for both, loaded by the even CTA only
+          }
+        }
+        drain_wait(bar, (k / NST) & 1u, P.budget_ns);
+      }
+    }
+    cluster_sync_all();
+  } else {
+    if (*s_abort && threadIdx.x == 0) {
+      const uint32_t n0 = s_issued[0], n1 = s_issued[1], n = max(n0, n1);
+      for (uint32_t k = n > NST ? n - NST : 0u; k < n; ++k) {
+        uint64_t* bar = &full[k % NST];
+        if (k >= min(n0, n1)) mbar_arrive(bar);
+        drain_wait(bar, (k / NST) & 1u, P.budget_ns);
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
   }
 }
 
@@ -879,6 +1035,7 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
   };
   prob(P.p[0], f.hp, 2 * f.ip);
   prob(P.p[1], f.ip, p.H);
+  P.poff = m.poff;
   P.counts = m.counts;
   P.E = static_cast<int>(p.E);
   P.ticket = c.tickets;
@@ -894,16 +1051,48 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
   P.status = env.status;
   P.budget_ns = env.budget_ns;
   if (!*env.mx4_set) {  // once per context
-    if (cudaFuncSetAttribute(gmm_mx4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, XSMEM) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(gmm_mx4_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             XSMEM) != cudaSuccess ||
+        cudaFuncSetAttribute(gmm_mx4_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             XSMEM) != cudaSuccess)
       return HMM_ERR_CUDA;
     *env.mx4_set = true;
   }
   const int64_t tiles = (p.R / XM) * ((2 * f.ip + 127) / 128 + (p.H + 127) / 128);
   if (tiles >= (int64_t(1) << 31)) return HMM_ERR_SHAPE;
+  // Pairs: six token blocks per expert on average (an odd last one idles a CTA),
+  // two GMM1 tiles per CTA, contractions long beside a tile's epilogue; both
+  // sides' figures are at the kernel.
+  const bool pair =
+      p.TK >= int64_t(6) * XM * p.E && p.H >= 2048 &&
+      p.TK / (2 * XM) * ((2 * f.ip + XN - 1) / XN) >= int64_t(2) * env.num_sms;
+  if (pair) {
+    // as many pairs as can be resident at once: the tiles wait for one another
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(env.num_sms / 2 * 2));
+    cfg.blockDim = dim3(XTHREADS);
+    cfg.dynamicSmemBytes = XSMEM;
+    cfg.stream = env.stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int active = 0;
+    if (cudaOccupancyMaxActiveClusters(&active, gmm_mx4_kernel<true>, &cfg) != cudaSuccess ||
+        active <= 0)
+      return HMM_ERR_CUDA;
+    const unsigned clusters = static_cast<unsigned>(std::min(active, env.num_sms / 2));
+    return launch_kernel(gmm_mx4_kernel<true>, 2 * clusters, XTHREADS, XSMEM, env.stream, env.pdl,
+                         2, P, maps) == cudaSuccess
+               ? HMM_OK
+               : HMM_ERR_CUDA;
+  }
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(env.num_sms, tiles));
-  return launch_kernel(gmm_mx4_kernel, grid, XTHREADS, XSMEM, env.stream, env.pdl, 1, P, maps) ==
-                 cudaSuccess
+  return launch_kernel(gmm_mx4_kernel<false>, grid, XTHREADS, XSMEM, env.stream, env.pdl, 1, P,
+                       maps) == cudaSuccess
              ? HMM_OK
              : HMM_ERR_CUDA;
 }

@@ -97,6 +97,32 @@ def test_long_batch_like_short_ones(T, H, I, E, K):
         assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("T,H,I,E,K,hot", [(2000, 2064, 2600, 2, 2, None),
+                                           (5000, 2048, 2016, 5, 1, (0, 301, 4442, 257, 0)),
+                                           (1900, 6032, 2928, 2, 2, None),
+                                           (4096, 2048, 1416, 4, 2, (4096, 129, 1, 3966)),
+                                           (3900, 2304, 2640, 2, 1, (128, 3772))])
+def test_pairs_of_blocks(T, H, I, E, K, hot):
+    """Many rows per expert run on pairs of blocks: experts without tokens, with
+    one row, with an odd number of blocks, widths whose last tile is narrow.
+    What the short batches give, bit for bit, and the formula's values."""
+    ids = None
+    if hot is not None:
+        assert sum(hot) == T * K
+        ids = torch.repeat_interleave(torch.arange(E), torch.tensor(hot))
+        ids = ids.reshape(K, T).T.flip(0).contiguous()
+    args = make(T, H, I, E, K, seed=T, ids=ids)
+    check(*args, tokens=np.random.default_rng(1).integers(0, T, 12))
+    x, ids, w, W1, W2 = (t.to(DEV) for t in args)
+    up, down = hmm.mx4_quantize_experts(W1, gate_up=True), hmm.mx4_quantize_experts(W2)
+    want = torch.cat([hmm.moe_ffn_mx4(a.contiguous(), b.contiguous(), c.contiguous(), up, down)
+                      for a, b, c in zip(x.split(100), ids.split(100), w.split(100))])
+    torch.cuda.synchronize()
+    got = [hmm.moe_ffn_mx4(x, ids, w, up, down) for _ in range(12)]
+    for y in got:
+        assert torch.equal(y, want)
+
+
 def test_repeatable_and_other_stream():
     args = make(500, 512, 384, 16, 4, seed=5)
     y, up, down = run(*args)
@@ -152,6 +178,26 @@ def test_a_wait_that_runs_out_is_reported():
     want, up, down = run(*args)
     c = hmm.Context(torch.device(DEV, 0))
     shape = hmm.make_shape(40, 256, 128, 4, 2, hmm.HMM_DTYPE_F32)
+    ws = torch.empty(hmm.hmm_mx4_workspace_size(shape), dtype=torch.uint8, device=DEV)
+    y = torch.empty_like(want)
+    x, ids, w = (t.to(DEV) for t in args[:3])
+    call = (c.handle, shape, x, ids, w, up.codes, up.scales, down.codes, down.scales, y, ws)
+    c.set_option(hmm.HMM_OPT_WAIT_BUDGET_NS, 20_000_000)
+    c.set_option(hmm.HMM_OPT_INJECT_SKIP_READY, 1)
+    hmm.hmm_forward_mx4(*call)
+    assert hmm.hmm_status(c.handle) == (hmm.HMM_ERR_TIMEOUT, hmm.HMM_STATUS_TIMEOUT)
+    hmm.hmm_forward_mx4(*call)
+    assert hmm.hmm_status(c.handle) == (0, 0) and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T,hot", [(2000, (2000, 2000)), (2000, (1999, 2001)),
+                                   (2000, (129, 3871))])
+def test_a_wait_that_runs_out_in_pairs_is_reported(T, hot):
+    ids = torch.repeat_interleave(torch.arange(2), torch.tensor(hot)).reshape(2, T).T.contiguous()
+    args = make(T, 2048, 2592, 2, 2, seed=9, ids=ids)
+    want, up, down = run(*args)
+    c = hmm.Context(torch.device(DEV, 0))
+    shape = hmm.make_shape(T, 2048, 2592, 2, 2, hmm.HMM_DTYPE_F32)
     ws = torch.empty(hmm.hmm_mx4_workspace_size(shape), dtype=torch.uint8, device=DEV)
     y = torch.empty_like(want)
     x, ids, w = (t.to(DEV) for t in args[:3])
