@@ -367,9 +367,9 @@ __device__ __forceinline__ void ld_token(const void* p, int64_t row, int q, int 
 // works on 32 / LT tokens at once.  Lane q of a token holds the experts
 // (i LT + q) 4 .. + 3 (16-byte loads); its keys also sit in shared memory,
 // where a round of the selection reaches them by a computed index, and the
-// maxima of its runs of eight in registers.  A round costs about 70
-// instructions for all of the warp's tokens (the one-warp kernel above: 100
-// for one).  Needs E to be a multiple of 4.
+// maxima of its runs of eight in registers.  A round serves all of the warp's
+// tokens with about the instructions that the kernel above spends on one.
+// Needs E to be a multiple of 4.
 template <int N, int LT, bool BF16, bool SIG>
 __global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 6 : 8)
     gate_forward_many_kernel(const GateArgs a, const void* __restrict__ logits,
@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 6 : 8)
   int* chosen = worths;
   auto piece = [&](int of_lane, int i) {
     return reinterpret_cast<int4*>(wkeys + of_lane * N) +
-           (N == 32 ? i ^ (of_lane & 7) : (N == 16 ? i ^ ((of_lane >> 1) & 3) : i));
+           (N == 32 ? i ^ (of_lane & 7)
+                    : (N == 16 ? i ^ ((of_lane >> 1) & 3) : i ^ ((of_lane >> 2) & 1)));
   };
   const bool by_logit = !SIG && bias == nullptr && a.group_top == 1;
   grid_dep_wait();
@@ -447,27 +448,40 @@ __global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 6 : 8)
   __syncwarp();
   if (a.groups > 1) {
     const int n = a.E / a.groups;
-    // lane q: the worths of groups q, q + LT, ..
-    for (int g = q; g < a.groups; g += LT) {
+    // the worths: a lane per group, or several where there are fewer groups than
+    // lanes (E = 300 in 4 groups, T = 65537: 112 us with one lane each, 92 so)
+    int parts = 1;
+    while (2 * parts * a.groups <= LT) parts *= 2;
+    const int part = q % parts;
+    for (int g0 = 0; g0 < a.groups; g0 += LT / parts) {
+      const int g = g0 + q / parts;
       int k1 = CLOSED, k2 = CLOSED;
-      if (n % 4) {  // groups that end inside a vector
-        for (int e = g * n; e < (g + 1) * n; ++e) {
-          const int k = reinterpret_cast<const int*>(
-              piece(tok * LT + (e >> 2) % LT, (e >> 2) / LT))[e & 3];
-          k2 = max(k2, min(k1, k));
-          k1 = max(k1, k);
-        }
-      } else {
-        for (int e = g * n; e < (g + 1) * n; e += 4) {
-          const int4 k = *piece(tok * LT + (e >> 2) % LT, (e >> 2) / LT);
-          const int h1 = max(k.x, k.y), h2 = max(k.z, k.w);
-          const int s2 = max(min(h1, h2), max(min(k.x, k.y), min(k.z, k.w)));
-          const int s1 = max(h1, h2);
-          k2 = max(min(k1, s1), max(k2, s2));
-          k1 = max(k1, s1);
+      if (g < a.groups) {
+        if (n % 4) {  // groups that end inside a vector
+          for (int e = g * n + part; e < (g + 1) * n; e += parts) {
+            const int k = reinterpret_cast<const int*>(
+                piece(tok * LT + (e >> 2) % LT, (e >> 2) / LT))[e & 3];
+            k2 = max(k2, min(k1, k));
+            k1 = max(k1, k);
+          }
+        } else {
+          for (int e = g * n + 4 * part; e < (g + 1) * n; e += 4 * parts) {
+            const int4 k = *piece(tok * LT + (e >> 2) % LT, (e >> 2) / LT);
+            const int h1 = max(k.x, k.y), h2 = max(k.z, k.w);
+            const int s2 = max(min(h1, h2), max(min(k.x, k.y), min(k.z, k.w)));
+            const int s1 = max(h1, h2);
+            k2 = max(min(k1, s1), max(k2, s2));
+            k1 = max(k1, s1);
+          }
         }
       }
-      worths[g] = a.group_top == 1 ? k1 : order_key(key_value(k1) + key_value(k2));
+      for (int d = parts / 2; d > 0; d >>= 1) {
+        const int o1 = __shfl_xor_sync(FULL, k1, d), o2 = __shfl_xor_sync(FULL, k2, d);
+        k2 = max(min(k1, o1), max(k2, o2));
+        k1 = max(k1, o1);
+      }
+      if (g < a.groups && part == 0)
+        worths[g] = a.group_top == 1 ? k1 : order_key(key_value(k1) + key_value(k2));
     }
     __syncwarp();
     uint32_t open = 0u;
@@ -1006,12 +1020,20 @@ cudaError_t launch_gate_forward(const hmm_gate& g, const void* logits, const flo
       aligned_to(scores, 16)) {
     // 32 to 40 experts per lane (E = 256, T = 65537: 64 per lane 64 us, few warps
     // fit; 32 51 us; 16 72 us, fewer tokens share a round.  E = 160, T = 131072: 40
-    // per lane 59 us, 24 63 us)
+    // per lane 59 us, 24 63 us), and 24 where they leave fewer places empty (grouped
+    // sigmoid, 32 and 24 per lane: E = 192, T = 65536 55 and 45 us, E = 300 135 and
+    // 113, E = 384, T = 32768 57 and 49, E = 768 127 and 107; E = 32 with 16 and 8 per
+    // lane 20 and 16)
+    if (g.E <= 32) return run_many<8, 4>(g, logits, bias, ids, weights, scores, st, pdl);
     if (g.E <= 64) return run_many<16, 4>(g, logits, bias, ids, weights, scores, st, pdl);
+    if (g.E <= 96) return run_many<24, 4>(g, logits, bias, ids, weights, scores, st, pdl);
     if (g.E <= 128) return run_many<32, 4>(g, logits, bias, ids, weights, scores, st, pdl);
     if (g.E <= 160) return run_many<40, 4>(g, logits, bias, ids, weights, scores, st, pdl);
+    if (g.E <= 192) return run_many<24, 8>(g, logits, bias, ids, weights, scores, st, pdl);
     if (g.E <= 256) return run_many<32, 8>(g, logits, bias, ids, weights, scores, st, pdl);
+    if (g.E <= 384) return run_many<24, 16>(g, logits, bias, ids, weights, scores, st, pdl);
     if (g.E <= 512) return run_many<32, 16>(g, logits, bias, ids, weights, scores, st, pdl);
+    if (g.E <= 768) return run_many<24, 32>(g, logits, bias, ids, weights, scores, st, pdl);
     return run_many<32, 32>(g, logits, bias, ids, weights, scores, st, pdl);
   }
   return by_length<RunForward>(g, vec, logits, bias, ids, weights, scores, st, pdl);
@@ -1030,16 +1052,26 @@ cudaError_t launch_gate_backward(const hmm_gate& g, const void* logits, const in
   if (g.T >= GATE_MANY && g.E % 4 == 0 && g.ld_logits % 4 == 0 &&
       aligned_to(logits, 4 * bytes) && aligned_to(d_logits, 4 * bytes) &&
       aligned_to(d_scores, 16)) {
+    if (g.E <= 32)
+      return run_backward_many<8, 4>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
     if (g.E <= 64)
       return run_backward_many<16, 4>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
+    if (g.E <= 96)
+      return run_backward_many<24, 4>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
     if (g.E <= 128)
       return run_backward_many<32, 4>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
     if (g.E <= 160)
       return run_backward_many<40, 4>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
+    if (g.E <= 192)
+      return run_backward_many<24, 8>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
     if (g.E <= 256)
       return run_backward_many<32, 8>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
+    if (g.E <= 384)
+      return run_backward_many<24, 16>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
     if (g.E <= 512)
       return run_backward_many<32, 16>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
+    if (g.E <= 768)
+      return run_backward_many<24, 32>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
     return run_backward_many<32, 32>(g, logits, ids, d_weights, d_scores, d_logits, st, pdl);
   }
   const bool vec = gate_vec(a, bytes, g.ld_logits, logits) && gate_vec(a, bytes, g.E, d_logits);

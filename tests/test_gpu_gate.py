@@ -206,6 +206,18 @@ def test_many_tokens_gradient_like_few(score, E, K, dtype):
             assert ((got - want).abs() <= lim).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K,groups,topk_groups,group_top", [
+    (32, 4, 2, 1, 2), (20, 5, 1, 1, 1), (72, 6, 3, 2, 2), (96, 6, 6, 4, 1), (180, 8, 4, 2, 2),
+    (192, 8, 2, 1, 2), (192, 7, 32, 9, 1), (356, 8, 4, 3, 2), (384, 6, 3, 2, 2), (400, 8, 5, 2, 2),
+    (640, 8, 5, 3, 2), (768, 10, 16, 4, 2), (1020, 8, 4, 1, 2)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_tokens_every_lane_width(score, E, K, groups, topk_groups, group_top, dtype):
+    """8 to 40 experts per lane; groups of several lanes, lanes of several groups."""
+    test_many_tokens_like_few(score, E, K, groups, topk_groups, group_top, dtype)
+    test_many_tokens_gradient_like_few(score, E, K, dtype)
+
+
 def test_equal_keys_go_to_the_lowest_index():
     l = torch.zeros((3, 70), device=DEV)
     l[1, 40:] = 1.0
