@@ -142,6 +142,28 @@ def test_repeatable_and_other_stream():
     assert torch.equal(z, hmm.moe_ffn_mx4(x, ids, w, up, down)) and not torch.equal(z, y)
 
 
+def test_pairs_in_a_graph_on_another_stream():
+    x, ids, w, W1, W2 = (t.to(DEV) for t in make(2000, 2048, 2592, 2, 2, seed=4))
+    up, down = hmm.mx4_quantize_experts(W1, gate_up=True), hmm.mx4_quantize_experts(W2)
+    want = hmm.moe_ffn_mx4(x, ids, w, up, down)
+    flipped = hmm.moe_ffn_mx4(x.flip(0), ids.flip(0), w.flip(0), up, down)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        y = hmm.moe_ffn_mx4(x, ids, w, up, down)
+    s.synchronize()
+    assert torch.equal(y, want) and torch.equal(flipped, want.flip(0))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = hmm.moe_ffn_mx4(x, ids, w, up, down)
+    for a in (x, ids, w):
+        a.copy_(a.flip(0))
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, flipped)
+
+
 def test_stale_workspace_does_not_matter():
     """Padding rows, unused scale bytes and stale tiles hold NaN patterns."""
     x, ids, w, W1, W2 = make(70, 288, 96, 6, 2, seed=8)
