@@ -739,7 +739,7 @@ class Mx4Tensor:
             raise TypeError("dtype must be bfloat16 or float32")
         dev = self.codes.device
         out = torch.empty(self.shape, dtype=dtype, device=dev)
-        d = HmmMx4(self.batch, self.rows, self.cols, self.cols, code, self.layout)
+        d = _mx4_args(self.batch, self.rows, self.cols, self.cols, code, self.layout)[0]
         rc = load_library().hmm_mx4_dequantize(
             Context.for_device(dev).handle, ctypes.byref(d), self.codes.data_ptr(),
             self.scales.data_ptr(), out.data_ptr(), _raw_stream(_current_device()))
@@ -748,9 +748,15 @@ class Mx4Tensor:
         return out
 
 
+@functools.lru_cache(maxsize=64)
+def _mx4_args(batch, rows, cols, ld, dtype, layout):
+    """(hmm_mx4, shape of the codes, of the scales) of an operand."""
+    return (HmmMx4(batch, rows, cols, ld, dtype, layout),
+            *Mx4Tensor._shapes(batch, rows, cols, layout))
+
+
 def _mx4_of(values, batch, rows, cols, ld, layout):
-    cs, ss = Mx4Tensor._shapes(batch, rows, cols, layout)
-    d = HmmMx4(batch, rows, cols, ld, _WDTYPES[values.dtype], layout)
+    d, cs, ss = _mx4_args(batch, rows, cols, ld, _WDTYPES[values.dtype], layout)
     dev = values.device
     codes = torch.empty(cs, dtype=torch.uint8, device=dev)
     scales = torch.empty(ss, dtype=torch.uint8, device=dev)
