@@ -78,7 +78,7 @@ struct XParams {
   const int32_t* poff;
   const int32_t* counts;
   int E;
-  int* ticket;      // tiles taken after every CTA's first
+  int* ticket;      // tiles taken
   int* ready;       // per 128 token rows: epilogue warps of GMM1 that are done
   int signal;       // 0: test-only fault injection, nothing is released
   uint8_t* a_codes;
@@ -413,20 +413,23 @@ __global__ void __launch_bounds__(XTHREADS, 1)
     else
       mbar_arrive_peer(mapa_shared(smem_u32(bar), 0));
   };
-  const uint32_t step = PAIR ? ncluster_x() : gridDim.x;
 
   if (warp == 2 + XEPI_WARPS) {
     // --------------------------------------------------------- tile scheduler
-    // The first tile is the CTA's own index, the others come by ticket.  A
-    // ticket is drawn only when the producer is about to need it (`want`): the
-    // atomic's latency is hidden, and a CTA does not sit on a second tile while
-    // another has none.  (With tickets drawn as soon as a slot was free, half
-    // of the CTAs took two of a decode step's 128 GMM1 tiles.)
+    // Every tile comes by ticket, the first one too: a tile belongs to a CTA
+    // that runs, however many of the grid's CTAs have an SM (another stream's
+    // kernel may hold some), so that GMM2's wait for GMM1 below cannot wait for
+    // a CTA that has not started.  The first ticket is drawn beside the prefix
+    // scan, the later ones only when the producer is about to need them
+    // (`want`): the atomic's latency is hidden, and a CTA does not sit on a
+    // second tile while another has none.  (With tickets drawn as soon as a slot
+    // was free, half of the CTAs took two of a decode step's 128 GMM1 tiles.)
+    uint32_t t = 0;
+    if (lane == 0 && leader) t = static_cast<uint32_t>(atomicAdd(P.ticket, 1));
     if (leader) xschedule<PAIR>(P, s_pref);
     if (lane == 0 && leader) {
       int slot = 0;
       uint32_t phase = 0, want_phase = 0;
-      uint32_t t = PAIR ? cluster_id_x() : blockIdx.x;
       for (;;) {
         XTile ti{-1, 0, 0, 0, 0, 0};
         xlocate<PAIR>(P, s_pref, t, ti);
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         if (ti.prob < 0) break;
         if (!mbar_wait(want, want_phase, wc)) break;
         want_phase ^= 1u;
-        t = step + static_cast<uint32_t>(atomicAdd(P.ticket, 1));
+        t = static_cast<uint32_t>(atomicAdd(P.ticket, 1));
       }
     }
   } else if (warp == 0 || warp == XTOKEN_WARP) {
@@ -520,9 +523,9 @@ __global__ void __launch_bounds__(XTHREADS, 1)
         const CUtensorMap* msa = &maps.sa[ti.prob];
         const uint32_t bytes = PAIR ? 2 * XP_T_BYTES : (few ? 32 : XM) * 128 + XS_BYTES;
         if (ti.prob == 1 && ti.rows > XM * static_cast<int>(rank)) {
-          // a comes from this launch's GMM1 tiles; each has a smaller ticket, so
-          // its CTA is running or done.  Order the counter's acquire with the
-          // asynchronous copies of a.
+          // a comes from this launch's GMM1 tiles; each has a smaller ticket,
+          // which a running CTA drew, and GMM1 tiles wait for no other tile.
+          // Order the counter's acquire with the asynchronous copies of a.
           // (all of GMM1's tiles of these rows, every epilogue warp once)
           const int done =
               XEPI_WARPS * xtiles(P.p[0], PAIR ? XN : xwidth(P.p[0], s_pref[P.E] >> 7));
