@@ -598,7 +598,7 @@ def _gate_forward(logits, gate, bias, return_scores):
     rc = load_library().hmm_gate_forward(
         Context.for_device(dev).handle, ctypes.byref(gate), logits.data_ptr(),
         None if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(),
-        None if scores is None else scores.data_ptr(), _raw_stream(_current_device()))
+        None if scores is None else scores.data_ptr(), _raw_stream(dev.index))
     if rc != HMM_OK:
         raise HmmError(rc, "hmm_gate_forward")
     return ids, w, scores
@@ -628,8 +628,7 @@ class _MoEGate(torch.autograd.Function):
         rc = load_library().hmm_gate_backward(
             Context.for_device(dev).handle, ctypes.byref(ctx.gate), logits.data_ptr(),
             ids.data_ptr(), None if dw is None else dw.data_ptr(),
-            None if ds is None else ds.data_ptr(), dl.data_ptr(),
-            _raw_stream(_current_device()))
+            None if ds is None else ds.data_ptr(), dl.data_ptr(), _raw_stream(dev.index))
         if rc != HMM_OK:
             raise HmmError(rc, "hmm_gate_backward")
         return dl, None, None, None
@@ -742,7 +741,7 @@ class Mx4Tensor:
         d = _mx4_args(self.batch, self.rows, self.cols, self.cols, code, self.layout)[0]
         rc = load_library().hmm_mx4_dequantize(
             Context.for_device(dev).handle, ctypes.byref(d), self.codes.data_ptr(),
-            self.scales.data_ptr(), out.data_ptr(), _raw_stream(_current_device()))
+            self.scales.data_ptr(), out.data_ptr(), _raw_stream(dev.index))
         if rc != HMM_OK:
             raise HmmError(rc, "hmm_mx4_dequantize")
         return out
@@ -762,7 +761,7 @@ def _mx4_of(values, batch, rows, cols, ld, layout):
     scales = torch.empty(ss, dtype=torch.uint8, device=dev)
     rc = load_library().hmm_mx4_quantize(
         Context.for_device(dev).handle, ctypes.byref(d), values.data_ptr(), codes.data_ptr(),
-        scales.data_ptr(), _raw_stream(_current_device()))
+        scales.data_ptr(), _raw_stream(dev.index))
     if rc != HMM_OK:
         raise HmmError(rc, "hmm_mx4_quantize")
     return Mx4Tensor(codes, scales, batch, rows, cols, layout)
@@ -832,10 +831,10 @@ def moe_ffn_mx4(x, topk_ids, topk_weights, up_proj, down_proj):
     if not (x.is_cuda and topk_ids.is_cuda and topk_weights.is_cuda and x.is_contiguous()
             and topk_ids.is_contiguous() and topk_weights.is_contiguous()):
         raise ValueError("all arguments must be contiguous CUDA tensors")
+    dev = x.device
     if (x.requires_grad or topk_weights.requires_grad) and torch.is_grad_enabled():
         raise RuntimeError("moe_ffn_mx4 has no backward: call it under torch.no_grad(), or train "
                            "with moe_ffn")
-    dev = x.device
     shape, size = _mx4_call(T, H, I, E, K, wdt)
     ws = torch.empty(size, dtype=torch.uint8, device=dev)
     y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
@@ -843,7 +842,7 @@ def moe_ffn_mx4(x, topk_ids, topk_weights, up_proj, down_proj):
         Context.for_device(dev).handle, ctypes.byref(shape), x.data_ptr(), topk_ids.data_ptr(),
         topk_weights.data_ptr(), up_proj.codes.data_ptr(), up_proj.scales.data_ptr(),
         down_proj.codes.data_ptr(), down_proj.scales.data_ptr(), y.data_ptr(), ws.data_ptr(), size,
-        _raw_stream(_current_device()))
+        _raw_stream(dev.index))
     if rc != HMM_OK:
         raise HmmError(rc, "hmm_forward_mx4")
     return y
