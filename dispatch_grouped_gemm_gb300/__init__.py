@@ -831,7 +831,11 @@ def moe_ffn_mx4(x, topk_ids, topk_weights, up_proj, down_proj):
     if not (x.is_cuda and topk_ids.is_cuda and topk_weights.is_cuda and x.is_contiguous()
             and topk_ids.is_contiguous() and topk_weights.is_contiguous()):
         raise ValueError("all arguments must be contiguous CUDA tensors")
-    dev = x.device
+    dev, at = x.device, x.get_device()
+    for t in (topk_ids, topk_weights, up_proj.codes, up_proj.scales, down_proj.codes,
+              down_proj.scales):
+        if t.get_device() != at:
+            raise ValueError(f"all arguments must be on x's device, {dev}, got one on {t.device}")
     if (x.requires_grad or topk_weights.requires_grad) and torch.is_grad_enabled():
         raise RuntimeError("moe_ffn_mx4 has no backward: call it under torch.no_grad(), or train "
                            "with moe_ffn")

@@ -1,6 +1,7 @@
 """The torch layer of the router and the 4-bit experts in a process with several
-devices, on stand-ins for tensors (no GPU): a call goes to
-the current stream of its tensors' device, whichever device is current."""
+devices, on stand-ins for tensors (no GPU): operands of different devices are
+refused before any device work, and a call goes to the current stream of its
+tensors' device, whichever device is current."""
 import ctypes
 import types
 
@@ -74,6 +75,20 @@ def ffn_arguments(index):
     return [Fake((3, 64), torch.bfloat16, index), Fake((3, 2), torch.int32, index),
             Fake((3, 2), torch.float32, index), stack(hmm.HMM_MX4_GATE_UP, 64, 64, 64),
             stack(hmm.HMM_MX4_COLUMNS, 64, 64, 32)]
+
+
+def test_operands_of_two_devices_are_refused(calls):
+    other = ffn_arguments(1)
+    for i in range(5):
+        mixed = ffn_arguments(0)
+        mixed[i] = other[i]
+        with pytest.raises(ValueError, match="device"):
+            hmm.moe_ffn_mx4(*mixed)
+    scales_elsewhere = ffn_arguments(0)
+    scales_elsewhere[4].scales = other[4].scales
+    with pytest.raises(ValueError, match="device"):
+        hmm.moe_ffn_mx4(*scales_elsewhere)
+    assert not calls
 
 
 @pytest.mark.parametrize("index", [0, 1])
