@@ -11,6 +11,10 @@
 //         lowest index
 //   topk_weights = scale * p[topk_ids], over sum_k p[topk_ids] with renormalize
 //
+// Renormalised softmax weights are the softmax of the K selected logits: they
+// come from these alone, so that scores too small for fp32 (a bias can choose
+// them) keep their weights and their gradient.
+//
 // One warp per token.  Lane i holds the c = ceil(E / 32) consecutive experts
 // from c i in registers, so that the lowest of equal keys is in the lowest
 // lane, a row of logits is read once with vector loads, and (E a multiple of
@@ -126,26 +130,29 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
+template <int L = 32>
+__device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, d));
+  for (int d = L / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, d));
   return v;
 }
+// The largest of some logits of a row as its exponentials subtract it: 0 where
+// they are all -inf, closed experts, whose exponentials are 0.
+__device__ __forceinline__ float row_shift(float m) { return m == -INFINITY ? 0.0f : m; }
+__device__ __forceinline__ float nonzero(float sum) { return sum == 0.0f ? 1.0f : sum; }
 
 // 1 / (1 + exp(-l)) with the accurate exponential and a correctly rounded
 // reciprocal: the selection compares these values, so they are rounded as the
 // formula's own fp32 evaluation rounds them.
 __device__ __forceinline__ float sigmoid_rn(float l) { return __frcp_rn(1.0f + expf(-l)); }
 
-// Largest logit of a row, 0 for a row that is all -inf: its experts are all
-// closed, their exponentials 0.  (A NaN turns the row's sum into NaN.)
+// Largest logit of a row.  (A NaN turns the row's sum into NaN.)
 template <int C>
 __device__ __forceinline__ float row_max(const float (&l)[C]) {
   float m = l[0];
 #pragma unroll
   for (int j = 1; j < C; ++j) m = fmaxf(m, l[j]);
-  m = warp_max(m);
-  return m == -INFINITY ? 0.0f : m;
+  return row_shift(lanes_max(m));
 }
 
 template <int C>
@@ -156,8 +163,7 @@ __device__ __forceinline__ float exp_row(const float (&l)[C], float m, float (&p
     p[j] = expf(l[j] - m);
     z += p[j];
   }
-  z = lanes_sum(z);
-  return z == 0.0f ? 1.0f : z;
+  return nonzero(lanes_sum(z));
 }
 
 }  // namespace
@@ -313,14 +319,16 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
       }
     }
     // the selected scores again, from their logits
-    float w = 0.0f;
-    if (lane < a.K) {
-      const float lk = ld_logit<BF16>(logits, t * a.ld + my_id);
-      w = SIG ? sigmoid_rn(lk) : expf(lk - m) / z;
+    const float lk = lane < a.K ? ld_logit<BF16>(logits, t * a.ld + my_id) : -INFINITY;
+    float shift = m, div = z;
+    if (!SIG && a.renorm) {
+      shift = row_shift(lanes_max(lk));
+      div = 1.0f;
     }
+    float w = SIG ? sigmoid_rn(lk) : expf(lk - shift) / div;
     if (a.renorm) {
-      const float sum = lanes_sum(w);
-      w = w / (sum == 0.0f ? 1.0f : sum);
+      w = w / nonzero(lanes_sum(w));
+      if (z != z) w = z;  // a NaN that was not selected shows all the same
     }
     if (lane < a.K) {
       w *= a.scale;
@@ -406,13 +414,12 @@ __global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 6 : 8)
     for (int j = 1; j < N; ++j) m = fmaxf(m, l[j]);
 #pragma unroll
     for (int d = LT / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, d));
-    if (m == -INFINITY) m = 0.0f;
+    m = row_shift(m);
     if (scores || !by_logit || !a.renorm) {
       z = 0.0f;
 #pragma unroll
       for (int j = 0; j < N; ++j) z += expf(l[j] - m);
-      z = lanes_sum<LT>(z);
-      if (z == 0.0f) z = 1.0f;
+      z = nonzero(lanes_sum<LT>(z));
     }
   }
   int seg[S];
@@ -553,24 +560,31 @@ __global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 6 : 8)
   }
   __syncwarp();
   float w[32 / LT];
-  float sum = 0.0f;
+  float sum = 0.0f, top = -INFINITY;
 #pragma unroll
   for (int x = 0; x < 32 / LT; ++x) {
     const int k = q + x * LT;
-    w[x] = 0.0f;
-    if (k < a.K) {
-      const float lk = ld_logit<BF16>(logits, t * a.ld + chosen[k]);
-      w[x] = SIG ? sigmoid_rn(lk) : expf(lk - m) / z;
-      sum += w[x];
-    }
+    w[x] = k < a.K ? ld_logit<BF16>(logits, t * a.ld + chosen[k]) : -INFINITY;
+    top = fmaxf(top, w[x]);
   }
-  if (a.renorm) sum = lanes_sum<LT>(sum);
+  float shift = m, div = z;
+  if (!SIG && a.renorm) {
+    shift = row_shift(lanes_max<LT>(top));
+    div = 1.0f;
+  }
+#pragma unroll
+  for (int x = 0; x < 32 / LT; ++x) {
+    if (x * LT >= a.K) break;
+    w[x] = SIG ? sigmoid_rn(w[x]) : expf(w[x] - shift) / div;
+    sum += w[x];
+  }
+  if (a.renorm) sum = nonzero(lanes_sum<LT>(sum));
 #pragma unroll
   for (int x = 0; x < 32 / LT; ++x) {
     const int k = q + x * LT;
     if (k < a.K && live) {
       float v = w[x];
-      if (a.renorm) v = v / (sum == 0.0f ? 1.0f : sum);
+      if (a.renorm) v = z == z ? v / sum : z;  // (a NaN that was not selected shows all the same)
       v *= a.scale;
       ids[t * a.K + k] = chosen[k];
       if (a.weights_f32)
@@ -588,7 +602,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 6 : 8)
 //   sigmoid  dl = dp p (1 - p)
 //   softmax  dl = p (dp - sum dp p); the renormalised weights' part of that sum
 //            is D - D = 0, so their gradient n_k (g_k - D) stays on the
-//            selected experts.
+//            selected experts; n is the softmax of their logits.
 // This kernel: every expert has a gradient (d_scores, or softmax weights that
 // are not renormalised).  One warp per token, the forward's layout; the
 // selected part is scattered through shared memory.
@@ -611,7 +625,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
     float l[C], p[C];
     ld_chunk<C, BF16, VEC>(logits, t * a.ld, base, a.c, a.E, l);
     int id = -1;
-    float g = 0.0f, ps = 0.0f, m = 0.0f, z = 1.0f;
+    float g = 0.0f, lk = -INFINITY, m = 0.0f, z = 1.0f;
     if constexpr (SIG) {
 #pragma unroll
       for (int j = 0; j < C; ++j) p[j] = sigmoid_rn(l[j]);
@@ -626,17 +640,21 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
       if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.E)) id = -1;
       g = a.scale * ld_w(d_weights, t * a.K + lane, a.weights_f32);
     }
-    if (id >= 0) {
-      const float lk = ld_logit<BF16>(logits, t * a.ld + id);
-      ps = SIG ? sigmoid_rn(lk) : expf(lk - m) * z;
-    }
+    if (id >= 0) lk = ld_logit<BF16>(logits, t * a.ld + id);
+    const bool selected_softmax = !SIG && a.renorm;  // g becomes its part of dl itself
     float sum = 0.0f;  // softmax: sum dp p
-    if (a.renorm) {
-      float tot = lanes_sum(ps);
-      if (tot == 0.0f) tot = 1.0f;
-      g = (g - lanes_sum(g * (ps / tot))) / tot;
+    if (selected_softmax) {
+      float n = expf(lk - row_shift(lanes_max(lk)));
+      n /= nonzero(lanes_sum(n));
+      g = n * (g - lanes_sum(g * n));
     } else {
-      sum = g * ps;
+      const float ps = id < 0 ? 0.0f : (SIG ? sigmoid_rn(lk) : expf(lk - m) * z);
+      if (a.renorm) {
+        const float tot = nonzero(lanes_sum(ps));
+        g = (g - lanes_sum(g * (ps / tot))) / tot;
+      } else {
+        sum = g * ps;
+      }
     }
     if (id >= 0) sd[id] = g;
     __syncwarp();
@@ -653,7 +671,8 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
     for (int j = 0; j < C; ++j) {
       const bool in = VEC || (j < a.c && base + j < a.E);
       const float s = in ? sd[base + j] : 0.0f;
-      dp[j] = SIG ? (s + dp[j]) * p[j] * sigmoid_rn(-l[j]) : p[j] * (s + (dp[j] - sum));
+      dp[j] = SIG ? (s + dp[j]) * p[j] * sigmoid_rn(-l[j])
+                  : (selected_softmax ? s + p[j] * (dp[j] - sum) : p[j] * (s + (dp[j] - sum)));
     }
     st_chunk<C, BF16, VEC>(d_logits, t * a.E, base, a.c, a.E, dp);
     __syncwarp();
@@ -693,47 +712,53 @@ __global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 4 : 5)
     for (int j = 1; j < N; ++j) m = fmaxf(m, p[j]);
 #pragma unroll
     for (int d = LT / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, d));
-    if (m == -INFINITY) m = 0.0f;
+    m = row_shift(m);
     z = 0.0f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       p[j] = expf(p[j] - m);
       z += p[j];
     }
-    z = lanes_sum<LT>(z);
-    z = z == 0.0f ? 1.0f : 1.0f / z;
+    z = 1.0f / nonzero(lanes_sum<LT>(z));
   }
   // the selected experts, KL per lane
+  const bool selected_softmax = !SIG && a.renorm;  // g becomes its part of dl itself
   int id[KL];
-  float g[KL], ps[KL], tot = 0.0f, gn = 0.0f;
+  float g[KL], ps[KL], top = -INFINITY, tot = 0.0f, gn = 0.0f;
 #pragma unroll
   for (int x = 0; x < KL; ++x) {
     const int k = q + x * LT;
     id[x] = -1;
-    g[x] = ps[x] = 0.0f;
+    g[x] = 0.0f;
+    ps[x] = -INFINITY;
     if (k < a.K && d_weights) {
       id[x] = ids[t * a.K + k];
       if (static_cast<unsigned>(id[x]) >= static_cast<unsigned>(a.E)) id[x] = -1;
       g[x] = a.scale * ld_w(d_weights, t * a.K + k, a.weights_f32);
-      if (id[x] >= 0) {
-        const float lk = ld_logit<BF16>(logits, t * a.ld + id[x]);
-        ps[x] = SIG ? sigmoid_rn(lk) : expf(lk - m) * z;
-      }
+      if (id[x] >= 0) ps[x] = ld_logit<BF16>(logits, t * a.ld + id[x]);
     }
+    top = fmaxf(top, ps[x]);
+  }
+  const float shift = selected_softmax ? row_shift(lanes_max<LT>(top)) : m;
+  const float times = selected_softmax ? 1.0f : z;
+#pragma unroll
+  for (int x = 0; x < KL; ++x) {
+    if (x * LT >= a.K) break;
+    ps[x] = SIG ? sigmoid_rn(ps[x]) : expf(ps[x] - shift) * times;
     tot += ps[x];
     gn += g[x] * ps[x];
   }
   float sum = gn;  // softmax: sum dp p
   if (a.renorm) {
-    tot = lanes_sum<LT>(tot);
-    if (tot == 0.0f) tot = 1.0f;
+    tot = nonzero(lanes_sum<LT>(tot));
     gn = lanes_sum<LT>(gn) / tot;
     sum = 0.0f;
   }
   __syncwarp();
 #pragma unroll
   for (int x = 0; x < KL; ++x)
-    if (id[x] >= 0) sd[id[x]] = a.renorm ? (g[x] - gn) / tot : g[x];
+    if (id[x] >= 0)
+      sd[id[x]] = !a.renorm ? g[x] : (g[x] - gn) * (SIG ? 1.0f : ps[x]) / tot;
   __syncwarp();
   float4 ds[N / 4];
 #pragma unroll
@@ -761,7 +786,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32, N > 32 ? 4 : 5)
     for (int r = 0; r < 4; ++r) {
       const float v = p[4 * i + r];
       d[r] = SIG ? (sv[r] + dv[r]) * sigmoid_rn(v) * sigmoid_rn(-v)
-                 : v * (sv[r] + (dv[r] - sum));
+                 : (selected_softmax ? sv[r] + v * (dv[r] - sum) : v * (sv[r] + (dv[r] - sum)));
     }
     if constexpr (BF16) {
       const __nv_bfloat162 lo = __floats2bfloat162_rn(d[0], d[1]);
@@ -817,21 +842,15 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
   if constexpr (SIG) {
     const float p = id >= 0 ? sigmoid_rn(lk) : 0.0f;
     if (a.renorm) {
-      float tot = lanes_sum<L>(p);
-      if (tot == 0.0f) tot = 1.0f;
+      const float tot = nonzero(lanes_sum<L>(p));
       g = (g - lanes_sum<L>(g * (p / tot))) / tot;
     }
     d = g * p * sigmoid_rn(-lk);
     if (lk == -INFINITY) d = 0.0f;
   } else {
     // n_k: softmax over the selected logits
-    float m = lk;
-#pragma unroll
-    for (int x = L / 2; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
-    if (m == -INFINITY) m = 0.0f;
-    float n = expf(lk - m);
-    const float tot = lanes_sum<L>(n);
-    n = n / (tot == 0.0f ? 1.0f : tot);
+    float n = expf(lk - row_shift(lanes_max<L>(lk)));
+    n /= nonzero(lanes_sum<L>(n));
     d = n * (g - lanes_sum<L>(g * n));
   }
   __syncwarp();  // the zeros come first

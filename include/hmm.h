@@ -348,7 +348,10 @@ int hmm_backward_dw(hmm_ctx* ctx, const hmm_shape* shape, const void* saved,
  *   topk_ids     = the K best keys of the open groups, best first; equal keys
  *                  by ascending expert.  Always K distinct ids in [0, E).
  *   topk_weights = scale * p[topk_ids], with renormalize divided by the sum of
- *                  the K selected p (the bias only selects).
+ *                  the K selected p (the bias only selects); for softmax that
+ *                  is the softmax of the K selected logits, and is computed
+ *                  as such: a selected p below fp32's range keeps its weight
+ *                  and its gradient.
  * A logit of -inf closes its expert: p = 0, chosen after every other open
  * expert.  A row with every logit -inf has p = 0 and weights 0 (softmax or
  * renormalize divide by 1 there) and a zero gradient.  NaN is chosen first and

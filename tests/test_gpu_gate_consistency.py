@@ -1,0 +1,47 @@
+"""The router where scores are too small for fp32, where keys are rounded sums
+and where arguments have no effect on the formula.  Tolerances as derived in
+tests/test_gpu_gate.py."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import dispatch_grouped_gemm_gb300 as hmm
+from tests import gate_ref as ref
+from tests.test_gpu_gate import close, logits_of, run
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.mark.parametrize("T", [5, 4100])
+@pytest.mark.parametrize("E,K", [(64, 6), (33, 3), (300, 9)])
+@pytest.mark.parametrize("scored", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_renormalised_weights_of_scores_below_fp32(T, E, K, scored, dtype):
+    """A bias selects experts whose softmax scores underflow: their renormalised
+    weights are the formula's, and the gradient is that of these weights.  (The
+    selected logits lie within 20 of one another, as the tolerances assume.)"""
+    g = torch.Generator().manual_seed(E)
+    l = logits_of(T, E, dtype, E)
+    few = torch.randperm(E, generator=g)[:K]
+    l[:, few] = (-200.0 + l[:, few].float()).to(dtype)
+    l[0, few[1:]] = -math.inf  # one selected expert that is open
+    l[1] = -math.inf           # none
+    l[2, few[0]] = 9.0         # one large score among those that underflow
+    bias = torch.zeros(E)
+    bias[few] = 4.0 + torch.arange(K).float()  # distinct keys
+    dw = torch.randn((T, K), generator=g)
+    ds = 0.1 * torch.randn((T, E), generator=g) if scored else None
+    out, dl = run(l, K, torch.float32, bias, ds, dw, renormalize=True, scale=1.5)
+    l64 = l.double().numpy()
+    key = ref.keys(l64, "softmax", bias.numpy())
+    ids = ref.select(key, K, np.ones((T, E), bool))
+    assert np.array_equal(out[0].cpu().numpy(), ids)
+    p = ref.scores(l64, "softmax")
+    close(out[1].detach(), ref.weights(p, ids, True, 1.5), 5e-6)
+    want, mag = ref.d_logits(l64, ids, dw.numpy(), None if ds is None else ds.numpy(), "softmax",
+                             True, 1.5)
+    assert np.abs(want[3:][:, few.numpy()]).max() > 0.01
+    close(dl, want, 2e-5, mag, dtype)
