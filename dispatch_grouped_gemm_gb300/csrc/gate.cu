@@ -3,8 +3,8 @@
 // backward.
 //
 //   p = softmax(l) or sigmoid(l)                                    [T, E]
-//   key = p + bias (softmax without a bias, groups counted by one key: l
-//         itself, whose order is that of p)
+//   key = p + bias (softmax without a bias, one group or groups counted by one
+//         key: l itself, whose order is that of p)
 //   groups > 1: a group of E / groups experts counts by the sum of its
 //         group_top best keys; the topk_groups best groups stay open
 //   topk_ids = the K best keys of the open groups, best first, ties to the
@@ -875,7 +875,7 @@ GateArgs gate_args(const hmm_gate& g) {
   a.c = (a.E + 31) / 32;
   a.groups = g.groups;
   a.topk_groups = g.topk_groups;
-  a.group_top = g.group_top;
+  a.group_top = g.groups > 1 ? g.group_top : 1;  // (one group needs no worth)
   a.lane_groups = a.E % 32 == 0 && 32 % a.groups == 0 && a.group_top <= 2;
   a.weights_f32 = g.weights_dtype == HMM_DTYPE_F32;
   a.renorm = g.renormalize;

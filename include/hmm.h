@@ -340,8 +340,9 @@ int hmm_backward_dw(hmm_ctx* ctx, const hmm_shape* shape, const void* saved,
 /* Router: scores of E experts per token, selection and routing weights, in
  * front of hmm_forward (topk_ids and topk_weights are its inputs).
  *   p            = softmax(logits) or sigmoid(logits), fp32            [T, E]
- *   key          = p + bias.  Softmax without a bias and with group_top 1 goes
- *                  by the logit instead: the same order, with no rounding.
+ *   key          = p + bias.  Softmax without a bias and with groups or
+ *                  group_top 1 goes by the logit instead: the same order, with
+ *                  no rounding.
  *   groups > 1:    a group of E / groups consecutive experts counts by the sum
  *                  of its group_top best keys; only the topk_groups best
  *                  groups (ties: lower group) are open.
@@ -370,7 +371,7 @@ typedef struct hmm_gate {
   int32_t renormalize;    /* 0 / 1 */
   int32_t groups;         /* 1 .. 32, divides E */
   int32_t topk_groups;    /* 1 .. groups */
-  int32_t group_top;      /* 1 .. E / groups */
+  int32_t group_top;      /* 1 .. E / groups (no effect with groups 1) */
   float scale;            /* finite */
 } hmm_gate;
 

@@ -45,3 +45,14 @@ def test_renormalised_weights_of_scores_below_fp32(T, E, K, scored, dtype):
                              True, 1.5)
     assert np.abs(want[3:][:, few.numpy()]).max() > 0.01
     close(dl, want, 2e-5, mag, dtype)
+
+
+@pytest.mark.parametrize("T", [3, 4100])
+def test_group_top_has_no_effect_without_groups(T):
+    """Logits whose softmax scores are equal in fp32: the selection goes by the
+    logits, whatever group_top says of the one group."""
+    l = (torch.arange(40, device=DEV) * 1e-9).expand(T, 40).contiguous()
+    want = torch.arange(39, 33, -1, dtype=torch.int32, device=DEV).expand(T, 6)
+    for top in (1, 2, 7):
+        ids, w = hmm.moe_gate(l, 6, group_top=top)
+        assert torch.equal(ids, want) and torch.allclose(w, torch.full_like(w, 1 / 40))
