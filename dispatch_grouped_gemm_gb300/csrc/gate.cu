@@ -166,6 +166,37 @@ __device__ __forceinline__ float exp_row(const float (&l)[C], float m, float (&p
   return nonzero(lanes_sum(z));
 }
 
+// Lanes per token in the kernels for many tokens (up to 40 experts per lane).
+__host__ __device__ constexpr int many_lanes(int E) {
+  return E <= 160 ? 4 : (E <= 256 ? 8 : (E <= 512 ? 16 : 32));
+}
+
+// Sum over a row's p in the order of gate_forward_many_kernel: lane q of
+// many_lanes(E) adds the experts (i LT + q) 4 .. + 3, then the lanes add theirs.
+// Keys that hold the sum's rounding are then the same in a long batch and in a
+// short one, and with them the selection.  row: 33 c values (a place left free
+// after every 32, so that lanes do not meet in a bank).  (Softmax with a bias, us
+// with the butterfly of exp_row alone and with this: E = 256, T = 1 2.8 and 3.3, T =
+// 2000 4.6 and 5.3; E = 1024, T = 2000 17.7 and 20.8.)
+template <int C>
+__device__ __forceinline__ float sum_like_many(const float (&p)[C], int base, int c, int E,
+                                               int lane, float* row) {
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+    if (j < c && base + j < E) row[base + j + ((base + j) >> 5)] = p[j];
+  __syncwarp();
+  const int lanes = many_lanes(E);
+  float z = 0.0f;
+  for (int e = 4 * (lane & (lanes - 1)); e < E; e += 4 * lanes) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (e + r < E) z += row[e + r + (e >> 5)];
+  }
+  __syncwarp();
+  for (int d = lanes / 2; d > 0; d >>= 1) z += __shfl_xor_sync(FULL, z, d);
+  return nonzero(z);
+}
+
 }  // namespace
 
 struct GateArgs {
@@ -257,7 +288,8 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
     gate_forward_kernel(const GateArgs a, const void* __restrict__ logits,
                         const float* __restrict__ bias, int32_t* __restrict__ ids,
                         void* __restrict__ weights, float* __restrict__ scores) {
-  extern __shared__ int gate_smem[];  // per warp [E] (groups that are no lane runs)
+  // per warp [33 c] (groups that are no lane runs, softmax keys that are no logits)
+  extern __shared__ int gate_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int base = lane * a.c;
   const bool by_logit = !SIG && bias == nullptr && a.group_top == 1;
@@ -276,6 +308,9 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
       m = row_max(l);
       // (renormalised weights of the best logits need no sum over the row)
       if (scores || !by_logit || !a.renorm) z = exp_row(l, m, p);
+      if (!by_logit)
+        z = sum_like_many(p, base, a.c, a.E, lane,
+                          reinterpret_cast<float*>(gate_smem) + warp * 33 * a.c);
       if (scores || !by_logit) {
 #pragma unroll
         for (int j = 0; j < C; ++j) p[j] = p[j] / z;
@@ -289,7 +324,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
       if (bias && in) v += __ldg(bias + base + j);
       key[j] = in ? order_key(v) : CLOSED;
     }
-    if (a.groups > 1) keep_groups<C>(a, key, lane, base, gate_smem + warp * a.E);
+    if (a.groups > 1) keep_groups<C>(a, key, lane, base, gate_smem + warp * 33 * a.c);
     // K rounds: the best key of the lanes' best; lane k keeps expert k
     int bk = key[0], bj = 0;
 #pragma unroll
@@ -931,7 +966,9 @@ struct RunForward {
   static cudaError_t run(const hmm_gate& g, const void* logits, const float* bias, int32_t* ids,
                          void* weights, float* scores, cudaStream_t st, bool pdl) {
     const GateArgs a = gate_args(g);
-    const size_t smem = a.groups > 1 && !a.lane_groups ? sizeof(float) * GATE_WARPS * a.E : 0;
+    const bool rounded_sums = !SIG && (bias || a.group_top > 1);
+    const size_t smem = rounded_sums || (a.groups > 1 && !a.lane_groups)
+                            ? sizeof(float) * GATE_WARPS * 33 * a.c : 0;
     return launch_kernel(gate_forward_kernel<C, BF16, SIG, VEC>, gate_grid(g.T), GATE_WARPS * 32,
                          smem, st, pdl, 1, a, logits, bias, ids, weights, scores);
   }
@@ -1042,7 +1079,7 @@ cudaError_t launch_gate_forward(const hmm_gate& g, const void* logits, const flo
     // per lane 59 us, 24 63 us), and 24 where they leave fewer places empty (grouped
     // sigmoid, 32 and 24 per lane: E = 192, T = 65536 55 and 45 us, E = 300 135 and
     // 113, E = 384, T = 32768 57 and 49, E = 768 127 and 107; E = 32 with 16 and 8 per
-    // lane 20 and 16)
+    // lane 20 and 16).  The second number is many_lanes(E).
     if (g.E <= 32) return run_many<8, 4>(g, logits, bias, ids, weights, scores, st, pdl);
     if (g.E <= 64) return run_many<16, 4>(g, logits, bias, ids, weights, scores, st, pdl);
     if (g.E <= 96) return run_many<24, 4>(g, logits, bias, ids, weights, scores, st, pdl);

@@ -56,3 +56,32 @@ def test_group_top_has_no_effect_without_groups(T):
     for top in (1, 2, 7):
         ids, w = hmm.moe_gate(l, 6, group_top=top)
         assert torch.equal(ids, want) and torch.allclose(w, torch.full_like(w, 1 / 40))
+
+
+@pytest.mark.parametrize("E,K,groups,topk_groups,group_top", [
+    (8, 3, 1, 1, 1), (64, 6, 1, 1, 1), (100, 7, 5, 3, 2), (128, 8, 1, 1, 1), (160, 6, 8, 3, 2),
+    (164, 6, 1, 1, 1), (256, 8, 8, 4, 2), (260, 5, 1, 1, 1), (384, 8, 8, 4, 2), (512, 9, 32, 5, 2),
+    (516, 9, 1, 1, 1), (768, 10, 16, 4, 2), (1024, 16, 1, 1, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_softmax_selection_does_not_depend_on_the_batch(E, K, groups, topk_groups, group_top, dtype):
+    """Keys that are rounded sums, p + bias and sums of two p: the same experts
+    and scores in a long batch, in short ones and for rows that are not aligned
+    (all rows, ties and near ties among them)."""
+    T = 4103
+    l = logits_of(T, E, dtype, E)
+    l[::3] = (l[::3] * 8).round() / 8  # many equal and nearly equal scores
+    l[5], l[6] = -math.inf, 0.0
+    l[torch.rand((T, E), generator=torch.Generator().manual_seed(3)) < 0.05] = -math.inf
+    l = l.to(DEV)
+    bias = (torch.randint(-20, 21, (E,), generator=torch.Generator().manual_seed(4)) * 1e-3).to(DEV)
+    odd = torch.empty((T, E + 3), dtype=dtype, device=DEV)[:, 3:]
+    odd.copy_(l)
+    for b in (None, bias):
+        kw = dict(bias=b, groups=groups, topk_groups=topk_groups, group_top=group_top,
+                  return_scores=True)
+        ids, w, p = hmm.moe_gate(l, K, **kw)
+        short = [torch.cat(t) for t in zip(*(hmm.moe_gate(x, K, **kw) for x in l.split(1024)))]
+        for other in (short, hmm.moe_gate(odd, K, **kw)):
+            assert torch.equal(other[0], ids)
+            if b is not None or group_top > 1:
+                assert torch.equal(other[1], w) and torch.equal(other[2], p)
