@@ -604,6 +604,21 @@ def _gate_forward(logits, gate, bias, return_scores):
     return ids, w, scores
 
 
+class _FirstOrder(torch.autograd.Function):
+    """A gradient under create_graph: the kernels that computed it have no
+    backward of their own, so that differentiating it is an error rather than a
+    constant.  (`inputs` make it require a gradient.)"""
+
+    @staticmethod
+    def forward(ctx, name, grad, *inputs):
+        ctx.name = name
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError(f"{ctx.name} has no second derivative")
+
+
 class _MoEGate(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, gate, bias, return_scores):
@@ -631,6 +646,8 @@ class _MoEGate(torch.autograd.Function):
             None if ds is None else ds.data_ptr(), dl.data_ptr(), _raw_stream(dev.index))
         if rc != HMM_OK:
             raise HmmError(rc, "hmm_gate_backward")
+        if torch.is_grad_enabled():  # create_graph
+            dl = _FirstOrder.apply("moe_gate", dl, logits)
         return dl, None, None, None
 
 
@@ -645,8 +662,9 @@ def moe_gate(logits, k, *, score="softmax", bias=None, groups=1, topk_groups=Non
     groups > 1 only inside the topk_groups best of `groups` groups of
     consecutive experts, a group counting by the sum of its group_top best
     keys; the weights are scale * p of the selected experts, divided by their
-    sum with renormalize.  A logit of -inf closes its expert.  Differentiable
-    in the logits through the weights and the scores."""
+    sum with renormalize.  A logit of -inf has p = 0: without a bias its expert
+    comes last; with one its key is the bias alone.  Differentiable (once) in
+    the logits through the weights and the scores."""
     if logits.dim() != 2:
         raise ValueError("logits [T, E] expected")
     ldt, wdt = _WDTYPES.get(logits.dtype), _WDTYPES.get(weights_dtype)

@@ -85,3 +85,19 @@ def test_softmax_selection_does_not_depend_on_the_batch(E, K, groups, topk_group
             assert torch.equal(other[0], ids)
             if b is not None or group_top > 1:
                 assert torch.equal(other[1], w) and torch.equal(other[2], p)
+
+
+def test_second_derivatives_are_refused():
+    """With create_graph the gradient is the same, and differentiating it raises
+    (it would lose its dependence on the logits, silently beside other terms)."""
+    l = logits_of(9, 40, torch.float32).to(DEV).requires_grad_()
+    extra = torch.ones((), device=DEV, requires_grad=True)
+    for through in (lambda out: out[1].sum(), lambda out: out[1].square().sum(),
+                    lambda out: (out[2] * extra).square().sum()):
+        for renorm in (False, True):
+            kw = dict(renormalize=renorm, return_scores=True)
+            want, = torch.autograd.grad(through(hmm.moe_gate(l, 3, **kw)), l)
+            got, = torch.autograd.grad(through(hmm.moe_gate(l, 3, **kw)), l, create_graph=True)
+            assert torch.equal(got, want)
+            with pytest.raises(RuntimeError, match="moe_gate has no second derivative"):
+                (got.square().sum() + extra).backward()
