@@ -353,10 +353,11 @@ int hmm_backward_dw(hmm_ctx* ctx, const hmm_shape* shape, const void* saved,
  *                  is the softmax of the K selected logits, and is computed
  *                  as such: a selected p below fp32's range keeps its weight
  *                  and its gradient.
- * A logit of -inf closes its expert: p = 0, chosen after every other open
- * expert.  A row with every logit -inf has p = 0 and weights 0 (softmax or
- * renormalize divide by 1 there) and a zero gradient.  NaN is chosen first and
- * shows in the weights. */
+ * A logit of -inf has p = 0.  Without a bias its expert is chosen after every
+ * other open expert; with one its key is the bias alone, so that an expert is
+ * closed to every token by a bias of -inf.  A row with every logit -inf has p =
+ * 0 and weights 0 (softmax or renormalize divide by 1 there) and a zero gradient.
+ * NaN is chosen first and shows in the weights. */
 #define HMM_SCORE_SOFTMAX 0
 #define HMM_SCORE_SIGMOID 1
 

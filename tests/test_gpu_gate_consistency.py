@@ -101,3 +101,23 @@ def test_second_derivatives_are_refused():
             assert torch.equal(got, want)
             with pytest.raises(RuntimeError, match="moe_gate has no second derivative"):
                 (got.square().sum() + extra).backward()
+
+
+@pytest.mark.parametrize("T", [3, 4100])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_closed_logits_under_a_bias(T, score):
+    """A logit of -inf has p = 0; its key is the bias, which may choose it, with
+    weight 0 and no gradient; a bias of -inf closes an expert to every token."""
+    l = torch.zeros((T, 8), device=DEV)
+    l[:, 2:4] = -math.inf
+    bias = torch.tensor([0.0, -2.0, 3.0, -1.0, -math.inf, -2.0, -2.0, -2.0], device=DEV)
+    x = l.clone().requires_grad_()
+    ids, w = hmm.moe_gate(x, 3, score=score, bias=bias)
+    assert (ids == torch.tensor([2, 0, 3], device=DEV)).all()
+    assert (w[:, 0] == 0).all() and (w[:, 1] > 0).all() and (w[:, 2] == 0).all()
+    g, = torch.autograd.grad(w.sum(), x)
+    assert (g[:, 2:4] == 0).all() and torch.isfinite(g).all() and (g[:, 0] > 0).all()
+    ids, w = hmm.moe_gate(l, 8, score=score, bias=bias)
+    assert (ids[:, 7] == 4).all()
+    ids, w = hmm.moe_gate(l, 8, score=score)
+    assert (ids == torch.tensor([0, 1, 4, 5, 6, 7, 2, 3], device=DEV)).all()
