@@ -526,6 +526,28 @@ class Context:
         return dx, dW1, dW2, dw, dWs1, dWs2
 
 
+class _FirstOrder(torch.autograd.Function):
+    """A gradient under create_graph: the kernels that computed it have no
+    backward of their own, so that differentiating it is an error rather than a
+    constant.  (`inputs` make it require a gradient.)"""
+
+    @staticmethod
+    def forward(ctx, name, grad, *inputs):
+        ctx.name = name
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError(f"{ctx.name} has no second derivative")
+
+
+def _first_order(name, grads, inputs):
+    """The gradients, marked as above where create_graph asks for it."""
+    if not torch.is_grad_enabled():
+        return grads
+    return tuple(g if g is None else _FirstOrder.apply(name, g, *inputs) for g in grads)
+
+
 class _MoEFFN(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, topk_ids, topk_weights, W1, W2):
@@ -540,7 +562,9 @@ class _MoEFFN(torch.autograd.Function):
         need = (ctx.needs_input_grad[0], ctx.needs_input_grad[3], ctx.needs_input_grad[4],
                 ctx.needs_input_grad[2])
         c = Context.for_device(x.device)
-        dx, dW1, dW2, dw = c.backward(dy, x, topk_ids, topk_weights, W1, W2, saved, need)
+        dx, dW1, dW2, dw = _first_order(
+            "moe_ffn", c.backward(dy, x, topk_ids, topk_weights, W1, W2, saved, need),
+            (x, topk_weights, W1, W2))
         return dx, None, dw, dW1, dW2
 
 
@@ -557,9 +581,10 @@ class _MoEFFNShared(torch.autograd.Function):
         x, topk_ids, topk_weights, W1, W2, Ws1, Ws2, saved = ctx.saved_tensors
         n = ctx.needs_input_grad
         c = Context.for_device(x.device)
-        dx, dW1, dW2, dw, dWs1, dWs2 = c.backward(dy, x, topk_ids, topk_weights, W1, W2, saved,
-                                                  (n[0], n[3], n[4], n[2]), Ws1=Ws1, Ws2=Ws2,
-                                                  need_shared=(n[5], n[6]))
+        grads = c.backward(dy, x, topk_ids, topk_weights, W1, W2, saved, (n[0], n[3], n[4], n[2]),
+                           Ws1=Ws1, Ws2=Ws2, need_shared=(n[5], n[6]))
+        dx, dW1, dW2, dw, dWs1, dWs2 = _first_order(
+            "moe_ffn", grads, (x, topk_weights, W1, W2, Ws1, Ws2))
         return dx, None, dw, dW1, dW2, dWs1, dWs2
 
 
@@ -568,8 +593,8 @@ def moe_ffn(x, topk_ids, topk_weights, up_proj_weight, down_proj_weight, *,
     """y[T,H] = sum_k topk_weights[t,k] * FFN_{topk_ids[t,k]}(x[t]) with SwiGLU
     experts (gate = first I columns of up_proj's 2I outputs), plus FFN_s(x[t])
     of the optional shared expert (keyword-only weights [H, 2I] and [I, H]).
-    Differentiable in x, topk_weights and every weight tensor; topk_ids is
-    not."""
+    Differentiable (once) in x, topk_weights and every weight tensor; topk_ids
+    is not."""
     shared = (shared_up_proj_weight, shared_down_proj_weight)
     has_shared = shared[0] is not None or shared[1] is not None
     tensors = (x, topk_weights, up_proj_weight, down_proj_weight) + (shared if has_shared else ())
@@ -604,21 +629,6 @@ def _gate_forward(logits, gate, bias, return_scores):
     return ids, w, scores
 
 
-class _FirstOrder(torch.autograd.Function):
-    """A gradient under create_graph: the kernels that computed it have no
-    backward of their own, so that differentiating it is an error rather than a
-    constant.  (`inputs` make it require a gradient.)"""
-
-    @staticmethod
-    def forward(ctx, name, grad, *inputs):
-        ctx.name = name
-        return grad.view_as(grad)
-
-    @staticmethod
-    def backward(ctx, _):
-        raise RuntimeError(f"{ctx.name} has no second derivative")
-
-
 class _MoEGate(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, gate, bias, return_scores):
@@ -646,9 +656,7 @@ class _MoEGate(torch.autograd.Function):
             None if ds is None else ds.data_ptr(), dl.data_ptr(), _raw_stream(dev.index))
         if rc != HMM_OK:
             raise HmmError(rc, "hmm_gate_backward")
-        if torch.is_grad_enabled():  # create_graph
-            dl = _FirstOrder.apply("moe_gate", dl, logits)
-        return dl, None, None, None
+        return *_first_order("moe_gate", (dl,), (logits,)), None, None, None
 
 
 def moe_gate(logits, k, *, score="softmax", bias=None, groups=1, topk_groups=None, group_top=1,
