@@ -1066,9 +1066,10 @@ int launch_forward_mx4(const GemmEnv& env, const Plan& p, const FfnMx4Plan& f, M
   // Pairs: six token blocks per expert on average (an odd last one idles a CTA),
   // two GMM1 tiles per CTA, contractions long beside a tile's epilogue; both
   // sides' figures are at the kernel.
-  const bool pair =
+  const bool pays =
       p.TK >= int64_t(6) * XM * p.E && p.H >= 2048 &&
       p.TK / (2 * XM) * ((2 * f.ip + XN - 1) / XN) >= int64_t(2) * env.num_sms;
+  const bool pair = env.mx4_pairs == 1 || (env.mx4_pairs == 2 && pays);
   if (pair) {
     // as many pairs as can be resident at once: the tiles wait for one another
     cudaLaunchConfig_t cfg = {};

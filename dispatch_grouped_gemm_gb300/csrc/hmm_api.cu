@@ -298,6 +298,7 @@ GemmEnv env_of(hmm_ctx* ctx, const Plan& p, cudaStream_t st) {
   e.budget_ns = ctx->budget_ns;
   e.stream = st;
   e.pdl = ctx->overlap != 0;
+  e.mx4_pairs = ctx->pair_rows == 3 ? 0 : ctx->pair_rows;
   e.mx4_set = &ctx->mx4_set;
   return e;
 }

@@ -202,7 +202,8 @@ struct GemmEnv {
   uint64_t budget_ns;
   cudaStream_t stream;
   bool pdl;          // programmatic dependent launches (launch_kernel)
-  bool* mx4_set;     // the 4-bit GEMM kernel's shared-memory attribute is set
+  int mx4_pairs;     // 4-bit GEMM kernel: 0 single CTAs, 1 CTA pairs, 2 automatic
+  bool* mx4_set;     // its shared-memory attribute is set
 };
 
 // forward GMM1(+SwiGLU) and GMM2 in one persistent launch with per-token-block

@@ -140,8 +140,10 @@ int hmm_destroy(hmm_ctx* ctx);
  *                         rows and deeper pipelines (weight streaming);
  *                         2 (default): automatic, 1 when the routed rows
  *                         average at least 256 per expert (T * K >= 256 * E),
- *                         3 below 64 per expert, else 0.  Results do not
- *                         depend on it. */
+ *                         3 below 64 per expert, else 0.  hmm_forward_mx4:
+ *                         1 CTA pairs, 0 and 3 single CTAs (tiles of 128 token
+ *                         rows per CTA, 256 or 128 weight rows), 2 pairs for
+ *                         long batches.  Results do not depend on it. */
 #define HMM_OPT_PAIR_ROWS 7
 /*   HMM_OPT_OVERLAP_LAUNCHES  0/1: launch every kernel with programmatic
  *                         stream serialization, so that it is scheduled and
