@@ -334,7 +334,13 @@ cudaError_t launch_dispatch_dy(const Plan& p, const void* dy, const void* w, int
 
 cudaError_t launch_combine_y(const Plan& p, const void* o, const void* w, int w_dtype, MetaPtrs m,
                              void* y, cudaStream_t st, bool pdl) {
-  const bool few = p.T < FEW_TOKENS && !p.shared;
+  // All K rows loaded before the first is added pays while latency counts: the
+  // fewer loads per lane cost more the more there are, and the rows to overlap
+  // are K (us of this launch with and without, experts of I = 64: K = 8, H = 7168,
+  // T = 1 6.3 and 8.4, T = 128 10.4 and 10.6, T = 512 20.5 and 14.6, T = 1000 38.8
+  // and 27.2; H = 2048, T = 512 9.0 and 9.8, T = 1000 12.5 and 10.4; K = 2, H = 2048,
+  // T = 128 6.3 and 6.2, T = 512 8.2 and 6.5).
+  const bool few = p.T < FEW_TOKENS && !p.shared && p.T * p.H <= p.K << 17;
   auto kern = p.shared ? combine_rows_kernel<true, true, UNROLL, 1>
               : few    ? combine_rows_kernel<true, false, 1, 8>
                        : combine_rows_kernel<true, false, UNROLL, 1>;
