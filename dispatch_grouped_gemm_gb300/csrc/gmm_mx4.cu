@@ -92,17 +92,21 @@ struct XParams {
   unsigned long long budget_ns;
 };
 
-// Weight rows per tile: 256, or 128 where a problem has at most one tile of 256
-// per CTA, so that the work spreads over more SMs (a graph of 21 calls, one set
-// of experts for all tokens, 128 and 256 wide: T = 1, H = 1024, I = 512 16.1 and
-// 17.5 us; T = 47, H = 3792, I = 536 23.2 and 26.5 us; above the limit T = 700, H
-// = I = 1024 33.1 and 29.5 us).  The token blocks are known on the device only,
-// so every CTA decides there.
+// Weight rows per tile: 256, or 128 where a problem has at most one tile of 128
+// per CTA, so that the work spreads over more SMs (a graph of 21 calls, 128 and
+// 256 wide in both problems, even and Zipf(1.2) routing: within the limit T = 1, H =
+// 1024, I = 512 15.8 and 16.9, 15.5 and 16.8 us; T = 1, H = 2048, I = 1408 20.1 and
+// 20.8, 20.1 and 20.8; T = 64, E = 8, H = 1024, I = 512 17.3 and 18.3, 17.2 and
+// 18.4; above it T = 47, E = 30, H = 3792, I = 536 35.1 and 32.6, 34.3 and 33.6; T =
+// 512, E = 8, H = 4096, I = 1024 33.4 and 31.5, 33.4 and 31.7; T = 700, E = 8, H = I =
+// 1024 24.0 and 22.9, 23.3 and 22.9).  The token blocks are known on the device
+// only, so every CTA decides there, which costs about a microsecond beside kernels
+// built for one width (T = 1, H = 2048 21.4, T = 1, H = 1024 15.6).
 __device__ __forceinline__ uint32_t xtiles(const XProb& p, uint32_t tn) {
   return (static_cast<uint32_t>(p.n) + tn - 1) / tn;
 }
 __device__ __forceinline__ uint32_t xwidth(const XProb& p, uint32_t blocks) {
-  return blocks * xtiles(p, XN) <= gridDim.x ? XN / 2 : XN;
+  return blocks * xtiles(p, XN / 2) <= gridDim.x ? XN / 2 : XN;
 }
 
 struct XMaps {
