@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32)
       for (int j = 0; j < C; ++j) p[j] = sigmoid_rn(l[j]);
     } else {
       m = row_max(l);
-      z = 1.0f / exp_row(l, m, p);
+      z = 1.0f / exp_row(l, m, p);  // (p: one rounding more than the forward's division)
 #pragma unroll
       for (int j = 0; j < C; ++j) p[j] *= z;
     }
@@ -955,7 +955,7 @@ cudaError_t by_length(const hmm_gate& g, bool vec, Args&&... args) {
   return by_type<F, 32>(g, vec, args...);
 }
 
-// one token per warp up to 64 blocks per SM's worth, then several in turn
+// one token per warp, several in turn past 2^20 blocks
 unsigned gate_grid(int64_t tokens) {
   return static_cast<unsigned>(
       std::min<int64_t>((tokens + GATE_WARPS - 1) / GATE_WARPS, int64_t(1) << 20));
@@ -1005,10 +1005,16 @@ cudaError_t run_backward_many(const hmm_gate& g, const void* logits, const int32
                        smem, st, pdl, 1, gate_args(g), logits, ids, d_weights, d_scores, d_logits);
 }
 
-// Tokens from which the kernels for many tokens are the faster ones (forward,
-// one and the other kernel: E = 64, T = 4000 8.2 and 8.2 us, T = 8000 10.2 and
-// 8.2; E = 256 grouped 12.3 and 14.3, 16.4 and 16.4; E = 160 10.2 and 12.3, 14.3
-// and 12.3).
+// Tokens from which the kernels for many tokens run.  One limit for every E,
+// near where most of them cross (us of a call in a graph of 20, one token per
+// warp and many; s: softmax, g: sigmoid in 8 groups, 4 for E = 64; T = 2048,
+// 4096, 8192: E = 64 s 2.8 and 3.6, 3.8 and 3.6, 5.7 and 4.0, g 3.4 and 5.5, 5.6
+// and 5.5, 6.6 and 6.1; E = 160 s 4.2 and 5.1, 5.7 and 5.1, 9.7 and 5.7, g 5.7 and
+// 9.5, 8.8 and 9.6, 12.7 and 10.3; E = 256 s 4.0 and 4.5, 5.5 and 5.0, 9.2 and 6.4,
+// g 5.7 and 8.1, 8.8 and 8.7, 12.4 and 10.3; the worst at the limit, E = 128 g, 4.2
+// and 8.4, 6.6 and 8.4, 8.7 and 9.2.  From E = 512 on the many win earlier, E = 1024
+// g 22.3 and 10.3, 30.9 and 15.7.  Dense backward: E = 64 2.8 and 2.9, 3.4 and 3.0,
+// E = 256 3.9 and 3.1, 6.1 and 3.5).
 constexpr int64_t GATE_MANY = 4096;
 
 struct RunBackward {

@@ -87,14 +87,21 @@ CtrlPtrs ctrl_at(const Plan& p, void* base);
 // Every kernel of the library may be launched with programmatic stream
 // serialization (pdl): it is then scheduled while the previous kernel of its
 // stream drains, runs its set-up (barriers, TMEM) meanwhile, and calls
-// grid_dep_wait() before its first access to global memory; that returns once
-// the previous kernel has completed and its writes are visible, and is a
-// no-op in a kernel launched without the attribute.  grid_dep_launch() lets
-// the stream's next kernel be scheduled once every CTA has called it (or
+// grid_dep_wait() before its first access to what earlier kernels write; that
+// returns once the previous kernel has completed and its writes are visible,
+// and is a no-op in a kernel launched without the attribute.  grid_dep_launch()
+// lets the stream's next kernel be scheduled once every CTA has called it (or
 // exited): the short kernels call it right after their wait, the persistent
 // GEMMs when a CTA has issued the loads of its last tile, so that the next
 // kernel's CTAs wait beside the GEMM's tail only.  Event records and waits
 // between launches keep their full ordering.
+//   A kernel whose predecessor calls grid_dep_launch() after its own
+// grid_dep_wait() may use, without a wait, what was complete when the predecessor
+// started.  Two do: dispatch_mx4_kernel (few tokens) reads x, behind the routing;
+// gmm_mx4_kernel reads the weights and the routing's results and draws tickets,
+// behind the dispatch.  So the routing kernels and the dispatch have to keep that
+// order.  gmm_mx4_kernel itself may call grid_dep_launch() first (only its token
+// producer waits): the kernel behind it, the combine, waits before everything.
 #ifdef __CUDACC__
 __device__ __forceinline__ void grid_dep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -428,8 +428,9 @@ typedef struct hmm_mx4 {
 /* Sizes in bytes of the codes and the scales (either pointer may be NULL). */
 int hmm_mx4_size(const hmm_mx4* desc, size_t* codes_bytes, size_t* scales_bytes);
 
-/* Values to codes and scales, and back (bf16 and fp32 hold every finite 4-bit
- * value exactly, fp32 subnormals included; a NaN block comes back as NaN).
+/* Values to codes and scales, and back (bf16 and fp32 hold every value of a
+ * scale that hmm_mx4_quantize writes, s up to 252, exactly, fp32 subnormals
+ * included; 253 and 254 may overflow; a NaN block comes back as NaN).
  * All pointers 16-byte aligned. */
 int hmm_mx4_quantize(hmm_ctx* ctx, const hmm_mx4* desc, const void* values, void* codes,
                      void* scales, void* stream);
