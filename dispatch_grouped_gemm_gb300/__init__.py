@@ -14,6 +14,11 @@ the HyperMegaMoE API (§3.1) and its DFunction semantics (§3.2).
 ``moe_gate`` is the router in front of it (differentiable in the logits);
 ``mx4_quantize_experts`` and ``moe_ffn_mx4`` serve the same layer with
 microscaled 4-bit expert weights.
+
+``moe_route``, ``moe_dispatch``, ``moe_grouped_mm`` and ``moe_combine`` are the
+pieces of a layer whose experts are not SwiGLU FFNs, each with its gradients;
+``orthogonalize`` is the Newton-Schulz step of an optimiser for stacked expert
+weights (Muon).
 """
 from __future__ import annotations
 
@@ -33,12 +38,17 @@ __all__ = [
     "hmm_mx4_size", "hmm_mx4_quantize", "hmm_mx4_dequantize", "hmm_mx4_workspace_size",
     "hmm_forward_mx4", "HmmMx4", "make_mx4", "Mx4Tensor", "mx4_quantize", "mx4_quantize_experts",
     "moe_ffn_mx4",
+    "hmm_dispatch", "hmm_dispatch_grad", "hmm_combine", "hmm_combine_grad", "hmm_grouped_mm",
+    "hmm_grouped_mm_dx", "hmm_grouped_mm_dw", "hmm_orthogonalize",
+    "hmm_orthogonalize_workspace_size", "HmmRows", "HmmGmm", "HmmOrtho", "make_rows", "make_gmm",
+    "make_ortho", "MoeRouting", "moe_route", "moe_dispatch", "moe_combine", "moe_grouped_mm",
+    "orthogonalize", "MUON_COEFFICIENTS",
     "hmm_status",
     "hmm_error_string", "Context", "moe_ffn", "library_path", "load_library",
     "hmm_profile_read", "hmm_phase_name", "hmm_set_trace",
     "HMM_OPT_VALIDATE", "HMM_OPT_WAIT_BUDGET_NS", "HMM_OPT_INJECT_SKIP_READY", "HMM_OPT_PROFILE",
     "HMM_OPT_PAIR_ROWS", "HMM_OPT_OVERLAP_LAUNCHES", "HMM_OPT_FUSED_COMBINE",
-    "HMM_DTYPE_BF16", "HMM_DTYPE_F32", "HMM_SCORE_SOFTMAX", "HMM_SCORE_SIGMOID",
+    "HMM_DTYPE_BF16", "HMM_DTYPE_F32", "HMM_DTYPE_F16", "HMM_W_KN", "HMM_W_NK", "HMM_SCORE_SOFTMAX", "HMM_SCORE_SIGMOID",
     "HMM_MX4_ROWS", "HMM_MX4_COLUMNS", "HMM_MX4_GATE_UP", "HMM_STATUS_EXPERT_ID", "HMM_STATUS_TIMEOUT",
 ]
 
@@ -72,6 +82,9 @@ HMM_OPT_OVERLAP_LAUNCHES = _C["HMM_OPT_OVERLAP_LAUNCHES"]
 HMM_OPT_FUSED_COMBINE = _C["HMM_OPT_FUSED_COMBINE"]
 HMM_DTYPE_BF16 = _C["HMM_DTYPE_BF16"]
 HMM_DTYPE_F32 = _C["HMM_DTYPE_F32"]
+HMM_DTYPE_F16 = _C["HMM_DTYPE_F16"]
+HMM_W_KN = _C["HMM_W_KN"]
+HMM_W_NK = _C["HMM_W_NK"]
 HMM_SCORE_SOFTMAX = _C["HMM_SCORE_SOFTMAX"]
 HMM_SCORE_SIGMOID = _C["HMM_SCORE_SIGMOID"]
 HMM_MX4_ROWS = _C["HMM_MX4_ROWS"]
@@ -99,6 +112,26 @@ class HmmGate(ctypes.Structure):
 class HmmMx4(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32)]
+
+
+class HmmRows(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("E", ctypes.c_int64), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("weights_dtype", ctypes.c_int32)]
+
+
+class HmmGmm(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("E", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("ld_dy", ctypes.c_int64),
+                ("ld_w", ctypes.c_int64), ("stride_w", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("w_layout", ctypes.c_int32)]
+
+
+class HmmOrtho(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("M", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("steps", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("coefficients", ctypes.POINTER(ctypes.c_float))]
 
 
 class HmmError(RuntimeError):
@@ -134,6 +167,7 @@ def load_library():
         vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
         sp, gp = ctypes.POINTER(HmmShape), ctypes.POINTER(HmmGate)
         mp, szp = ctypes.POINTER(HmmMx4), ctypes.POINTER(sz)
+        rp, mmp, op = ctypes.POINTER(HmmRows), ctypes.POINTER(HmmGmm), ctypes.POINTER(HmmOrtho)
         sig = {
             "hmm_create": [ctypes.POINTER(vp), i32],
             "hmm_destroy": [vp],
@@ -156,6 +190,15 @@ def load_library():
             "hmm_mx4_dequantize": [vp, mp, vp, vp, vp, vp],
             "hmm_mx4_workspace_size": [sp, szp],
             "hmm_forward_mx4": [vp, sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+            "hmm_dispatch": [vp, rp, vp, vp, vp, vp, vp],
+            "hmm_dispatch_grad": [vp, rp, vp, vp, vp, vp],
+            "hmm_combine": [vp, rp, vp, vp, vp, vp, vp],
+            "hmm_combine_grad": [vp, rp, vp, vp, vp, vp, vp, vp, vp, vp],
+            "hmm_grouped_mm": [vp, mmp, vp, vp, vp, vp, vp],
+            "hmm_grouped_mm_dx": [vp, mmp, vp, vp, vp, vp, vp],
+            "hmm_grouped_mm_dw": [vp, mmp, vp, vp, vp, vp, vp],
+            "hmm_orthogonalize_workspace_size": [op, szp],
+            "hmm_orthogonalize": [vp, op, vp, vp, vp, sz, vp],
             "hmm_status": [vp, vp, ctypes.POINTER(i32)],
             "hmm_profile_read": [vp, i32, ctypes.POINTER(ctypes.c_double),
                                  ctypes.POINTER(ctypes.c_int64)],
@@ -369,6 +412,87 @@ def hmm_forward_mx4(ctx, shape, x, topk_ids, topk_weights, up_codes, up_scales, 
                                         _ptr(down_codes), _ptr(down_scales), _ptr(y),
                                         _ptr(workspace), _nbytes(workspace), _stream(stream))
     _check(rc, "hmm_forward_mx4")
+
+
+def make_rows(T, H, K, E, *, ld=None, dtype=HMM_DTYPE_BF16, weights_dtype=HMM_DTYPE_F32) -> HmmRows:
+    return HmmRows(int(T), int(H), int(K), int(E), int(H if ld is None else ld), int(dtype),
+                   int(weights_dtype))
+
+
+def hmm_dispatch(ctx, desc, x, offsets, slot2row, rows, stream=None):
+    rc = load_library().hmm_dispatch(ctx, ctypes.byref(desc), _ptr(x), _ptr(offsets),
+                                     _ptr(slot2row), _ptr(rows), _stream(stream))
+    _check(rc, "hmm_dispatch")
+
+
+def hmm_dispatch_grad(ctx, desc, d_rows, slot2row, dx, stream=None):
+    rc = load_library().hmm_dispatch_grad(ctx, ctypes.byref(desc), _ptr(d_rows), _ptr(slot2row),
+                                          _ptr(dx), _stream(stream))
+    _check(rc, "hmm_dispatch_grad")
+
+
+def hmm_combine(ctx, desc, rows, slot2row, topk_weights, y, stream=None):
+    rc = load_library().hmm_combine(ctx, ctypes.byref(desc), _ptr(rows), _ptr(slot2row),
+                                    _ptr(topk_weights), _ptr(y), _stream(stream))
+    _check(rc, "hmm_combine")
+
+
+def hmm_combine_grad(ctx, desc, rows, offsets, slot2row, topk_weights, dy, d_rows,
+                     d_topk_weights, stream=None):
+    rc = load_library().hmm_combine_grad(ctx, ctypes.byref(desc), _ptr(rows), _ptr(offsets),
+                                         _ptr(slot2row), _ptr(topk_weights), _ptr(dy),
+                                         _ptr(d_rows), _ptr(d_topk_weights), _stream(stream))
+    _check(rc, "hmm_combine_grad")
+
+
+def make_gmm(R, K, N, E, *, ld_x=None, ld_dy=None, ld_w=None, stride_w=None,
+             dtype=HMM_DTYPE_BF16, w_layout=HMM_W_KN) -> HmmGmm:
+    return HmmGmm(int(R), int(K), int(N), int(E), int(K if ld_x is None else ld_x),
+                  int(N if ld_dy is None else ld_dy),
+                  int((N if w_layout == HMM_W_KN else K) if ld_w is None else ld_w),
+                  int(K * N if stride_w is None else stride_w), int(dtype), int(w_layout))
+
+
+def hmm_grouped_mm(ctx, desc, x, w, offsets, y, stream=None):
+    rc = load_library().hmm_grouped_mm(ctx, ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(offsets),
+                                       _ptr(y), _stream(stream))
+    _check(rc, "hmm_grouped_mm")
+
+
+def hmm_grouped_mm_dx(ctx, desc, dy, w, offsets, dx, stream=None):
+    rc = load_library().hmm_grouped_mm_dx(ctx, ctypes.byref(desc), _ptr(dy), _ptr(w),
+                                          _ptr(offsets), _ptr(dx), _stream(stream))
+    _check(rc, "hmm_grouped_mm_dx")
+
+
+def hmm_grouped_mm_dw(ctx, desc, x, dy, offsets, dw, stream=None):
+    rc = load_library().hmm_grouped_mm_dw(ctx, ctypes.byref(desc), _ptr(x), _ptr(dy),
+                                          _ptr(offsets), _ptr(dw), _stream(stream))
+    _check(rc, "hmm_grouped_mm_dw")
+
+
+def make_ortho(batch, M, N, coefficients, *, ld=None, stride=None, dtype=HMM_DTYPE_BF16,
+               out_dtype=HMM_DTYPE_BF16, eps=1e-7, scale=1.0) -> HmmOrtho:
+    """coefficients: one (a, b, c) per step."""
+    flat = [float(v) for step in coefficients for v in step]
+    array = (ctypes.c_float * max(len(flat), 1))(*flat)
+    return HmmOrtho(int(batch), int(M), int(N), int(N if ld is None else ld),
+                    int(M * N if stride is None else stride), int(dtype), int(out_dtype),
+                    len(flat) // 3, float(eps), float(scale),
+                    ctypes.cast(array, ctypes.POINTER(ctypes.c_float)))
+
+
+def hmm_orthogonalize_workspace_size(desc) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().hmm_orthogonalize_workspace_size(ctypes.byref(desc), ctypes.byref(n)),
+           "hmm_orthogonalize_workspace_size")
+    return n.value
+
+
+def hmm_orthogonalize(ctx, desc, g, out, workspace, stream=None):
+    rc = load_library().hmm_orthogonalize(ctx, ctypes.byref(desc), _ptr(g), _ptr(out),
+                                          _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check(rc, "hmm_orthogonalize")
 
 
 def hmm_status(ctx, stream=None):
@@ -876,3 +1000,361 @@ def moe_ffn_mx4(x, topk_ids, topk_weights, up_proj, down_proj):
     if rc != HMM_OK:
         raise HmmError(rc, "hmm_forward_mx4")
     return y
+
+
+# -------------------------------------------------- the open expert layer
+_DTYPES = {torch.bfloat16: HMM_DTYPE_BF16, torch.float32: HMM_DTYPE_F32,
+           torch.float16: HMM_DTYPE_F16}
+
+
+class MoeRouting:
+    """Where the rows of T tokens lie in expert order (what moe_route gives):
+    int32 counts [E] and offsets [E + 1] of the experts' rows, slot2row [T, K] the
+    row of each slot (-1: an id outside [0, E)), row2slot [T * K] the slot
+    t * K + k of each row."""
+
+    __slots__ = ("counts", "offsets", "slot2row", "row2slot")
+
+    def __init__(self, counts, offsets, slot2row, row2slot):
+        if slot2row.dim() != 2 or counts.dim() != 1:
+            raise ValueError("counts [E], offsets [E + 1], slot2row [T, K], row2slot [T * K] "
+                             "expected")
+        T, K = slot2row.shape
+        if offsets.shape != (counts.shape[0] + 1,) or row2slot.shape != (T * K,):
+            raise ValueError("offsets must be [E + 1] and row2slot [T * K]")
+        at = slot2row.get_device()
+        for t in (counts, offsets, slot2row, row2slot):
+            if t.dtype != torch.int32:
+                raise TypeError("routing tensors must be int32")
+            if not t.is_cuda or not t.is_contiguous() or t.get_device() != at:
+                raise ValueError("routing tensors must be contiguous tensors of one CUDA device")
+        self.counts, self.offsets = counts, offsets
+        self.slot2row, self.row2slot = slot2row, row2slot
+
+
+@functools.lru_cache(maxsize=64)
+def _route_call(T, E, K):
+    """(hmm_shape, workspace bytes) of a routing."""
+    shape = HmmShape(T, 8, 8, E, K, HMM_DTYPE_F32, 0)
+    return shape, max(hmm_workspace_size(shape, False)[0], 16)
+
+
+def moe_route(topk_ids, num_experts):
+    """The routing of topk_ids (int32 [T, K], contiguous) over num_experts
+    experts, computed on the device: slots sorted by expert, stable.  An id
+    outside [0, num_experts) sets the context's status and gets no row."""
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids [T, K] expected")
+    if topk_ids.dtype != torch.int32:
+        raise TypeError("topk_ids must be int32")
+    if not topk_ids.is_cuda or not topk_ids.is_contiguous():
+        raise ValueError("topk_ids must be a contiguous CUDA tensor")
+    T, K = topk_ids.shape
+    E, dev = int(num_experts), topk_ids.device
+    shape, size = _route_call(T, E, K)
+    # one allocation: counts | offsets | slot2row | row2slot
+    n = T * K
+    buf = torch.empty(2 * E + 1 + 2 * n, dtype=torch.int32, device=dev)
+    counts, offsets = buf[:E], buf[E:2 * E + 1]
+    slot2row, row2slot = buf[2 * E + 1:2 * E + 1 + n].view(T, K), buf[2 * E + 1 + n:]
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    rc = load_library().hmm_route(
+        Context.for_device(dev).handle, ctypes.byref(shape), topk_ids.data_ptr(),
+        counts.data_ptr(), offsets.data_ptr(), slot2row.data_ptr(), row2slot.data_ptr(),
+        ws.data_ptr(), size, _raw_stream(dev.index))
+    if rc != HMM_OK:
+        raise HmmError(rc, "hmm_route")
+    routing = MoeRouting.__new__(MoeRouting)
+    routing.counts, routing.offsets = counts, offsets
+    routing.slot2row, routing.row2slot = slot2row, row2slot
+    return routing
+
+
+def _token_rows(x):
+    """(x, elements between its rows); copied where rows overlap or have no unit
+    stride."""
+    T, H = x.shape
+    if H > 1 and x.stride(1) != 1:
+        x = x.contiguous()
+    ld = x.stride(0) if T > 1 else H
+    return (x, ld) if ld >= H else (x.contiguous(), H)
+
+
+def _rows_desc(routing, H, ld, dtype, weights_dtype=HMM_DTYPE_F32):
+    T, K = routing.slot2row.shape
+    return HmmRows(T, H, K, routing.counts.shape[0], ld, _DTYPES[dtype], weights_dtype)
+
+
+def _same_device(at, *tensors):
+    for t in tensors:
+        if t.get_device() != at:
+            raise ValueError(f"all arguments must be on one CUDA device, got devices {at} and "
+                             f"{t.get_device()}")
+
+
+def _dispatch_rows(x, routing):
+    x, ld = _token_rows(x)
+    T, H = x.shape
+    dev = x.device
+    d = _rows_desc(routing, H, ld, x.dtype)
+    rows = torch.empty((T * d.K, H), dtype=x.dtype, device=dev)
+    rc = load_library().hmm_dispatch(
+        Context.for_device(dev).handle, ctypes.byref(d), x.data_ptr(), routing.offsets.data_ptr(),
+        routing.slot2row.data_ptr(), rows.data_ptr(), _raw_stream(dev.index))
+    if rc != HMM_OK:
+        raise HmmError(rc, "hmm_dispatch")
+    return rows
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, routing):
+        ctx.routing = routing
+        ctx.save_for_backward(x, routing.slot2row)
+        return _dispatch_rows(x, routing)
+
+    @staticmethod
+    def backward(ctx, d_rows):
+        x, slot2row = ctx.saved_tensors
+        d_rows = d_rows.contiguous()
+        dev = x.device
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        d = _rows_desc(ctx.routing, x.shape[1], x.shape[1], x.dtype)
+        rc = load_library().hmm_dispatch_grad(
+            Context.for_device(dev).handle, ctypes.byref(d), d_rows.data_ptr(),
+            slot2row.data_ptr(), dx.data_ptr(), _raw_stream(dev.index))
+        if rc != HMM_OK:
+            raise HmmError(rc, "hmm_dispatch_grad")
+        return *_first_order("moe_dispatch", (dx,), (x,)), None
+
+
+def moe_dispatch(x, routing):
+    """rows [T * K, H] of x [T, H] (bfloat16, float16 or float32) in the expert
+    order of a routing: row slot2row[t, k] is x[t]; rows behind the last expert's
+    (slots of invalid ids have none) are zeros.  Differentiable (once) in x."""
+    if x.dim() != 2 or x.shape[0] != routing.slot2row.shape[0]:
+        raise ValueError("x [T, H] expected, T as in the routing")
+    if x.dtype not in _DTYPES:
+        raise TypeError("x must be bfloat16, float16 or float32")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    _same_device(x.get_device(), routing.slot2row)
+    if x.requires_grad and torch.is_grad_enabled():
+        return _Dispatch.apply(x, routing)
+    return _dispatch_rows(x, routing)
+
+
+def _combine_rows(rows, routing, w):
+    rows, w = rows.contiguous(), w.contiguous()
+    H, dev = rows.shape[1], rows.device
+    d = _rows_desc(routing, H, H, rows.dtype, _WDTYPES[w.dtype])
+    y = torch.empty((d.T, H), dtype=rows.dtype, device=dev)
+    rc = load_library().hmm_combine(
+        Context.for_device(dev).handle, ctypes.byref(d), rows.data_ptr(),
+        routing.slot2row.data_ptr(), w.data_ptr(), y.data_ptr(), _raw_stream(dev.index))
+    if rc != HMM_OK:
+        raise HmmError(rc, "hmm_combine")
+    return y
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, routing, w):
+        ctx.routing = routing
+        ctx.save_for_backward(rows, w, routing.slot2row, routing.offsets)
+        return _combine_rows(rows, routing, w)
+
+    @staticmethod
+    def backward(ctx, dy):
+        saved_rows, saved_w, slot2row, offsets = ctx.saved_tensors
+        rows, w = saved_rows.contiguous(), saved_w.contiguous()
+        dy, ld = _token_rows(dy)
+        dev = rows.device
+        d_rows = torch.empty_like(rows) if ctx.needs_input_grad[0] else None
+        dw = torch.empty_like(w) if ctx.needs_input_grad[2] else None
+        d = _rows_desc(ctx.routing, rows.shape[1], ld, rows.dtype, _WDTYPES[w.dtype])
+        rc = load_library().hmm_combine_grad(
+            Context.for_device(dev).handle, ctypes.byref(d), rows.data_ptr(), offsets.data_ptr(),
+            slot2row.data_ptr(), w.data_ptr(), dy.data_ptr(), _ptr(d_rows), _ptr(dw),
+            _raw_stream(dev.index))
+        if rc != HMM_OK:
+            raise HmmError(rc, "hmm_combine_grad")
+        d_rows, dw = _first_order("moe_combine", (d_rows, dw), (saved_rows, saved_w))
+        return d_rows, None, dw
+
+
+def moe_combine(rows, routing, topk_weights):
+    """y[t] = sum_k topk_weights[t, k] * rows[slot2row[t, k]], [T, H] of rows
+    [T * K, H] (bfloat16, float16 or float32) in the expert order of a routing and
+    topk_weights [T, K] (bfloat16 or float32).  fp32 sums in the order of k,
+    rounded once.  Differentiable (once) in rows and topk_weights."""
+    T, K = routing.slot2row.shape
+    if rows.dim() != 2 or rows.shape[0] != T * K or topk_weights.shape != (T, K):
+        raise ValueError("rows [T * K, H] and topk_weights [T, K] expected, T and K as in the "
+                         "routing")
+    if rows.dtype not in _DTYPES:
+        raise TypeError("rows must be bfloat16, float16 or float32")
+    if topk_weights.dtype not in _WDTYPES:
+        raise TypeError("topk_weights must be bfloat16 or float32")
+    if not rows.is_cuda:
+        raise ValueError("rows must be a CUDA tensor")
+    _same_device(rows.get_device(), routing.slot2row, topk_weights)
+    if (rows.requires_grad or topk_weights.requires_grad) and torch.is_grad_enabled():
+        return _Combine.apply(rows, routing, topk_weights)
+    return _combine_rows(rows, routing, topk_weights)
+
+
+def _tma_rows(x):
+    """(x, elements between its rows) as the tensor maps take it: 16-byte aligned
+    rows of unit stride; copied where they are not."""
+    R, C = x.shape
+    ld = x.stride(0) if R > 1 else C
+    if x.stride(1) != 1 or ld < C or ld % 8 or x.data_ptr() % 16:
+        return x.clone(memory_format=torch.contiguous_format), C
+    return x, ld
+
+
+def _tma_weights(w):
+    """(w, layout, elements between its stored rows, between experts)."""
+    E, K, N = w.shape
+    for layout, unit, rows, n, c in ((HMM_W_KN, 2, 1, K, N), (HMM_W_NK, 1, 2, N, K)):
+        ld = w.stride(rows)
+        per = w.stride(0) if E > 1 else n * ld
+        if (w.stride(unit) == 1 and ld >= c and ld % 8 == 0 and per % 8 == 0
+                and per >= (n - 1) * ld + c and w.data_ptr() % 16 == 0):
+            return w, layout, ld, per
+    return w.clone(memory_format=torch.contiguous_format), HMM_W_KN, N, K * N
+
+
+def _gmm(name, desc, a, b, offsets, out):
+    dev = a.device
+    rc = getattr(load_library(), name)(
+        Context.for_device(dev).handle, ctypes.byref(desc), a.data_ptr(), b.data_ptr(),
+        offsets.data_ptr(), out.data_ptr(), _raw_stream(dev.index))
+    if rc != HMM_OK:
+        raise HmmError(rc, name)
+    return out
+
+
+def _gmm_forward(x, w, offsets):
+    x, ld = _tma_rows(x)
+    w, layout, ld_w, per = _tma_weights(w)
+    E, K, N = w.shape
+    R = x.shape[0]
+    d = HmmGmm(R, K, N, E, ld, N, ld_w, per, _DTYPES[x.dtype], layout)
+    return _gmm("hmm_grouped_mm", d, x, w, offsets,
+                torch.empty((R, N), dtype=x.dtype, device=x.device))
+
+
+class _GroupedMM(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        ctx.save_for_backward(x, w, offsets)
+        return _gmm_forward(x, w, offsets)
+
+    @staticmethod
+    def backward(ctx, dy):
+        saved_x, saved_w, offsets = ctx.saved_tensors
+        x, ld_x = _tma_rows(saved_x)
+        w, layout, ld_w, per = _tma_weights(saved_w)
+        dy, ld_dy = _tma_rows(dy)
+        E, K, N = w.shape
+        R, dev = x.shape[0], x.device
+        d = HmmGmm(R, K, N, E, ld_x, ld_dy, ld_w, per, _DTYPES[x.dtype], layout)
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            dx = _gmm("hmm_grouped_mm_dx", d, dy, w, offsets,
+                      torch.empty((R, K), dtype=x.dtype, device=dev))
+        if ctx.needs_input_grad[1]:
+            shape = (E, K, N) if layout == HMM_W_KN else (E, N, K)
+            dw = _gmm("hmm_grouped_mm_dw", d, x, dy, offsets,
+                      torch.empty(shape, dtype=x.dtype, device=dev))
+            if layout == HMM_W_NK:
+                dw = dw.transpose(1, 2)
+        dx, dw = _first_order("moe_grouped_mm", (dx, dw), (saved_x, saved_w))
+        return dx, dw, None
+
+
+def moe_grouped_mm(x, w, offsets):
+    """y [R, N]: y[r] = x[r] @ w[e] for the rows offsets[e] <= r < offsets[e + 1] of
+    expert e, zeros for rows of no expert.  x [R, K] and w [E, K, N] bfloat16 or
+    float16 (one type; K and N multiples of 8), offsets int32 [E + 1] on their
+    device, as moe_route gives them.  w may be a transposed view of weights stored
+    [E, N, K]; rows of x may lie apart.  (Other strides, and operands that are not
+    16-byte aligned, are copied.)  fp32 sums, rounded once.  Differentiable (once)
+    in x and w."""
+    if x.dim() != 2 or w.dim() != 3 or x.shape[1] != w.shape[1]:
+        raise ValueError("x [R, K] and w [E, K, N] expected")
+    E, K, N = w.shape
+    if offsets.shape != (E + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be a contiguous [{E + 1}] tensor")
+    if x.dtype not in (torch.bfloat16, torch.float16) or w.dtype != x.dtype:
+        raise TypeError("x and w must both be bfloat16 or both float16")
+    if offsets.dtype != torch.int32:
+        raise TypeError("offsets must be int32")
+    if K == 0 or N == 0 or K % 8 or N % 8:
+        raise ValueError(f"K and N must be positive multiples of 8, got {K} and {N}")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    _same_device(x.get_device(), w, offsets)
+    if (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
+        return _GroupedMM.apply(x, w, offsets)
+    return _gmm_forward(x, w, offsets)
+
+
+#: Coefficients of the quintic step that the Muon optimiser uses.
+MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+@functools.lru_cache(maxsize=64)
+def _ortho_call(batch, M, N, ld, stride, dtype, out_dtype, coefficients, eps, scale):
+    """(hmm_ortho, workspace bytes) of a call."""
+    d = make_ortho(batch, M, N, coefficients, ld=ld, stride=stride, dtype=dtype,
+                   out_dtype=out_dtype, eps=eps, scale=scale)
+    return d, hmm_orthogonalize_workspace_size(d)
+
+
+def orthogonalize(g, *, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, scale=1.0,
+                  out_dtype=None):
+    """scale * X of each matrix G of g [..., M, N] (bfloat16, float16 or float32):
+    X = G / (|G|_F + eps), then `steps` times X <- a X + (b A + c A A) X with A = X X^T,
+    which brings the singular values near 1 and keeps the singular vectors (the
+    update of the Muon optimiser; the gradients of stacked expert weights are such a
+    stack).  coefficients: (a, b, c), or one for each step.  out_dtype: bfloat16
+    (default) or float16 (default for float16).  Not differentiable."""
+    if g.dim() < 2:
+        raise ValueError("g [..., M, N] expected")
+    if g.dtype not in _DTYPES:
+        raise TypeError("g must be bfloat16, float16 or float32")
+    if out_dtype is None:
+        out_dtype = torch.float16 if g.dtype == torch.float16 else torch.bfloat16
+    if out_dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("out_dtype must be bfloat16 or float16 (the products take 16-bit operands)")
+    if not isinstance(coefficients[0], (tuple, list)):
+        coefficients = (tuple(coefficients),) * int(steps)
+    coefficients = tuple(tuple(float(v) for v in c) for c in coefficients)
+    if len(coefficients) != steps or any(len(c) != 3 for c in coefficients):
+        raise ValueError("coefficients must be (a, b, c), or `steps` of them")
+    if not g.is_cuda:
+        raise ValueError("g must be a CUDA tensor")
+    if g.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError("orthogonalize has no backward: call it under torch.no_grad()")
+    shape, dev = g.shape, g.device
+    M, N = shape[-2:]
+    out = torch.empty(shape, dtype=out_dtype, device=dev)
+    if out.numel() == 0:
+        return out
+    g = g.detach().reshape(-1, M, N)
+    if (N > 1 and g.stride(2) != 1) or (M > 1 and g.stride(1) < N):
+        g = g.contiguous()
+    batch = g.shape[0]
+    d, size = _ortho_call(batch, M, N, g.stride(1) if M > 1 else N,
+                          g.stride(0) if batch > 1 else M * N, _DTYPES[g.dtype],
+                          _DTYPES[out_dtype], coefficients, float(eps), float(scale))
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    rc = load_library().hmm_orthogonalize(
+        Context.for_device(dev).handle, ctypes.byref(d), g.data_ptr(), out.data_ptr(),
+        ws.data_ptr(), size, _raw_stream(dev.index))
+    if rc != HMM_OK:
+        raise HmmError(rc, "hmm_orthogonalize")
+    return out

@@ -17,6 +17,7 @@
 #include <utility>
 #include <vector>
 
+#include "gmm_open.h"
 #include "hmm_internal.h"
 
 namespace {
@@ -303,6 +304,50 @@ GemmEnv env_of(hmm_ctx* ctx, const Plan& p, cudaStream_t st) {
   return e;
 }
 
+// What the products of the open expert layer need (they have no tilings to choose).
+GemmEnv open_env(hmm_ctx* ctx, void* stream) {
+  GemmEnv e{};
+  e.encode = ctx->encode;
+  e.num_sms = ctx->num_sms;
+  e.status = ctx->status;
+  e.budget_ns = ctx->budget_ns;
+  e.stream = static_cast<cudaStream_t>(stream);
+  e.pdl = ctx->overlap != 0;
+  return e;
+}
+
+bool aligned_to(const void* p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == HMM_DTYPE_F32 ? 3u : 1u)) == 0;
+}
+
+int check_gmm(const hmm_gmm* d) {
+  if (!d) return HMM_ERR_ARG;
+  if (d->dtype != HMM_DTYPE_BF16 && d->dtype != HMM_DTYPE_F16) return HMM_ERR_DTYPE;
+  if (d->w_layout != HMM_W_KN && d->w_layout != HMM_W_NK) return HMM_ERR_ARG;
+  if (d->R < 0 || d->R > INT32_MAX - 1024 || d->K <= 0 || d->N <= 0 || d->E <= 0 ||
+      d->K > (1 << 20) || d->N > (1 << 20) || d->E > MAX_E)
+    return HMM_ERR_SHAPE;
+  const int64_t rows_w = d->w_layout == HMM_W_KN ? d->K : d->N;
+  const int64_t cols_w = d->w_layout == HMM_W_KN ? d->N : d->K;
+  // (strides of a tensor map stay below 2^40 bytes; its last one is the whole array's)
+  constexpr int64_t far = int64_t(1) << 38;
+  if (d->ld_x < d->K || d->ld_dy < d->N || d->ld_w < cols_w || d->ld_x > far ||
+      d->ld_dy > far || d->ld_w > far || d->stride_w > far || d->stride_w < 0)
+    return HMM_ERR_SHAPE;
+  if (d->E > 1 && d->stride_w < (rows_w - 1) * d->ld_w + cols_w) return HMM_ERR_SHAPE;
+  if ((d->K | d->N | d->ld_x | d->ld_dy | d->ld_w | d->stride_w) % 8 != 0) return HMM_ERR_LAYOUT;
+  const int64_t rows = std::max<int64_t>(d->R, 1);
+  if (d->ld_x > far / rows || d->ld_dy > far / rows || d->K * d->N > far) return HMM_ERR_SHAPE;
+  return HMM_OK;
+}
+
+// w [E][rows][cols] as it is stored
+OpenOperand gmm_weights(const hmm_gmm& d, const void* w) {
+  const bool kn = d.w_layout == HMM_W_KN;
+  // (one expert has no stride to the next; a tensor map wants some)
+  return {w, kn ? d.K : d.N, kn ? d.N : d.K, d.E, d.ld_w, d.E > 1 ? d.stride_w : d.ld_w};
+}
+
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? HMM_OK : HMM_ERR_CUDA; }
 
 int read_route_error(hmm_ctx* ctx, cudaStream_t st) {
@@ -452,12 +497,10 @@ int hmm_route(hmm_ctx* ctx, const hmm_shape* shape, const int32_t* topk_ids, int
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CtrlPtrs c = ctrl_at(p, workspace);
   MetaPtrs m = meta_at(p, static_cast<uint8_t*>(workspace) + p.ctrl_bytes);
+  m.counts = counts;
+  m.offsets = offsets;
   rc = cuda_rc(launch_route(p, topk_ids, m, c, slot2row, row2slot, ctx->status, st,
                                   ctx->overlap != 0));
-  if (rc != HMM_OK) return rc;
-  rc = cuda_rc(cudaMemcpyAsync(counts, m.counts, 4 * p.E, cudaMemcpyDeviceToDevice, st));
-  if (rc != HMM_OK) return rc;
-  rc = cuda_rc(cudaMemcpyAsync(offsets, m.offsets, 4 * (p.E + 1), cudaMemcpyDeviceToDevice, st));
   if (rc != HMM_OK) return rc;
   if (ctx->validate) return read_route_error(ctx, st);
   return HMM_OK;
@@ -866,6 +909,162 @@ int hmm_forward_mx4(hmm_ctx* ctx, const hmm_shape* shape, const void* x, const i
   PhaseScope ps(ctx, PH_COMBINE_Y, st);
   return cuda_rc(launch_combine_y(p, ws + f.off_o, topk_weights, shape->weights_dtype, m, y, st,
                                   pdl));
+}
+
+int hmm_dispatch(hmm_ctx* ctx, const hmm_rows* d, const void* x, const int32_t* offsets,
+                 const int32_t* slot2row, void* rows, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  const int rc = check_rows(d);
+  if (rc != HMM_OK) return rc;
+  if (d->T == 0) return HMM_OK;
+  if (!x || !offsets || !slot2row || !rows) return HMM_ERR_ARG;
+  if (!aligned_to(x, d->dtype) || !aligned_to(rows, d->dtype) ||
+      !aligned_to(offsets, HMM_DTYPE_F32) || !aligned_to(slot2row, HMM_DTYPE_F32))
+    return HMM_ERR_LAYOUT;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return HMM_ERR_CUDA;
+  RowsArgs a{d->T, d->H, d->K, d->E, d->ld, offsets, slot2row, x, nullptr, rows, nullptr,
+             nullptr, 0};
+  return cuda_rc(launch_rows_dispatch(a, d->dtype, static_cast<cudaStream_t>(stream),
+                                      ctx->overlap != 0));
+}
+
+int hmm_dispatch_grad(hmm_ctx* ctx, const hmm_rows* d, const void* d_rows,
+                      const int32_t* slot2row, void* dx, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  const int rc = check_rows(d);
+  if (rc != HMM_OK) return rc;
+  if (d->T == 0) return HMM_OK;
+  if (!d_rows || !slot2row || !dx) return HMM_ERR_ARG;
+  if (!aligned_to(d_rows, d->dtype) || !aligned_to(dx, d->dtype) ||
+      !aligned_to(slot2row, HMM_DTYPE_F32))
+    return HMM_ERR_LAYOUT;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return HMM_ERR_CUDA;
+  RowsArgs a{d->T, d->H, d->K, d->E, d->H, nullptr, slot2row, d_rows, nullptr, dx, nullptr,
+             nullptr, 0};
+  return cuda_rc(launch_rows_sum(a, d->dtype, static_cast<cudaStream_t>(stream),
+                                 ctx->overlap != 0));
+}
+
+int hmm_combine(hmm_ctx* ctx, const hmm_rows* d, const void* rows, const int32_t* slot2row,
+                const void* topk_weights, void* y, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  const int rc = check_rows(d);
+  if (rc != HMM_OK) return rc;
+  if (d->T == 0) return HMM_OK;
+  if (!rows || !slot2row || !topk_weights || !y) return HMM_ERR_ARG;
+  if (!aligned_to(rows, d->dtype) || !aligned_to(y, d->dtype) ||
+      !aligned_to(topk_weights, d->weights_dtype) || !aligned_to(slot2row, HMM_DTYPE_F32))
+    return HMM_ERR_LAYOUT;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return HMM_ERR_CUDA;
+  RowsArgs a{d->T, d->H, d->K, d->E, d->H, nullptr, slot2row, rows, nullptr, y, topk_weights,
+             nullptr, d->weights_dtype};
+  return cuda_rc(launch_rows_sum(a, d->dtype, static_cast<cudaStream_t>(stream),
+                                 ctx->overlap != 0));
+}
+
+int hmm_combine_grad(hmm_ctx* ctx, const hmm_rows* d, const void* rows, const int32_t* offsets,
+                     const int32_t* slot2row, const void* topk_weights, const void* dy,
+                     void* d_rows, void* d_topk_weights, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  const int rc = check_rows(d);
+  if (rc != HMM_OK) return rc;
+  if (d->T == 0 || (!d_rows && !d_topk_weights)) return HMM_OK;
+  if (!offsets || !slot2row || !topk_weights || !dy || (d_topk_weights && !rows))
+    return HMM_ERR_ARG;
+  for (const void* p : {rows, dy, static_cast<const void*>(d_rows)})
+    if (!aligned_to(p, d->dtype)) return HMM_ERR_LAYOUT;
+  if (!aligned_to(topk_weights, d->weights_dtype) ||
+      !aligned_to(d_topk_weights, d->weights_dtype) || !aligned_to(offsets, HMM_DTYPE_F32) ||
+      !aligned_to(slot2row, HMM_DTYPE_F32))
+    return HMM_ERR_LAYOUT;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return HMM_ERR_CUDA;
+  RowsArgs a{d->T, d->H, d->K, d->E, d->ld, offsets, slot2row, rows, dy, d_rows, topk_weights,
+             d_topk_weights, d->weights_dtype};
+  return cuda_rc(launch_rows_combine_grad(a, d->dtype, static_cast<cudaStream_t>(stream),
+                                          ctx->overlap != 0));
+}
+
+int hmm_grouped_mm(hmm_ctx* ctx, const hmm_gmm* d, const void* x, const void* w,
+                   const int32_t* offsets, void* y, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  const int rc = check_gmm(d);
+  if (rc != HMM_OK) return rc;
+  if (d->R == 0) return HMM_OK;
+  if (!x || !w || !offsets || !y) return HMM_ERR_ARG;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned_to(offsets, HMM_DTYPE_F32))
+    return HMM_ERR_LAYOUT;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return HMM_ERR_CUDA;
+  return launch_open_rows(open_env(ctx, stream), d->dtype == HMM_DTYPE_F16, gmm_weights(*d, w),
+                          d->w_layout == HMM_W_KN, x, d->ld_x, d->R, d->K, d->N, d->E, offsets, y);
+}
+
+int hmm_grouped_mm_dx(hmm_ctx* ctx, const hmm_gmm* d, const void* dy, const void* w,
+                      const int32_t* offsets, void* dx, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  const int rc = check_gmm(d);
+  if (rc != HMM_OK) return rc;
+  if (d->R == 0) return HMM_OK;
+  if (!dy || !w || !offsets || !dx) return HMM_ERR_ARG;
+  if (!aligned16(dy) || !aligned16(w) || !aligned16(dx) || !aligned_to(offsets, HMM_DTYPE_F32))
+    return HMM_ERR_LAYOUT;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return HMM_ERR_CUDA;
+  return launch_open_rows(open_env(ctx, stream), d->dtype == HMM_DTYPE_F16, gmm_weights(*d, w),
+                          d->w_layout == HMM_W_NK, dy, d->ld_dy, d->R, d->N, d->K, d->E, offsets,
+                          dx);
+}
+
+int hmm_grouped_mm_dw(hmm_ctx* ctx, const hmm_gmm* d, const void* x, const void* dy,
+                      const int32_t* offsets, void* dw, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  const int rc = check_gmm(d);
+  if (rc != HMM_OK) return rc;
+  if (!dw) return HMM_ERR_ARG;
+  if (!aligned16(dw)) return HMM_ERR_LAYOUT;
+  if (d->R > 0) {
+    if (!x || !dy || !offsets) return HMM_ERR_ARG;
+    if (!aligned16(x) || !aligned16(dy) || !aligned_to(offsets, HMM_DTYPE_F32))
+      return HMM_ERR_LAYOUT;
+  }
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return HMM_ERR_CUDA;
+  if (d->R == 0)
+    return cuda_rc(cudaMemsetAsync(dw, 0, static_cast<size_t>(d->E) * d->K * d->N * 2,
+                                   static_cast<cudaStream_t>(stream)));
+  const bool f16 = d->dtype == HMM_DTYPE_F16;
+  if (d->w_layout == HMM_W_KN)
+    return launch_open_depth(open_env(ctx, stream), f16, x, d->ld_x, d->K, dy, d->ld_dy, d->N,
+                             d->R, d->E, offsets, dw);
+  return launch_open_depth(open_env(ctx, stream), f16, dy, d->ld_dy, d->N, x, d->ld_x, d->K, d->R,
+                           d->E, offsets, dw);
+}
+
+int hmm_orthogonalize_workspace_size(const hmm_ortho* desc, size_t* workspace_bytes) {
+  const int rc = check_ortho(desc);
+  if (rc != HMM_OK) return rc;
+  if (workspace_bytes) *workspace_bytes = ortho_plan(*desc).bytes;
+  return HMM_OK;
+}
+
+int hmm_orthogonalize(hmm_ctx* ctx, const hmm_ortho* d, const void* g, void* out, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  if (!ctx) return HMM_ERR_ARG;
+  const int rc = check_ortho(d);
+  if (rc != HMM_OK) return rc;
+  if (d->batch == 0) return HMM_OK;
+  if (!g || !out || !workspace) return HMM_ERR_ARG;
+  if (!aligned_to(g, d->dtype) || !aligned_to(out, d->out_dtype) || !aligned16(workspace))
+    return HMM_ERR_LAYOUT;
+  const OrthoPlan p = ortho_plan(*d);
+  if (workspace_bytes < p.bytes) return HMM_ERR_CAPACITY;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return HMM_ERR_CUDA;
+  return launch_ortho(open_env(ctx, stream), *d, p, g, out, static_cast<uint8_t*>(workspace));
 }
 
 int hmm_status(hmm_ctx* ctx, void* stream, int* device_error) {

@@ -192,6 +192,37 @@ struct FfnMx4Plan {
 };
 FfnMx4Plan ffn_mx4_plan(const Plan& p);
 
+// The open expert layer (rows.cu): arguments of one call.
+struct RowsArgs {
+  int64_t T, H, K, E;
+  int64_t ld;               // of x or dy
+  const int32_t* offsets;   // [E + 1]
+  const int32_t* slot2row;  // [T, K]
+  const void *src, *src2;   // what is read (combine_grad: rows, dy)
+  void* dst;
+  const void* w;            // routing weights (null: 1)
+  void* dw;
+  int w_dtype;
+};
+int check_rows(const hmm_rows* d);
+cudaError_t launch_rows_dispatch(const RowsArgs& a, int dtype, cudaStream_t st, bool pdl);
+cudaError_t launch_rows_sum(const RowsArgs& a, int dtype, cudaStream_t st, bool pdl);
+cudaError_t launch_rows_combine_grad(const RowsArgs& a, int dtype, cudaStream_t st, bool pdl);
+
+// The orthogonalised update (ortho.cu): workspace
+//   [sums of squares | X hi, lo | next X hi, lo | A | B]
+struct OrthoPlan {
+  int64_t m, ld_x, ld_a;  // smaller side; padded rows of X and of A, B
+  int pieces;             // blocks per matrix of the norm and the first conversion
+  int64_t rows_per_piece;
+  size_t off_x[4], off_a, off_b, bytes;
+};
+struct GemmEnv;
+int check_ortho(const hmm_ortho* d);
+OrthoPlan ortho_plan(const hmm_ortho& d);
+int launch_ortho(const GemmEnv& env, const hmm_ortho& d, const OrthoPlan& p, const void* g,
+                 void* out, uint8_t* ws);
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,

@@ -1,0 +1,304 @@
+// rows.cu -- rows into expert order and back, with their gradients, for expert
+// layers that are put together from single operators.
+//
+//   dispatch        rows[slot2row[t, k]] = x[t]
+//   dispatch_grad   dx[t] = sum_k d_rows[slot2row[t, k]]
+//   combine         y[t] = sum_k w[t, k] rows[slot2row[t, k]]
+//   combine_grad    d_rows[slot2row[t, k]] = w[t, k] dy[t];  d_w[t, k] = <rows[..], dy[t]>
+//
+// The rows are dense and in expert order without padding (move.cu has the padded
+// form that moe_ffn keeps).  All four move memory and compute next to nothing, so
+// each reads what it reads once from HBM: the dispatch loads a piece of a token's
+// row and writes it K times, the merges load K pieces and add them in registers
+// (fp32, in the order of k, one rounding; no atomics), the combine's gradient takes
+// a slot per warp (or block), so that dy comes from L2 for all but one of the K
+// slots of a token.  Slots of invalid ids (row -1) are left out of sums and have
+// d_w = 0; the rows behind offsets[E], which no slot has, are written as zeros.
+// A row index outside [0, T K) is treated as -1.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "hmm_internal.h"
+
+namespace hmm {
+
+namespace {
+
+constexpr int ROW_THREADS = 256;
+constexpr int ROW_WARPS = ROW_THREADS / 32;
+// warps from which a lane takes four vectors instead of one (fewer warps than
+// this leave SMs without loads in flight)
+constexpr int64_t ROW_WIDE_WARPS = 152 * 16;
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+  static __device__ float get(float v) { return v; }
+  static __device__ float put(float v) { return v; }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static __device__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<__half> {
+  static __device__ float get(__half v) { return __half2float(v); }
+  static __device__ __half put(float v) { return __float2half_rn(v); }
+};
+
+// V elements: 16 bytes, or one where rows are not aligned to that.
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T v[V];
+};
+
+__device__ __forceinline__ float row_weight(const void* w, int64_t i, int dtype) {
+  return dtype == HMM_DTYPE_F32 ? static_cast<const float*>(w)[i]
+                                : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
+}
+
+// Row of slot t*K + lane (lane < K), -1 for none.
+__device__ __forceinline__ int slot_row(const RowsArgs& a, int64_t t, int lane) {
+  int r = -1;
+  if (lane < a.K) r = a.slot2row[t * a.K + lane];
+  return r >= 0 && r < a.T * a.K ? r : -1;
+}
+
+// The rows behind the last expert's.
+template <typename T, int V>
+__device__ void zero_tail(const RowsArgs& a, T* rows, int64_t warp, int64_t nwarps, int lane) {
+  const int64_t R = a.T * a.K;
+  const int64_t last = min(max(static_cast<int64_t>(a.offsets[a.E]), int64_t(0)), R);
+  Vec<T, V> z;
+#pragma unroll
+  for (int i = 0; i < V; ++i) z.v[i] = Elem<T>::put(0.f);
+  for (int64_t r = last + warp; r < R; r += nwarps)
+    for (int64_t c = lane; c < a.H / V; c += 32)
+      *reinterpret_cast<Vec<T, V>*>(rows + r * a.H + c * V) = z;
+}
+
+// A warp: one piece of 32 U vectors of a token's row.
+template <typename T, int V, int U>
+__global__ void __launch_bounds__(ROW_THREADS) rows_dispatch_kernel(const RowsArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + (threadIdx.x >> 5);
+  const int64_t hv = a.H / V, pieces = (hv + 32 * U - 1) / (32 * U);
+  const T* x = static_cast<const T*>(a.src);
+  T* rows = static_cast<T*>(a.dst);
+  if (warp < a.T * pieces) {
+    const int64_t t = warp / pieces, c0 = (warp - t * pieces) * (32 * U) + lane;
+    const int mine = slot_row(a, t, lane);
+    Vec<T, V> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + 32 * u < hv)
+        v[u] = *reinterpret_cast<const Vec<T, V>*>(x + t * a.ld + (c0 + 32 * u) * V);
+    for (int k = 0; k < a.K; ++k) {
+      const int64_t r = __shfl_sync(0xffffffffu, mine, k);
+      if (r < 0) continue;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + 32 * u < hv)
+          *reinterpret_cast<Vec<T, V>*>(rows + r * a.H + (c0 + 32 * u) * V) = v[u];
+    }
+  }
+  zero_tail<T, V>(a, rows, warp, static_cast<int64_t>(gridDim.x) * ROW_WARPS, lane);
+}
+
+// The same pieces summed over the slots of a token (w null: weights 1).
+template <typename T, int V, int U>
+__global__ void __launch_bounds__(ROW_THREADS) rows_sum_kernel(const RowsArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + (threadIdx.x >> 5);
+  const int64_t hv = a.H / V, pieces = (hv + 32 * U - 1) / (32 * U);
+  if (warp >= a.T * pieces) return;
+  const T* rows = static_cast<const T*>(a.src);
+  T* y = static_cast<T*>(a.dst);
+  const int64_t t = warp / pieces, c0 = (warp - t * pieces) * (32 * U) + lane;
+  const int mine = slot_row(a, t, lane);
+  float w_mine = 1.f;
+  if (a.w && lane < a.K) w_mine = row_weight(a.w, t * a.K + lane, a.w_dtype);
+  float acc[U][V];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
+#pragma unroll 2
+  for (int k = 0; k < a.K; ++k) {
+    const int64_t r = __shfl_sync(0xffffffffu, mine, k);
+    const float w = __shfl_sync(0xffffffffu, w_mine, k);
+    if (r < 0) continue;
+    Vec<T, V> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + 32 * u < hv)
+        v[u] = *reinterpret_cast<const Vec<T, V>*>(rows + r * a.H + (c0 + 32 * u) * V);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + 32 * u < hv) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[u][i] = fmaf(w, Elem<T>::get(v[u].v[i]), acc[u][i]);
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (c0 + 32 * u >= hv) continue;
+    Vec<T, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.v[i] = Elem<T>::put(acc[u][i]);
+    *reinterpret_cast<Vec<T, V>*>(y + t * a.H + (c0 + 32 * u) * V) = o;
+  }
+}
+
+// A slot per warp, or per block (WPS warps) where there are few slots.
+template <typename T, int V, int WPS>
+__global__ void __launch_bounds__(ROW_THREADS) rows_combine_grad_kernel(const RowsArgs a) {
+  __shared__ float part[ROW_WARPS];
+  grid_dep_wait();
+  grid_dep_launch();
+  constexpr int U = 4;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + wid;
+  const int64_t s = warp / WPS, hv = a.H / V;
+  const T* rows = static_cast<const T*>(a.src);
+  const T* dy = static_cast<const T*>(a.src2);
+  T* d_rows = static_cast<T*>(a.dst);
+  const bool in = s < a.T * a.K;
+  float dot = 0.f;
+  int r = -1;
+  if (in) {
+    r = a.slot2row[s];
+    if (r >= a.T * a.K) r = -1;
+  }
+  if (r >= 0) {
+    const int64_t t = s / a.K;
+    const float w = row_weight(a.w, s, a.w_dtype);
+    const T* row = rows + static_cast<int64_t>(r) * a.H;
+    T* out = d_rows + static_cast<int64_t>(r) * a.H;
+    const int64_t first = WPS == 1 ? 0 : wid * 32;
+    for (int64_t c = first + lane; c < hv; c += 32 * WPS * U) {
+      Vec<T, V> g[U], v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t cu = c + 32 * WPS * u;
+        if (cu < hv) {
+          g[u] = *reinterpret_cast<const Vec<T, V>*>(dy + t * a.ld + cu * V);
+          if (a.dw) v[u] = *reinterpret_cast<const Vec<T, V>*>(row + cu * V);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t cu = c + 32 * WPS * u;
+        if (cu < hv) {
+          if (a.dw) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              dot = fmaf(Elem<T>::get(v[u].v[i]), Elem<T>::get(g[u].v[i]), dot);
+          }
+          if (d_rows) {
+            Vec<T, V> o;
+#pragma unroll
+            for (int i = 0; i < V; ++i) o.v[i] = Elem<T>::put(w * Elem<T>::get(g[u].v[i]));
+            *reinterpret_cast<Vec<T, V>*>(out + cu * V) = o;
+          }
+        }
+      }
+    }
+  }
+  if (a.dw) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+    if constexpr (WPS > 1) {
+      if (lane == 0) part[wid] = dot;
+      __syncthreads();
+      dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < WPS; ++i) dot += part[i];
+    }
+    if (in && lane == 0 && (WPS == 1 || wid == 0)) {
+      if (a.w_dtype == HMM_DTYPE_F32)
+        static_cast<float*>(a.dw)[s] = dot;
+      else
+        static_cast<__nv_bfloat16*>(a.dw)[s] = __float2bfloat16_rn(dot);
+    }
+  }
+  if (d_rows)
+    zero_tail<T, V>(a, d_rows, warp, static_cast<int64_t>(gridDim.x) * ROW_WARPS, lane);
+}
+
+enum RowsOp { ROWS_DISPATCH, ROWS_SUM, ROWS_COMBINE_GRAD };
+
+template <typename T, int V>
+cudaError_t launch_rows_v(RowsOp op, const RowsArgs& a, cudaStream_t st, bool pdl) {
+  const int64_t hv = a.H / V;
+  const auto blocks = [](int64_t warps) {
+    return static_cast<unsigned>((warps + ROW_WARPS - 1) / ROW_WARPS);
+  };
+  if (op == ROWS_COMBINE_GRAD) {
+    const int64_t slots = a.T * a.K;
+    if (slots < ROW_WIDE_WARPS)
+      return launch_kernel(rows_combine_grad_kernel<T, V, ROW_WARPS>, blocks(slots * ROW_WARPS),
+                           ROW_THREADS, 0, st, pdl, 1, a);
+    return launch_kernel(rows_combine_grad_kernel<T, V, 1>, blocks(slots), ROW_THREADS, 0, st, pdl,
+                         1, a);
+  }
+  const int64_t wide = a.T * ((hv + 127) / 128), narrow = a.T * ((hv + 31) / 32);
+  const bool u4 = wide >= ROW_WIDE_WARPS;
+  auto kern = op == ROWS_DISPATCH
+                  ? (u4 ? rows_dispatch_kernel<T, V, 4> : rows_dispatch_kernel<T, V, 1>)
+                  : (u4 ? rows_sum_kernel<T, V, 4> : rows_sum_kernel<T, V, 1>);
+  return launch_kernel(kern, blocks(u4 ? wide : narrow), ROW_THREADS, 0, st, pdl, 1, a);
+}
+
+template <typename T>
+cudaError_t launch_rows_t(RowsOp op, const RowsArgs& a, cudaStream_t st, bool pdl) {
+  constexpr int V = 16 / sizeof(T);
+  uintptr_t bits = static_cast<uintptr_t>(a.H | a.ld) * sizeof(T);
+  for (const void* p : {a.src, a.src2, static_cast<const void*>(a.dst)})
+    bits |= reinterpret_cast<uintptr_t>(p);
+  return (bits & 15u) == 0 ? launch_rows_v<T, V>(op, a, st, pdl)
+                           : launch_rows_v<T, 1>(op, a, st, pdl);
+}
+
+cudaError_t launch_rows(RowsOp op, const RowsArgs& a, int dtype, cudaStream_t st, bool pdl) {
+  if (dtype == HMM_DTYPE_F32) return launch_rows_t<float>(op, a, st, pdl);
+  if (dtype == HMM_DTYPE_F16) return launch_rows_t<__half>(op, a, st, pdl);
+  return launch_rows_t<__nv_bfloat16>(op, a, st, pdl);
+}
+
+}  // namespace
+
+int check_rows(const hmm_rows* d) {
+  if (!d) return HMM_ERR_ARG;
+  for (int dt : {d->dtype, d->weights_dtype})
+    if (dt != HMM_DTYPE_BF16 && dt != HMM_DTYPE_F32 && dt != HMM_DTYPE_F16) return HMM_ERR_DTYPE;
+  if (d->weights_dtype == HMM_DTYPE_F16) return HMM_ERR_DTYPE;
+  if (d->T < 0 || d->H <= 0 || d->E <= 0 || d->K <= 0) return HMM_ERR_SHAPE;
+  if (d->E > MAX_E || d->K > 32 || d->H > (1 << 20)) return HMM_ERR_SHAPE;
+  if (d->ld < d->H || d->ld > (int64_t(1) << 40)) return HMM_ERR_SHAPE;
+  // grids: a warp per 32 elements of a token, eight per slot
+  if (d->T >= (int64_t(1) << 31) / d->K) return HMM_ERR_SHAPE;
+  const int64_t warps = d->T * std::max<int64_t>((d->H + 31) / 32, d->K);
+  if (warps / ROW_WARPS >= (int64_t(1) << 31) - 1) return HMM_ERR_SHAPE;
+  return HMM_OK;
+}
+
+cudaError_t launch_rows_dispatch(const RowsArgs& a, int dtype, cudaStream_t st, bool pdl) {
+  return launch_rows(ROWS_DISPATCH, a, dtype, st, pdl);
+}
+cudaError_t launch_rows_sum(const RowsArgs& a, int dtype, cudaStream_t st, bool pdl) {
+  return launch_rows(ROWS_SUM, a, dtype, st, pdl);
+}
+cudaError_t launch_rows_combine_grad(const RowsArgs& a, int dtype, cudaStream_t st, bool pdl) {
+  return launch_rows(ROWS_COMBINE_GRAD, a, dtype, st, pdl);
+}
+
+}  // namespace hmm

@@ -86,6 +86,7 @@ extern "C" {
 /* dtype codes */
 #define HMM_DTYPE_BF16 0
 #define HMM_DTYPE_F32 1
+#define HMM_DTYPE_F16 2 /* the open expert layer and hmm_orthogonalize only */
 
 typedef struct hmm_ctx hmm_ctx;
 
@@ -451,6 +452,109 @@ int hmm_forward_mx4(hmm_ctx* ctx, const hmm_shape* shape, const void* x,
                     const void* up_codes, const void* up_scales,
                     const void* down_codes, const void* down_scales, void* y,
                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------ the open expert layer
+ * hmm_forward fuses dispatch, SwiGLU experts and combine.  The entry points below
+ * are the pieces of a layer whose experts are something else: with the routing of
+ * hmm_route, rows go to expert order (hmm_dispatch), through products grouped by
+ * expert (hmm_grouped_mm), and back (hmm_combine); each has its gradients.  The
+ * rows are dense and in the order of hmm_route: row slot2row[t*K + k] belongs to
+ * slot (t, k), rows offsets[e] .. offsets[e + 1] - 1 to expert e.
+ *
+ * hmm_rows: T tokens, K slots each, of E experts; H elements a row of `dtype`
+ * (bf16, fp16 or fp32), routing weights of weights_dtype (bf16 or fp32).  x and dy
+ * have rows ld elements apart; y, dx and all [T K, H] arrays are dense.  Sums are
+ * fp32, over k in ascending order, rounded once.  Slots without a row (slot2row -1:
+ * an id out of range) are left out, their d_w is 0, and the rows behind offsets[E]
+ * are zeros where rows are written.  Element alignment is enough (16-byte aligned
+ * rows are moved faster). */
+typedef struct hmm_rows {
+  int64_t T;              /* tokens (may be 0) */
+  int64_t H;              /* elements per row */
+  int64_t K;              /* slots per token, 1 .. 32 */
+  int64_t E;              /* experts, 1 .. 1024 */
+  int64_t ld;             /* elements from one row of x / dy to the next, >= H */
+  int32_t dtype;          /* HMM_DTYPE_* of the rows */
+  int32_t weights_dtype;  /* HMM_DTYPE_BF16 or HMM_DTYPE_F32 */
+} hmm_rows;
+
+/* rows[slot2row[t, k]] = x[t] */
+int hmm_dispatch(hmm_ctx* ctx, const hmm_rows* desc, const void* x, const int32_t* offsets,
+                 const int32_t* slot2row, void* rows, void* stream);
+/* dx[t] = sum_k d_rows[slot2row[t, k]] */
+int hmm_dispatch_grad(hmm_ctx* ctx, const hmm_rows* desc, const void* d_rows,
+                      const int32_t* slot2row, void* dx, void* stream);
+/* y[t] = sum_k topk_weights[t, k] * rows[slot2row[t, k]] */
+int hmm_combine(hmm_ctx* ctx, const hmm_rows* desc, const void* rows, const int32_t* slot2row,
+                const void* topk_weights, void* y, void* stream);
+/* d_rows[slot2row[t, k]] = topk_weights[t, k] * dy[t] and d_topk_weights[t, k] =
+ * <rows[slot2row[t, k]], dy[t]>.  Either output may be NULL (rows may be NULL
+ * without d_topk_weights). */
+int hmm_combine_grad(hmm_ctx* ctx, const hmm_rows* desc, const void* rows, const int32_t* offsets,
+                     const int32_t* slot2row, const void* topk_weights, const void* dy,
+                     void* d_rows, void* d_topk_weights, void* stream);
+
+/* Matrix products grouped by expert over R rows, with offsets int32 [E + 1] on the
+ * device (not decreasing; the rows of one expert may be none or all):
+ *   hmm_grouped_mm     y[r] = x[r] . w[e]        for offsets[e] <= r < offsets[e + 1]
+ *   hmm_grouped_mm_dx  dx[r] = dy[r] . w[e]^T
+ *   hmm_grouped_mm_dw  dw[e] = x_e^T . dy_e      (zeros for an expert without rows)
+ * Rows of no expert (in front of offsets[0], behind offsets[E]) are zeros in y and
+ * dx and take no part in dw.  Operands and results are bf16 or fp16 (one type);
+ * products accumulate in fp32 and are rounded once.
+ *   w, dw   HMM_W_KN [E, K, N]; HMM_W_NK the transposed storage [E, N, K]
+ *   x, dy   rows ld_x / ld_dy elements apart; y, dx, dw dense
+ * K, N and every stride are multiples of 8, all pointers 16-byte aligned.  Offsets
+ * out of [0, R] count as the nearest one inside; with decreasing offsets results
+ * are unspecified (no access leaves the arrays). */
+#define HMM_W_KN 0
+#define HMM_W_NK 1
+
+typedef struct hmm_gmm {
+  int64_t R;              /* rows (may be 0), below 2^31 - 1024 */
+  int64_t K, N;           /* multiples of 8, at most 2^20 */
+  int64_t E;              /* experts, 1 .. 1024 */
+  int64_t ld_x, ld_dy;    /* multiples of 8, >= K / >= N */
+  int64_t ld_w, stride_w; /* elements between rows of w, between experts (w, not dw) */
+  int32_t dtype;          /* HMM_DTYPE_BF16 or HMM_DTYPE_F16 */
+  int32_t w_layout;       /* HMM_W_KN or HMM_W_NK */
+} hmm_gmm;
+
+int hmm_grouped_mm(hmm_ctx* ctx, const hmm_gmm* desc, const void* x, const void* w,
+                   const int32_t* offsets, void* y, void* stream);
+int hmm_grouped_mm_dx(hmm_ctx* ctx, const hmm_gmm* desc, const void* dy, const void* w,
+                      const int32_t* offsets, void* dx, void* stream);
+int hmm_grouped_mm_dw(hmm_ctx* ctx, const hmm_gmm* desc, const void* x, const void* dy,
+                      const int32_t* offsets, void* dw, void* stream);
+
+/* Orthogonalised update of a stack of matrices by Newton-Schulz products (the Muon
+ * optimiser's step), each matrix G [M, N] by itself:
+ *   X = G / (|G|_F + eps)
+ *   `steps` times, with the step's (a, b, c):  A = X X^T, X <- a X + (b A + c A A) X
+ *   out = scale * X
+ * (for M > N by A = X^T X on the other side: the same values).  Rows of G lie ld,
+ * matrices `stride` elements apart; out is dense [batch, M, N], bf16 or fp16.
+ * Products take fp16 operands and sum in fp32, X is held in 22 bits between them.
+ * The norm is safe from overflow; a matrix of zeros gives zeros; an infinity or a
+ * NaN in a matrix gives NaN in it.  Coefficients that let a singular value of X
+ * grow past 2^20 are refused (HMM_ERR_ARG). */
+#define HMM_ORTHO_MAX_STEPS 32
+
+typedef struct hmm_ortho {
+  int64_t batch;              /* matrices, 0 .. 65535 */
+  int64_t M, N;               /* 1 .. 2^17 */
+  int64_t ld, stride;         /* of G, in elements */
+  int32_t dtype;              /* of G: HMM_DTYPE_BF16, _F16 or _F32 */
+  int32_t out_dtype;          /* HMM_DTYPE_BF16 or HMM_DTYPE_F16 */
+  int32_t steps;              /* 1 .. HMM_ORTHO_MAX_STEPS */
+  float eps;                  /* finite, >= 0 */
+  float scale;                /* finite */
+  const float* coefficients;  /* host memory, [steps][3], read during the call */
+} hmm_ortho;
+
+int hmm_orthogonalize_workspace_size(const hmm_ortho* desc, size_t* workspace_bytes);
+int hmm_orthogonalize(hmm_ctx* ctx, const hmm_ortho* desc, const void* g, void* out,
+                      void* workspace, size_t workspace_bytes, void* stream);
 
 /* Read and clear the device status word in `stream` order, then wait for
  * `stream` (only that stream: other streams of the device keep running).
