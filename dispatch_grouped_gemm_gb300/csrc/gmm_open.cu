@@ -18,8 +18,7 @@
 //
 // Rows of one expert start anywhere, and a block of them may end inside a box.
 // ROWS loads whole boxes: rows of the next expert fill columns of the accumulator
-// that are not stored; a chunk of results that the expert's last row cuts is
-// written by ordinary stores, the others by TMA.  In DEPTH the extra rows of an
+// that are not stored.  In DEPTH the extra rows of an
 // expert's last box would be summed: the MMAs of whole 16-row steps behind the end
 // are left out, and a warp of each CTA sets the rest of the last step to zero in
 // shared memory, in both operands (the rows may hold infinities), before the MMA
@@ -28,8 +27,9 @@
 // Two CTAs of a cluster compute a 256 x (up to 256) tile with 2-SM MMAs: each
 // loads its 128 rows of A and half of B's rows and accumulates its 128 rows over
 // all columns.  Warp 0 issues TMA (both CTAs, one thread), warp 1 the MMAs (even
-// CTA), the others drain TMEM (both CTAs) while the next tile accumulates in the
-// other half of it.  Every role walks the same static list of tiles: pair c of C
+// CTA), eight others drain TMEM (both CTAs) while the next tile accumulates in the
+// other half of it: in chunks of 32 x 32 results that a warp turns in 2 KB of
+// shared memory and stores as rows of 64 bytes.  Every role walks the same static list of tiles: pair c of C
 // takes tiles c, 2C - 1 - c, 2C + c, ... (back and forth, so that a list sorted by
 // cost, as DEPTH's experts are by rows, loads the pairs evenly).  Every wait is
 // bounded.
@@ -49,25 +49,24 @@ constexpr int OK_ = 64;                  // k per stage: one 128-byte swizzle ro
 constexpr int OA_BYTES = 128 * OK_ * 2;  // this CTA's 128 rows of A
 constexpr int OB_BYTES = 128 * OK_ * 2;  // this CTA's half of B's rows, at most 128
 constexpr int OSTAGE = OA_BYTES + OB_BYTES;
-constexpr int OBUF = 2048;             // staging of one 32 x 32 chunk of 16-bit results
+constexpr int OBUF = 2048;             // a warp's staging of one 32 x 32 chunk of 16-bit results
 constexpr uint32_t O_TMEM_COLS = 512;  // two accumulators of 256 columns
 constexpr int O_SORT_MAX_E = 512;      // experts that DEPTH sorts by rows (E^2 / threads compares)
-constexpr int O_LIST_BYTES = 4 * (MAX_E + 4);
+constexpr int O_CUT_AHEAD = 3;         // blocks that a block to be cut is loaded early
+constexpr int O_LIST_BYTES = 2 * 4 * (MAX_E + 4);
 
 template <int KIND>
 struct Cfg {
-  // ROWS streams weights for few rows: all the stages that fit.  The others have
-  // long epilogues (two results, or a mirrored one): eight warps for them.
-  static constexpr int STAGES = KIND == OPEN_ROWS ? 6 : 5;
-  static constexpr int EPI_WARPS = KIND == OPEN_ROWS ? 4 : 8;
+  static constexpr int STAGES = 6;
+  static constexpr int EPI_WARPS = 8;
   // DEPTH: one more warp, for the ends of the experts
   static constexpr int THREADS = 32 * (2 + EPI_WARPS + (KIND == OPEN_DEPTH ? 1 : 0));
-  static constexpr int SMEM = 1024 + STAGES * OSTAGE + EPI_WARPS * 2 * OBUF + 1024 + O_LIST_BYTES;
+  static constexpr int SMEM = 1024 + STAGES * OSTAGE + EPI_WARPS * OBUF + 1024 + O_LIST_BYTES;
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
 struct OpenMaps {
-  CUtensorMap a, b, out, out2;
+  CUtensorMap a, b;
   CUtensorMap brows[8];  // ROWS: x in boxes of 16, 32 .. 128 rows
 };
 
@@ -85,83 +84,102 @@ __device__ __forceinline__ int64_t open_index(int64_t i) {
   return i * C + ((i & 1) ? C - 1 - c : c);
 }
 
-// offsets clamped into [0, R]: whatever the caller's offsets hold, every access stays inside.
-__device__ __forceinline__ int open_off(const OpenParams& P, int e) {
-  return min(max(P.offsets[e], 0), P.R);
-}
+// What the tiles are decoded from, in shared memory.
+struct OpenList {
+  int* at;    // rows of the experts: [Z + 1] offsets clamped into [0, R], so that
+              // whatever the caller's offsets hold, every access stays inside
+  int* list;  // ROWS: blocks of the experts before e (Z + 1 entries); DEPTH: experts
+              // by rows, descending (Z up to O_SORT_MAX_E)
+};
 
 __device__ __forceinline__ int open_blocks(int rows) { return (rows + 255) >> 8; }
 
-// list: ROWS: blocks of the experts before e (E + 1 entries); DEPTH: experts by
-// rows, descending.  All threads of the CTA; ends with a barrier.
+__device__ __forceinline__ int open_rows_of(const OpenList& l, int e) {
+  return max(0, l.at[e + 1] - l.at[e]);
+}
+
+// All threads of the CTA; ends with a barrier.
 template <int KIND>
-__device__ void open_list(const OpenParams& P, int* list) {
+__device__ void open_list(const OpenParams& P, const OpenList& l) {
+  if constexpr (KIND == OPEN_STACK) return;
+  for (int e = threadIdx.x; e <= P.Z; e += blockDim.x)
+    l.at[e] = min(max(P.offsets[e], 0), P.R);
+  __syncthreads();
   if constexpr (KIND == OPEN_ROWS) {
     if (threadIdx.x < 32) {
       const int lane = threadIdx.x;
       int carry = 0;
-      if (lane == 0) list[0] = 0;
+      if (lane == 0) l.list[0] = 0;
       for (int base = 0; base < P.Z; base += 32) {
         const int e = base + lane;
-        int v = e < P.Z ? open_blocks(max(0, open_off(P, e + 1) - open_off(P, e))) : 0;
+        int v = e < P.Z ? open_blocks(open_rows_of(l, e)) : 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int n = __shfl_up_sync(0xffffffffu, v, d);
           if (lane >= d) v += n;
         }
-        if (e < P.Z) list[e + 1] = carry + v;
+        if (e < P.Z) l.list[e + 1] = carry + v;
         carry += __shfl_sync(0xffffffffu, v, 31);
       }
     }
-  } else if constexpr (KIND == OPEN_DEPTH) {
-    if (P.Z > O_SORT_MAX_E) {
-      for (int e = threadIdx.x; e < P.Z; e += blockDim.x) list[e] = e;
-    } else {
-      int* rows = list + O_SORT_MAX_E;
-      for (int e = threadIdx.x; e < P.Z; e += blockDim.x)
-        rows[e] = max(0, open_off(P, e + 1) - open_off(P, e));
-      __syncthreads();
-      for (int e = threadIdx.x; e < P.Z; e += blockDim.x) {
-        const int re = rows[e];
-        int rank = 0;
-        for (int f = 0; f < P.Z; ++f) rank += (rows[f] > re || (rows[f] == re && f < e)) ? 1 : 0;
-        list[rank] = e;
+  } else if (P.Z <= O_SORT_MAX_E) {
+    for (int e = threadIdx.x; e < P.Z; e += blockDim.x) {
+      const int re = open_rows_of(l, e);
+      int rank = 0;
+      for (int f = 0; f < P.Z; ++f) {
+        const int rf = open_rows_of(l, f);
+        rank += (rf > re || (rf == re && f < e)) ? 1 : 0;
       }
+      l.list[rank] = e;
     }
   }
   __syncthreads();
 }
 
 template <int KIND>
-__device__ __forceinline__ int64_t open_total(const OpenParams& P, const int* list) {
-  if constexpr (KIND == OPEN_ROWS) return static_cast<int64_t>(list[P.Z]) * P.mt;
+__device__ __forceinline__ int64_t open_total(const OpenParams& P, const OpenList& l) {
+  if constexpr (KIND == OPEN_ROWS) return static_cast<int64_t>(l.list[P.Z]) * P.mt;
   return static_cast<int64_t>(P.Z) * P.tiles;
 }
 
+// u / d and the rest (u beyond 32 bits is rare, and its division slow)
+__device__ __forceinline__ int open_div(int64_t u, int d, int& rest) {
+  int q;
+  if (u < (int64_t(1) << 32))
+    q = static_cast<int>(static_cast<uint32_t>(u) / static_cast<uint32_t>(d));
+  else
+    q = static_cast<int>(u / d);
+  rest = static_cast<int>(u - static_cast<int64_t>(q) * d);
+  return q;
+}
+
+// The pair's i-th tile; false behind the last.
 template <int KIND>
-__device__ __forceinline__ void open_tile(const OpenParams& P, const int* list, int64_t u,
-                                          OpenTile& t) {
+__device__ __forceinline__ bool open_tile(const OpenParams& P, const OpenList& l, int64_t total,
+                                          int64_t index, OpenTile& t) {
+  const int64_t u = open_index(index);
+  if (u >= total) return false;
+  int r;
   if constexpr (KIND == OPEN_ROWS) {
-    const int blk = static_cast<int>(u / P.mt);
-    t.m0 = static_cast<int>(u - static_cast<int64_t>(blk) * P.mt) * 256;
+    const int blk = open_div(u, P.mt, r);
+    t.m0 = r * 256;
     int lo = 0, hi = P.Z - 1;  // the largest e with list[e] <= blk
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (list[mid] <= blk)
+      if (l.list[mid] <= blk)
         lo = mid;
       else
         hi = mid - 1;
     }
-    const int o = open_off(P, lo), rows = open_off(P, lo + 1) - o;
-    const int nblk = open_blocks(rows), j = blk - list[lo];
+    const int o = l.at[lo], rows = open_rows_of(l, lo);
+    const int nblk = open_blocks(rows), j = blk - l.list[lo];
     t.z = lo;
     t.nb = ((rows + nblk - 1) / nblk + 15) & ~15;
     t.n0 = o + j * t.nb;
     t.nv = min(t.nb, rows - j * t.nb);
     t.kb = P.kb;
   } else {
-    const int i = static_cast<int>(u / P.tiles);
-    int r = static_cast<int>(u - static_cast<int64_t>(i) * P.tiles);
+    const int i = open_div(u, P.tiles, r);
     t.nv = t.nb = 256;
     if (P.sym) {  // tiles on and right of the diagonal, row by row
       int mi = 0;
@@ -171,26 +189,38 @@ __device__ __forceinline__ void open_tile(const OpenParams& P, const int* list, 
       }
       t.m0 = mi * 256;
       t.n0 = (mi + r) * 256;
+    } else if (P.mt <= P.nt) {  // the shorter side inside: what runs at once is near square
+      t.m0 = r % P.mt * 256;
+      t.n0 = r / P.mt * 256;
     } else {
       t.m0 = r / P.nt * 256;
       t.n0 = r % P.nt * 256;
     }
     if constexpr (KIND == OPEN_DEPTH) {
-      t.z = list[i];
-      t.k0 = open_off(P, t.z);
-      t.k1 = max(t.k0, open_off(P, t.z + 1));
+      t.z = P.Z <= O_SORT_MAX_E ? l.list[i] : i;
+      t.k0 = l.at[t.z];
+      t.k1 = max(t.k0, l.at[t.z + 1]);
       t.kb = (t.k1 - t.k0 + OK_ - 1) / OK_;
     } else {
       t.z = i;
       t.kb = P.kb;
     }
   }
+  return true;
 }
 
-// Rows of the tile's last K block (DEPTH) if it ends inside a 16-row step, else 0.
+// Rows of the tile's last K block (DEPTH) if it ends inside a 16-row step and has to
+// be cut, else 0.
 __device__ __forceinline__ int open_tail(const OpenTile& t) {
   const int v = (t.k1 - t.k0) & (OK_ - 1);
   return (v & 15) ? v : 0;
+}
+
+// Place in the order of the loads of a block to be cut: a few blocks before the end,
+// so that it is cut by the time the MMAs of the others, which go first, are issued.
+// (No more than the ring holds: the slot stays taken meanwhile.)
+__device__ __forceinline__ int open_cut_place(const OpenTile& t) {
+  return max(0, t.kb - 1 - O_CUT_AHEAD);
 }
 
 __device__ __forceinline__ uint32_t pack16(bool f16, float lo, float hi) {
@@ -201,9 +231,16 @@ __device__ __forceinline__ uint32_t pack16(bool f16, float lo, float hi) {
   return pack_bf16(lo, hi);
 }
 
-// A warp's 32 x 32 chunk (lane = m, register = n) to staging rows of n, m
-// contiguous (64 bytes a row, plain): neighbouring lanes swap halves, so that each
-// store is a pair of m and a warp's store covers two whole rows, all banks once.
+// A warp's staging buffer: 32 rows of 64 bytes, the 16-byte unit u of row r at
+// u ^ ((r >> 1) & 3), so that a row per lane, a column per lane and eight rows per
+// access all meet every bank once.
+__device__ __forceinline__ uint8_t* unit_at(uint8_t* sb, int row, int unit) {
+  return sb + row * 64 + 16 * (unit ^ ((row >> 1) & 3));
+}
+
+// A 32 x 32 chunk (lane = m, register = n) as rows of n, m contiguous: neighbouring
+// lanes swap halves, so that each store is a pair of m and a warp's store covers two
+// whole rows.
 __device__ __forceinline__ void stage_t(uint8_t* sb, int lane, bool f16, const float (&v)[32]) {
   const bool odd = lane & 1;
 #pragma unroll
@@ -212,12 +249,12 @@ __device__ __forceinline__ void stage_t(uint8_t* sb, int lane, bool f16, const f
     const float got = __shfl_xor_sync(0xffffffffu, send, 1);
     // even lane: row i, columns (lane, lane + 1); odd: row i + 1, columns (lane - 1, lane)
     const uint32_t p = odd ? pack16(f16, got, v[i + 1]) : pack16(f16, v[i], got);
-    *reinterpret_cast<uint32_t*>(sb + (i + (odd ? 1 : 0)) * 64 + (lane >> 1) * 4) = p;
+    *reinterpret_cast<uint32_t*>(unit_at(sb, i + (odd ? 1 : 0), lane >> 3) +
+                                 ((lane >> 1) & 3) * 4) = p;
   }
 }
 
-// The same chunk as rows of m, n contiguous: lane = row, its 16-byte unit u at
-// u ^ ((row >> 1) & 3) (the 64-byte swizzle of the map).
+// The same chunk as rows of m, n contiguous.
 __device__ __forceinline__ void stage_d(uint8_t* sb, int lane, bool f16, const float (&v)[32]) {
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
@@ -226,18 +263,47 @@ __device__ __forceinline__ void stage_d(uint8_t* sb, int lane, bool f16, const f
     q.y = pack16(f16, v[8 * u + 2], v[8 * u + 3]);
     q.z = pack16(f16, v[8 * u + 4], v[8 * u + 5]);
     q.w = pack16(f16, v[8 * u + 6], v[8 * u + 7]);
-    *reinterpret_cast<uint4*>(sb + lane * 64 + 16 * (u ^ ((lane >> 1) & 3))) = q;
+    *reinterpret_cast<uint4*>(unit_at(sb, lane, u)) = q;
   }
 }
 
-__device__ __forceinline__ float half_round(float v) { return __half2float(__float2half_rn(v)); }
+// Staged rows to dst (row, column of its first element; ld elements between rows),
+// those below `rows` and units of eight columns that begin below `cols`.
+__device__ __forceinline__ void emit(uint8_t* sb, int lane, uint16_t* dst, int64_t ld, int rows,
+                                     int cols) {
+  const int unit = lane & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = (lane >> 2) + 8 * j;
+    if (r < rows && unit * 8 < cols)
+      *reinterpret_cast<uint4*>(dst + r * ld + unit * 8) =
+          *reinterpret_cast<const uint4*>(unit_at(sb, r, unit));
+  }
+}
 
-// 32 consecutive fp16 values (16-byte aligned)
-__device__ __forceinline__ void load32h(const __half* p, float (&v)[32]) {
+// The reverse, in two steps: rows of 64 bytes to registers, and through the staging
+// buffer to a row per lane.
+__device__ __forceinline__ void fetch(const __half* src, int lane, int64_t ld, int rows, int cols,
+                                      uint4 (&q)[4]) {
+  const int unit = lane & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = (lane >> 2) + 8 * j;
+    q[j] = make_uint4(0, 0, 0, 0);
+    if (r < rows && unit * 8 < cols)
+      q[j] = __ldcg(reinterpret_cast<const uint4*>(src + r * ld + unit * 8));
+  }
+}
+__device__ __forceinline__ void turn(uint8_t* sb, int lane, const uint4 (&q)[4], float (&v)[32]) {
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(unit_at(sb, (lane >> 2) + 8 * j, lane & 3)) = q[j];
+  __syncwarp();
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p + 8 * u);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const uint4 t = *reinterpret_cast<const uint4*>(unit_at(sb, lane, u));
+    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
@@ -246,6 +312,8 @@ __device__ __forceinline__ void load32h(const __half* p, float (&v)[32]) {
     }
   }
 }
+
+__device__ __forceinline__ float half_round(float v) { return __half2float(__float2half_rn(v)); }
 
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 1)
@@ -257,7 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* stages = smem;
   uint8_t* obufs = smem + ST * OSTAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(obufs + C::EPI_WARPS * 2 * OBUF);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(obufs + C::EPI_WARPS * OBUF);
   uint64_t* full = bars;         // used in the even CTA: bytes of both
   uint64_t* empty = full + ST;   // both CTAs
   uint64_t* tfull = empty + ST;  // both CTAs
@@ -272,7 +340,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   uint32_t* s_issued = s_tmem + 2;
   uint32_t* s_sbytes = s_tmem + 3;   // [ST] bytes of this CTA's last load per slot
   uint32_t* s_peer = s_sbytes + ST;  // [2 + ST]
-  int* list = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 1024);
+  const OpenList list{reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 1024),
+                      reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 1024) + MAX_E + 4};
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -315,15 +384,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
     if (lane == 0) {
       // ------------------------------------------------------- TMA producer
       tma_prefetch_desc(&maps.a);
-      tma_prefetch_desc(&maps.out);
       uint32_t stage = 0, sphase = 0, issued = 0;
       uint32_t landed_phase = 0, landed_used = 0;  // a bit per slot
       bool ok = true;
-      for (int64_t i = 0; ok; ++i) {
-        const int64_t u = open_index(i);
-        if (u >= total) break;
-        OpenTile t;
-        open_tile<KIND>(P, list, u, t);
+      OpenTile t, next;
+      bool more = open_tile<KIND>(P, list, total, 0, t);
+      for (int64_t i = 1; ok && more; ++i, t = next) {
         const int ma = t.m0 + 128 * static_cast<int>(rank);
         // B: this CTA's half of the columns, in boxes of a multiple of 16 rows
         const int half = t.nb >> 1;
@@ -331,15 +397,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         const int box = (half + 15) >> 4;
         const uint32_t b_bytes = KIND == OPEN_ROWS ? box * 16 * OK_ * 2 : OB_BYTES;
         const CUtensorMap* bm = KIND == OPEN_ROWS ? &maps.brows[box - 1] : &maps.b;
-        for (int kb = 0; kb < t.kb; ++kb) {
+        const bool tail = KIND == OPEN_DEPTH && open_tail(t) != 0;
+        const int place = open_cut_place(t);
+        const int ask = min(t.kb, ST) - 1;  // the next tile is decoded with the ring filled
+        if (t.kb == 0) more = open_tile<KIND>(P, list, total, i, next);
+        for (int j = 0; j < t.kb; ++j) {
           if (!mbar_wait(&empty[stage], sphase ^ 1u, wc)) {
             ok = false;
             break;
           }
           uint8_t* sA = stages + stage * OSTAGE;
           uint8_t* sB = sA + OA_BYTES;
+          // block of the j-th load
+          const int kb = !tail || j < place ? j : (j == place ? t.kb - 1 : j - 1);
           const int k = kb * OK_;
-          if (KIND == OPEN_DEPTH && kb == t.kb - 1 && open_tail(t) != 0) {
+          if (tail && j == place) {
             // counted on this CTA's own barrier; `full` completes at once
             if (leader) mbar_arrive(&full[stage]);
             s_sbytes[stage] = 0;
@@ -374,6 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
             stage = 0;
             sphase ^= 1u;
           }
+          if (j == ask) more = open_tile<KIND>(P, list, total, i, next);
         }
       }
       // after an abort: this CTA's own copies (the others are drained at teardown)
@@ -395,49 +468,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       const uint32_t a_lbo = a_mn ? OA_BYTES / 2 : 16, b_lbo = b_mn ? OB_BYTES / 2 : 16;
       uint32_t stage = 0, sphase = 0, acc = 0, acc_phase = 0, cut_phase = 0;
       bool ok = true;
-      for (int64_t i = 0; ok; ++i) {
-        const int64_t u = open_index(i);
-        if (u >= total) break;
-        OpenTile t;
-        open_tile<KIND>(P, list, u, t);
-        if (t.kb == 0) continue;
+      OpenTile t, next;
+      bool more = open_tile<KIND>(P, list, total, 0, t);
+      // the MMAs of the block in slot `at`, the first `steps` of them
+      const auto block = [&](uint32_t at, int steps, uint32_t d_tmem, uint32_t idesc, bool first) {
+        tc_fence_after();
+        const uint32_t a_base = smem_u32(stages + at * OSTAGE);
+        const uint32_t b_base = a_base + OA_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < OK_ / 16; ++kk) {
+          if (KIND == OPEN_DEPTH && kk >= steps) break;
+          const uint64_t ad = smem_desc(a_base + kk * a_step, a_lbo, 1024, LAYOUT_SW128);
+          const uint64_t bd = smem_desc(b_base + kk * b_step, b_lbo, 1024, LAYOUT_SW128);
+          umma_bf16_pair(d_tmem, ad, bd, idesc, first && kk == 0 ? 0u : 1u);
+        }
+        umma_commit_pair(&empty[at], 0x3);
+      };
+      for (int64_t i = 1; ok && more; ++i, t = next) {
+        if (t.kb == 0) {
+          more = open_tile<KIND>(P, list, total, i, next);
+          continue;
+        }
         const uint32_t idesc = P.idesc | (static_cast<uint32_t>(t.nb >> 3) << 17);
         if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, wc)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
-        for (int kb = 0; kb < t.kb; ++kb) {
-          if (!mbar_wait(&full[stage], sphase, wc)) {
-            ok = false;
-            break;
-          }
-          int steps = OK_ / 16;
-          if (KIND == OPEN_DEPTH && kb == t.kb - 1) {
-            steps = (t.k1 - t.k0 - kb * OK_ + 15) >> 4;
-            if (open_tail(t) != 0) {
-              if (!mbar_wait<true>(&cut[stage], cut_phase >> stage & 1u, wc)) {
-                ok = false;
-                break;
-              }
-              cut_phase ^= 1u << stage;
+        const bool tail = KIND == OPEN_DEPTH && open_tail(t) != 0;
+        const int place = tail ? open_cut_place(t) : -1;
+        // steps of the tile's last block (DEPTH)
+        const int last_steps = KIND == OPEN_DEPTH ? (t.k1 - t.k0 - (t.kb - 1) * OK_ + 15) >> 4 : 4;
+        uint32_t held = 0, held_phase = 0;
+        bool first = true;
+        for (int j = 0; j < t.kb; ++j) {
+          if (j == place) {  // its MMAs go last
+            held = stage;
+            held_phase = sphase;
+          } else {
+            if (!mbar_wait(&full[stage], sphase, wc)) {
+              ok = false;
+              break;
             }
+            block(stage, !tail && j == t.kb - 1 ? last_steps : 4, d_tmem, idesc, first);
+            first = false;
           }
-          tc_fence_after();
-          const uint32_t a_base = smem_u32(stages + stage * OSTAGE);
-          const uint32_t b_base = a_base + OA_BYTES;
-#pragma unroll
-          for (int kk = 0; kk < OK_ / 16; ++kk) {
-            if (KIND == OPEN_DEPTH && kk >= steps) break;
-            const uint64_t ad = smem_desc(a_base + kk * a_step, a_lbo, 1024, LAYOUT_SW128);
-            const uint64_t bd = smem_desc(b_base + kk * b_step, b_lbo, 1024, LAYOUT_SW128);
-            umma_bf16_pair(d_tmem, ad, bd, idesc, (kb == 0 && kk == 0) ? 0u : 1u);
-          }
-          umma_commit_pair(&empty[stage], 0x3);
           if (++stage == ST) {
             stage = 0;
             sphase ^= 1u;
           }
+          if (j == 0) more = open_tile<KIND>(P, list, total, i, next);  // beside the MMAs
         }
         if (!ok) break;
+        if (tail) {
+          if (!mbar_wait(&full[held], held_phase, wc) ||
+              !mbar_wait<true>(&cut[held], cut_phase >> held & 1u, wc)) {
+            ok = false;
+            break;
+          }
+          cut_phase ^= 1u << held;
+          block(held, last_steps, d_tmem, idesc, first);
+        }
         umma_commit_pair(&tfull[acc], 0x3);
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
@@ -451,13 +540,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
     // this CTA: a row is 128 bytes in each of the four 64-wide chunks, swizzled
     // inside itself.
     uint32_t slot = 0, landed_phase = 0;
-    for (int64_t i = 0;; ++i) {
-      const int64_t u = open_index(i);
-      if (u >= total) break;
-      OpenTile t;
-      open_tile<KIND>(P, list, u, t);
+    OpenTile t;
+    for (int64_t i = 0; open_tile<KIND>(P, list, total, i, t); ++i) {
       if (t.kb == 0) continue;
-      const uint32_t last = (slot + t.kb - 1) % ST;
+      const uint32_t last = (slot + open_cut_place(t)) % ST;
       slot = (slot + t.kb) % ST;
       const int v = open_tail(t);
       if (v == 0) continue;
@@ -479,32 +565,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   } else {
     // ------------------------------------------------------------- epilogue
     const int q4 = warp & 3;
-    // chunks of 32 columns: all of them, or every other one of the warp's lane quarter
+    // every other chunk of 32 columns of the warp's lane quarter
     constexpr int SHARE = C::EPI_WARPS / 4;
-    const int first = SHARE == 1 ? 0 : (warp - 2) >> 2;
-    uint8_t* obuf = obufs + (warp - 2) * 2 * OBUF;
+    const int first = (warp - 2) >> 2;
+    uint8_t* sb = obufs + (warp - 2) * OBUF;
     const bool f16 = P.out_f16 != 0;
-    uint32_t ck = 0;  // buffers this warp has stored from
+    uint16_t* out = static_cast<uint16_t*>(P.out);
     uint32_t acc = 0, acc_phase = 0;
     const uint32_t tempty_cl[2] = {mapa_shared(smem_u32(&tempty[0]), 0),
                                    mapa_shared(smem_u32(&tempty[1]), 0)};
-    // the next staging buffer, its earlier store read out
-    const auto take_buf = [&]() {
-      if (lane == 0) bulk_wait_group_read<1>();
+    // staged results (after stage_d / stage_t of every lane) to memory
+    const auto put_d = [&](bool half16, const float (&v)[32], uint16_t* dst, int64_t ld, int rows,
+                           int cols) {
       __syncwarp();
-      return obuf + (ck++ & 1u) * OBUF;
+      stage_d(sb, lane, half16, v);
+      __syncwarp();
+      emit(sb, lane, dst, ld, rows, cols);
     };
-    const auto send = [&](const CUtensorMap* m, const uint8_t* sb, int c0, int c1, int c2) {
-      fence_proxy_async_smem();
+    const auto put_t = [&](bool half16, const float (&v)[32], uint16_t* dst, int64_t ld, int rows,
+                           int cols) {
       __syncwarp();
-      if (lane == 0) {
-        tma_store_3d(m, sb, c0, c1, c2);
-        bulk_commit_group();
-      }
+      stage_t(sb, lane, half16, v);
+      __syncwarp();
+      emit(sb, lane, dst, ld, rows, cols);
     };
     if constexpr (KIND == OPEN_ROWS) {
       // rows of no expert (in front of the first, behind the last) are zero
-      const int r0 = open_off(P, 0), r1 = max(r0, open_off(P, P.Z));
+      const int r0 = list.at[0], r1 = max(r0, list.at[P.Z]);
       const int64_t per = P.M / 8, n = (static_cast<int64_t>(r0) + P.R - r1) * per;
       const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * C::EPI_WARPS);
       for (int64_t i = static_cast<int64_t>(blockIdx.x) * (32 * C::EPI_WARPS) +
@@ -513,140 +600,99 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         int64_t r = i / per;
         const int64_t c = i - r * per;
         if (r >= r0) r += r1 - r0;
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + r * P.M + c * 8) =
-            make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(out + r * P.M + c * 8) = make_uint4(0, 0, 0, 0);
       }
     }
-    for (int64_t i = 0;; ++i) {
-      const int64_t u = open_index(i);
-      if (u >= total) break;
-      OpenTile t;
-      open_tile<KIND>(P, list, u, t);
+    OpenTile t;
+    for (int64_t i = 0; open_tile<KIND>(P, list, total, i, t); ++i) {
       const int mw = t.m0 + 128 * static_cast<int>(rank) + q4 * 32;  // this warp's rows of m
+      const int mrows = P.M - mw;                                    // ... those that exist
+      // chunks that hold results
+      const int nch = mrows <= 0 ? 0
+                      : KIND == OPEN_ROWS
+                          ? (t.nv + 31) >> 5
+                          : min(8, (P.N - t.n0 + 31) >> 5);
       if constexpr (KIND == OPEN_DEPTH) {
         if (t.kb == 0) {  // an expert with no rows: zeros
-          float z[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = 0.f;
-          if (mw < P.M)
-            for (int c = first; c < 8 && t.n0 + 32 * c < P.N; c += SHARE) {
-              uint8_t* sb = take_buf();
-              stage_d(sb, lane, f16, z);
-              send(&maps.out, sb, t.n0 + 32 * c, mw, t.z);
-            }
+          uint16_t* dst = out + (static_cast<int64_t>(t.z) * P.M + mw) * P.N + t.n0;
+          for (int j = lane; j < 32 * 32; j += 32) {
+            const int row = j >> 5, col = (j & 31) * 8;
+            if (row < mrows && t.n0 + col < P.N && (col >> 7) == first)
+              *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(row) * P.N + col) =
+                  make_uint4(0, 0, 0, 0);
+          }
           continue;
         }
       }
+      // STACK: what a chunk adds, loaded a chunk ahead
+      uint4 qh[4], ql[4];
+      const int64_t in_at = (static_cast<int64_t>(t.z) * P.M + mw) * P.ld_in + t.n0;
+      const auto fetch_in = [&](int c) {
+        const int cols = static_cast<int>(P.ld_in) - t.n0 - 32 * c;  // (rows are padded to 8)
+        fetch(P.in_hi + in_at + 32 * c, lane, P.ld_in, mrows, cols, qh);
+        if (P.epi != OPEN_EPI_POLY) fetch(P.in_lo + in_at + 32 * c, lane, P.ld_in, mrows, cols, ql);
+      };
+      const bool adds = KIND == OPEN_STACK && P.epi != OPEN_EPI_GRAM;
+      if (adds && first < nch) fetch_in(first);
       bool got = false;
       if (lane == 0) got = mbar_wait(&tfull[acc], acc_phase, wc);
       __syncwarp();
       if (!__shfl_sync(0xffffffffu, got, 0)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q4 * 32) << 16) + acc * 256;
-      // chunks that hold results
-      const int nch = mw >= P.M ? 0
-                      : KIND == OPEN_ROWS
-                          ? (t.nv + 31) >> 5
-                          : min(8, (P.N - t.n0 + 31) >> 5);
+      uint32_t r[32];
+      if (first < nch) tmem_ld32(taddr + first * 32, r);
       for (int c = first; c < nch; c += SHARE) {
-        uint32_t r[32];
-        tmem_ld32(taddr + c * 32, r);
         tmem_ld_wait_for(r);
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        if (c + SHARE < nch) tmem_ld32(taddr + (c + SHARE) * 32, r);  // beside this chunk's work
+        const int n = t.n0 + 32 * c;
         if constexpr (KIND == OPEN_ROWS) {
-          const int rows = min(32, t.nv - 32 * c);
-          uint8_t* sb = take_buf();
-          stage_t(sb, lane, f16, v);
-          if (rows == 32) {
-            send(&maps.out, sb, mw, t.n0 + 32 * c, 0);
-          } else {
-            // the expert's last rows: eight rows of 64 bytes at a time
-            __syncwarp();
-            const int col = mw + (lane & 3) * 8;
-            for (int j = lane >> 2; j < rows; j += 8)
-              if (col < P.M)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) +
-                                          static_cast<int64_t>(t.n0 + 32 * c + j) * P.M + col) =
-                    *reinterpret_cast<const uint4*>(sb + j * 64 + (lane & 3) * 16);
-            __syncwarp();
-          }
+          put_t(f16, v, out + static_cast<int64_t>(n) * P.M + mw, P.M, t.nv - 32 * c, mrows);
         } else if constexpr (KIND == OPEN_DEPTH) {
-          uint8_t* sb = take_buf();
-          stage_d(sb, lane, f16, v);
-          send(&maps.out, sb, t.n0 + 32 * c, mw, t.z);
+          put_d(f16, v, out + (static_cast<int64_t>(t.z) * P.M + mw) * P.N + n, P.N, mrows,
+                P.N - n);
         } else {
-          const int n = t.n0 + 32 * c, m = mw + lane;
+          const int m = mw + lane;
+          const int64_t at = in_at + 32 * c;
+          const int cols = static_cast<int>(P.ld_in) - n;
+          float h[32];
           if (P.epi == OPEN_EPI_GRAM || P.epi == OPEN_EPI_POLY) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= P.alpha;
             if (P.epi == OPEN_EPI_POLY) {
-              float s[32];
-#pragma unroll
-              for (int j = 0; j < 32; ++j) s[j] = 0.f;
-              if (m < P.M) {
-                // (rows are padded to 8 elements: what lies behind N is not stored)
-                const __half* src = P.in_hi + (static_cast<int64_t>(t.z) * P.M + m) * P.ld_in + n;
-                if (n + 32 <= P.ld_in) {
-                  load32h(src, s);
-                } else {
-#pragma unroll
-                  for (int j = 0; j < 32; ++j)
-                    if (n + j < P.ld_in) s[j] = __half2float(src[j]);
-                }
-              }
+              turn(sb, lane, qh, h);
+              if (c + SHARE < nch) fetch_in(c + SHARE);
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                v[j] = fmaf(P.beta, s[j], v[j]) + (m == n + j ? P.gamma : 0.f);
+                v[j] = fmaf(P.beta, h[j], v[j]) + (m == n + j ? P.gamma : 0.f);
             }
-            uint8_t* sb = take_buf();
-            stage_d(sb, lane, true, v);
-            send(&maps.out, sb, n, mw, t.z);
-            if (t.n0 > t.m0) {  // the mirrored chunk (the results are symmetric)
-              sb = take_buf();
-              stage_t(sb, lane, true, v);
-              send(&maps.out2, sb, mw, n, t.z);
-            }
+            put_d(true, v, out + at, P.ld_in, mrows, cols);
+            if (t.n0 > t.m0)  // the mirrored chunk (the results are symmetric)
+              put_t(true, v, out + (static_cast<int64_t>(t.z) * P.M + n) * P.ld_in + mw, P.ld_in,
+                    P.M - n, static_cast<int>(P.ld_in) - mw);
           } else {
             // X <- alpha acc + beta hi + gamma lo
-            float h[32], l[32];
+            turn(sb, lane, qh, h);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) h[j] = l[j] = 0.f;
-            if (m < P.M) {
-              const int64_t at = (static_cast<int64_t>(t.z) * P.M + m) * P.ld_in + n;
-              if (n + 32 <= P.ld_in) {
-                load32h(P.in_hi + at, h);
-                load32h(P.in_lo + at, l);
-              } else {
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(P.beta, h[j], P.alpha * v[j]);
+            turn(sb, lane, ql, h);
+            if (c + SHARE < nch) fetch_in(c + SHARE);
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (n + j < P.ld_in) {
-                    h[j] = __half2float(P.in_hi[at + j]);
-                    l[j] = __half2float(P.in_lo[at + j]);
-                  }
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              v[j] = fmaf(P.gamma, l[j], fmaf(P.beta, h[j], P.alpha * v[j]));
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(P.gamma, h[j], v[j]);
             if (P.epi == OPEN_EPI_UPDATE) {
+              put_d(true, v, out + at, P.ld_in, mrows, cols);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) l[j] = v[j] - half_round(v[j]);
-              uint8_t* sb = take_buf();
-              stage_d(sb, lane, true, v);
-              send(&maps.out, sb, n, mw, t.z);
-              sb = take_buf();
-              stage_d(sb, lane, true, l);
-              send(&maps.out2, sb, n, mw, t.z);
+              for (int j = 0; j < 32; ++j) v[j] -= half_round(v[j]);
+              put_d(true, v, static_cast<uint16_t*>(P.out_lo) + at, P.ld_in, mrows, cols);
             } else if (!P.plain_out) {
-              uint8_t* sb = take_buf();
-              stage_d(sb, lane, f16, v);
-              send(&maps.out, sb, n, mw, t.z);
-            } else if (m < P.M) {
-              // rows of the result that no tensor map can describe (N no multiple of 8)
-              uint16_t* dst =
-                  static_cast<uint16_t*>(P.out) + (static_cast<int64_t>(t.z) * P.M + m) * P.N + n;
+              put_d(f16, v, out + (static_cast<int64_t>(t.z) * P.M + mw) * P.N + n, P.N, mrows,
+                    P.N - n);
+            } else if (lane < mrows) {
+              // rows of the result that are not 16-byte aligned (N no multiple of 8)
+              uint16_t* dst = out + (static_cast<int64_t>(t.z) * P.M + m) * P.N + n;
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 if (n + j < P.N) dst[j] = static_cast<uint16_t>(pack16(f16, v[j], 0.f) & 0xFFFFu);
@@ -665,7 +711,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       acc ^= 1u;
       if (acc == 0) acc_phase ^= 1u;
     }
-    if (lane == 0) bulk_wait_group<0>();  // every store has landed
   }
 
   tc_fence_before();
@@ -678,28 +723,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
 }
 
 // ------------------------------------------------------------------ host side
-// A map of rank 3: dimensions d0 (contiguous), d1, d2 with strides in elements.
-int encode3(const GemmEnv& env, CUtensorMap* m, bool f16, const void* base, int64_t d0, int64_t d1,
-            int64_t d2, int64_t s1, int64_t s2, int b0, int b1, CUtensorMapSwizzle sw) {
-  const cuuint64_t gd[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1),
-                            static_cast<cuuint64_t>(d2)};
-  const cuuint64_t gs[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
-  const cuuint32_t bx[3] = {static_cast<cuuint32_t>(b0), static_cast<cuuint32_t>(b1), 1};
-  const cuuint32_t es[3] = {1, 1, 1};
-  const CUresult r = env.encode(
-      m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-      const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-      sw == CU_TENSOR_MAP_SWIZZLE_128B ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
-                                       : CU_TENSOR_MAP_L2_PROMOTION_NONE,
-      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? HMM_OK : HMM_ERR_CUDA;
-}
-
 // An operand [batch][rows][cols] as loaded: K-major (cols = k): boxes of 64 x
 // `box` rows; MN-major (rows = k): boxes of 64 columns x 64 rows.
 int encode_operand(const GemmEnv& env, CUtensorMap* m, bool f16, const OpenOperand& o, int box) {
-  return encode3(env, m, f16, o.ptr, o.cols, o.rows, o.batch, o.ld, o.stride, 64, box,
-                 CU_TENSOR_MAP_SWIZZLE_128B);
+  const cuuint64_t gd[3] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows),
+                            static_cast<cuuint64_t>(o.batch)};
+  const cuuint64_t gs[2] = {static_cast<cuuint64_t>(o.ld) * 2,
+                            static_cast<cuuint64_t>(o.stride) * 2};
+  const cuuint32_t bx[3] = {64, static_cast<cuuint32_t>(box), 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = env.encode(
+      m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+      const_cast<void*>(o.ptr), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? HMM_OK : HMM_ERR_CUDA;
 }
 
 template <int KIND>
@@ -749,7 +787,6 @@ int launch_open_rows(const GemmEnv& env, bool f16, const OpenOperand& w, bool w_
   int rc = encode_operand(env, &maps.a, f16, w, w_mn ? 64 : 128);
   const OpenOperand xo{x, R, K, 1, ld_x, R * ld_x};
   for (int i = 0; i < 8; ++i) rc |= encode_operand(env, &maps.brows[i], f16, xo, 16 * (i + 1));
-  rc |= encode3(env, &maps.out, f16, out, M, R, 1, M, R * M, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (rc != HMM_OK) return HMM_ERR_CUDA;
   // at most a partly filled block per expert beside the full ones
   const int64_t blocks = std::min<int64_t>(R, R / 256 + E);
@@ -776,7 +813,6 @@ int launch_open_depth(const GemmEnv& env, bool f16, const void* a, int64_t ld_a,
   P.out_f16 = f16;
   int rc = encode_operand(env, &maps.a, f16, OpenOperand{a, R, M, 1, ld_a, R * ld_a}, OK_);
   rc |= encode_operand(env, &maps.b, f16, OpenOperand{b, R, N, 1, ld_b, R * ld_b}, OK_);
-  rc |= encode3(env, &maps.out, f16, out, N, M, E, N, M * N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (rc != HMM_OK) return HMM_ERR_CUDA;
   return launch_open<OPEN_DEPTH>(env, P, maps, E * static_cast<int64_t>(P.tiles));
 }
@@ -804,27 +840,13 @@ int launch_open_stack(const GemmEnv& env, const OpenStack& s) {
   P.in_lo = static_cast<const __half*>(s.in_lo);
   P.ld_in = s.ld_in;
   P.out = s.out;
+  P.out_lo = s.out_lo;
   P.out_f16 = s.out_f16;
   int rc = encode_operand(env, &maps.a, true, s.a, s.a_mn ? 64 : 128);
   rc |= encode_operand(env, &maps.b, true, s.b, s.b_mn ? 64 : 128);
-  const int64_t Z = s.a.batch;
-  // results: rows of ld_out elements; the mirrored or low ones beside them
-  const bool last = s.epi == OPEN_EPI_LAST;
-  P.plain_out = last && (s.ld_out % 8 != 0 || (reinterpret_cast<uintptr_t>(s.out) & 15u) != 0);
-  const bool f16 = !last || s.out_f16;
-  if (P.plain_out)
-    maps.out = maps.a;  // (prefetched, not used)
-  else
-    rc |= encode3(env, &maps.out, f16, s.out, s.N, s.M, Z, s.ld_out, s.M * s.ld_out, 32, 32,
-                  CU_TENSOR_MAP_SWIZZLE_64B);
-  if (P.sym)
-    rc |= encode3(env, &maps.out2, true, s.out, s.M, s.N, Z, s.ld_out, s.M * s.ld_out, 32, 32,
-                  CU_TENSOR_MAP_SWIZZLE_NONE);
-  else if (s.epi == OPEN_EPI_UPDATE)
-    rc |= encode3(env, &maps.out2, true, s.out_lo, s.N, s.M, Z, s.ld_out, s.M * s.ld_out, 32, 32,
-                  CU_TENSOR_MAP_SWIZZLE_64B);
+  P.plain_out = s.N % 8 != 0 || (reinterpret_cast<uintptr_t>(s.out) & 15u) != 0;
   if (rc != HMM_OK) return HMM_ERR_CUDA;
-  return launch_open<OPEN_STACK>(env, P, maps, Z * static_cast<int64_t>(P.tiles));
+  return launch_open<OPEN_STACK>(env, P, maps, P.Z * static_cast<int64_t>(P.tiles));
 }
 
 }  // namespace hmm

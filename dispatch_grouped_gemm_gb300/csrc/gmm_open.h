@@ -41,8 +41,8 @@ struct OpenParams {
   float alpha, beta, gamma;
   const int32_t* offsets;  // [Z + 1] rows of the experts
   const __half *in_hi, *in_lo;
-  int64_t ld_in;
-  void* out;
+  int64_t ld_in;           // of in_hi, in_lo and of fp16 results
+  void *out, *out_lo;
   unsigned* status;
   unsigned long long budget_ns;
 };
@@ -54,9 +54,8 @@ struct OpenStack {
   int epi;
   float alpha, beta, gamma;
   const void *in_hi, *in_lo;
-  int64_t ld_in;
+  int64_t ld_in;           // of in_hi, in_lo and the fp16 results (LAST is dense)
   void *out, *out_lo;
-  int64_t ld_out;
   int out_f16;
 };
 

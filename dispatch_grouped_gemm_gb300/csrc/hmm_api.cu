@@ -273,8 +273,9 @@ struct DeviceGuard {
   int prev = -1;
   bool ok = false;
   explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) return;
-    ok = prev == dev || cudaSetDevice(dev) == cudaSuccess;
+    // (set even where it is the current one: a thread that has not used the device
+    // yet, as autograd's may be, has no context, and tensor maps are encoded in one)
+    ok = cudaGetDevice(&prev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
   }
   ~DeviceGuard() {
     if (ok && prev >= 0) cudaSetDevice(prev);

@@ -344,7 +344,7 @@ int launch_ortho(const GemmEnv& env, const hmm_ortho& d, const OrthoPlan& p, con
     q.epi = OPEN_EPI_GRAM;
     q.alpha = s.alpha_a;
     q.out = ws + p.off_a;
-    q.ld_out = la;
+    q.ld_in = la;
     int rc = launch_open_stack(env, q);
     if (rc != HMM_OK) return rc;
     // B + d I
@@ -358,7 +358,6 @@ int launch_ortho(const GemmEnv& env, const hmm_ortho& d, const OrthoPlan& p, con
     q.in_hi = ws + p.off_a;
     q.ld_in = la;
     q.out = ws + p.off_b;
-    q.ld_out = la;
     rc = launch_open_stack(env, q);
     if (rc != HMM_OK) return rc;
     // X: B X (X's rows are the contraction) or X B
@@ -378,7 +377,6 @@ int launch_ortho(const GemmEnv& env, const hmm_ortho& d, const OrthoPlan& p, con
     q.ld_in = lx;
     q.out = last ? out : ws + p.off_x[to];
     q.out_lo = last ? nullptr : ws + p.off_x[to + 1];
-    q.ld_out = last ? d.N : lx;
     q.out_f16 = last ? d.out_dtype == HMM_DTYPE_F16 : 1;
     rc = launch_open_stack(env, q);
     if (rc != HMM_OK) return rc;
