@@ -464,8 +464,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       // 16 rows of 128 bytes on (two 64-wide chunks half a tile apart)
       const bool a_mn = KIND == OPEN_DEPTH || P.a_mn;
       const bool b_mn = KIND == OPEN_DEPTH || (KIND == OPEN_STACK && P.b_mn);
-      const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
-      const uint32_t a_lbo = a_mn ? OA_BYTES / 2 : 16, b_lbo = b_mn ? OB_BYTES / 2 : 16;
+      const uint32_t a_step = (a_mn ? 2048 : 32) / 16, b_step = (b_mn ? 2048 : 32) / 16;
+      const uint64_t a_desc =
+          smem_desc(smem_u32(stages), a_mn ? OA_BYTES / 2 : 16, 1024, LAYOUT_SW128);
+      const uint64_t b_desc =
+          smem_desc(smem_u32(stages) + OA_BYTES, b_mn ? OB_BYTES / 2 : 16, 1024, LAYOUT_SW128);
       uint32_t stage = 0, sphase = 0, acc = 0, acc_phase = 0, cut_phase = 0;
       bool ok = true;
       OpenTile t, next;
@@ -473,14 +476,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       // the MMAs of the block in slot `at`, the first `steps` of them
       const auto block = [&](uint32_t at, int steps, uint32_t d_tmem, uint32_t idesc, bool first) {
         tc_fence_after();
-        const uint32_t a_base = smem_u32(stages + at * OSTAGE);
-        const uint32_t b_base = a_base + OA_BYTES;
+        // (the address field counts 16 bytes and cannot overflow inside shared memory)
+        uint64_t ad = a_desc + at * (OSTAGE / 16), bd = b_desc + at * (OSTAGE / 16);
+        umma_bf16_pair(d_tmem, ad, bd, idesc, first ? 0u : 1u);
+        if (KIND != OPEN_DEPTH || steps == OK_ / 16) {
 #pragma unroll
-        for (int kk = 0; kk < OK_ / 16; ++kk) {
-          if (KIND == OPEN_DEPTH && kk >= steps) break;
-          const uint64_t ad = smem_desc(a_base + kk * a_step, a_lbo, 1024, LAYOUT_SW128);
-          const uint64_t bd = smem_desc(b_base + kk * b_step, b_lbo, 1024, LAYOUT_SW128);
-          umma_bf16_pair(d_tmem, ad, bd, idesc, first && kk == 0 ? 0u : 1u);
+          for (int kk = 1; kk < OK_ / 16; ++kk) {
+            ad += a_step;
+            bd += b_step;
+            umma_bf16_pair(d_tmem, ad, bd, idesc, 1u);
+          }
+        } else {
+          for (int kk = 1; kk < steps; ++kk) {
+            ad += a_step;
+            bd += b_step;
+            umma_bf16_pair(d_tmem, ad, bd, idesc, 1u);
+          }
         }
         umma_commit_pair(&empty[at], 0x3);
       };
