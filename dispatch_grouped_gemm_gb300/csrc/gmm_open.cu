@@ -45,19 +45,24 @@ namespace hmm {
 
 namespace {
 
-constexpr int OK_ = 64;                  // k per stage: one 128-byte swizzle row of 16-bit elements
-constexpr int OA_BYTES = 128 * OK_ * 2;  // this CTA's 128 rows of A
-constexpr int OB_BYTES = 128 * OK_ * 2;  // this CTA's half of B's rows, at most 128
+// K per stage.  One thread issues the loads and one the MMAs, and both pay for every
+// barrier they wait on and every box they ask for (a wait and a box each take 130 -
+// 300 cycles, beside 512 of MMA work for 64 deep): with 128 a stage takes four boxes
+// (of 64 x 128 elements, 128 bytes wide) and eight MMAs.
+constexpr int OK_ = 128;
+constexpr int OCHUNK = 128 * 128;        // a box: 128 rows of 128 bytes, swizzled
+constexpr int OA_BYTES = 2 * OCHUNK;     // this CTA's 128 rows of A
+constexpr int OB_BYTES = 2 * OCHUNK;     // this CTA's half of B's rows, at most 128
 constexpr int OSTAGE = OA_BYTES + OB_BYTES;
 constexpr int OBUF = 2048;             // a warp's staging of one 32 x 32 chunk of 16-bit results
 constexpr uint32_t O_TMEM_COLS = 512;  // two accumulators of 256 columns
 constexpr int O_SORT_MAX_E = 512;      // experts that DEPTH sorts by rows (E^2 / threads compares)
-constexpr int O_CUT_AHEAD = 3;         // blocks that a block to be cut is loaded early
+constexpr int O_CUT_AHEAD = 1;         // blocks that a block to be cut is loaded early
 constexpr int O_LIST_BYTES = 2 * 4 * (MAX_E + 4);
 
 template <int KIND>
 struct Cfg {
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = 3;
   static constexpr int EPI_WARPS = 8;
   // DEPTH: one more warp, for the ends of the experts
   static constexpr int THREADS = 32 * (2 + EPI_WARPS + (KIND == OPEN_DEPTH ? 1 : 0));
@@ -395,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         const int half = t.nb >> 1;
         const int nbase = t.n0 + half * static_cast<int>(rank);
         const int box = (half + 15) >> 4;
-        const uint32_t b_bytes = KIND == OPEN_ROWS ? box * 16 * OK_ * 2 : OB_BYTES;
+        const uint32_t b_box = KIND == OPEN_ROWS ? box * 16 * 128 : OCHUNK;
         const CUtensorMap* bm = KIND == OPEN_ROWS ? &maps.brows[box - 1] : &maps.b;
         const bool tail = KIND == OPEN_DEPTH && open_tail(t) != 0;
         const int place = open_cut_place(t);
@@ -411,6 +416,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           // block of the j-th load
           const int kb = !tail || j < place ? j : (j == place ? t.kb - 1 : j - 1);
           const int k = kb * OK_;
+          // K-major operands come in two boxes of 64 deep, the second one only if K
+          // reaches it; MN-major ones in two boxes of 64 wide
+          const bool deep = KIND == OPEN_DEPTH || k + 64 < P.K;
           if (tail && j == place) {
             // counted on this CTA's own barrier; `full` completes at once
             if (leader) mbar_arrive(&full[stage]);
@@ -419,26 +427,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
             landed_used |= 1u << stage;
             landed_phase ^= 1u << stage;
             tma_load_3d(sA, &maps.a, &landed[stage], ma, t.k0 + k, 0);
-            tma_load_3d(sA + OA_BYTES / 2, &maps.a, &landed[stage], ma + 64, t.k0 + k, 0);
+            tma_load_3d(sA + OCHUNK, &maps.a, &landed[stage], ma + 64, t.k0 + k, 0);
             tma_load_3d(sB, bm, &landed[stage], nbase, t.k0 + k, 0);
-            tma_load_3d(sB + OB_BYTES / 2, bm, &landed[stage], nbase + 64, t.k0 + k, 0);
+            tma_load_3d(sB + OCHUNK, bm, &landed[stage], nbase + 64, t.k0 + k, 0);
           } else {
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (OA_BYTES + b_bytes));
-            s_sbytes[stage] = OA_BYTES + b_bytes;
+            const bool a_mn = KIND == OPEN_DEPTH || P.a_mn;
+            const bool b_mn = KIND == OPEN_DEPTH || (KIND == OPEN_STACK && P.b_mn);
+            const uint32_t a_bytes = a_mn || deep ? OA_BYTES : OCHUNK;
+            const uint32_t b_bytes = b_mn || deep ? 2 * b_box : b_box;
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (a_bytes + b_bytes));
+            s_sbytes[stage] = a_bytes + b_bytes;
             const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
             // coordinates of an MN-major box: (m or n, c1, c2)
             const int c1 = KIND == OPEN_DEPTH ? t.k0 + k : k, c2 = KIND == OPEN_DEPTH ? 0 : t.z;
-            if (KIND == OPEN_DEPTH || P.a_mn) {
+            if (a_mn) {
               tma_load_3d_pair(sA, &maps.a, bar, ma, c1, c2);
-              tma_load_3d_pair(sA + OA_BYTES / 2, &maps.a, bar, ma + 64, c1, c2);
+              tma_load_3d_pair(sA + OCHUNK, &maps.a, bar, ma + 64, c1, c2);
             } else {
               tma_load_3d_pair(sA, &maps.a, bar, k, ma, t.z);
+              if (deep) tma_load_3d_pair(sA + OCHUNK, &maps.a, bar, k + 64, ma, t.z);
             }
-            if (KIND == OPEN_DEPTH || (KIND == OPEN_STACK && P.b_mn)) {
+            if (b_mn) {
               tma_load_3d_pair(sB, bm, bar, nbase, c1, c2);
-              tma_load_3d_pair(sB + OB_BYTES / 2, bm, bar, nbase + 64, c1, c2);
+              tma_load_3d_pair(sB + OCHUNK, bm, bar, nbase + 64, c1, c2);
             } else {
-              tma_load_3d_pair(sB, bm, bar, k, nbase, KIND == OPEN_ROWS ? 0 : t.z);
+              const int z = KIND == OPEN_ROWS ? 0 : t.z;
+              tma_load_3d_pair(sB, bm, bar, k, nbase, z);
+              if (deep) tma_load_3d_pair(sB + OCHUNK, bm, bar, k + 64, nbase, z);
             }
           }
           ++issued;
@@ -460,15 +475,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ------------------------------------------------------------ MMA issue
-      // 16 deep per MMA: K-major 32 bytes on inside the swizzled row, MN-major
-      // 16 rows of 128 bytes on (two 64-wide chunks half a tile apart)
+      // 16 deep per MMA: K-major 32 bytes on inside the swizzled row, after four of
+      // them in the next box; MN-major 16 rows of 128 bytes on (the two 64-wide boxes
+      // are the leading-dimension stride)
       const bool a_mn = KIND == OPEN_DEPTH || P.a_mn;
       const bool b_mn = KIND == OPEN_DEPTH || (KIND == OPEN_STACK && P.b_mn);
       const uint32_t a_step = (a_mn ? 2048 : 32) / 16, b_step = (b_mn ? 2048 : 32) / 16;
-      const uint64_t a_desc =
-          smem_desc(smem_u32(stages), a_mn ? OA_BYTES / 2 : 16, 1024, LAYOUT_SW128);
+      const uint32_t a_jump = (a_mn ? 4 * 2048 : OCHUNK) / 16, b_jump = (b_mn ? 4 * 2048 : OCHUNK) / 16;
+      const uint64_t a_desc = smem_desc(smem_u32(stages), a_mn ? OCHUNK : 16, 1024, LAYOUT_SW128);
       const uint64_t b_desc =
-          smem_desc(smem_u32(stages) + OA_BYTES, b_mn ? OB_BYTES / 2 : 16, 1024, LAYOUT_SW128);
+          smem_desc(smem_u32(stages) + OA_BYTES, b_mn ? OCHUNK : 16, 1024, LAYOUT_SW128);
       uint32_t stage = 0, sphase = 0, acc = 0, acc_phase = 0, cut_phase = 0;
       bool ok = true;
       OpenTile t, next;
@@ -477,21 +493,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       const auto block = [&](uint32_t at, int steps, uint32_t d_tmem, uint32_t idesc, bool first) {
         tc_fence_after();
         // (the address field counts 16 bytes and cannot overflow inside shared memory)
-        uint64_t ad = a_desc + at * (OSTAGE / 16), bd = b_desc + at * (OSTAGE / 16);
-        umma_bf16_pair(d_tmem, ad, bd, idesc, first ? 0u : 1u);
-        if (KIND != OPEN_DEPTH || steps == OK_ / 16) {
+        const uint64_t ad = a_desc + at * (OSTAGE / 16), bd = b_desc + at * (OSTAGE / 16);
+        const auto one = [&](int kk) {
+          umma_bf16_pair(d_tmem, ad + (kk >> 2) * a_jump + (kk & 3) * a_step,
+                         bd + (kk >> 2) * b_jump + (kk & 3) * b_step, idesc,
+                         first && kk == 0 ? 0u : 1u);
+        };
+        if (steps == OK_ / 16) {
 #pragma unroll
-          for (int kk = 1; kk < OK_ / 16; ++kk) {
-            ad += a_step;
-            bd += b_step;
-            umma_bf16_pair(d_tmem, ad, bd, idesc, 1u);
-          }
+          for (int kk = 0; kk < OK_ / 16; ++kk) one(kk);
         } else {
-          for (int kk = 1; kk < steps; ++kk) {
-            ad += a_step;
-            bd += b_step;
-            umma_bf16_pair(d_tmem, ad, bd, idesc, 1u);
-          }
+#pragma unroll 1
+          for (int kk = 0; kk < steps; ++kk) one(kk);
         }
         umma_commit_pair(&empty[at], 0x3);
       };
@@ -506,8 +519,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         const uint32_t d_tmem = tmem_base + acc * 256;
         const bool tail = KIND == OPEN_DEPTH && open_tail(t) != 0;
         const int place = tail ? open_cut_place(t) : -1;
-        // steps of the tile's last block (DEPTH)
-        const int last_steps = KIND == OPEN_DEPTH ? (t.k1 - t.k0 - (t.kb - 1) * OK_ + 15) >> 4 : 4;
+        // steps of the tile's last block
+        const int depth = KIND == OPEN_DEPTH ? t.k1 - t.k0 : P.K;
+        const int last_steps = (depth - (t.kb - 1) * OK_ + 15) >> 4;
         uint32_t held = 0, held_phase = 0;
         bool first = true;
         for (int j = 0; j < t.kb; ++j) {
@@ -519,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
               ok = false;
               break;
             }
-            block(stage, !tail && j == t.kb - 1 ? last_steps : 4, d_tmem, idesc, first);
+            block(stage, !tail && j == t.kb - 1 ? last_steps : OK_ / 16, d_tmem, idesc, first);
             first = false;
           }
           if (++stage == ST) {
@@ -566,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       const int rows = 16 - (v & 15);
       for (int j = lane; j < 4 * 8 * rows; j += 32) {
         const int chunk = j & 3, unit = j >> 2 & 7, row = v + (j >> 5);
-        *reinterpret_cast<uint4*>(stages + last * OSTAGE + chunk * (OA_BYTES / 2) + row * 128 +
+        *reinterpret_cast<uint4*>(stages + last * OSTAGE + chunk * OCHUNK + row * 128 +
                                   unit * 16) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();
@@ -734,9 +748,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
 }
 
 // ------------------------------------------------------------------ host side
-// An operand [batch][rows][cols] as loaded: K-major (cols = k): boxes of 64 x
-// `box` rows; MN-major (rows = k): boxes of 64 columns x 64 rows.
-int encode_operand(const GemmEnv& env, CUtensorMap* m, bool f16, const OpenOperand& o, int box) {
+// An operand [batch][rows][cols] as loaded: boxes of 64 columns (k, or m / n) x `box`
+// rows (m / n, or k).
+int encode_operand(const GemmEnv& env, CUtensorMap* m, bool f16, const OpenOperand& o,
+                   int box = 128) {
   const cuuint64_t gd[3] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows),
                             static_cast<cuuint64_t>(o.batch)};
   const cuuint64_t gs[2] = {static_cast<cuuint64_t>(o.ld) * 2,
@@ -790,12 +805,13 @@ int launch_open_rows(const GemmEnv& env, bool f16, const OpenOperand& w, bool w_
   P.M = static_cast<int>(M);
   P.Z = static_cast<int>(E);
   P.R = static_cast<int>(R);
+  P.K = static_cast<int>(K);
   P.kb = static_cast<int>((K + OK_ - 1) / OK_);
   P.mt = static_cast<int>((M + 255) / 256);
   P.offsets = offsets;
   P.out = out;
   P.out_f16 = f16;
-  int rc = encode_operand(env, &maps.a, f16, w, w_mn ? 64 : 128);
+  int rc = encode_operand(env, &maps.a, f16, w);
   const OpenOperand xo{x, R, K, 1, ld_x, R * ld_x};
   for (int i = 0; i < 8; ++i) rc |= encode_operand(env, &maps.brows[i], f16, xo, 16 * (i + 1));
   if (rc != HMM_OK) return HMM_ERR_CUDA;
@@ -822,8 +838,8 @@ int launch_open_depth(const GemmEnv& env, bool f16, const void* a, int64_t ld_a,
   P.offsets = offsets;
   P.out = out;
   P.out_f16 = f16;
-  int rc = encode_operand(env, &maps.a, f16, OpenOperand{a, R, M, 1, ld_a, R * ld_a}, OK_);
-  rc |= encode_operand(env, &maps.b, f16, OpenOperand{b, R, N, 1, ld_b, R * ld_b}, OK_);
+  int rc = encode_operand(env, &maps.a, f16, OpenOperand{a, R, M, 1, ld_a, R * ld_a});
+  rc |= encode_operand(env, &maps.b, f16, OpenOperand{b, R, N, 1, ld_b, R * ld_b});
   if (rc != HMM_OK) return HMM_ERR_CUDA;
   return launch_open<OPEN_DEPTH>(env, P, maps, E * static_cast<int64_t>(P.tiles));
 }
@@ -838,6 +854,7 @@ int launch_open_stack(const GemmEnv& env, const OpenStack& s) {
   P.M = static_cast<int>(s.M);
   P.N = static_cast<int>(s.N);
   P.Z = static_cast<int>(s.a.batch);
+  P.K = static_cast<int>(s.K);
   P.kb = static_cast<int>((s.K + OK_ - 1) / OK_);
   P.mt = static_cast<int>((s.M + 255) / 256);
   P.nt = static_cast<int>((s.N + 255) / 256);
@@ -853,8 +870,8 @@ int launch_open_stack(const GemmEnv& env, const OpenStack& s) {
   P.out = s.out;
   P.out_lo = s.out_lo;
   P.out_f16 = s.out_f16;
-  int rc = encode_operand(env, &maps.a, true, s.a, s.a_mn ? 64 : 128);
-  rc |= encode_operand(env, &maps.b, true, s.b, s.b_mn ? 64 : 128);
+  int rc = encode_operand(env, &maps.a, true, s.a);
+  rc |= encode_operand(env, &maps.b, true, s.b);
   P.plain_out = s.N % 8 != 0 || (reinterpret_cast<uintptr_t>(s.out) & 15u) != 0;
   if (rc != HMM_OK) return HMM_ERR_CUDA;
   return launch_open<OPEN_STACK>(env, P, maps, P.Z * static_cast<int64_t>(P.tiles));

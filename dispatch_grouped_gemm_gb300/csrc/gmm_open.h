@@ -33,7 +33,7 @@ struct OpenOperand {
 
 struct OpenParams {
   int M, N, Z, R;     // extent of m, of n; experts or matrices; rows
-  int kb;             // K blocks (DEPTH: per expert)
+  int K, kb;          // depth, in blocks (DEPTH: per expert)
   int mt, nt, tiles;  // 256-tiles of m, of n, per expert or matrix
   int a_mn, b_mn;     // operands with m / n contiguous
   int sym, epi, out_f16, plain_out;
