@@ -127,18 +127,10 @@ struct XTile {
 };
 
 // ---------------------------------------------------------------------- PTX
-// True in one lane of a converged warp.  The issuing warps run their loops with
-// all lanes and issue under this predicate: the operands of the asynchronous
-// instructions then stay in uniform registers.  (With a lane == 0 branch around
-// the loops an MMA took 205 and a scale copy 111 cycles to issue, 1490 per K
-// block, for 540 cycles of tensor work.)
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
+// The issuing warps run their loops with all lanes and issue under elect_one().
+// (With a lane == 0 branch around the loops an MMA took 205 and a scale copy 111
+// cycles to issue, 1490 per K block, for 540 cycles of tensor work.)
+//
 // Store the box at src to the tensor at {c0, c1}; parts outside it are left out.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int c0,
                                              int c1) {
@@ -209,9 +201,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-
-// One answer for the whole warp (a bounded wait may give up in single lanes).
-__device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
 
 // ---------------------------------------------------------------- scheduling
 // Tickets run over the GMM1 tiles of all experts, then over the GMM2 tiles.

@@ -385,58 +385,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   open_list<KIND>(P, list);
   const int64_t total = open_total<KIND>(P, list);
 
+  // The two issuing warps run converged and elect a lane for each group of
+  // instructions, whose operands then stay in uniform registers: under a branch on
+  // the lane an MMA took 95 cycles to issue and a stage 1070, whatever its columns.
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------- TMA producer
-      tma_prefetch_desc(&maps.a);
-      uint32_t stage = 0, sphase = 0, issued = 0;
-      uint32_t landed_phase = 0, landed_used = 0;  // a bit per slot
-      bool ok = true;
-      OpenTile t, next;
-      bool more = open_tile<KIND>(P, list, total, 0, t);
-      for (int64_t i = 1; ok && more; ++i, t = next) {
-        const int ma = t.m0 + 128 * static_cast<int>(rank);
-        // B: this CTA's half of the columns, in boxes of a multiple of 16 rows
-        const int half = t.nb >> 1;
-        const int nbase = t.n0 + half * static_cast<int>(rank);
-        const int box = (half + 15) >> 4;
-        const uint32_t b_box = KIND == OPEN_ROWS ? box * 16 * 128 : OCHUNK;
-        const CUtensorMap* bm = KIND == OPEN_ROWS ? &maps.brows[box - 1] : &maps.b;
-        const bool tail = KIND == OPEN_DEPTH && open_tail(t) != 0;
-        const int place = open_cut_place(t);
-        const int ask = min(t.kb, ST) - 1;  // the next tile is decoded with the ring filled
-        if (t.kb == 0) more = open_tile<KIND>(P, list, total, i, next);
-        for (int j = 0; j < t.kb; ++j) {
-          if (!mbar_wait(&empty[stage], sphase ^ 1u, wc)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sA = stages + stage * OSTAGE;
-          uint8_t* sB = sA + OA_BYTES;
-          // block of the j-th load
-          const int kb = !tail || j < place ? j : (j == place ? t.kb - 1 : j - 1);
-          const int k = kb * OK_;
-          // K-major operands come in two boxes of 64 deep, the second one only if K
-          // reaches it; MN-major ones in two boxes of 64 wide
-          const bool deep = KIND == OPEN_DEPTH || k + 64 < P.K;
-          if (tail && j == place) {
+    // --------------------------------------------------------- TMA producer
+    if (elect_one()) tma_prefetch_desc(&maps.a);
+    uint32_t stage = 0, sphase = 0, issued = 0;
+    uint32_t landed_phase = 0, landed_used = 0;  // a bit per slot
+    bool ok = true;
+    OpenTile t, next;
+    bool more = open_tile<KIND>(P, list, total, 0, t);
+    const bool a_mn = KIND == OPEN_DEPTH || P.a_mn;
+    const bool b_mn = KIND == OPEN_DEPTH || (KIND == OPEN_STACK && P.b_mn);
+    for (int64_t i = 1; ok && more; ++i, t = next) {
+      const int ma = t.m0 + 128 * static_cast<int>(rank);
+      // B: this CTA's half of the columns, in boxes of a multiple of 16 rows
+      const int half = t.nb >> 1;
+      const int nbase = t.n0 + half * static_cast<int>(rank);
+      const int box = (half + 15) >> 4;
+      const uint32_t b_box = KIND == OPEN_ROWS ? box * 16 * 128 : OCHUNK;
+      const CUtensorMap* bm = KIND == OPEN_ROWS ? &maps.brows[box - 1] : &maps.b;
+      const bool tail = KIND == OPEN_DEPTH && open_tail(t) != 0;
+      const int place = open_cut_place(t);
+      const int ask = min(t.kb, ST) - 1;  // the next tile is decoded with the ring filled
+      if (t.kb == 0) more = open_tile<KIND>(P, list, total, i, next);
+      for (int j = 0; j < t.kb; ++j) {
+        ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
+        if (!ok) break;
+        // block of the j-th load
+        const int kb = !tail || j < place ? j : (j == place ? t.kb - 1 : j - 1);
+        const int k = kb * OK_;
+        // K-major operands come in two boxes of 64 deep, the second one only if K
+        // reaches it; MN-major ones in two boxes of 64 wide
+        const bool deep = KIND == OPEN_DEPTH || k + 64 < P.K;
+        const bool cutting = tail && j == place;
+        uint8_t* sA = stages + stage * OSTAGE;
+        uint8_t* sB = sA + OA_BYTES;
+        const uint32_t bytes =
+            (a_mn || deep ? OA_BYTES : OCHUNK) + (b_mn || deep ? 2 * b_box : b_box);
+        if (elect_one()) {
+          if (cutting) {
             // counted on this CTA's own barrier; `full` completes at once
             if (leader) mbar_arrive(&full[stage]);
             s_sbytes[stage] = 0;
             mbar_arrive_expect_tx(&landed[stage], OSTAGE);
-            landed_used |= 1u << stage;
-            landed_phase ^= 1u << stage;
             tma_load_3d(sA, &maps.a, &landed[stage], ma, t.k0 + k, 0);
             tma_load_3d(sA + OCHUNK, &maps.a, &landed[stage], ma + 64, t.k0 + k, 0);
             tma_load_3d(sB, bm, &landed[stage], nbase, t.k0 + k, 0);
             tma_load_3d(sB + OCHUNK, bm, &landed[stage], nbase + 64, t.k0 + k, 0);
           } else {
-            const bool a_mn = KIND == OPEN_DEPTH || P.a_mn;
-            const bool b_mn = KIND == OPEN_DEPTH || (KIND == OPEN_STACK && P.b_mn);
-            const uint32_t a_bytes = a_mn || deep ? OA_BYTES : OCHUNK;
-            const uint32_t b_bytes = b_mn || deep ? 2 * b_box : b_box;
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (a_bytes + b_bytes));
-            s_sbytes[stage] = a_bytes + b_bytes;
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+            s_sbytes[stage] = bytes;
             const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
             // coordinates of an MN-major box: (m or n, c1, c2)
             const int c1 = KIND == OPEN_DEPTH ? t.k0 + k : k, c2 = KIND == OPEN_DEPTH ? 0 : t.z;
@@ -456,32 +456,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
               if (deep) tma_load_3d_pair(sB + OCHUNK, bm, bar, k + 64, nbase, z);
             }
           }
-          ++issued;
-          if (++stage == ST) {
-            stage = 0;
-            sphase ^= 1u;
-          }
-          if (j == ask) more = open_tile<KIND>(P, list, total, i, next);
         }
+        if (cutting) {
+          landed_used |= 1u << stage;
+          landed_phase ^= 1u << stage;
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == ST) {
+          stage = 0;
+          sphase ^= 1u;
+        }
+        if (j == ask) more = open_tile<KIND>(P, list, total, i, next);
       }
+    }
+    if (lane == 0) {
       // after an abort: this CTA's own copies (the others are drained at teardown)
       if (KIND == OPEN_DEPTH && !ok)
         for (int s = 0; s < ST; ++s)
           if (landed_used >> s & 1u)
             drain_wait(&landed[s], (landed_phase >> s & 1u) ^ 1u, P.budget_ns);
       *s_issued = issued;
-      grid_dep_launch();  // this CTA is in its last tile
     }
+    grid_dep_launch();  // this CTA is in its last tile
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ------------------------------------------------------------ MMA issue
       // 16 deep per MMA: K-major 32 bytes on inside the swizzled row, after four of
       // them in the next box; MN-major 16 rows of 128 bytes on (the two 64-wide boxes
-      // are the leading-dimension stride)
+      // are the leading-dimension stride).  Descriptor addresses count 16 bytes.
       const bool a_mn = KIND == OPEN_DEPTH || P.a_mn;
       const bool b_mn = KIND == OPEN_DEPTH || (KIND == OPEN_STACK && P.b_mn);
       const uint32_t a_step = (a_mn ? 2048 : 32) / 16, b_step = (b_mn ? 2048 : 32) / 16;
-      const uint32_t a_jump = (a_mn ? 4 * 2048 : OCHUNK) / 16, b_jump = (b_mn ? 4 * 2048 : OCHUNK) / 16;
+      const uint32_t a_jump = (a_mn ? 4 * 2048 : OCHUNK) / 16;
+      const uint32_t b_jump = (b_mn ? 4 * 2048 : OCHUNK) / 16;
       const uint64_t a_desc = smem_desc(smem_u32(stages), a_mn ? OCHUNK : 16, 1024, LAYOUT_SW128);
       const uint64_t b_desc =
           smem_desc(smem_u32(stages) + OA_BYTES, b_mn ? OCHUNK : 16, 1024, LAYOUT_SW128);
@@ -492,21 +500,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       // the MMAs of the block in slot `at`, the first `steps` of them
       const auto block = [&](uint32_t at, int steps, uint32_t d_tmem, uint32_t idesc, bool first) {
         tc_fence_after();
-        // (the address field counts 16 bytes and cannot overflow inside shared memory)
-        const uint64_t ad = a_desc + at * (OSTAGE / 16), bd = b_desc + at * (OSTAGE / 16);
-        const auto one = [&](int kk) {
-          umma_bf16_pair(d_tmem, ad + (kk >> 2) * a_jump + (kk & 3) * a_step,
-                         bd + (kk >> 2) * b_jump + (kk & 3) * b_step, idesc,
-                         first && kk == 0 ? 0u : 1u);
-        };
-        if (steps == OK_ / 16) {
+        if (elect_one()) {
+          const uint64_t ad = a_desc + at * (OSTAGE / 16), bd = b_desc + at * (OSTAGE / 16);
+          if (steps == OK_ / 16) {
 #pragma unroll
-          for (int kk = 0; kk < OK_ / 16; ++kk) one(kk);
-        } else {
+            for (int kk = 0; kk < OK_ / 16; ++kk)
+              umma_bf16_pair(d_tmem, ad + (kk >> 2) * a_jump + (kk & 3) * a_step,
+                             bd + (kk >> 2) * b_jump + (kk & 3) * b_step, idesc,
+                             first && kk == 0 ? 0u : 1u);
+          } else {
 #pragma unroll 1
-          for (int kk = 0; kk < steps; ++kk) one(kk);
+            for (int kk = 0; kk < steps; ++kk)
+              umma_bf16_pair(d_tmem, ad + (kk >> 2) * a_jump + (kk & 3) * a_step,
+                             bd + (kk >> 2) * b_jump + (kk & 3) * b_step, idesc,
+                             first && kk == 0 ? 0u : 1u);
+          }
+          umma_commit_pair(&empty[at], 0x3);
         }
-        umma_commit_pair(&empty[at], 0x3);
+        __syncwarp();
       };
       for (int64_t i = 1; ok && more; ++i, t = next) {
         if (t.kb == 0) {
@@ -514,7 +525,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           continue;
         }
         const uint32_t idesc = P.idesc | (static_cast<uint32_t>(t.nb >> 3) << 17);
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, wc)) break;
+        ok = warp_all(mbar_wait(&tempty[acc], acc_phase ^ 1u, wc));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
         const bool tail = KIND == OPEN_DEPTH && open_tail(t) != 0;
@@ -529,10 +541,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
             held = stage;
             held_phase = sphase;
           } else {
-            if (!mbar_wait(&full[stage], sphase, wc)) {
-              ok = false;
-              break;
-            }
+            ok = warp_all(mbar_wait(&full[stage], sphase, wc));
+            if (!ok) break;
             block(stage, !tail && j == t.kb - 1 ? last_steps : OK_ / 16, d_tmem, idesc, first);
             first = false;
           }
@@ -544,19 +554,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         }
         if (!ok) break;
         if (tail) {
-          if (!mbar_wait(&full[held], held_phase, wc) ||
-              !mbar_wait<true>(&cut[held], cut_phase >> held & 1u, wc)) {
-            ok = false;
-            break;
-          }
+          ok = warp_all(mbar_wait(&full[held], held_phase, wc)) &&
+               warp_all(mbar_wait<true>(&cut[held], cut_phase >> held & 1u, wc));
+          if (!ok) break;
           cut_phase ^= 1u << held;
           block(held, last_steps, d_tmem, idesc, first);
         }
-        umma_commit_pair(&tfull[acc], 0x3);
+        if (elect_one()) umma_commit_pair(&tfull[acc], 0x3);
+        __syncwarp();
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
       }
-      umma_commit_pair(mma_done, 0x1);
+      if (elect_one()) umma_commit_pair(mma_done, 0x1);
+      __syncwarp();
       drain_wait(mma_done, 0, P.budget_ns);
     }
   } else if (KIND == OPEN_DEPTH && warp == 2 + C::EPI_WARPS) {

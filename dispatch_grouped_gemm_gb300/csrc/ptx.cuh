@@ -526,6 +526,19 @@ __device__ __forceinline__ void pair_teardown(bool leader, uint32_t issued, int 
   cluster_sync_all();
 }
 
+// True in one lane of a converged warp, always the same one.  A warp that issues
+// asynchronous instructions runs its loops with all lanes and issues under this
+// predicate: the instructions' operands then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// One answer for the whole warp (a bounded wait may give up in single lanes).
+__device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
+
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31u; }
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
