@@ -13,8 +13,8 @@
 //           most 256 and few rows cost few columns of work, while the weights,
 //           256 columns per pair, fill the M side.
 //   DEPTH   dw[e] = x_e^T . dy_e: the contraction runs over the rows of the expert.
-//   STACK   products of a stack of matrices, with the epilogues of the
-//           Newton-Schulz step (gmm_open.h).
+//   CHAIN   the products of the Newton-Schulz steps over a stack of matrices, all of
+//           them in one launch (gmm_open.h).
 //
 // Rows of one expert start anywhere, and a block of them may end inside a box.
 // ROWS loads whole boxes: rows of the next expert fill columns of the accumulator
@@ -29,10 +29,14 @@
 // all columns.  Warp 0 issues TMA (both CTAs, one thread), warp 1 the MMAs (even
 // CTA), eight others drain TMEM (both CTAs) while the next tile accumulates in the
 // other half of it: in chunks of 32 x 32 results that a warp turns in 2 KB of
-// shared memory and stores as rows of 64 bytes.  Every role walks the same static list of tiles: pair c of C
-// takes tiles c, 2C - 1 - c, 2C + c, ... (back and forth, so that a list sorted by
-// cost, as DEPTH's experts are by rows, loads the pairs evenly).  Every wait is
-// bounded.
+// shared memory and stores as rows of 64 bytes.  Of ROWS and DEPTH every role
+// walks the same static list of tiles: pair c of C takes tiles c, 2C - 1 - c, 2C + c,
+// ... (back and forth, so that a list sorted by cost, as DEPTH's experts are by rows,
+// loads the pairs evenly).  A tile of CHAIN needs the product before it of its
+// matrix: its tiles go out by ticket, so that a tile only waits for tiles that running
+// CTAs have, whatever else the device runs.  Three matrices are in three different
+// products at a time (each third of the stack one behind the other): products that
+// move memory run beside those that compute.  Every wait is bounded.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -59,20 +63,21 @@ constexpr uint32_t O_TMEM_COLS = 512;  // two accumulators of 256 columns
 constexpr int O_SORT_MAX_E = 512;      // experts that DEPTH sorts by rows (E^2 / threads compares)
 constexpr int O_CUT_AHEAD = 1;         // blocks that a block to be cut is loaded early
 constexpr int O_LIST_BYTES = 2 * 4 * (MAX_E + 4);
+constexpr int O_RING = 4;               // tickets on their way (CHAIN)
 
 template <int KIND>
 struct Cfg {
   static constexpr int STAGES = 3;
   static constexpr int EPI_WARPS = 8;
-  // DEPTH: one more warp, for the ends of the experts
-  static constexpr int THREADS = 32 * (2 + EPI_WARPS + (KIND == OPEN_DEPTH ? 1 : 0));
+  // one more warp: DEPTH for the ends of the experts, CHAIN for the tickets
+  static constexpr int THREADS = 32 * (2 + EPI_WARPS + (KIND == OPEN_ROWS ? 0 : 1));
   static constexpr int SMEM = 1024 + STAGES * OSTAGE + EPI_WARPS * OBUF + 1024 + O_LIST_BYTES;
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
 struct OpenMaps {
-  CUtensorMap a, b;
-  CUtensorMap brows[8];  // ROWS: x in boxes of 16, 32 .. 128 rows
+  CUtensorMap a, b;      // CHAIN: A, B
+  CUtensorMap brows[8];  // ROWS: x in boxes of 16, 32 .. 128 rows; CHAIN: X of even, odd steps
 };
 
 struct OpenTile {
@@ -80,7 +85,7 @@ struct OpenTile {
   int m0, n0;  // ROWS: n0 = first row of the block
   int nv, nb;  // ROWS: rows of the block, MMA columns (a multiple of 16); else 256
   int kb;      // K blocks
-  int k0, k1;  // DEPTH: the expert's rows
+  int k0, k1;  // DEPTH: the expert's rows; CHAIN: product (3 per step) and its kind
 };
 
 // The pair's i-th tile (tiles go back and forth over the pairs).
@@ -94,8 +99,15 @@ struct OpenList {
   int* at;    // rows of the experts: [Z + 1] offsets clamped into [0, R], so that
               // whatever the caller's offsets hold, every access stays inside
   int* list;  // ROWS: blocks of the experts before e (Z + 1 entries); DEPTH: experts
-              // by rows, descending (Z up to O_SORT_MAX_E)
+              // by rows, descending (Z up to O_SORT_MAX_E); CHAIN: tiles of the slots
+              // before e
 };
+
+// CHAIN: tiles of a matrix in product p (0 outside the chain).
+__device__ __forceinline__ int chain_tiles(const OpenParams& P, int p) {
+  if (p < 0 || p >= 3 * P.steps) return 0;
+  return P.ph[p % 3].tiles;
+}
 
 __device__ __forceinline__ int open_blocks(int rows) { return (rows + 255) >> 8; }
 
@@ -106,24 +118,34 @@ __device__ __forceinline__ int open_rows_of(const OpenList& l, int e) {
 // All threads of the CTA; ends with a barrier.
 template <int KIND>
 __device__ void open_list(const OpenParams& P, const OpenList& l) {
-  if constexpr (KIND == OPEN_STACK) return;
-  for (int e = threadIdx.x; e <= P.Z; e += blockDim.x)
-    l.at[e] = min(max(P.offsets[e], 0), P.R);
-  __syncthreads();
-  if constexpr (KIND == OPEN_ROWS) {
+  if constexpr (KIND != OPEN_CHAIN) {
+    for (int e = threadIdx.x; e <= P.Z; e += blockDim.x)
+      l.at[e] = min(max(P.offsets[e], 0), P.R);
+    __syncthreads();
+  }
+  if constexpr (KIND != OPEN_DEPTH) {
     if (threadIdx.x < 32) {
       const int lane = threadIdx.x;
+      const int entries = KIND == OPEN_ROWS ? P.Z : 3 * P.steps + 2;
       int carry = 0;
       if (lane == 0) l.list[0] = 0;
-      for (int base = 0; base < P.Z; base += 32) {
+      for (int base = 0; base < entries; base += 32) {
         const int e = base + lane;
-        int v = e < P.Z ? open_blocks(open_rows_of(l, e)) : 0;
+        int v = 0;
+        if (e < entries) {
+          if constexpr (KIND == OPEN_ROWS) {
+            v = open_blocks(open_rows_of(l, e));
+          } else {  // tiles of slot e: every third matrix in product e, e - 1, e - 2
+#pragma unroll
+            for (int g = 0; g < 3; ++g) v += chain_tiles(P, e - g) * ((P.Z + 2 - g) / 3);
+          }
+        }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int n = __shfl_up_sync(0xffffffffu, v, d);
           if (lane >= d) v += n;
         }
-        if (e < P.Z) l.list[e + 1] = carry + v;
+        if (e < entries) l.list[e + 1] = carry + v;
         carry += __shfl_sync(0xffffffffu, v, 31);
       }
     }
@@ -143,6 +165,7 @@ __device__ void open_list(const OpenParams& P, const OpenList& l) {
 
 template <int KIND>
 __device__ __forceinline__ int64_t open_total(const OpenParams& P, const OpenList& l) {
+  if constexpr (KIND == OPEN_CHAIN) return l.list[3 * P.steps + 2];
   if constexpr (KIND == OPEN_ROWS) return static_cast<int64_t>(l.list[P.Z]) * P.mt;
   return static_cast<int64_t>(P.Z) * P.tiles;
 }
@@ -156,6 +179,61 @@ __device__ __forceinline__ int open_div(int64_t u, int d, int& rest) {
     q = static_cast<int>(u / d);
   rest = static_cast<int>(u - static_cast<int64_t>(q) * d);
   return q;
+}
+
+// Tile (r of the matrix, in its product) of a rectangle of mt x nt tiles, or of the
+// triangle on and right of its diagonal, row by row.
+__device__ __forceinline__ void open_place(int r, int mt, int nt, bool sym, OpenTile& t) {
+  if (sym) {
+    int mi = 0;
+    for (int w = mt; r >= w; --w) {
+      r -= w;
+      ++mi;
+    }
+    t.m0 = mi * 256;
+    t.n0 = (mi + r) * 256;
+  } else if (mt <= nt) {  // the shorter side inside: what runs at once is near square
+    t.m0 = r % mt * 256;
+    t.n0 = r / mt * 256;
+  } else {
+    t.m0 = r / nt * 256;
+    t.n0 = r % nt * 256;
+  }
+}
+
+// Tile of a ticket (CHAIN).  Slot e holds, for every k, matrix 3 k in product e, matrix
+// 3 k + 1 in product e - 1 and matrix 3 k + 2 in product e - 2.
+__device__ __forceinline__ void chain_tile(const OpenParams& P, const OpenList& l, int u,
+                                           OpenTile& t) {
+  int lo = 0, hi = 3 * P.steps + 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (l.list[mid] <= u)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  int r = u - l.list[lo];
+  const int n[3] = {chain_tiles(P, lo), chain_tiles(P, lo - 1), chain_tiles(P, lo - 2)};
+  const int unit = n[0] + n[1] + n[2], whole = P.Z / 3;
+  int k = min(r / unit, whole);
+  r -= k * unit;
+  int g = 0;
+  if (r >= n[0]) {
+    r -= n[0];
+    g = 1;
+    if (r >= n[1]) {
+      r -= n[1];
+      g = 2;
+    }
+  }
+  t.z = 3 * k + g;
+  t.k0 = lo - g;
+  t.k1 = t.k0 % 3;
+  t.nv = t.nb = 256;
+  const OpenPhase& ph = P.ph[t.k1];
+  t.kb = ph.kb;
+  open_place(r, ph.mt, ph.nt, ph.sym, t);
 }
 
 // The pair's i-th tile; false behind the last.
@@ -186,30 +264,11 @@ __device__ __forceinline__ bool open_tile(const OpenParams& P, const OpenList& l
   } else {
     const int i = open_div(u, P.tiles, r);
     t.nv = t.nb = 256;
-    if (P.sym) {  // tiles on and right of the diagonal, row by row
-      int mi = 0;
-      for (int w = P.mt; r >= w; --w) {
-        r -= w;
-        ++mi;
-      }
-      t.m0 = mi * 256;
-      t.n0 = (mi + r) * 256;
-    } else if (P.mt <= P.nt) {  // the shorter side inside: what runs at once is near square
-      t.m0 = r % P.mt * 256;
-      t.n0 = r / P.mt * 256;
-    } else {
-      t.m0 = r / P.nt * 256;
-      t.n0 = r % P.nt * 256;
-    }
-    if constexpr (KIND == OPEN_DEPTH) {
-      t.z = P.Z <= O_SORT_MAX_E ? l.list[i] : i;
-      t.k0 = l.at[t.z];
-      t.k1 = max(t.k0, l.at[t.z + 1]);
-      t.kb = (t.k1 - t.k0 + OK_ - 1) / OK_;
-    } else {
-      t.z = i;
-      t.kb = P.kb;
-    }
+    open_place(r, P.mt, P.nt, false, t);
+    t.z = P.Z <= O_SORT_MAX_E ? l.list[i] : i;
+    t.k0 = l.at[t.z];
+    t.k1 = max(t.k0, l.at[t.z + 1]);
+    t.kb = (t.k1 - t.k0 + OK_ - 1) / OK_;
   }
   return true;
 }
@@ -228,8 +287,9 @@ __device__ __forceinline__ int open_cut_place(const OpenTile& t) {
   return max(0, t.kb - 1 - O_CUT_AHEAD);
 }
 
-__device__ __forceinline__ uint32_t pack16(bool f16, float lo, float hi) {
-  if (f16) {
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (F16) {
     __half2 p = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&p);
   }
@@ -246,28 +306,30 @@ __device__ __forceinline__ uint8_t* unit_at(uint8_t* sb, int row, int unit) {
 // A 32 x 32 chunk (lane = m, register = n) as rows of n, m contiguous: neighbouring
 // lanes swap halves, so that each store is a pair of m and a warp's store covers two
 // whole rows.
-__device__ __forceinline__ void stage_t(uint8_t* sb, int lane, bool f16, const float (&v)[32]) {
+template <bool F16>
+__device__ __forceinline__ void stage_t(uint8_t* sb, int lane, const float (&v)[32]) {
   const bool odd = lane & 1;
+  uint8_t* at = unit_at(sb, odd ? 1 : 0, 0) + ((lane >> 1) & 3) * 4;
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
     const float send = odd ? v[i] : v[i + 1];
     const float got = __shfl_xor_sync(0xffffffffu, send, 1);
     // even lane: row i, columns (lane, lane + 1); odd: row i + 1, columns (lane - 1, lane)
-    const uint32_t p = odd ? pack16(f16, got, v[i + 1]) : pack16(f16, v[i], got);
-    *reinterpret_cast<uint32_t*>(unit_at(sb, i + (odd ? 1 : 0), lane >> 3) +
-                                 ((lane >> 1) & 3) * 4) = p;
+    const uint32_t p = odd ? pack16<F16>(got, v[i + 1]) : pack16<F16>(v[i], got);
+    *reinterpret_cast<uint32_t*>(at + i * 64 + 16 * ((lane >> 3) ^ ((i >> 1) & 3))) = p;
   }
 }
 
 // The same chunk as rows of m, n contiguous.
-__device__ __forceinline__ void stage_d(uint8_t* sb, int lane, bool f16, const float (&v)[32]) {
+template <bool F16>
+__device__ __forceinline__ void stage_d(uint8_t* sb, int lane, const float (&v)[32]) {
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     uint4 q;
-    q.x = pack16(f16, v[8 * u], v[8 * u + 1]);
-    q.y = pack16(f16, v[8 * u + 2], v[8 * u + 3]);
-    q.z = pack16(f16, v[8 * u + 4], v[8 * u + 5]);
-    q.w = pack16(f16, v[8 * u + 6], v[8 * u + 7]);
+    q.x = pack16<F16>(v[8 * u], v[8 * u + 1]);
+    q.y = pack16<F16>(v[8 * u + 2], v[8 * u + 3]);
+    q.z = pack16<F16>(v[8 * u + 4], v[8 * u + 5]);
+    q.w = pack16<F16>(v[8 * u + 6], v[8 * u + 7]);
     *reinterpret_cast<uint4*>(unit_at(sb, lane, u)) = q;
   }
 }
@@ -287,7 +349,7 @@ __device__ __forceinline__ void emit(uint8_t* sb, int lane, uint16_t* dst, int64
 }
 
 // The reverse, in two steps: rows of 64 bytes to registers, and through the staging
-// buffer to a row per lane.
+// buffer to a row per lane, element by element to f(column, value).
 __device__ __forceinline__ void fetch(const __half* src, int lane, int64_t ld, int rows, int cols,
                                       uint4 (&q)[4]) {
   const int unit = lane & 3;
@@ -299,7 +361,8 @@ __device__ __forceinline__ void fetch(const __half* src, int lane, int64_t ld, i
       q[j] = __ldcg(reinterpret_cast<const uint4*>(src + r * ld + unit * 8));
   }
 }
-__device__ __forceinline__ void turn(uint8_t* sb, int lane, const uint4 (&q)[4], float (&v)[32]) {
+template <typename F>
+__device__ __forceinline__ void turn(uint8_t* sb, int lane, const uint4 (&q)[4], const F& f) {
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -311,14 +374,69 @@ __device__ __forceinline__ void turn(uint8_t* sb, int lane, const uint4 (&q)[4],
     const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-      v[8 * u + 2 * j] = f.x;
-      v[8 * u + 2 * j + 1] = f.y;
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      f(8 * u + 2 * j, x.x);
+      f(8 * u + 2 * j + 1, x.y);
     }
   }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 __device__ __forceinline__ float half_round(float v) { return __half2float(__float2half_rn(v)); }
+
+// The ring of tickets (CHAIN): the even CTA's scheduler fills both CTAs'.
+struct OpenRing {
+  int* ticket;     // [O_RING], -1: no more
+  uint64_t* full;  // both CTAs
+  uint64_t* empty; // even CTA: every reader arrives
+};
+
+// Where a role is in its tiles.
+struct OpenWalk {
+  int64_t i = 0;
+  uint32_t slot = 0, phase = 0;
+};
+
+// Whether a converged warp's next tile is known (the ticket behind may wait for the
+// tile that the warp is in, so it must not wait for the ticket there).
+template <int KIND>
+__device__ __forceinline__ bool open_known(const OpenRing& ring, bool leader, const OpenWalk& w) {
+  if constexpr (KIND != OPEN_CHAIN) return true;
+  return warp_all(leader ? mbar_test_wait<false>(&ring.full[w.slot], w.phase)
+                         : mbar_test_wait<true>(&ring.full[w.slot], w.phase));
+}
+
+// A converged warp's next tile; false behind the last (or after an abort).
+template <int KIND>
+__device__ __forceinline__ bool open_next(const OpenParams& P, const OpenList& l, int64_t total,
+                                          const OpenRing& ring, bool leader, const WaitCtl& wc,
+                                          OpenWalk& w, OpenTile& t) {
+  if constexpr (KIND != OPEN_CHAIN) {
+    return open_tile<KIND>(P, l, total, w.i++, t);
+  } else {
+    const bool ok = leader ? mbar_wait(&ring.full[w.slot], w.phase, wc)
+                           : mbar_wait<true>(&ring.full[w.slot], w.phase, wc);
+    if (!warp_all(ok)) return false;
+    const int u = ring.ticket[w.slot];
+    __syncwarp();
+    if (elect_one()) {
+      if (leader)
+        mbar_arrive(&ring.empty[w.slot]);
+      else
+        mbar_arrive_peer(mapa_shared(smem_u32(&ring.empty[w.slot]), 0));
+    }
+    if (++w.slot == O_RING) {
+      w.slot = 0;
+      w.phase ^= 1u;
+    }
+    if (u < 0) return false;
+    chain_tile(P, l, u, t);
+    return true;
+  }
+}
 
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 1)
@@ -340,11 +458,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   // own), and it is cut (even CTA: one arrival per CTA)
   uint64_t* landed = mma_done + 1;
   uint64_t* cut = landed + ST;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(cut + ST);
+  uint64_t* ring_full = cut + ST;
+  uint64_t* ring_empty = ring_full + O_RING;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(ring_empty + O_RING);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   uint32_t* s_issued = s_tmem + 2;
   uint32_t* s_sbytes = s_tmem + 3;   // [ST] bytes of this CTA's last load per slot
   uint32_t* s_peer = s_sbytes + ST;  // [2 + ST]
+  const OpenRing ring{reinterpret_cast<int*>(s_peer + 2 + ST), ring_full, ring_empty};
   const OpenList list{reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 1024),
                       reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 1024) + MAX_E + 4};
 
@@ -365,6 +486,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       mbar_init(&tempty[a], 2 * C::EPI_WARPS);
     }
     mbar_init(mma_done, 1);
+    for (int r = 0; r < O_RING; ++r) {
+      mbar_init(&ring_full[r], 1);
+      // readers: both producers, the MMA issuer, the epilogue warps of both CTAs
+      mbar_init(&ring_empty[r], 3 + 2 * C::EPI_WARPS);
+    }
     *s_abort = 0;
     *s_issued = 0;
     for (int i = 0; i < ST; ++i) s_sbytes[i] = OSTAGE;
@@ -391,14 +517,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   if (warp == 0) {
     // --------------------------------------------------------- TMA producer
     if (elect_one()) tma_prefetch_desc(&maps.a);
+    OpenWalk walk;
+    const auto advance = [&](OpenTile& t) {
+      return open_next<KIND>(P, list, total, ring, leader, wc, walk, t);
+    };
     uint32_t stage = 0, sphase = 0, issued = 0;
     uint32_t landed_phase = 0, landed_used = 0;  // a bit per slot
     bool ok = true;
     OpenTile t, next;
-    bool more = open_tile<KIND>(P, list, total, 0, t);
-    const bool a_mn = KIND == OPEN_DEPTH || P.a_mn;
-    const bool b_mn = KIND == OPEN_DEPTH || (KIND == OPEN_STACK && P.b_mn);
-    for (int64_t i = 1; ok && more; ++i, t = next) {
+    bool more = advance(t);
+    bool a_mn = KIND == OPEN_DEPTH || P.a_mn, b_mn = KIND == OPEN_DEPTH;
+    const CUtensorMap* am = &maps.a;
+    int depth = P.K;
+    for (; ok && more; t = next) {
       const int ma = t.m0 + 128 * static_cast<int>(rank);
       // B: this CTA's half of the columns, in boxes of a multiple of 16 rows
       const int half = t.nb >> 1;
@@ -406,10 +537,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       const int box = (half + 15) >> 4;
       const uint32_t b_box = KIND == OPEN_ROWS ? box * 16 * 128 : OCHUNK;
       const CUtensorMap* bm = KIND == OPEN_ROWS ? &maps.brows[box - 1] : &maps.b;
+      if constexpr (KIND == OPEN_CHAIN) {
+        const OpenPhase& ph = P.ph[t.k1];
+        const CUtensorMap* x = &maps.brows[t.k0 / 3 & 1];
+        a_mn = ph.a_mn;
+        b_mn = ph.b_mn;
+        am = ph.a == 0 ? x : ph.a == 1 ? &maps.a : &maps.b;
+        bm = ph.b == 0 ? x : ph.b == 1 ? &maps.a : &maps.b;
+        depth = ph.K;
+        // what this tile reads was written by other CTAs of this launch: the scheduler
+        // acquired their counter; order that with the asynchronous copies
+        fence_proxy_async_global();
+        if (t.k1 == 2) {  // what the epilogue adds, into L2 meanwhile
+          const OpenFactors& fa = P.f[t.k0 / 3];
+          const int from = t.k0 / 3 & 1;
+          const int rows = min(128, ph.M - ma), lines = min(4, (ph.N - t.n0 + 63) >> 6);
+          const int64_t at = (static_cast<int64_t>(t.z) * ph.M + ma) * P.ld_x + t.n0;
+          for (int j = lane; j < 4 * rows; j += 32) {
+            if ((j & 3) >= lines) continue;
+            const int64_t o = at + (j >> 2) * P.ld_x + (j & 3) * 64;
+            prefetch_l2(P.x_hi[from] + o);
+            if (fa.low) prefetch_l2(P.x_lo[from] + o);
+          }
+          __syncwarp();
+        }
+      }
       const bool tail = KIND == OPEN_DEPTH && open_tail(t) != 0;
       const int place = open_cut_place(t);
       const int ask = min(t.kb, ST) - 1;  // the next tile is decoded with the ring filled
-      if (t.kb == 0) more = open_tile<KIND>(P, list, total, i, next);
+      bool known = false;
       for (int j = 0; j < t.kb; ++j) {
         ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
         if (!ok) break;
@@ -418,7 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         const int k = kb * OK_;
         // K-major operands come in two boxes of 64 deep, the second one only if K
         // reaches it; MN-major ones in two boxes of 64 wide
-        const bool deep = KIND == OPEN_DEPTH || k + 64 < P.K;
+        const bool deep = KIND == OPEN_DEPTH || k + 64 < depth;
         const bool cutting = tail && j == place;
         uint8_t* sA = stages + stage * OSTAGE;
         uint8_t* sB = sA + OA_BYTES;
@@ -430,8 +586,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
             if (leader) mbar_arrive(&full[stage]);
             s_sbytes[stage] = 0;
             mbar_arrive_expect_tx(&landed[stage], OSTAGE);
-            tma_load_3d(sA, &maps.a, &landed[stage], ma, t.k0 + k, 0);
-            tma_load_3d(sA + OCHUNK, &maps.a, &landed[stage], ma + 64, t.k0 + k, 0);
+            tma_load_3d(sA, am, &landed[stage], ma, t.k0 + k, 0);
+            tma_load_3d(sA + OCHUNK, am, &landed[stage], ma + 64, t.k0 + k, 0);
             tma_load_3d(sB, bm, &landed[stage], nbase, t.k0 + k, 0);
             tma_load_3d(sB + OCHUNK, bm, &landed[stage], nbase + 64, t.k0 + k, 0);
           } else {
@@ -441,11 +597,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
             // coordinates of an MN-major box: (m or n, c1, c2)
             const int c1 = KIND == OPEN_DEPTH ? t.k0 + k : k, c2 = KIND == OPEN_DEPTH ? 0 : t.z;
             if (a_mn) {
-              tma_load_3d_pair(sA, &maps.a, bar, ma, c1, c2);
-              tma_load_3d_pair(sA + OCHUNK, &maps.a, bar, ma + 64, c1, c2);
+              tma_load_3d_pair(sA, am, bar, ma, c1, c2);
+              tma_load_3d_pair(sA + OCHUNK, am, bar, ma + 64, c1, c2);
             } else {
-              tma_load_3d_pair(sA, &maps.a, bar, k, ma, t.z);
-              if (deep) tma_load_3d_pair(sA + OCHUNK, &maps.a, bar, k + 64, ma, t.z);
+              tma_load_3d_pair(sA, am, bar, k, ma, t.z);
+              if (deep) tma_load_3d_pair(sA + OCHUNK, am, bar, k + 64, ma, t.z);
             }
             if (b_mn) {
               tma_load_3d_pair(sB, bm, bar, nbase, c1, c2);
@@ -467,8 +623,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           stage = 0;
           sphase ^= 1u;
         }
-        if (j == ask) more = open_tile<KIND>(P, list, total, i, next);
+        if (j == ask && (known = open_known<KIND>(ring, leader, walk))) more = advance(next);
       }
+      if (ok && !known) more = advance(next);
     }
     if (lane == 0) {
       // after an abort: this CTA's own copies (the others are drained at teardown)
@@ -485,23 +642,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       // 16 deep per MMA: K-major 32 bytes on inside the swizzled row, after four of
       // them in the next box; MN-major 16 rows of 128 bytes on (the two 64-wide boxes
       // are the leading-dimension stride).  Descriptor addresses count 16 bytes.
-      const bool a_mn = KIND == OPEN_DEPTH || P.a_mn;
-      const bool b_mn = KIND == OPEN_DEPTH || (KIND == OPEN_STACK && P.b_mn);
-      const uint32_t a_step = (a_mn ? 2048 : 32) / 16, b_step = (b_mn ? 2048 : 32) / 16;
-      const uint32_t a_jump = (a_mn ? 4 * 2048 : OCHUNK) / 16;
-      const uint32_t b_jump = (b_mn ? 4 * 2048 : OCHUNK) / 16;
-      const uint64_t a_desc = smem_desc(smem_u32(stages), a_mn ? OCHUNK : 16, 1024, LAYOUT_SW128);
-      const uint64_t b_desc =
-          smem_desc(smem_u32(stages) + OA_BYTES, b_mn ? OCHUNK : 16, 1024, LAYOUT_SW128);
+      const uint64_t a_k = smem_desc(smem_u32(stages), 16, 1024, LAYOUT_SW128);
+      const uint64_t a_m = smem_desc(smem_u32(stages), OCHUNK, 1024, LAYOUT_SW128);
+      bool a_mn = KIND == OPEN_DEPTH || P.a_mn, b_mn = KIND == OPEN_DEPTH;
       uint32_t stage = 0, sphase = 0, acc = 0, acc_phase = 0, cut_phase = 0;
       bool ok = true;
+      OpenWalk walk;
+      const auto advance = [&](OpenTile& t) {
+        return open_next<KIND>(P, list, total, ring, leader, wc, walk, t);
+      };
       OpenTile t, next;
-      bool more = open_tile<KIND>(P, list, total, 0, t);
+      bool more = advance(t);
       // the MMAs of the block in slot `at`, the first `steps` of them
       const auto block = [&](uint32_t at, int steps, uint32_t d_tmem, uint32_t idesc, bool first) {
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t ad = a_desc + at * (OSTAGE / 16), bd = b_desc + at * (OSTAGE / 16);
+          const uint32_t a_step = (a_mn ? 2048 : 32) / 16, b_step = (b_mn ? 2048 : 32) / 16;
+          const uint32_t a_jump = (a_mn ? 4 * 2048 : OCHUNK) / 16;
+          const uint32_t b_jump = (b_mn ? 4 * 2048 : OCHUNK) / 16;
+          const uint64_t ad = (a_mn ? a_m : a_k) + at * (OSTAGE / 16);
+          const uint64_t bd = (b_mn ? a_m : a_k) + at * (OSTAGE / 16) + OA_BYTES / 16;
           if (steps == OK_ / 16) {
 #pragma unroll
             for (int kk = 0; kk < OK_ / 16; ++kk)
@@ -519,12 +679,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         }
         __syncwarp();
       };
-      for (int64_t i = 1; ok && more; ++i, t = next) {
+      for (; ok && more; t = next) {
         if (t.kb == 0) {
-          more = open_tile<KIND>(P, list, total, i, next);
+          more = advance(next);
           continue;
         }
-        const uint32_t idesc = P.idesc | (static_cast<uint32_t>(t.nb >> 3) << 17);
+        uint32_t idesc = P.idesc | (static_cast<uint32_t>(t.nb >> 3) << 17);
+        int depth = KIND == OPEN_DEPTH ? t.k1 - t.k0 : P.K;
+        if constexpr (KIND == OPEN_CHAIN) {
+          const OpenPhase& ph = P.ph[t.k1];
+          a_mn = ph.a_mn;
+          b_mn = ph.b_mn;
+          idesc |= ph.idesc;
+          depth = ph.K;
+        }
         ok = warp_all(mbar_wait(&tempty[acc], acc_phase ^ 1u, wc));
         if (!ok) break;
         tc_fence_after();
@@ -532,10 +700,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         const bool tail = KIND == OPEN_DEPTH && open_tail(t) != 0;
         const int place = tail ? open_cut_place(t) : -1;
         // steps of the tile's last block
-        const int depth = KIND == OPEN_DEPTH ? t.k1 - t.k0 : P.K;
         const int last_steps = (depth - (t.kb - 1) * OK_ + 15) >> 4;
         uint32_t held = 0, held_phase = 0;
-        bool first = true;
+        bool first = true, known = false;
         for (int j = 0; j < t.kb; ++j) {
           if (j == place) {  // its MMAs go last
             held = stage;
@@ -550,7 +717,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
             stage = 0;
             sphase ^= 1u;
           }
-          if (j == 0) more = open_tile<KIND>(P, list, total, i, next);  // beside the MMAs
+          if (j == 0 && (known = open_known<KIND>(ring, leader, walk)))
+            more = advance(next);  // beside the MMAs
         }
         if (!ok) break;
         if (tail) {
@@ -564,6 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         __syncwarp();
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
+        if (!known) more = advance(next);
       }
       if (elect_one()) umma_commit_pair(mma_done, 0x1);
       __syncwarp();
@@ -597,6 +766,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&cut[last]), 0));
     }
+  } else if (KIND == OPEN_CHAIN && warp == 2 + C::EPI_WARPS) {
+    if (leader && lane == 0) {
+      // -------------------------------------------------------- tile scheduler
+      uint32_t slot = 0, phase = 0;
+      int u = atomicAdd(P.ticket, 1);
+      for (;;) {
+        int now = -1;
+        bool ok = true;
+        if (u < total) {
+          now = u;
+          u = atomicAdd(P.ticket, 1);  // the next one, used a tile later
+          OpenTile t;
+          chain_tile(P, list, now, t);
+          // every tile of the matrix in the products before: an arrival per
+          // epilogue warp of both CTAs
+          const int before = t.k0 / 3 * (P.ph[0].tiles + P.ph[1].tiles + P.ph[2].tiles) +
+                             (t.k1 > 0 ? P.ph[0].tiles : 0) + (t.k1 > 1 ? P.ph[1].tiles : 0);
+          if (before > 0) ok = counter_wait(&P.done[t.z], before * 2 * C::EPI_WARPS, wc);
+        }
+        if (!ok || !mbar_wait(&ring_empty[slot], phase ^ 1u, wc)) break;
+        ring.ticket[slot] = now;
+        st_shared_cluster(mapa_shared(smem_u32(&ring.ticket[slot]), 1), now);
+        mbar_arrive_cluster(mapa_shared(smem_u32(&ring_full[slot]), 1));
+        mbar_arrive(&ring_full[slot]);
+        if (++slot == O_RING) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        if (now < 0) break;
+      }
+    }
   } else {
     // ------------------------------------------------------------- epilogue
     const int q4 = warp & 3;
@@ -609,18 +809,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
     uint32_t acc = 0, acc_phase = 0;
     const uint32_t tempty_cl[2] = {mapa_shared(smem_u32(&tempty[0]), 0),
                                    mapa_shared(smem_u32(&tempty[1]), 0)};
-    // staged results (after stage_d / stage_t of every lane) to memory
+    // a chunk to memory, as rows of m or (transposed) of n
     const auto put_d = [&](bool half16, const float (&v)[32], uint16_t* dst, int64_t ld, int rows,
                            int cols) {
       __syncwarp();
-      stage_d(sb, lane, half16, v);
+      if (half16)
+        stage_d<true>(sb, lane, v);
+      else
+        stage_d<false>(sb, lane, v);
       __syncwarp();
       emit(sb, lane, dst, ld, rows, cols);
     };
     const auto put_t = [&](bool half16, const float (&v)[32], uint16_t* dst, int64_t ld, int rows,
                            int cols) {
       __syncwarp();
-      stage_t(sb, lane, half16, v);
+      if (half16)
+        stage_t<true>(sb, lane, v);
+      else
+        stage_t<false>(sb, lane, v);
       __syncwarp();
       emit(sb, lane, dst, ld, rows, cols);
     };
@@ -638,15 +844,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         *reinterpret_cast<uint4*>(out + r * P.M + c * 8) = make_uint4(0, 0, 0, 0);
       }
     }
+    // CHAIN: this warp's part of a tile of matrix z is written (by all its lanes; later
+    // products of the matrix load it by asynchronous copies)
+    const auto written = [&](int z) {
+      fence_proxy_async_global();
+      __syncwarp();
+      if (lane == 0) red_release_add(&P.done[z], 1);
+    };
+    int pending = -1;  // matrix of a tile that is yet to be signalled
+    OpenWalk walk;
     OpenTile t;
-    for (int64_t i = 0; open_tile<KIND>(P, list, total, i, t); ++i) {
+    bool more = open_next<KIND>(P, list, total, ring, leader, wc, walk, t);
+    const auto advance = [&]() {
+      more = open_next<KIND>(P, list, total, ring, leader, wc, walk, t);
+    };
+    while (more) {
       const int mw = t.m0 + 128 * static_cast<int>(rank) + q4 * 32;  // this warp's rows of m
-      const int mrows = P.M - mw;                                    // ... those that exist
+      const OpenPhase& ph = P.ph[KIND == OPEN_CHAIN ? t.k1 : 0];
+      const int M = KIND == OPEN_CHAIN ? ph.M : P.M, N = KIND == OPEN_CHAIN ? ph.N : P.N;
+      const int mrows = M - mw;  // ... those that exist
       // chunks that hold results
       const int nch = mrows <= 0 ? 0
                       : KIND == OPEN_ROWS
                           ? (t.nv + 31) >> 5
-                          : min(8, (P.N - t.n0 + 31) >> 5);
+                          : min(8, (N - t.n0 + 31) >> 5);
       if constexpr (KIND == OPEN_DEPTH) {
         if (t.kb == 0) {  // an expert with no rows: zeros
           uint16_t* dst = out + (static_cast<int64_t>(t.z) * P.M + mw) * P.N + t.n0;
@@ -656,82 +877,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
               *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(row) * P.N + col) =
                   make_uint4(0, 0, 0, 0);
           }
+          advance();
           continue;
         }
       }
-      // STACK: what a chunk adds, loaded a chunk ahead
+      // CHAIN: v = alpha acc + beta h + gamma l (+ d on the diagonal), h and l loaded a
+      // chunk ahead.  (One body for the three products: with a copy for each, and two
+      // chunks in flight, its instructions came from L2 and a chunk took 2300 cycles.)
+      const bool sum = KIND == OPEN_CHAIN && t.k1 == 1;   // B = c A A + b A + d I
+      const bool upd = KIND == OPEN_CHAIN && t.k1 == 2;   // X
+      const int step = KIND == OPEN_CHAIN ? t.k0 / 3 : 0;
+      const bool last = upd && step == P.steps - 1;       // ... the result
+      const OpenFactors& fa = P.f[step];
+      const bool low = upd && fa.low;                     // X has a lo
+      const int64_t ld = KIND == OPEN_CHAIN ? (upd ? P.ld_x : P.ld_a) : N;
+      const int64_t in_at = (static_cast<int64_t>(t.z) * M + mw) * ld + t.n0;
+      const int from = step & 1;
+      const __half* in_h = sum ? P.a_out : P.x_hi[from];
+      const __half* in_l = P.x_lo[from];
       uint4 qh[4], ql[4];
-      const int64_t in_at = (static_cast<int64_t>(t.z) * P.M + mw) * P.ld_in + t.n0;
       const auto fetch_in = [&](int c) {
-        const int cols = static_cast<int>(P.ld_in) - t.n0 - 32 * c;  // (rows are padded to 8)
-        fetch(P.in_hi + in_at + 32 * c, lane, P.ld_in, mrows, cols, qh);
-        if (P.epi != OPEN_EPI_POLY) fetch(P.in_lo + in_at + 32 * c, lane, P.ld_in, mrows, cols, ql);
+        const int cols = static_cast<int>(ld) - t.n0 - 32 * c;  // (rows are padded to 8)
+        if (sum || upd) fetch(in_h + in_at + 32 * c, lane, ld, mrows, cols, qh);
+        if (low) fetch(in_l + in_at + 32 * c, lane, ld, mrows, cols, ql);
       };
-      const bool adds = KIND == OPEN_STACK && P.epi != OPEN_EPI_GRAM;
-      if (adds && first < nch) fetch_in(first);
+      float alpha = 1.f, beta = 0.f, gamma = 0.f;
+      if constexpr (KIND == OPEN_CHAIN) {
+        if (first < nch) fetch_in(first);
+        // scale of the stored first X (1 afterwards)
+        const float rz = step == 0 && !sum ? __ldcg(P.factor + t.z) : 1.f;
+        alpha = sum ? fa.alpha_b : upd ? fa.alpha_x * rz : fa.alpha_a * (rz * rz);
+        beta = sum ? fa.beta_b : fa.beta_x * rz;
+        gamma = fa.gamma_x * rz;
+        if (pending >= 0) written(pending);  // the tile before, behind this one's first loads
+        pending = -1;
+      }
       bool got = false;
       if (lane == 0) got = mbar_wait(&tfull[acc], acc_phase, wc);
       __syncwarp();
       if (!__shfl_sync(0xffffffffu, got, 0)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q4 * 32) << 16) + acc * 256;
-      uint32_t r[32];
-      if (first < nch) tmem_ld32(taddr + first * 32, r);
-      for (int c = first; c < nch; c += SHARE) {
-        tmem_ld_wait_for(r);
-        float v[32];
+      if constexpr (KIND != OPEN_CHAIN) {
+        uint32_t r[32];
+        if (first < nch) tmem_ld32(taddr + first * 32, r);
+        for (int c = first; c < nch; c += SHARE) {
+          tmem_ld_wait_for(r);
+          float v[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-        if (c + SHARE < nch) tmem_ld32(taddr + (c + SHARE) * 32, r);  // beside this chunk's work
-        const int n = t.n0 + 32 * c;
-        if constexpr (KIND == OPEN_ROWS) {
-          put_t(f16, v, out + static_cast<int64_t>(n) * P.M + mw, P.M, t.nv - 32 * c, mrows);
-        } else if constexpr (KIND == OPEN_DEPTH) {
-          put_d(f16, v, out + (static_cast<int64_t>(t.z) * P.M + mw) * P.N + n, P.N, mrows,
-                P.N - n);
-        } else {
-          const int m = mw + lane;
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          if (c + SHARE < nch) tmem_ld32(taddr + (c + SHARE) * 32, r);  // beside this chunk's work
+          if constexpr (KIND == OPEN_ROWS)
+            put_t(f16, v, out + static_cast<int64_t>(t.n0 + 32 * c) * P.M + mw, P.M,
+                  t.nv - 32 * c, mrows);
+          else
+            put_d(f16, v, out + in_at + 32 * c, ld, mrows, N - t.n0 - 32 * c);
+        }
+      } else {
+        uint16_t* dst = reinterpret_cast<uint16_t*>(sum ? P.b_out : upd ? P.x_hi[from ^ 1] : P.a_out);
+        const bool mirror = !upd && t.n0 > t.m0, split = upd && !last && P.f[step + 1].low;
+#pragma unroll 1
+        for (int c = first; c < nch; c += SHARE) {
+          uint32_t r[32];
+          float v[32];
+          tmem_ld32(taddr + c * 32, r);
+          tmem_ld_wait_for(r);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = alpha * __uint_as_float(r[j]);
+          if (sum || upd) turn(sb, lane, qh, [&](int j, float x) { v[j] = fmaf(beta, x, v[j]); });
+          if (low) turn(sb, lane, ql, [&](int j, float x) { v[j] = fmaf(gamma, x, v[j]); });
+          if (c + SHARE < nch) fetch_in(c + SHARE);
+          const int n = t.n0 + 32 * c;
+          if (sum && n == mw) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += lane == j ? fa.gamma_b : 0.f;
+          }
+          if (last) {
+            uint16_t* to = out + (static_cast<int64_t>(t.z) * M + mw) * N + n;
+            if (!P.plain_out) {
+              put_d(f16, v, to, N, mrows, N - n);
+            } else {  // rows that are not 16-byte aligned: a row of 32 elements at a time
+              __syncwarp();
+              if (f16)
+                stage_d<true>(sb, lane, v);
+              else
+                stage_d<false>(sb, lane, v);
+              __syncwarp();
+              if (n + lane < N)
+#pragma unroll 4
+                for (int j = 0; j < min(32, mrows); ++j)
+                  to[static_cast<int64_t>(j) * N + lane] = *reinterpret_cast<const uint16_t*>(
+                      unit_at(sb, j, lane >> 3) + (lane & 7) * 2);
+            }
+            continue;
+          }
           const int64_t at = in_at + 32 * c;
-          const int cols = static_cast<int>(P.ld_in) - n;
-          float h[32];
-          if (P.epi == OPEN_EPI_GRAM || P.epi == OPEN_EPI_POLY) {
+          const int cols = static_cast<int>(ld) - n;
+          put_d(true, v, dst + at, ld, mrows, cols);
+          if (mirror)  // (the results are symmetric)
+            put_t(true, v, dst + (static_cast<int64_t>(t.z) * M + n) * ld + mw, ld, M - n,
+                  static_cast<int>(ld) - mw);
+          if (split) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= P.alpha;
-            if (P.epi == OPEN_EPI_POLY) {
-              turn(sb, lane, qh, h);
-              if (c + SHARE < nch) fetch_in(c + SHARE);
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                v[j] = fmaf(P.beta, h[j], v[j]) + (m == n + j ? P.gamma : 0.f);
-            }
-            put_d(true, v, out + at, P.ld_in, mrows, cols);
-            if (t.n0 > t.m0)  // the mirrored chunk (the results are symmetric)
-              put_t(true, v, out + (static_cast<int64_t>(t.z) * P.M + n) * P.ld_in + mw, P.ld_in,
-                    P.M - n, static_cast<int>(P.ld_in) - mw);
-          } else {
-            // X <- alpha acc + beta hi + gamma lo
-            turn(sb, lane, qh, h);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fmaf(P.beta, h[j], P.alpha * v[j]);
-            turn(sb, lane, ql, h);
-            if (c + SHARE < nch) fetch_in(c + SHARE);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fmaf(P.gamma, h[j], v[j]);
-            if (P.epi == OPEN_EPI_UPDATE) {
-              put_d(true, v, out + at, P.ld_in, mrows, cols);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] -= half_round(v[j]);
-              put_d(true, v, static_cast<uint16_t*>(P.out_lo) + at, P.ld_in, mrows, cols);
-            } else if (!P.plain_out) {
-              put_d(f16, v, out + (static_cast<int64_t>(t.z) * P.M + mw) * P.N + n, P.N, mrows,
-                    P.N - n);
-            } else if (lane < mrows) {
-              // rows of the result that are not 16-byte aligned (N no multiple of 8)
-              uint16_t* dst = out + (static_cast<int64_t>(t.z) * P.M + m) * P.N + n;
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (n + j < P.N) dst[j] = static_cast<uint16_t>(pack16(f16, v[j], 0.f) & 0xFFFFu);
-            }
+            for (int j = 0; j < 32; ++j) v[j] -= half_round(v[j]);
+            put_d(true, v, reinterpret_cast<uint16_t*>(P.x_lo[from ^ 1]) + at, ld, mrows, cols);
           }
         }
       }
@@ -745,7 +994,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       }
       acc ^= 1u;
       if (acc == 0) acc_phase ^= 1u;
+      if constexpr (KIND == OPEN_CHAIN) {
+        pending = t.z;
+        if (!open_known<KIND>(ring, leader, walk)) {  // the next one may wait for this one
+          written(pending);
+          pending = -1;
+        }
+      }
+      advance();
     }
+    if (pending >= 0) written(pending);
   }
 
   tc_fence_before();
@@ -837,7 +1095,7 @@ int launch_open_depth(const GemmEnv& env, bool f16, const void* a, int64_t ld_a,
   OpenMaps maps;
   open_common(env, &P);
   P.idesc = open_idesc(f16, true, true);
-  P.a_mn = P.b_mn = 1;
+  P.a_mn = 1;
   P.M = static_cast<int>(M);
   P.N = static_cast<int>(N);
   P.Z = static_cast<int>(E);
@@ -854,37 +1112,69 @@ int launch_open_depth(const GemmEnv& env, bool f16, const void* a, int64_t ld_a,
   return launch_open<OPEN_DEPTH>(env, P, maps, E * static_cast<int64_t>(P.tiles));
 }
 
-int launch_open_stack(const GemmEnv& env, const OpenStack& s) {
+int64_t open_chain_tiles(int64_t M, int64_t N, int64_t Z, int64_t steps) {
+  const int64_t m = (std::min(M, N) + 255) / 256, n = (std::max(M, N) + 255) / 256;
+  return Z * steps * (m * (m + 1) + m * n);
+}
+
+int launch_open_chain(const GemmEnv& env, const OpenChain& s) {
   OpenParams P{};
   OpenMaps maps;
   open_common(env, &P);
-  P.idesc = open_idesc(true, s.a_mn, s.b_mn);
-  P.a_mn = s.a_mn;
-  P.b_mn = s.b_mn;
-  P.M = static_cast<int>(s.M);
-  P.N = static_cast<int>(s.N);
-  P.Z = static_cast<int>(s.a.batch);
-  P.K = static_cast<int>(s.K);
-  P.kb = static_cast<int>((s.K + OK_ - 1) / OK_);
-  P.mt = static_cast<int>((s.M + 255) / 256);
-  P.nt = static_cast<int>((s.N + 255) / 256);
-  P.epi = s.epi;
-  P.sym = s.epi == OPEN_EPI_GRAM || s.epi == OPEN_EPI_POLY;
-  P.tiles = P.sym ? P.mt * (P.mt + 1) / 2 : P.mt * P.nt;
-  P.alpha = s.alpha;
-  P.beta = s.beta;
-  P.gamma = s.gamma;
-  P.in_hi = static_cast<const __half*>(s.in_hi);
-  P.in_lo = static_cast<const __half*>(s.in_lo);
-  P.ld_in = s.ld_in;
+  const bool wide = s.M <= s.N;
+  const int64_t m = std::min(s.M, s.N);
+  P.idesc = open_idesc(true, false, false);
+  P.Z = static_cast<int>(s.Z);
+  P.steps = s.steps;
+  std::copy(s.f, s.f + s.steps, P.f);
+  const auto phase = [&](OpenPhase& p, int64_t M, int64_t N, int64_t K, int a, bool a_mn, int b,
+                         bool b_mn, bool sym) {
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.K = static_cast<int>(K);
+    p.kb = static_cast<int>((K + OK_ - 1) / OK_);
+    p.mt = static_cast<int>((M + 255) / 256);
+    p.nt = static_cast<int>((N + 255) / 256);
+    p.sym = sym;
+    p.tiles = sym ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
+    p.a = a;
+    p.b = b;
+    p.a_mn = a_mn;
+    p.b_mn = b_mn;
+    p.idesc = open_idesc(true, a_mn, b_mn);
+  };
+  // A: the rows (wide) or columns of X against each other; B: A A; X: B X (X's rows are
+  // the contraction) or X B
+  phase(P.ph[0], m, m, wide ? s.N : s.M, 0, !wide, 0, !wide, true);
+  phase(P.ph[1], m, m, m, 1, false, 1, false, true);
+  if (wide)
+    phase(P.ph[2], s.M, s.N, m, 2, false, 0, true, false);
+  else
+    phase(P.ph[2], s.M, s.N, m, 0, false, 2, false, false);
+  P.ld_x = s.ld_x;
+  P.ld_a = s.ld_a;
+  for (int i = 0; i < 2; ++i) {
+    P.x_hi[i] = s.x_hi[i];
+    P.x_lo[i] = s.x_lo[i];
+  }
+  P.a_out = s.a;
+  P.b_out = s.b;
+  P.factor = s.factor;
+  P.ticket = s.ticket;
+  P.done = s.done;
   P.out = s.out;
-  P.out_lo = s.out_lo;
   P.out_f16 = s.out_f16;
-  int rc = encode_operand(env, &maps.a, true, s.a);
-  rc |= encode_operand(env, &maps.b, true, s.b);
   P.plain_out = s.N % 8 != 0 || (reinterpret_cast<uintptr_t>(s.out) & 15u) != 0;
+  int rc = HMM_OK;
+  for (int i = 0; i < 2; ++i)
+    rc |= encode_operand(env, &maps.brows[i], true,
+                         OpenOperand{s.x_hi[i], s.M, s.N, s.Z, s.ld_x, s.M * s.ld_x});
+  rc |= encode_operand(env, &maps.a, true, OpenOperand{s.a, m, m, s.Z, s.ld_a, m * s.ld_a});
+  rc |= encode_operand(env, &maps.b, true, OpenOperand{s.b, m, m, s.Z, s.ld_a, m * s.ld_a});
   if (rc != HMM_OK) return HMM_ERR_CUDA;
-  return launch_open<OPEN_STACK>(env, P, maps, P.Z * static_cast<int64_t>(P.tiles));
+  // (a product of the whole stack at once is all that can run)
+  const int64_t most = s.Z * std::max(P.ph[2].tiles, P.ph[0].tiles);
+  return launch_open<OPEN_CHAIN>(env, P, maps, most);
 }
 
 }  // namespace hmm

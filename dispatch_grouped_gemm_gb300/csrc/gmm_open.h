@@ -10,19 +10,29 @@ namespace hmm {
 
 constexpr int OPEN_ROWS = 0;
 constexpr int OPEN_DEPTH = 1;
-constexpr int OPEN_STACK = 2;
+constexpr int OPEN_CHAIN = 2;
 
-// Epilogues of OPEN_STACK on acc(m, n), operands and results in fp16:
-//   GRAM    out = alpha acc                                   symmetric
-//   POLY    out = alpha acc + beta in_hi + gamma [m = n]      symmetric
-//   UPDATE  v = alpha acc + beta in_hi + gamma in_lo; out = fp16(v), out_lo = fp16(v - out)
-//   LAST    the same v as the caller's result (bf16 or fp16)
-// A symmetric result is computed for tiles on and above the diagonal and written
-// twice.
-constexpr int OPEN_EPI_GRAM = 0;
-constexpr int OPEN_EPI_POLY = 1;
-constexpr int OPEN_EPI_UPDATE = 2;
-constexpr int OPEN_EPI_LAST = 3;
+// OPEN_CHAIN: `steps` Newton-Schulz steps over Z matrices in one launch, three products
+// a step, operands and results in fp16 (gmm_open.cu; ortho.cu has the mathematics):
+//   0  A  = alpha_a X X^T                              symmetric
+//   1  B  = alpha_b A A + beta_b A + gamma_b I         symmetric
+//   2  v  = alpha_x B X + beta_x hi + gamma_x lo;  hi' = fp16(v), lo' = fp16(v - hi'),
+//      of the last step the caller's result (bf16 or fp16)
+// A symmetric result is computed for tiles on and above the diagonal and written twice.
+// The first X is stored without a factor `factor[z]` of its matrix.
+struct OpenFactors {
+  float alpha_a, alpha_b, beta_b, gamma_b, alpha_x, beta_x, gamma_x;
+  int low;  // the X that this step reads has a lo
+};
+
+struct OpenPhase {
+  int M, N, K, kb;    // extents, depth in blocks
+  int mt, nt, tiles;  // 256-tiles of m, of n, per matrix
+  int sym;
+  int a, b;           // operands: 0 X, 1 A, 2 B
+  int a_mn, b_mn;     // ... with m / n contiguous
+  uint32_t idesc;
+};
 
 // [batch][rows][cols], rows ld and matrices stride elements apart (multiples of 8;
 // 16-byte aligned)
@@ -33,29 +43,35 @@ struct OpenOperand {
 
 struct OpenParams {
   int M, N, Z, R;     // extent of m, of n; experts or matrices; rows
-  int K, kb;          // depth, in blocks (DEPTH: per expert)
-  int mt, nt, tiles;  // 256-tiles of m, of n, per expert or matrix
-  int a_mn, b_mn;     // operands with m / n contiguous
-  int sym, epi, out_f16, plain_out;
+  int K, kb;          // depth, in blocks (ROWS)
+  int mt, nt, tiles;  // 256-tiles of m, of n, per expert (DEPTH)
+  int a_mn;           // w with m contiguous (ROWS)
+  int out_f16, plain_out;
   uint32_t idesc;
-  float alpha, beta, gamma;
   const int32_t* offsets;  // [Z + 1] rows of the experts
-  const __half *in_hi, *in_lo;
-  int64_t ld_in;           // of in_hi, in_lo and of fp16 results
-  void *out, *out_lo;
+  void* out;
   unsigned* status;
   unsigned long long budget_ns;
+  // CHAIN
+  int steps;
+  OpenPhase ph[3];
+  OpenFactors f[HMM_ORTHO_MAX_STEPS];
+  int64_t ld_x, ld_a;
+  __half *x_hi[2], *x_lo[2], *a_out, *b_out;
+  const float* factor;     // [Z]
+  int *ticket, *done;      // zero at launch; done [Z]
 };
 
-struct OpenStack {
-  OpenOperand a, b;
-  bool a_mn, b_mn;
-  int64_t M, N, K;
-  int epi;
-  float alpha, beta, gamma;
-  const void *in_hi, *in_lo;
-  int64_t ld_in;           // of in_hi, in_lo and the fp16 results (LAST is dense)
-  void *out, *out_lo;
+struct OpenChain {
+  int64_t M, N, Z;
+  int steps;
+  const OpenFactors* f;
+  __half *x_hi[2], *x_lo[2];  // [Z, M, ld_x], the first X in [0]
+  __half *a, *b;              // [Z, m, ld_a]
+  int64_t ld_x, ld_a;         // multiples of 8
+  const float* factor;        // [Z]
+  int *ticket, *done;         // device counters, zero
+  void* out;                  // [Z, M, N]
   int out_f16;
 };
 
@@ -68,6 +84,8 @@ int launch_open_rows(const GemmEnv& env, bool f16, const OpenOperand& w, bool w_
 int launch_open_depth(const GemmEnv& env, bool f16, const void* a, int64_t ld_a, int64_t M,
                       const void* b, int64_t ld_b, int64_t N, int64_t R, int64_t E,
                       const int32_t* offsets, void* out);
-int launch_open_stack(const GemmEnv& env, const OpenStack& s);
+// tiles of a chain (to be counted in 31 bits)
+int64_t open_chain_tiles(int64_t M, int64_t N, int64_t Z, int64_t steps);
+int launch_open_chain(const GemmEnv& env, const OpenChain& s);
 
 }  // namespace hmm

@@ -16,7 +16,8 @@
 // B X, only turns directions that X has, and is not multiplied.  So X is kept as
 // hi + lo, two fp16 (22 bits), and the epilogue adds a (hi + lo) in fp32, while the
 // products read hi alone: 0.2 % off for every spectrum, most of it the result's own
-// rounding to bf16 (0.17 %).  Three bits more than bf16 at the same rate are why it
+// rounding to bf16 (0.17 %).  (Where the steps that are left multiply by at most 4, hi
+// alone does: 0.19 %.)  Three bits more than bf16 at the same rate are why it
 // is fp16: its range is enough, because every matrix here has a known bound.
 //   Bounds.  All singular values of X lie in [0, u] with u = 1 at first and then
 // the largest |a s + b s^3 + c s^5| on [0, u]; an element is at most the largest
@@ -24,16 +25,20 @@
 // at most 2^14 in storage, a quarter of fp16's range.  B is stored as B + d I with d
 // = -(b + c): where X is nearly orthogonal its diagonal is near b + c, and without
 // it the rounding of the diagonal alone costs as much as all others; the epilogue
-// takes d hi off again.
+// takes d hi off again.  The first X is G times a power of two, the rest of 1 / (|G|
+// + eps), in [1, 2), goes into the first step's factors: so a 16-bit G is exact in hi
+// alone (but for elements 2^28 below the norm) and has no lo.
 //
-// Bounds of time: 3 m^2 n + m^3 operations per step (A and A A are symmetric: one
+// What bounds it: 3 m^2 n + m^3 operations per step (A and A A are symmetric: one
 // triangle of tiles each) at the tensor rate; between them X moves four times
-// (hi, lo in and out).  The norm and the first conversion read G twice.
+// (hi, lo in and out), which the other products hide.  The norm and the first
+// conversion read G twice.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "gmm_open.h"
 
@@ -42,7 +47,8 @@ namespace hmm {
 namespace {
 
 constexpr int ORTHO_THREADS = 256;
-constexpr int64_t ORTHO_PIECE = 32768;  // elements per block and matrix, at least
+constexpr int64_t ORTHO_PIECE = 8192;     // elements per block and matrix, at least
+constexpr int64_t ORTHO_BLOCKS = 152 * 8;  // blocks of the stack that fill the device
 constexpr int ORTHO_MAX_PIECES = 256;
 
 // Sums of squares in three ranges, so that neither the squares of large elements
@@ -68,6 +74,24 @@ __device__ __forceinline__ void sum_add(Sums& s, float v) {
   }
 }
 
+// The block's sums in its first thread.
+__device__ __forceinline__ void sums_reduce(Sums& s, Sums* part) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    s.big += __shfl_xor_sync(0xffffffffu, s.big, d);
+    s.mid += __shfl_xor_sync(0xffffffffu, s.mid, d);
+    s.small += __shfl_xor_sync(0xffffffffu, s.small, d);
+  }
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int w = 1; w < ORTHO_THREADS / 32; ++w) {
+      s.big += part[w].big;
+      s.mid += part[w].mid;
+      s.small += part[w].small;
+    }
+}
+
 __device__ __forceinline__ float ortho_get(float v) { return v; }
 __device__ __forceinline__ float ortho_get(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float ortho_get(__half v) { return __half2float(v); }
@@ -77,115 +101,149 @@ struct OrthoArgs {
   int64_t M, N, ld, stride;
   int pieces;
   int64_t rows_per_piece;
-  Sums* sums;  // [batch][pieces]
-  __half *hi, *lo;
+  Sums* sums;     // [batch][pieces]
+  float* factor;  // [batch]
+  int *ticket, *done;  // counters of the products: set to zero
+  __half *hi, *lo;     // lo null: not needed
   int64_t ld_x;
   float eps;
-  float scale;  // 2^e of the stored X
+  float scale;  // 2^e of X
 };
 
-// Eight elements of a row at a time (VEC: 16-byte aligned rows), the last ones of a
-// row one by one.
-template <typename T, bool VEC, typename F>
+// Eight elements from any element address, the first `valid` of them (the others 0):
+// as aligned 16-byte words that hold one of them, shifted together.
+template <typename T>
+__device__ __forceinline__ void load8(const T* src, int valid, float (&v)[8]) {
+  constexpr int B = sizeof(T), W = B == 4 ? 3 : 2;
+  if (valid == 8 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+    alignas(16) T e[8];
+#pragma unroll
+    for (int k = 0; k < B / 2; ++k)
+      reinterpret_cast<uint4*>(e)[k] = __ldg(reinterpret_cast<const uint4*>(src) + k);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = ortho_get(e[j]);
+    return;
+  }
+  const uintptr_t at = reinterpret_cast<uintptr_t>(src);
+  const int off = static_cast<int>(at & 15u);
+  const uint4* p = reinterpret_cast<const uint4*>(at - off);
+  uint32_t w[4 * W + 1];
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (16 * k < off + valid * B) q = __ldg(p + k);
+    w[4 * k] = q.x;
+    w[4 * k + 1] = q.y;
+    w[4 * k + 2] = q.z;
+    w[4 * k + 3] = q.w;
+  }
+  w[4 * W] = 0;
+  const int word = off >> 2;
+  if (word & 1) {
+#pragma unroll
+    for (int k = 0; k < 4 * W; ++k) w[k] = w[k + 1];
+  }
+  if (word & 2) {
+#pragma unroll
+    for (int k = 0; k < 4 * W - 1; ++k) w[k] = w[k + 2];
+  }
+  T e[8];
+  if constexpr (B == 2) {
+    uint32_t t[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t[k] = __funnelshift_r(w[k], w[k + 1], (off & 2) * 8);
+    memcpy(e, t, sizeof e);
+  } else {
+    memcpy(e, w, sizeof e);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = j < valid ? ortho_get(e[j]) : 0.f;
+}
+
+// The piece's rows in units of eight elements, four units of a thread in flight.
+template <typename T, typename F>
 __device__ __forceinline__ void ortho_walk(const OrthoArgs& a, const F& f) {
+  constexpr int U = 4;
   const int64_t r0 = blockIdx.x * a.rows_per_piece, r1 = min(a.M, r0 + a.rows_per_piece);
-  const int64_t per = (a.N + 7) / 8;
+  const uint32_t per = static_cast<uint32_t>((a.N + 7) / 8);
+  const uint32_t n = r1 > r0 ? static_cast<uint32_t>(r1 - r0) * per : 0;
   const T* g = static_cast<const T*>(a.g) + blockIdx.y * a.stride;
-  for (int64_t i = threadIdx.x; i < (r1 - r0) * per; i += ORTHO_THREADS) {
-    const int64_t q = i / per, r = r0 + q, c = (i - q * per) * 8;
-    const T* src = g + r * a.ld + c;
-    float v[8];
-    if (VEC && c + 8 <= a.N) {
-      alignas(16) T t[8];
+  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += U * ORTHO_THREADS) {
+    float v[U][8];
+    int64_t r[U];
+    int c[U];
 #pragma unroll
-      for (int j = 0; j < static_cast<int>(8 * sizeof(T) / 16); ++j)
-        reinterpret_cast<uint4*>(t)[j] = reinterpret_cast<const uint4*>(src)[j];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = ortho_get(t[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = c + j < a.N ? ortho_get(src[j]) : 0.f;
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = i0 + u * ORTHO_THREADS, q = i / per;
+      r[u] = r0 + q;
+      c[u] = static_cast<int>(i - q * per) * 8;
+      if (i < n) load8(g + r[u] * a.ld + c[u], static_cast<int>(min(int64_t(8), a.N - c[u])), v[u]);
     }
-    f(r, c, v);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * ORTHO_THREADS < n) f(r[u], c[u], v[u]);
   }
 }
 
-template <typename T, bool VEC>
+template <typename T>
 __global__ void __launch_bounds__(ORTHO_THREADS) ortho_norm_kernel(const OrthoArgs a) {
   __shared__ Sums part[ORTHO_THREADS / 32];
   grid_dep_wait();
   grid_dep_launch();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.done[blockIdx.y] = 0;
+    if (blockIdx.y == 0) *a.ticket = 0;
+  }
   Sums s{0.f, 0.f, 0.f};
-  ortho_walk<T, VEC>(a, [&](int64_t, int64_t, const float (&v)[8]) {
+  ortho_walk<T>(a, [&](int64_t, int, const float (&v)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum_add(s, v[j]);
   });
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    s.big += __shfl_xor_sync(0xffffffffu, s.big, d);
-    s.mid += __shfl_xor_sync(0xffffffffu, s.mid, d);
-    s.small += __shfl_xor_sync(0xffffffffu, s.small, d);
-  }
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < ORTHO_THREADS / 32; ++w) {
-      s.big += part[w].big;
-      s.mid += part[w].mid;
-      s.small += part[w].small;
-    }
-    a.sums[static_cast<int64_t>(blockIdx.y) * a.pieces + blockIdx.x] = s;
-  }
+  sums_reduce(s, part);
+  if (threadIdx.x == 0) a.sums[static_cast<int64_t>(blockIdx.y) * a.pieces + blockIdx.x] = s;
 }
 
-// Factor of the stored X_0 of a matrix, as two floats whose product it is (alone it
-// may lie outside fp32's range).  Every thread of a block.
-__device__ float2 ortho_factor(const OrthoArgs& a) {
-  __shared__ double part[3][ORTHO_THREADS / 32];
-  double big = 0, mid = 0, small = 0;
+// Power of two of the stored X_0 of a matrix, as two floats whose product it is (alone
+// it may lie outside fp32's range), and the rest of its factor.  Every thread of a block.
+__device__ float3 ortho_factor(const OrthoArgs& a) {
+  __shared__ Sums part[ORTHO_THREADS / 32];
+  __shared__ float3 result;
+  Sums s{0.f, 0.f, 0.f};
   for (int i = threadIdx.x; i < a.pieces; i += ORTHO_THREADS) {
-    const Sums s = a.sums[static_cast<int64_t>(blockIdx.y) * a.pieces + i];
-    big += s.big;
-    mid += s.mid;
-    small += s.small;
+    const Sums o = a.sums[static_cast<int64_t>(blockIdx.y) * a.pieces + i];
+    s.big += o.big;
+    s.mid += o.mid;
+    s.small += o.small;
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    big += __shfl_xor_sync(0xffffffffu, big, d);
-    mid += __shfl_xor_sync(0xffffffffu, mid, d);
-    small += __shfl_xor_sync(0xffffffffu, small, d);
-  }
-  if ((threadIdx.x & 31) == 0) {
-    part[0][threadIdx.x >> 5] = big;
-    part[1][threadIdx.x >> 5] = mid;
-    part[2][threadIdx.x >> 5] = small;
+  sums_reduce(s, part);
+  if (threadIdx.x == 0) {  // (the rate of 64-bit operations is low: one thread)
+    const double norm = sqrt(s.big * 0x1p160 + s.mid + s.small * 0x1p-160);
+    const double f = static_cast<double>(a.scale) / (norm + static_cast<double>(a.eps));
+    if (norm == 0.0) {  // a matrix of zeros stays zeros, with eps 0 too
+      result = make_float3(1.f, 1.f, 1.f);
+    } else if (!(f > 0.0)) {  // NaN, or 0 (infinite norm)
+      result = make_float3(1.f, 1.f, static_cast<float>(f));
+    } else {
+      int e = 0;
+      const double m = frexp(f, &e);  // f = 2 m 2^(e - 1), 2 m in [1, 2)
+      const int e1 = (e - 1) / 2;
+      result = make_float3(static_cast<float>(ldexp(1.0, e1)),
+                           static_cast<float>(ldexp(1.0, e - 1 - e1)), static_cast<float>(2.0 * m));
+    }
   }
   __syncthreads();
-  big = mid = small = 0;
-  for (int w = 0; w < ORTHO_THREADS / 32; ++w) {
-    big += part[0][w];
-    mid += part[1][w];
-    small += part[2][w];
-  }
-  const double norm = sqrt(big * 0x1p160 + mid + small * 0x1p-160);
-  const double f = static_cast<double>(a.scale) / (norm + static_cast<double>(a.eps));
-  // a matrix of zeros stays zeros, with eps 0 too
-  if (norm == 0.0) return make_float2(0.f, 0.f);
-  if (!(f > 0.0) || isinf(f)) return make_float2(static_cast<float>(f), 1.f);  // NaN, 0, inf
-  int e = 0;
-  const double m = frexp(f, &e);
-  const int e1 = e / 2;
-  return make_float2(static_cast<float>(ldexp(1.0, e1)), static_cast<float>(ldexp(m, e - e1)));
+  return result;
 }
 
-template <typename T, bool VEC>
+template <typename T>
 __global__ void __launch_bounds__(ORTHO_THREADS) ortho_first_kernel(const OrthoArgs a) {
   grid_dep_wait();
   grid_dep_launch();
-  const float2 f = ortho_factor(a);
+  const float3 f = ortho_factor(a);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.factor[blockIdx.y] = f.z;
   __half* hi = a.hi + blockIdx.y * a.M * a.ld_x;
-  __half* lo = a.lo + blockIdx.y * a.M * a.ld_x;
-  ortho_walk<T, VEC>(a, [&](int64_t r, int64_t c, const float (&v)[8]) {
+  __half* lo = a.lo ? a.lo + blockIdx.y * a.M * a.ld_x : nullptr;
+  ortho_walk<T>(a, [&](int64_t r, int c, const float (&v)[8]) {
     alignas(16) __half h[8], l[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -195,21 +253,17 @@ __global__ void __launch_bounds__(ORTHO_THREADS) ortho_first_kernel(const OrthoA
     }
     // (rows of X are padded to eight elements)
     *reinterpret_cast<uint4*>(hi + r * a.ld_x + c) = *reinterpret_cast<const uint4*>(h);
-    *reinterpret_cast<uint4*>(lo + r * a.ld_x + c) = *reinterpret_cast<const uint4*>(l);
+    if (lo) *reinterpret_cast<uint4*>(lo + r * a.ld_x + c) = *reinterpret_cast<const uint4*>(l);
   });
 }
 
 template <typename T>
 cudaError_t launch_first(const GemmEnv& env, const OrthoArgs& a, int64_t batch) {
-  const bool vec = (reinterpret_cast<uintptr_t>(a.g) & 15u) == 0 &&
-                   a.ld * sizeof(T) % 16 == 0 && a.stride * sizeof(T) % 16 == 0;
   const dim3 grid(static_cast<unsigned>(a.pieces), static_cast<unsigned>(batch));
-  cudaError_t e =
-      launch_kernel(vec ? ortho_norm_kernel<T, true> : ortho_norm_kernel<T, false>, grid,
-                    ORTHO_THREADS, 0, env.stream, env.pdl, 1, a);
+  cudaError_t e = launch_kernel(ortho_norm_kernel<T>, grid, ORTHO_THREADS, 0, env.stream, env.pdl,
+                                1, a);
   if (e != cudaSuccess) return e;
-  return launch_kernel(vec ? ortho_first_kernel<T, true> : ortho_first_kernel<T, false>, grid,
-                       ORTHO_THREADS, 0, env.stream, env.pdl, 1, a);
+  return launch_kernel(ortho_first_kernel<T>, grid, ORTHO_THREADS, 0, env.stream, env.pdl, 1, a);
 }
 
 int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
@@ -227,14 +281,8 @@ double largest(double u, const F& f) {
 // Exponent e with u 2^e at most 2^14.
 int scale_for(double u) { return static_cast<int>(std::floor(14 - std::log2(std::max(u, 1e-3)))); }
 
-struct OrthoStep {
-  float alpha_a;                     // A
-  float alpha_b, beta_b, gamma_b;    // B + d I
-  float alpha_x, beta_x, gamma_x;    // X
-};
-
 // The steps' factors; false if the coefficients let X grow past 2^20.
-bool ortho_steps(const hmm_ortho& d, OrthoStep* out) {
+bool ortho_steps(const hmm_ortho& d, OpenFactors* out) {
   constexpr double most = 1048576.0;
   double u = 1.0;
   int ex = scale_for(u);
@@ -248,7 +296,7 @@ bool ortho_steps(const hmm_ortho& d, OrthoStep* out) {
     const double un = largest(u, [&](double s) { return s * (a + b * s * s + c * s * s * s * s); });
     if (!(ub <= most && un <= most)) return false;
     const int ea = scale_for(u * u), eb = scale_for(ub), en = scale_for(un);
-    OrthoStep& s = out[i];
+    OpenFactors& s = out[i];
     s.alpha_a = static_cast<float>(std::ldexp(1.0, ea - 2 * ex));
     s.alpha_b = static_cast<float>(std::ldexp(c, eb - 2 * ea));
     s.beta_b = static_cast<float>(std::ldexp(b, eb - ea));
@@ -261,6 +309,11 @@ bool ortho_steps(const hmm_ortho& d, OrthoStep* out) {
     s.gamma_x = static_cast<float>(k * std::ldexp(a, e - ex));
     u = un;
     ex = en;
+  }
+  double gain = 1.0;  // of small singular values, in this step and those behind
+  for (int i = d.steps - 1; i >= 0; --i) {
+    gain *= std::max(1.0, std::fabs(static_cast<double>(d.coefficients[3 * i])));
+    out[i].low = gain > 4.0 && (i > 0 || d.dtype == HMM_DTYPE_F32);
   }
   return true;
 }
@@ -278,7 +331,9 @@ int check_ortho(const hmm_ortho* d) {
     return HMM_ERR_SHAPE;
   if (d->steps < 1 || d->steps > HMM_ORTHO_MAX_STEPS) return HMM_ERR_ARG;
   if (!(d->eps >= 0.f) || std::isinf(d->eps) || !std::isfinite(d->scale)) return HMM_ERR_ARG;
-  OrthoStep s[HMM_ORTHO_MAX_STEPS];
+  // (tickets of the products count in 31 bits)
+  if (open_chain_tiles(d->M, d->N, d->batch, d->steps) > INT32_MAX - 65536) return HMM_ERR_SHAPE;
+  OpenFactors s[HMM_ORTHO_MAX_STEPS];
   return ortho_steps(*d, s) ? HMM_OK : HMM_ERR_ARG;
 }
 
@@ -289,11 +344,14 @@ OrthoPlan ortho_plan(const hmm_ortho& d) {
   p.ld_a = round8(p.m);
   const int64_t n = d.M * round8(d.N);
   p.pieces = static_cast<int>(
-      std::min<int64_t>({(n + ORTHO_PIECE - 1) / ORTHO_PIECE, ORTHO_MAX_PIECES, d.M}));
+      std::min<int64_t>({(n + ORTHO_PIECE - 1) / ORTHO_PIECE, ORTHO_MAX_PIECES, d.M,
+                         ORTHO_BLOCKS / std::max<int64_t>(d.batch, 1) + 1}));
   p.rows_per_piece = (d.M + p.pieces - 1) / p.pieces;
   const size_t x = up256(static_cast<size_t>(d.batch) * d.M * p.ld_x * 2);
   const size_t a = up256(static_cast<size_t>(d.batch) * p.m * p.ld_a * 2);
-  size_t o = up256(static_cast<size_t>(d.batch) * p.pieces * sizeof(Sums));
+  p.off_factor = up256(static_cast<size_t>(d.batch) * p.pieces * sizeof(Sums));
+  p.off_ticket = p.off_factor + up256(static_cast<size_t>(d.batch) * sizeof(float));
+  size_t o = p.off_ticket + up256((static_cast<size_t>(d.batch) + 1) * sizeof(int));
   for (int i = 0; i < 4; ++i) {  // hi, lo of two X
     p.off_x[i] = o;
     o += x;
@@ -306,7 +364,7 @@ OrthoPlan ortho_plan(const hmm_ortho& d) {
 
 int launch_ortho(const GemmEnv& env, const hmm_ortho& d, const OrthoPlan& p, const void* g,
                  void* out, uint8_t* ws) {
-  OrthoStep steps[HMM_ORTHO_MAX_STEPS];
+  OpenFactors steps[HMM_ORTHO_MAX_STEPS];
   if (!ortho_steps(d, steps)) return HMM_ERR_ARG;
   OrthoArgs a{};
   a.g = g;
@@ -317,8 +375,11 @@ int launch_ortho(const GemmEnv& env, const hmm_ortho& d, const OrthoPlan& p, con
   a.pieces = p.pieces;
   a.rows_per_piece = p.rows_per_piece;
   a.sums = reinterpret_cast<Sums*>(ws);
+  a.factor = reinterpret_cast<float*>(ws + p.off_factor);
+  a.ticket = reinterpret_cast<int*>(ws + p.off_ticket);
+  a.done = a.ticket + 1;
   a.hi = reinterpret_cast<__half*>(ws + p.off_x[0]);
-  a.lo = reinterpret_cast<__half*>(ws + p.off_x[1]);
+  a.lo = steps[0].low ? reinterpret_cast<__half*>(ws + p.off_x[1]) : nullptr;
   a.ld_x = p.ld_x;
   a.eps = d.eps;
   a.scale = static_cast<float>(std::ldexp(1.0, scale_for(1.0)));
@@ -326,62 +387,26 @@ int launch_ortho(const GemmEnv& env, const hmm_ortho& d, const OrthoPlan& p, con
                         : d.dtype == HMM_DTYPE_F16 ? launch_first<__half>(env, a, d.batch)
                                                    : launch_first<__nv_bfloat16>(env, a, d.batch);
   if (e != cudaSuccess) return HMM_ERR_CUDA;
-  const bool wide = d.M <= d.N;
-  const int64_t m = p.m, lx = p.ld_x, la = p.ld_a;
-  const OpenOperand A{ws + p.off_a, m, m, d.batch, la, m * la};
-  const OpenOperand B{ws + p.off_b, m, m, d.batch, la, m * la};
-  for (int i = 0; i < d.steps; ++i) {
-    const OrthoStep& s = steps[i];
-    const int from = (i & 1) * 2, to = 2 - from;
-    const OpenOperand X{ws + p.off_x[from], d.M, d.N, d.batch, lx, d.M * lx};
-    const bool last = i == d.steps - 1;
-    // A: rows (wide) or columns of X against each other
-    OpenStack q{};
-    q.a = q.b = X;
-    q.a_mn = q.b_mn = !wide;
-    q.M = q.N = m;
-    q.K = wide ? d.N : d.M;
-    q.epi = OPEN_EPI_GRAM;
-    q.alpha = s.alpha_a;
-    q.out = ws + p.off_a;
-    q.ld_in = la;
-    int rc = launch_open_stack(env, q);
-    if (rc != HMM_OK) return rc;
-    // B + d I
-    q = OpenStack{};
-    q.a = q.b = A;
-    q.M = q.N = q.K = m;
-    q.epi = OPEN_EPI_POLY;
-    q.alpha = s.alpha_b;
-    q.beta = s.beta_b;
-    q.gamma = s.gamma_b;
-    q.in_hi = ws + p.off_a;
-    q.ld_in = la;
-    q.out = ws + p.off_b;
-    rc = launch_open_stack(env, q);
-    if (rc != HMM_OK) return rc;
-    // X: B X (X's rows are the contraction) or X B
-    q = OpenStack{};
-    q.a = wide ? B : X;
-    q.b = wide ? X : B;
-    q.b_mn = wide;
-    q.M = d.M;
-    q.N = d.N;
-    q.K = m;
-    q.epi = last ? OPEN_EPI_LAST : OPEN_EPI_UPDATE;
-    q.alpha = s.alpha_x;
-    q.beta = s.beta_x;
-    q.gamma = s.gamma_x;
-    q.in_hi = ws + p.off_x[from];
-    q.in_lo = ws + p.off_x[from + 1];
-    q.ld_in = lx;
-    q.out = last ? out : ws + p.off_x[to];
-    q.out_lo = last ? nullptr : ws + p.off_x[to + 1];
-    q.out_f16 = last ? d.out_dtype == HMM_DTYPE_F16 : 1;
-    rc = launch_open_stack(env, q);
-    if (rc != HMM_OK) return rc;
+  OpenChain c{};
+  c.M = d.M;
+  c.N = d.N;
+  c.Z = d.batch;
+  c.steps = d.steps;
+  c.f = steps;
+  for (int i = 0; i < 2; ++i) {
+    c.x_hi[i] = reinterpret_cast<__half*>(ws + p.off_x[2 * i]);
+    c.x_lo[i] = reinterpret_cast<__half*>(ws + p.off_x[2 * i + 1]);
   }
-  return HMM_OK;
+  c.a = reinterpret_cast<__half*>(ws + p.off_a);
+  c.b = reinterpret_cast<__half*>(ws + p.off_b);
+  c.ld_x = p.ld_x;
+  c.ld_a = p.ld_a;
+  c.factor = a.factor;
+  c.ticket = a.ticket;
+  c.done = a.done;
+  c.out = out;
+  c.out_f16 = d.out_dtype == HMM_DTYPE_F16;
+  return launch_open_chain(env, c);
 }
 
 }  // namespace hmm

@@ -82,6 +82,27 @@ __device__ __forceinline__ bool mbar_try_wait_s(uint64_t* bar, uint32_t parity) 
     return mbar_try_wait(bar, parity);
 }
 
+// One look at a phase, without waiting (CL: as above).
+template <bool CL>
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (CL)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], "
+        "%2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  return ok != 0;
+}
+
 // Abort state shared by the roles of one CTA.
 struct WaitCtl {
   volatile int* abort;  // shared-memory flag, raised by the first wait that gives up
