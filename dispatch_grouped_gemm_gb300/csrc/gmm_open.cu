@@ -389,7 +389,7 @@ __device__ __forceinline__ float half_round(float v) { return __half2float(__flo
 
 // The ring of tickets (CHAIN): the even CTA's scheduler fills both CTAs'.
 struct OpenRing {
-  int* ticket;     // [O_RING], -1: no more
+  int4* tile;      // [O_RING] matrix (-1: no more), product, m0, n0
   uint64_t* full;  // both CTAs
   uint64_t* empty; // even CTA: every reader arrives
 };
@@ -420,7 +420,7 @@ __device__ __forceinline__ bool open_next(const OpenParams& P, const OpenList& l
     const bool ok = leader ? mbar_wait(&ring.full[w.slot], w.phase, wc)
                            : mbar_wait<true>(&ring.full[w.slot], w.phase, wc);
     if (!warp_all(ok)) return false;
-    const int u = ring.ticket[w.slot];
+    const int4 u = ring.tile[w.slot];
     __syncwarp();
     if (elect_one()) {
       if (leader)
@@ -432,8 +432,14 @@ __device__ __forceinline__ bool open_next(const OpenParams& P, const OpenList& l
       w.slot = 0;
       w.phase ^= 1u;
     }
-    if (u < 0) return false;
-    chain_tile(P, l, u, t);
+    if (u.x < 0) return false;
+    t.z = u.x;
+    t.k0 = u.y;
+    t.k1 = u.y % 3;
+    t.m0 = u.z;
+    t.n0 = u.w;
+    t.nv = t.nb = 256;
+    t.kb = P.ph[t.k1].kb;
     return true;
   }
 }
@@ -465,7 +471,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   uint32_t* s_issued = s_tmem + 2;
   uint32_t* s_sbytes = s_tmem + 3;   // [ST] bytes of this CTA's last load per slot
   uint32_t* s_peer = s_sbytes + ST;  // [2 + ST]
-  const OpenRing ring{reinterpret_cast<int*>(s_peer + 2 + ST), ring_full, ring_empty};
+  const OpenRing ring{reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(bars) + 1024 - 16 * O_RING),
+                      ring_full, ring_empty};
   const OpenList list{reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 1024),
                       reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 1024) + MAX_E + 4};
 
@@ -772,13 +779,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       uint32_t slot = 0, phase = 0;
       int u = atomicAdd(P.ticket, 1);
       for (;;) {
-        int now = -1;
+        int4 now = make_int4(-1, 0, 0, 0);
         bool ok = true;
         if (u < total) {
-          now = u;
-          u = atomicAdd(P.ticket, 1);  // the next one, used a tile later
           OpenTile t;
-          chain_tile(P, list, now, t);
+          chain_tile(P, list, u, t);
+          u = atomicAdd(P.ticket, 1);  // the next one, used a tile later
+          now = make_int4(t.z, t.k0, t.m0, t.n0);
           // every tile of the matrix in the products before: an arrival per
           // epilogue warp of both CTAs
           const int before = t.k0 / 3 * (P.ph[0].tiles + P.ph[1].tiles + P.ph[2].tiles) +
@@ -786,15 +793,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           if (before > 0) ok = counter_wait(&P.done[t.z], before * 2 * C::EPI_WARPS, wc);
         }
         if (!ok || !mbar_wait(&ring_empty[slot], phase ^ 1u, wc)) break;
-        ring.ticket[slot] = now;
-        st_shared_cluster(mapa_shared(smem_u32(&ring.ticket[slot]), 1), now);
+        ring.tile[slot] = now;
+        const uint32_t dst = mapa_shared(smem_u32(&ring.tile[slot]), 1);
+        st_shared_cluster(dst, now.x);
+        st_shared_cluster(dst + 4, now.y);
+        st_shared_cluster(dst + 8, now.z);
+        st_shared_cluster(dst + 12, now.w);
         mbar_arrive_cluster(mapa_shared(smem_u32(&ring_full[slot]), 1));
         mbar_arrive(&ring_full[slot]);
         if (++slot == O_RING) {
           slot = 0;
           phase ^= 1u;
         }
-        if (now < 0) break;
+        if (now.x < 0) break;
       }
     }
   } else {

@@ -28,8 +28,12 @@ namespace {
 
 constexpr int ROW_THREADS = 256;
 constexpr int ROW_WARPS = ROW_THREADS / 32;
-// warps from which a lane takes four vectors instead of one (fewer warps than
-// this leave SMs without loads in flight)
+// Sums: blocks per SM that registers are held down to, so that the loads of 32 warps
+// are in flight.  (16384 tokens x 8 rows of 7168 bf16: all eight rows' vectors together
+// and 4 blocks 357 us, 5.9 TB/s; four rows of two vectors each 421 us.)
+constexpr int ROW_SUM_BLOCKS = 4;
+// Dispatch: warps from which a lane takes four vectors instead of one (fewer warps than
+// this leave SMs without loads in flight).
 constexpr int64_t ROW_WIDE_WARPS = 152 * 16;
 
 template <typename T>
@@ -111,9 +115,10 @@ __global__ void __launch_bounds__(ROW_THREADS) rows_dispatch_kernel(const RowsAr
   zero_tail<T, V>(a, rows, warp, static_cast<int64_t>(gridDim.x) * ROW_WARPS, lane);
 }
 
-// The same pieces summed over the slots of a token (w null: weights 1).
-template <typename T, int V, int U>
-__global__ void __launch_bounds__(ROW_THREADS) rows_sum_kernel(const RowsArgs a) {
+// The same pieces summed over the slots of a token (w null: weights 1), KB slots at a
+// time with their loads together.
+template <typename T, int V, int U, int KB>
+__global__ void __launch_bounds__(ROW_THREADS, ROW_SUM_BLOCKS) rows_sum_kernel(const RowsArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
@@ -125,28 +130,37 @@ __global__ void __launch_bounds__(ROW_THREADS) rows_sum_kernel(const RowsArgs a)
   const int64_t t = warp / pieces, c0 = (warp - t * pieces) * (32 * U) + lane;
   const int mine = slot_row(a, t, lane);
   float w_mine = 1.f;
-  if (a.w && lane < a.K) w_mine = row_weight(a.w, t * a.K + lane, a.w_dtype);
+  if (a.w && lane < a.K) w_mine = row_weight(a.w, t * a.K + lane, a.w_dtype);  // (K <= 32)
   float acc[U][V];
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
-#pragma unroll 2
-  for (int k = 0; k < a.K; ++k) {
-    const int64_t r = __shfl_sync(0xffffffffu, mine, k);
-    const float w = __shfl_sync(0xffffffffu, w_mine, k);
-    if (r < 0) continue;
-    Vec<T, V> v[U];
+  // (slots without a row load nothing and add 0 times 0)
+  for (int k0 = 0; k0 < a.K; k0 += KB) {
+    Vec<T, V> v[KB][U];
+    float w[KB];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c0 + 32 * u < hv)
-        v[u] = *reinterpret_cast<const Vec<T, V>*>(rows + r * a.H + (c0 + 32 * u) * V);
+    for (int i = 0; i < KB; ++i) {
+      const int64_t r = __shfl_sync(0xffffffffu, mine, k0 + i);  // (-1 for k0 + i >= K)
+      w[i] = __shfl_sync(0xffffffffu, w_mine, k0 + i);
+      if (r < 0) w[i] = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c0 + 32 * u < hv) {
+      for (int u = 0; u < U; ++u) {
+        if (r >= 0 && c0 + 32 * u < hv) {
+          v[i][u] = *reinterpret_cast<const Vec<T, V>*>(rows + r * a.H + (c0 + 32 * u) * V);
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[u][i] = fmaf(w, Elem<T>::get(v[u].v[i]), acc[u][i]);
+          for (int e = 0; e < V; ++e) v[i][u].v[e] = Elem<T>::put(0.f);
+        }
       }
+    }
+#pragma unroll
+    for (int i = 0; i < KB; ++i)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[u][e] = fmaf(w[i], Elem<T>::get(v[i][u].v[e]), acc[u][e]);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -250,12 +264,13 @@ cudaError_t launch_rows_v(RowsOp op, const RowsArgs& a, cudaStream_t st, bool pd
     return launch_kernel(rows_combine_grad_kernel<T, V, 1>, blocks(slots), ROW_THREADS, 0, st, pdl,
                          1, a);
   }
-  const int64_t wide = a.T * ((hv + 127) / 128), narrow = a.T * ((hv + 31) / 32);
-  const bool u4 = wide >= ROW_WIDE_WARPS;
+  const int u = op == ROWS_DISPATCH ? 4 : a.K > 4 ? 1 : a.K > 2 ? 2 : 4;
+  const int64_t wide = a.T * ((hv + 32 * u - 1) / (32 * u)), narrow = a.T * ((hv + 31) / 32);
+  const bool several = op != ROWS_DISPATCH || wide >= ROW_WIDE_WARPS;
   auto kern = op == ROWS_DISPATCH
-                  ? (u4 ? rows_dispatch_kernel<T, V, 4> : rows_dispatch_kernel<T, V, 1>)
-                  : (u4 ? rows_sum_kernel<T, V, 4> : rows_sum_kernel<T, V, 1>);
-  return launch_kernel(kern, blocks(u4 ? wide : narrow), ROW_THREADS, 0, st, pdl, 1, a);
+                  ? (several ? rows_dispatch_kernel<T, V, 4> : rows_dispatch_kernel<T, V, 1>)
+                  : (a.K > 4 ? rows_sum_kernel<T, V, 1, 8> : a.K > 2 ? rows_sum_kernel<T, V, 2, 4> : rows_sum_kernel<T, V, 4, 2>);
+  return launch_kernel(kern, blocks(several ? wide : narrow), ROW_THREADS, 0, st, pdl, 1, a);
 }
 
 template <typename T>
