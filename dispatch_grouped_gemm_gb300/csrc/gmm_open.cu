@@ -361,13 +361,15 @@ __device__ __forceinline__ void fetch(const __half* src, int lane, int64_t ld, i
       q[j] = __ldcg(reinterpret_cast<const uint4*>(src + r * ld + unit * 8));
   }
 }
-template <typename F>
-__device__ __forceinline__ void turn(uint8_t* sb, int lane, const uint4 (&q)[4], const F& f) {
+__device__ __forceinline__ void turn_in(uint8_t* sb, int lane, const uint4 (&q)[4]) {
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     *reinterpret_cast<uint4*>(unit_at(sb, (lane >> 2) + 8 * j, lane & 3)) = q[j];
   __syncwarp();
+}
+template <typename F>
+__device__ __forceinline__ void turn_out(uint8_t* sb, int lane, const F& f) {
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const uint4 t = *reinterpret_cast<const uint4*>(unit_at(sb, lane, u));
@@ -555,16 +557,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         // what this tile reads was written by other CTAs of this launch: the scheduler
         // acquired their counter; order that with the asynchronous copies
         fence_proxy_async_global();
-        if (t.k1 == 2) {  // what the epilogue adds, into L2 meanwhile
-          const OpenFactors& fa = P.f[t.k0 / 3];
-          const int from = t.k0 / 3 & 1;
+        if (t.k1 == 2 && P.f[t.k0 / 3].low) {  // what the epilogue adds, into L2 meanwhile
+          const __half* lo = P.x_lo[t.k0 / 3 & 1];
           const int rows = min(128, ph.M - ma), lines = min(4, (ph.N - t.n0 + 63) >> 6);
           const int64_t at = (static_cast<int64_t>(t.z) * ph.M + ma) * P.ld_x + t.n0;
           for (int j = lane; j < 4 * rows; j += 32) {
             if ((j & 3) >= lines) continue;
-            const int64_t o = at + (j >> 2) * P.ld_x + (j & 3) * 64;
-            prefetch_l2(P.x_hi[from] + o);
-            if (fa.low) prefetch_l2(P.x_lo[from] + o);
+            prefetch_l2(lo + at + (j >> 2) * P.ld_x + (j & 3) * 64);
           }
           __syncwarp();
         }
@@ -892,34 +891,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           continue;
         }
       }
-      // CHAIN: v = alpha acc + beta h + gamma l (+ d on the diagonal), h and l loaded a
-      // chunk ahead.  (One body for the three products: with a copy for each, and two
-      // chunks in flight, its instructions came from L2 and a chunk took 2300 cycles.)
-      const bool sum = KIND == OPEN_CHAIN && t.k1 == 1;   // B = c A A + b A + d I
+      // CHAIN: v = alpha acc + beta h (+ gamma on the diagonal), h (A for B, lo for X)
+      // loaded a chunk ahead.  (One body for the three products: the instructions of
+      // every role share a small cache, and with a copy for each product a chunk took
+      // 2300 cycles, with two copies of this body half as long again.)
+      const bool sum = KIND == OPEN_CHAIN && t.k1 == 1;   // B = c A A + b A + a I
       const bool upd = KIND == OPEN_CHAIN && t.k1 == 2;   // X
       const int step = KIND == OPEN_CHAIN ? t.k0 / 3 : 0;
       const bool last = upd && step == P.steps - 1;       // ... the result
       const OpenFactors& fa = P.f[step];
-      const bool low = upd && fa.low;                     // X has a lo
+      const bool adds = sum || (upd && fa.low);
       const int64_t ld = KIND == OPEN_CHAIN ? (upd ? P.ld_x : P.ld_a) : N;
       const int64_t in_at = (static_cast<int64_t>(t.z) * M + mw) * ld + t.n0;
       const int from = step & 1;
-      const __half* in_h = sum ? P.a_out : P.x_hi[from];
-      const __half* in_l = P.x_lo[from];
-      uint4 qh[4], ql[4];
+      const __half* in = sum ? P.a_out : P.x_lo[from];
+      uint4 q[4];
       const auto fetch_in = [&](int c) {
-        const int cols = static_cast<int>(ld) - t.n0 - 32 * c;  // (rows are padded to 8)
-        if (sum || upd) fetch(in_h + in_at + 32 * c, lane, ld, mrows, cols, qh);
-        if (low) fetch(in_l + in_at + 32 * c, lane, ld, mrows, cols, ql);
+        fetch(in + in_at + 32 * c, lane, ld, mrows, static_cast<int>(ld) - t.n0 - 32 * c, q);
       };
-      float alpha = 1.f, beta = 0.f, gamma = 0.f;
+      float alpha = 1.f, beta = 0.f;
       if constexpr (KIND == OPEN_CHAIN) {
-        if (first < nch) fetch_in(first);
+        if (adds && first < nch) fetch_in(first);
         // scale of the stored first X (1 afterwards)
         const float rz = step == 0 && !sum ? __ldcg(P.factor + t.z) : 1.f;
         alpha = sum ? fa.alpha_b : upd ? fa.alpha_x * rz : fa.alpha_a * (rz * rz);
         beta = sum ? fa.beta_b : fa.beta_x * rz;
-        gamma = fa.gamma_x * rz;
         if (pending >= 0) written(pending);  // the tile before, behind this one's first loads
         pending = -1;
       }
@@ -955,9 +951,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           tmem_ld_wait_for(r);
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = alpha * __uint_as_float(r[j]);
-          if (sum || upd) turn(sb, lane, qh, [&](int j, float x) { v[j] = fmaf(beta, x, v[j]); });
-          if (low) turn(sb, lane, ql, [&](int j, float x) { v[j] = fmaf(gamma, x, v[j]); });
-          if (c + SHARE < nch) fetch_in(c + SHARE);
+          if (adds) {
+            turn_in(sb, lane, q);
+            if (c + SHARE < nch) fetch_in(c + SHARE);
+            turn_out(sb, lane, [&](int j, float x) { v[j] = fmaf(beta, x, v[j]); });
+          }
           const int n = t.n0 + 32 * c;
           if (sum && n == mw) {
 #pragma unroll

@@ -16,12 +16,12 @@ constexpr int OPEN_CHAIN = 2;
 // a step, operands and results in fp16 (gmm_open.cu; ortho.cu has the mathematics):
 //   0  A  = alpha_a X X^T                              symmetric
 //   1  B  = alpha_b A A + beta_b A + gamma_b I         symmetric
-//   2  v  = alpha_x B X + beta_x hi + gamma_x lo;  hi' = fp16(v), lo' = fp16(v - hi'),
-//      of the last step the caller's result (bf16 or fp16)
+//   2  v  = alpha_x B X + beta_x lo;  X <- hi = fp16(v), lo = fp16(v - hi), of the last
+//      step the caller's result (bf16 or fp16)
 // A symmetric result is computed for tiles on and above the diagonal and written twice.
 // The first X is stored without a factor `factor[z]` of its matrix.
 struct OpenFactors {
-  float alpha_a, alpha_b, beta_b, gamma_b, alpha_x, beta_x, gamma_x;
+  float alpha_a, alpha_b, beta_b, gamma_b, alpha_x, beta_x;
   int low;  // the X that this step reads has a lo
 };
 

@@ -14,20 +14,19 @@
 // in directions that X hardly has: with X in fp16 alone a matrix of rank 64 + noise
 // comes out 2 % off, with bf16 18 %.  The rounding of A and B, and of the X inside
 // B X, only turns directions that X has, and is not multiplied.  So X is kept as
-// hi + lo, two fp16 (22 bits), and the epilogue adds a (hi + lo) in fp32, while the
-// products read hi alone: 0.2 % off for every spectrum, most of it the result's own
-// rounding to bf16 (0.17 %).  (Where the steps that are left multiply by at most 4, hi
-// alone does: 0.19 %.)  Three bits more than bf16 at the same rate are why it
-// is fp16: its range is enough, because every matrix here has a known bound.
+// hi + lo, two fp16 (22 bits): the products read hi alone, with B' = B + a I, and the
+// epilogue adds a lo, which is X <- a X + B X but for B lo: 0.2 % off for every
+// spectrum, most of it the result's own rounding to bf16 (0.17 %).  (Where the steps
+// that are left multiply by at most 4, hi alone does, to the same 0.2 %.)  Three bits
+// more than bf16 at the same rate are why it is fp16: its range is enough, because
+// every matrix here has a known bound.
 //   Bounds.  All singular values of X lie in [0, u] with u = 1 at first and then
 // the largest |a s + b s^3 + c s^5| on [0, u]; an element is at most the largest
 // singular value.  From that each matrix gets its power-of-two scale on the host,
-// at most 2^14 in storage, a quarter of fp16's range.  B is stored as B + d I with d
-// = -(b + c): where X is nearly orthogonal its diagonal is near b + c, and without
-// it the rounding of the diagonal alone costs as much as all others; the epilogue
-// takes d hi off again.  The first X is G times a power of two, the rest of 1 / (|G|
-// + eps), in [1, 2), goes into the first step's factors: so a 16-bit G is exact in hi
-// alone (but for elements 2^28 below the norm) and has no lo.
+// at most 2^14 in storage, a quarter of fp16's range.  The first X is G times a power
+// of two, the rest of 1 / (|G| + eps), in [1, 2), goes into the first step's factors:
+// so a 16-bit G is exact in hi alone (but for elements 2^28 below the norm) and has no
+// lo.
 //
 // What bounds it: 3 m^2 n + m^3 operations per step (A and A A are symmetric: one
 // triangle of tiles each) at the tensor rate; between them X moves four times
@@ -291,8 +290,7 @@ bool ortho_steps(const hmm_ortho& d, OpenFactors* out) {
                  c = d.coefficients[3 * i + 2];
     // (NaN fails the comparison)
     if (!(std::fabs(a) <= most && std::fabs(b) <= most && std::fabs(c) <= most)) return false;
-    const double shift = -(b + c);
-    const double ub = largest(u, [&](double s) { return b * s * s + c * s * s * s * s + shift; });
+    const double ub = largest(u, [&](double s) { return a + b * s * s + c * s * s * s * s; });
     const double un = largest(u, [&](double s) { return s * (a + b * s * s + c * s * s * s * s); });
     if (!(ub <= most && un <= most)) return false;
     const int ea = scale_for(u * u), eb = scale_for(ub), en = scale_for(un);
@@ -300,13 +298,12 @@ bool ortho_steps(const hmm_ortho& d, OpenFactors* out) {
     s.alpha_a = static_cast<float>(std::ldexp(1.0, ea - 2 * ex));
     s.alpha_b = static_cast<float>(std::ldexp(c, eb - 2 * ea));
     s.beta_b = static_cast<float>(std::ldexp(b, eb - ea));
-    s.gamma_b = static_cast<float>(std::ldexp(shift, eb));
+    s.gamma_b = static_cast<float>(std::ldexp(a, eb));
     const bool last = i == d.steps - 1;
     const double k = last ? d.scale : 1.0;
     const int e = last ? 0 : en;
     s.alpha_x = static_cast<float>(k * std::ldexp(1.0, e - eb - ex));
-    s.beta_x = static_cast<float>(k * std::ldexp(a - shift, e - ex));
-    s.gamma_x = static_cast<float>(k * std::ldexp(a, e - ex));
+    s.beta_x = static_cast<float>(k * std::ldexp(a, e - ex));
     u = un;
     ex = en;
   }

@@ -84,9 +84,8 @@ def orthogonalize(g, steps=5, coefficients=QUINTIC, eps=1e-7, scale=1.0, rounded
             if rounded:
                 hi = bits(x, 11)
                 s = bits(hi @ hi.T, 11)
-                d = -(b + c)
-                p = bits(b * s + c * (s @ s) + d * one, 11)
-                x = bits(a * x - d * hi + p @ hi, 22)
+                p = bits(b * s + c * (s @ s) + a * one, 11)
+                x = bits(p @ hi + a * (x - hi), 22)
             else:
                 s = x @ x.T
                 x = a * x + (b * s + c * (s @ s)) @ x
