@@ -39,7 +39,7 @@ __all__ = [
     "hmm_forward_mx4", "HmmMx4", "make_mx4", "Mx4Tensor", "mx4_quantize", "mx4_quantize_experts",
     "moe_ffn_mx4",
     "hmm_dispatch", "hmm_dispatch_grad", "hmm_combine", "hmm_combine_grad", "hmm_grouped_mm",
-    "hmm_grouped_mm_dx", "hmm_grouped_mm_dw", "hmm_orthogonalize",
+    "hmm_grouped_mm_dx", "hmm_grouped_mm_dw", "hmm_grouped_mm_workspace_size", "hmm_orthogonalize",
     "hmm_orthogonalize_workspace_size", "HmmRows", "HmmGmm", "HmmOrtho", "make_rows", "make_gmm",
     "make_ortho", "MoeRouting", "moe_route", "moe_dispatch", "moe_combine", "moe_grouped_mm",
     "orthogonalize", "MUON_COEFFICIENTS",
@@ -196,7 +196,8 @@ def load_library():
             "hmm_combine_grad": [vp, rp, vp, vp, vp, vp, vp, vp, vp, vp],
             "hmm_grouped_mm": [vp, mmp, vp, vp, vp, vp, vp],
             "hmm_grouped_mm_dx": [vp, mmp, vp, vp, vp, vp, vp],
-            "hmm_grouped_mm_dw": [vp, mmp, vp, vp, vp, vp, vp],
+            "hmm_grouped_mm_workspace_size": [mmp, szp],
+            "hmm_grouped_mm_dw": [vp, mmp, vp, vp, vp, vp, vp, sz, vp],
             "hmm_orthogonalize_workspace_size": [op, szp],
             "hmm_orthogonalize": [vp, op, vp, vp, vp, sz, vp],
             "hmm_status": [vp, vp, ctypes.POINTER(i32)],
@@ -465,9 +466,17 @@ def hmm_grouped_mm_dx(ctx, desc, dy, w, offsets, dx, stream=None):
     _check(rc, "hmm_grouped_mm_dx")
 
 
-def hmm_grouped_mm_dw(ctx, desc, x, dy, offsets, dw, stream=None):
+def hmm_grouped_mm_workspace_size(desc) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().hmm_grouped_mm_workspace_size(ctypes.byref(desc), ctypes.byref(n)),
+           "hmm_grouped_mm_workspace_size")
+    return n.value
+
+
+def hmm_grouped_mm_dw(ctx, desc, x, dy, offsets, dw, workspace=None, stream=None):
     rc = load_library().hmm_grouped_mm_dw(ctx, ctypes.byref(desc), _ptr(x), _ptr(dy),
-                                          _ptr(offsets), _ptr(dw), _stream(stream))
+                                          _ptr(offsets), _ptr(dw), _ptr(workspace),
+                                          _nbytes(workspace), _stream(stream))
     _check(rc, "hmm_grouped_mm_dw")
 
 
@@ -1236,6 +1245,12 @@ def _gmm(name, desc, a, b, offsets, out):
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _gmm_workspace(R, K, N, E):
+    """Workspace bytes of the weight gradient."""
+    return hmm_grouped_mm_workspace_size(make_gmm(R, K, N, E))
+
+
 def _gmm_forward(x, w, offsets):
     x, ld = _tma_rows(x)
     w, layout, ld_w, per = _tma_weights(w)
@@ -1267,8 +1282,14 @@ class _GroupedMM(torch.autograd.Function):
                       torch.empty((R, K), dtype=x.dtype, device=dev))
         if ctx.needs_input_grad[1]:
             shape = (E, K, N) if layout == HMM_W_KN else (E, N, K)
-            dw = _gmm("hmm_grouped_mm_dw", d, x, dy, offsets,
-                      torch.empty(shape, dtype=x.dtype, device=dev))
+            dw = torch.empty(shape, dtype=x.dtype, device=dev)
+            size = _gmm_workspace(R, K, N, E)
+            ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+            rc = load_library().hmm_grouped_mm_dw(
+                Context.for_device(dev).handle, ctypes.byref(d), x.data_ptr(), dy.data_ptr(),
+                offsets.data_ptr(), dw.data_ptr(), _ptr(ws), size, _raw_stream(dev.index))
+            if rc != HMM_OK:
+                raise HmmError(rc, "hmm_grouped_mm_dw")
             if layout == HMM_W_NK:
                 dw = dw.transpose(1, 2)
         dx, dw = _first_order("moe_grouped_mm", (dx, dw), (saved_x, saved_w))

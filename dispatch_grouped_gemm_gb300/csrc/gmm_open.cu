@@ -13,6 +13,9 @@
 //           most 256 and few rows cost few columns of work, while the weights,
 //           256 columns per pair, fill the M side.
 //   DEPTH   dw[e] = x_e^T . dy_e: the contraction runs over the rows of the expert.
+//   PIECES  the same where one expert's tiles are few: the rows of an expert are cut
+//           into pieces; the pieces of an expert that has several go to a workspace in
+//           fp32 and are added by a second kernel, in order.
 //   CHAIN   the products of the Newton-Schulz steps over a stack of matrices, all of
 //           them in one launch (gmm_open.h).
 //
@@ -62,8 +65,12 @@ constexpr int OBUF = 2048;             // a warp's staging of one 32 x 32 chunk 
 constexpr uint32_t O_TMEM_COLS = 512;  // two accumulators of 256 columns
 constexpr int O_SORT_MAX_E = 512;      // experts that DEPTH sorts by rows (E^2 / threads compares)
 constexpr int O_CUT_AHEAD = 1;         // blocks that a block to be cut is loaded early
-constexpr int O_LIST_BYTES = 2 * 4 * (MAX_E + 4);
+constexpr int O_LIST_BYTES = 4 * 4 * (MAX_E + 4);
 constexpr int O_RING = 4;               // tickets on their way (CHAIN)
+
+// DEPTH with whole experts or with pieces
+template <int KIND>
+constexpr bool DEPTH = KIND == OPEN_DEPTH || KIND == OPEN_PIECES;
 
 template <int KIND>
 struct Cfg {
@@ -83,7 +90,8 @@ struct OpenMaps {
 struct OpenTile {
   int z;       // expert or matrix
   int m0, n0;  // ROWS: n0 = first row of the block
-  int nv, nb;  // ROWS: rows of the block, MMA columns (a multiple of 16); else 256
+  int nv, nb;  // ROWS: rows of the block, MMA columns (a multiple of 16); else nb = 256,
+               // PIECES: nv = place in the workspace, -1: the expert's only piece
   int kb;      // K blocks
   int k0, k1;  // DEPTH: the expert's rows; CHAIN: product (3 per step) and its kind
 };
@@ -99,8 +107,10 @@ struct OpenList {
   int* at;    // rows of the experts: [Z + 1] offsets clamped into [0, R], so that
               // whatever the caller's offsets hold, every access stays inside
   int* list;  // ROWS: blocks of the experts before e (Z + 1 entries); DEPTH: experts
-              // by rows, descending (Z up to O_SORT_MAX_E); CHAIN: tiles of the slots
-              // before e
+              // by the rows of their last piece, descending (Z up to O_SORT_MAX_E); CHAIN:
+              // tiles of the slots before e
+  int* full;  // PIECES: pieces but the last of the experts before e
+  int* part;  // PIECES: pieces in the workspace of the experts before e
 };
 
 // CHAIN: tiles of a matrix in product p (0 outside the chain).
@@ -115,49 +125,92 @@ __device__ __forceinline__ int open_rows_of(const OpenList& l, int e) {
   return max(0, l.at[e + 1] - l.at[e]);
 }
 
+// Whole pieces in front of the last of `rows` rows (PIECES).
+__device__ __forceinline__ int open_full(const OpenParams& P, int rows) {
+  return rows > 0 ? (rows - 1) / P.split : 0;
+}
+
+// Exclusive prefix sums of f(0 .. n - 1) (n + 1 entries).  One warp.
+template <typename F>
+__device__ __forceinline__ void warp_prefix(int* list, int n, const F& f) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  if (lane == 0) list[0] = 0;
+  for (int base = 0; base < n; base += 32) {
+    const int e = base + lane;
+    int v = e < n ? f(e) : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int m = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += m;
+    }
+    if (e < n) list[e + 1] = carry + v;
+    carry += __shfl_sync(0xffffffffu, v, 31);
+  }
+}
+
 // All threads of the CTA; ends with a barrier.
 template <int KIND>
 __device__ void open_list(const OpenParams& P, const OpenList& l) {
-  if constexpr (KIND != OPEN_CHAIN) {
+  if constexpr (KIND == OPEN_CHAIN) {
+    // tiles of slot e: every third matrix in product e, e - 1, e - 2
+    if (threadIdx.x < 32)
+      warp_prefix(l.list, 3 * P.steps + 2, [&](int e) {
+        int v = 0;
+#pragma unroll
+        for (int g = 0; g < 3; ++g) v += chain_tiles(P, e - g) * ((P.Z + 2 - g) / 3);
+        return v;
+      });
+  } else {
     for (int e = threadIdx.x; e <= P.Z; e += blockDim.x)
       l.at[e] = min(max(P.offsets[e], 0), P.R);
     __syncthreads();
-  }
-  if constexpr (KIND != OPEN_DEPTH) {
-    if (threadIdx.x < 32) {
-      const int lane = threadIdx.x;
-      const int entries = KIND == OPEN_ROWS ? P.Z : 3 * P.steps + 2;
-      int carry = 0;
-      if (lane == 0) l.list[0] = 0;
-      for (int base = 0; base < entries; base += 32) {
-        const int e = base + lane;
-        int v = 0;
-        if (e < entries) {
-          if constexpr (KIND == OPEN_ROWS) {
-            v = open_blocks(open_rows_of(l, e));
-          } else {  // tiles of slot e: every third matrix in product e, e - 1, e - 2
+    const int warp = threadIdx.x >> 5;
+    if constexpr (KIND == OPEN_ROWS) {
+      if (warp == 0) warp_prefix(l.list, P.Z, [&](int e) { return open_blocks(open_rows_of(l, e)); });
+    } else {
+      if constexpr (KIND == OPEN_PIECES) {
+        // (the pieces' places in the workspace follow from sums of rows, which only offsets
+        // in order bound)
+        if (warp == 0) {
+          const int lane = threadIdx.x & 31;
+          int top = 0;
+          for (int base = 0; base <= P.Z; base += 32) {
+            const int e = base + lane;
+            int v = max(top, e <= P.Z ? l.at[e] : 0);
 #pragma unroll
-            for (int g = 0; g < 3; ++g) v += chain_tiles(P, e - g) * ((P.Z + 2 - g) / 3);
+            for (int d = 1; d < 32; d <<= 1) {
+              const int m = __shfl_up_sync(0xffffffffu, v, d);
+              if (lane >= d) v = max(v, m);
+            }
+            if (e <= P.Z) l.at[e] = v;
+            top = __shfl_sync(0xffffffffu, v, 31);
           }
         }
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int n = __shfl_up_sync(0xffffffffu, v, d);
-          if (lane >= d) v += n;
+        __syncthreads();
+        if (warp == 0)
+          warp_prefix(l.full, P.Z, [&](int e) { return open_full(P, open_rows_of(l, e)); });
+        if (warp == 1)
+          warp_prefix(l.part, P.Z, [&](int e) {
+            const int n = open_full(P, open_rows_of(l, e));
+            return n > 0 ? n + 1 : 0;
+          });
+      }
+      const auto last = [&](int e) {
+        const int rows = open_rows_of(l, e);
+        return KIND == OPEN_PIECES ? rows - open_full(P, rows) * P.split : rows;
+      };
+      if (P.Z <= O_SORT_MAX_E) {
+        for (int e = threadIdx.x; e < P.Z; e += blockDim.x) {
+          const int re = last(e);
+          int rank = 0;
+          for (int f = 0; f < P.Z; ++f) {
+            const int rf = last(f);
+            rank += (rf > re || (rf == re && f < e)) ? 1 : 0;
+          }
+          l.list[rank] = e;
         }
-        if (e < entries) l.list[e + 1] = carry + v;
-        carry += __shfl_sync(0xffffffffu, v, 31);
       }
-    }
-  } else if (P.Z <= O_SORT_MAX_E) {
-    for (int e = threadIdx.x; e < P.Z; e += blockDim.x) {
-      const int re = open_rows_of(l, e);
-      int rank = 0;
-      for (int f = 0; f < P.Z; ++f) {
-        const int rf = open_rows_of(l, f);
-        rank += (rf > re || (rf == re && f < e)) ? 1 : 0;
-      }
-      l.list[rank] = e;
     }
   }
   __syncthreads();
@@ -167,7 +220,7 @@ template <int KIND>
 __device__ __forceinline__ int64_t open_total(const OpenParams& P, const OpenList& l) {
   if constexpr (KIND == OPEN_CHAIN) return l.list[3 * P.steps + 2];
   if constexpr (KIND == OPEN_ROWS) return static_cast<int64_t>(l.list[P.Z]) * P.mt;
-  return static_cast<int64_t>(P.Z) * P.tiles;
+  return static_cast<int64_t>(P.Z + (KIND == OPEN_PIECES ? l.full[P.Z] : 0)) * P.tiles;
 }
 
 // u / d and the rest (u beyond 32 bits is rare, and its division slow)
@@ -179,6 +232,19 @@ __device__ __forceinline__ int open_div(int64_t u, int d, int& rest) {
     q = static_cast<int>(u / d);
   rest = static_cast<int>(u - static_cast<int64_t>(q) * d);
   return q;
+}
+
+// The largest e <= hi with list[e] <= u.
+__device__ __forceinline__ int open_find(const int* list, int hi, int u) {
+  int lo = 0;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (list[mid] <= u)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
 }
 
 // Tile (r of the matrix, in its product) of a rectangle of mt x nt tiles, or of the
@@ -205,14 +271,7 @@ __device__ __forceinline__ void open_place(int r, int mt, int nt, bool sym, Open
 // 3 k + 1 in product e - 1 and matrix 3 k + 2 in product e - 2.
 __device__ __forceinline__ void chain_tile(const OpenParams& P, const OpenList& l, int u,
                                            OpenTile& t) {
-  int lo = 0, hi = 3 * P.steps + 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (l.list[mid] <= u)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
+  const int lo = open_find(l.list, 3 * P.steps + 1, u);
   int r = u - l.list[lo];
   const int n[3] = {chain_tiles(P, lo), chain_tiles(P, lo - 1), chain_tiles(P, lo - 2)};
   const int unit = n[0] + n[1] + n[2], whole = P.Z / 3;
@@ -246,14 +305,7 @@ __device__ __forceinline__ bool open_tile(const OpenParams& P, const OpenList& l
   if constexpr (KIND == OPEN_ROWS) {
     const int blk = open_div(u, P.mt, r);
     t.m0 = r * 256;
-    int lo = 0, hi = P.Z - 1;  // the largest e with list[e] <= blk
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (l.list[mid] <= blk)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
+    const int lo = open_find(l.list, P.Z - 1, blk);
     const int o = l.at[lo], rows = open_rows_of(l, lo);
     const int nblk = open_blocks(rows), j = blk - l.list[lo];
     t.z = lo;
@@ -265,9 +317,25 @@ __device__ __forceinline__ bool open_tile(const OpenParams& P, const OpenList& l
     const int i = open_div(u, P.tiles, r);
     t.nv = t.nb = 256;
     open_place(r, P.mt, P.nt, false, t);
-    t.z = P.Z <= O_SORT_MAX_E ? l.list[i] : i;
-    t.k0 = l.at[t.z];
-    t.k1 = max(t.k0, l.at[t.z + 1]);
+    if constexpr (KIND == OPEN_PIECES) {
+      // the whole pieces first, then the last ones from the longest to the shortest
+      const int whole = l.full[P.Z];
+      int piece;
+      if (i < whole) {
+        t.z = open_find(l.full, P.Z - 1, i);
+        piece = i - l.full[t.z];
+      } else {
+        t.z = P.Z <= O_SORT_MAX_E ? l.list[i - whole] : i - whole;
+        piece = l.full[t.z + 1] - l.full[t.z];
+      }
+      t.k0 = l.at[t.z] + piece * P.split;
+      t.k1 = i < whole ? t.k0 + P.split : max(t.k0, l.at[t.z + 1]);
+      t.nv = l.part[t.z + 1] > l.part[t.z] ? l.part[t.z] + piece : -1;
+    } else {
+      t.z = P.Z <= O_SORT_MAX_E ? l.list[i] : i;
+      t.k0 = l.at[t.z];
+      t.k1 = max(t.k0, l.at[t.z + 1]);
+    }
     t.kb = (t.k1 - t.k0 + OK_ - 1) / OK_;
   }
   return true;
@@ -475,8 +543,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   uint32_t* s_peer = s_sbytes + ST;  // [2 + ST]
   const OpenRing ring{reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(bars) + 1024 - 16 * O_RING),
                       ring_full, ring_empty};
-  const OpenList list{reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 1024),
-                      reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 1024) + MAX_E + 4};
+  int* lists = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 1024);
+  const OpenList list{lists, lists + MAX_E + 4, lists + 2 * (MAX_E + 4), lists + 3 * (MAX_E + 4)};
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -519,6 +587,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   const WaitCtl wc{s_abort, P.status, P.budget_ns};
   open_list<KIND>(P, list);
   const int64_t total = open_total<KIND>(P, list);
+  if constexpr (KIND == OPEN_PIECES) {
+    if (blockIdx.x == 0)  // for the kernel that adds the pieces
+      for (int e = threadIdx.x; e <= P.Z; e += C::THREADS) P.part_at[e] = list.part[e];
+  }
 
   // The two issuing warps run converged and elect a lane for each group of
   // instructions, whose operands then stay in uniform registers: under a branch on
@@ -535,7 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
     bool ok = true;
     OpenTile t, next;
     bool more = advance(t);
-    bool a_mn = KIND == OPEN_DEPTH || P.a_mn, b_mn = KIND == OPEN_DEPTH;
+    bool a_mn = DEPTH<KIND> || P.a_mn, b_mn = DEPTH<KIND>;
     const CUtensorMap* am = &maps.a;
     int depth = P.K;
     for (; ok && more; t = next) {
@@ -568,7 +640,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           __syncwarp();
         }
       }
-      const bool tail = KIND == OPEN_DEPTH && open_tail(t) != 0;
+      const bool tail = DEPTH<KIND> && open_tail(t) != 0;
       const int place = open_cut_place(t);
       const int ask = min(t.kb, ST) - 1;  // the next tile is decoded with the ring filled
       bool known = false;
@@ -580,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         const int k = kb * OK_;
         // K-major operands come in two boxes of 64 deep, the second one only if K
         // reaches it; MN-major ones in two boxes of 64 wide
-        const bool deep = KIND == OPEN_DEPTH || k + 64 < depth;
+        const bool deep = DEPTH<KIND> || k + 64 < depth;
         const bool cutting = tail && j == place;
         uint8_t* sA = stages + stage * OSTAGE;
         uint8_t* sB = sA + OA_BYTES;
@@ -601,7 +673,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
             s_sbytes[stage] = bytes;
             const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
             // coordinates of an MN-major box: (m or n, c1, c2)
-            const int c1 = KIND == OPEN_DEPTH ? t.k0 + k : k, c2 = KIND == OPEN_DEPTH ? 0 : t.z;
+            const int c1 = DEPTH<KIND> ? t.k0 + k : k, c2 = DEPTH<KIND> ? 0 : t.z;
             if (a_mn) {
               tma_load_3d_pair(sA, am, bar, ma, c1, c2);
               tma_load_3d_pair(sA + OCHUNK, am, bar, ma + 64, c1, c2);
@@ -635,7 +707,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
     }
     if (lane == 0) {
       // after an abort: this CTA's own copies (the others are drained at teardown)
-      if (KIND == OPEN_DEPTH && !ok)
+      if (DEPTH<KIND> && !ok)
         for (int s = 0; s < ST; ++s)
           if (landed_used >> s & 1u)
             drain_wait(&landed[s], (landed_phase >> s & 1u) ^ 1u, P.budget_ns);
@@ -650,7 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       // are the leading-dimension stride).  Descriptor addresses count 16 bytes.
       const uint64_t a_k = smem_desc(smem_u32(stages), 16, 1024, LAYOUT_SW128);
       const uint64_t a_m = smem_desc(smem_u32(stages), OCHUNK, 1024, LAYOUT_SW128);
-      bool a_mn = KIND == OPEN_DEPTH || P.a_mn, b_mn = KIND == OPEN_DEPTH;
+      bool a_mn = DEPTH<KIND> || P.a_mn, b_mn = DEPTH<KIND>;
       uint32_t stage = 0, sphase = 0, acc = 0, acc_phase = 0, cut_phase = 0;
       bool ok = true;
       OpenWalk walk;
@@ -691,7 +763,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           continue;
         }
         uint32_t idesc = P.idesc | (static_cast<uint32_t>(t.nb >> 3) << 17);
-        int depth = KIND == OPEN_DEPTH ? t.k1 - t.k0 : P.K;
+        int depth = DEPTH<KIND> ? t.k1 - t.k0 : P.K;
         if constexpr (KIND == OPEN_CHAIN) {
           const OpenPhase& ph = P.ph[t.k1];
           a_mn = ph.a_mn;
@@ -703,7 +775,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
-        const bool tail = KIND == OPEN_DEPTH && open_tail(t) != 0;
+        const bool tail = DEPTH<KIND> && open_tail(t) != 0;
         const int place = tail ? open_cut_place(t) : -1;
         // steps of the tile's last block
         const int last_steps = (depth - (t.kb - 1) * OK_ + 15) >> 4;
@@ -744,7 +816,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       __syncwarp();
       drain_wait(mma_done, 0, P.budget_ns);
     }
-  } else if (KIND == OPEN_DEPTH && warp == 2 + C::EPI_WARPS) {
+  } else if (DEPTH<KIND> && warp == 2 + C::EPI_WARPS) {
     // ------------------------------------------------- the ends of the experts
     // Rows v .. of the last step of an expert's last block, of both operands and
     // this CTA: a row is 128 bytes in each of the four 64-wide chunks, swizzled
@@ -840,6 +912,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       __syncwarp();
       emit(sb, lane, dst, ld, rows, cols);
     };
+    // the same in fp32, 16 columns at a time
+    const auto put_f = [&](const float (&v)[32], float* dst, int64_t ld, int rows, int cols) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          *reinterpret_cast<float4*>(unit_at(sb, lane, u)) =
+              make_float4(v[16 * h + 4 * u], v[16 * h + 4 * u + 1], v[16 * h + 4 * u + 2],
+                          v[16 * h + 4 * u + 3]);
+        __syncwarp();
+        // (in units of 16 bytes, as `emit` counts them)
+        emit(sb, lane, reinterpret_cast<uint16_t*>(dst + 16 * h), 2 * ld, rows,
+             2 * (cols - 16 * h));
+      }
+    };
     if constexpr (KIND == OPEN_ROWS) {
       // rows of no expert (in front of the first, behind the last) are zero
       const int r0 = list.at[0], r1 = max(r0, list.at[P.Z]);
@@ -878,7 +966,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
                       : KIND == OPEN_ROWS
                           ? (t.nv + 31) >> 5
                           : min(8, (N - t.n0 + 31) >> 5);
-      if constexpr (KIND == OPEN_DEPTH) {
+      if constexpr (DEPTH<KIND>) {
         if (t.kb == 0) {  // an expert with no rows: zeros
           uint16_t* dst = out + (static_cast<int64_t>(t.z) * P.M + mw) * P.N + t.n0;
           for (int j = lane; j < 32 * 32; j += 32) {
@@ -937,8 +1025,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           if constexpr (KIND == OPEN_ROWS)
             put_t(f16, v, out + static_cast<int64_t>(t.n0 + 32 * c) * P.M + mw, P.M,
                   t.nv - 32 * c, mrows);
-          else
+          else if (KIND == OPEN_DEPTH || t.nv < 0)
             put_d(f16, v, out + in_at + 32 * c, ld, mrows, N - t.n0 - 32 * c);
+          else
+            put_f(v, P.parts + (static_cast<int64_t>(t.nv) * M + mw) * N + t.n0 + 32 * c, N, mrows,
+                  N - t.n0 - 32 * c);
         }
       } else {
         uint16_t* dst = reinterpret_cast<uint16_t*>(sum ? P.b_out : upd ? P.x_hi[from ^ 1] : P.a_out);
@@ -1024,6 +1115,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   }
 }
 
+// PIECES: the sums of the experts that have several, in order.  Blocks of 2048
+// elements, eight per thread, go round over the grid, expert after expert.
+__global__ void __launch_bounds__(256) open_join_kernel(const OpenParams P) {
+  __shared__ int part[MAX_E + 1];
+  grid_dep_wait();
+  for (int e = threadIdx.x; e <= P.Z; e += blockDim.x) part[e] = P.part_at[e];
+  __syncthreads();
+  const int64_t size = static_cast<int64_t>(P.M) * P.N;
+  const int64_t chunks = (size + 2047) / 2048;
+  int64_t at = blockIdx.x;  // the next chunk of this block, counted from expert e's first
+  for (int e = 0; e < P.Z; ++e) {
+    const int first = part[e], pieces = part[e + 1] - first;
+    if (pieces <= 0) continue;  // (written by its only tiles)
+    for (; at < chunks; at += gridDim.x) {
+      const int64_t i = at * 2048 + threadIdx.x * 8;
+      if (i >= size) continue;
+      const float* src = P.parts + first * size + i;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < pieces; ++k) {
+        const float4 a = *reinterpret_cast<const float4*>(src + k * size);
+        const float4 b = *reinterpret_cast<const float4*>(src + k * size + 4);
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+      }
+      uint32_t q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        q[j] = P.out_f16 ? pack16<true>(v[2 * j], v[2 * j + 1])
+                         : pack16<false>(v[2 * j], v[2 * j + 1]);
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + e * size + i) =
+          make_uint4(q[0], q[1], q[2], q[3]);
+    }
+    at -= chunks;
+  }
+}
+
 // ------------------------------------------------------------------ host side
 // An operand [batch][rows][cols] as loaded: boxes of 64 columns (k, or m / n) x `box`
 // rows (m / n, or k).
@@ -1097,9 +1227,36 @@ int launch_open_rows(const GemmEnv& env, bool f16, const OpenOperand& w, bool w_
   return launch_open<OPEN_ROWS>(env, P, maps, blocks * P.mt);
 }
 
+// Rows of a piece, 0: experts whole.  With whole experts the one with the most rows, say
+// half as many again as the mean, holds its pairs of SMs for all of them, while an even
+// split takes rows x tiles / pairs.  Pieces are half of that, and 2048 rows at least (10 us
+// of products).  The rows saved have to pay for the pieces' way through memory and for a
+// second kernel: 4096 and 128 per tile (us, whole -> pieces):
+//   rows of one expert      6000         16384         65536
+//     256 x 256          31 -> 21      74 -> 22     282 -> 31
+//     1024 x 1024        32 -> 25      78 -> 45     289 -> 102
+//     1408 x 2048       (34 -> 39)    (80 -> 90)    290 -> 244
+//   8 experts of 512 x 1024, rows as 1 / rank: 131071 rows 224 -> 114 (24570: 51 -> 48);
+//   16 even ones, whose tiles fill the device: (131056 rows 96 -> 130)
+int64_t open_depth_piece(int64_t M, int64_t N, int64_t R, int64_t E) {
+  constexpr int64_t pairs = 76;
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  const int64_t most = std::min(R, R * 3 / (2 * E)), even = R * tiles / pairs;
+  if (most - even < 4096 + 128 * tiles) return 0;
+  return std::max<int64_t>(2048, (even / 2 + OK_) / OK_ * OK_);
+}
+
+constexpr size_t O_TABLE = 4 * (MAX_E + 4);  // the workspace's first part: places of the experts
+
+size_t open_depth_workspace(int64_t M, int64_t N, int64_t R, int64_t E) {
+  const int64_t piece = open_depth_piece(M, N, R, E);
+  // an expert of n > 0 whole pieces and a last one has n + 1 <= 2 n places
+  return piece ? O_TABLE + static_cast<size_t>(2 * (R / piece)) * M * N * 4 : 0;
+}
+
 int launch_open_depth(const GemmEnv& env, bool f16, const void* a, int64_t ld_a, int64_t M,
                       const void* b, int64_t ld_b, int64_t N, int64_t R, int64_t E,
-                      const int32_t* offsets, void* out) {
+                      const int32_t* offsets, void* out, void* workspace) {
   OpenParams P{};
   OpenMaps maps;
   open_common(env, &P);
@@ -1118,7 +1275,20 @@ int launch_open_depth(const GemmEnv& env, bool f16, const void* a, int64_t ld_a,
   int rc = encode_operand(env, &maps.a, f16, OpenOperand{a, R, M, 1, ld_a, R * ld_a});
   rc |= encode_operand(env, &maps.b, f16, OpenOperand{b, R, N, 1, ld_b, R * ld_b});
   if (rc != HMM_OK) return HMM_ERR_CUDA;
-  return launch_open<OPEN_DEPTH>(env, P, maps, E * static_cast<int64_t>(P.tiles));
+  P.split = static_cast<int>(open_depth_piece(M, N, R, E));
+  if (P.split) {
+    P.part_at = static_cast<int*>(workspace);
+    P.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + O_TABLE);
+  }
+  const int64_t most = E + (P.split ? R / P.split : 0);
+  if (!P.split) return launch_open<OPEN_DEPTH>(env, P, maps, most * P.tiles);
+  rc = launch_open<OPEN_PIECES>(env, P, maps, most * P.tiles);
+  if (rc != HMM_OK) return rc;
+  const int64_t chunks = R / P.split * ((M * N + 2047) / 2048);
+  const int blocks = static_cast<int>(std::min<int64_t>(8 * env.num_sms, chunks));
+  return launch_kernel(open_join_kernel, blocks, 256, 0, env.stream, env.pdl, 1, P) == cudaSuccess
+             ? HMM_OK
+             : HMM_ERR_CUDA;
 }
 
 int64_t open_chain_tiles(int64_t M, int64_t N, int64_t Z, int64_t steps) {

@@ -10,6 +10,7 @@ namespace hmm {
 
 constexpr int OPEN_ROWS = 0;
 constexpr int OPEN_DEPTH = 1;
+constexpr int OPEN_PIECES = 3;
 constexpr int OPEN_CHAIN = 2;
 
 // OPEN_CHAIN: `steps` Newton-Schulz steps over Z matrices in one launch, three products
@@ -46,6 +47,9 @@ struct OpenParams {
   int K, kb;          // depth, in blocks (ROWS)
   int mt, nt, tiles;  // 256-tiles of m, of n, per expert (DEPTH)
   int a_mn;           // w with m contiguous (ROWS)
+  int split;          // rows of a piece (DEPTH; 0: whole experts)
+  int* part_at;       // [Z + 1]: places of the pieces of the experts before e
+  float* parts;       // [places][M][N]
   int out_f16, plain_out;
   uint32_t idesc;
   const int32_t* offsets;  // [Z + 1] rows of the experts
@@ -80,10 +84,12 @@ struct OpenChain {
 int launch_open_rows(const GemmEnv& env, bool f16, const OpenOperand& w, bool w_mn, const void* x,
                      int64_t ld_x, int64_t R, int64_t K, int64_t M, int64_t E,
                      const int32_t* offsets, void* out);
-// out[e] = a_e^T . b_e, dense [E, M, N]
+// out[e] = a_e^T . b_e, dense [E, M, N]; workspace of open_depth_workspace bytes (may be
+// null for 0), 16-byte aligned
+size_t open_depth_workspace(int64_t M, int64_t N, int64_t R, int64_t E);
 int launch_open_depth(const GemmEnv& env, bool f16, const void* a, int64_t ld_a, int64_t M,
                       const void* b, int64_t ld_b, int64_t N, int64_t R, int64_t E,
-                      const int32_t* offsets, void* out);
+                      const int32_t* offsets, void* out, void* workspace);
 // tiles of a chain (to be counted in 31 bits)
 int64_t open_chain_tiles(int64_t M, int64_t N, int64_t Z, int64_t steps);
 int launch_open_chain(const GemmEnv& env, const OpenChain& s);

@@ -1020,8 +1020,17 @@ int hmm_grouped_mm_dx(hmm_ctx* ctx, const hmm_gmm* d, const void* dy, const void
                           dx);
 }
 
+int hmm_grouped_mm_workspace_size(const hmm_gmm* d, size_t* dw_workspace_bytes) {
+  const int rc = check_gmm(d);
+  if (rc != HMM_OK) return rc;
+  // (the same for K x N and N x K)
+  if (dw_workspace_bytes) *dw_workspace_bytes = open_depth_workspace(d->K, d->N, d->R, d->E);
+  return HMM_OK;
+}
+
 int hmm_grouped_mm_dw(hmm_ctx* ctx, const hmm_gmm* d, const void* x, const void* dy,
-                      const int32_t* offsets, void* dw, void* stream) {
+                      const int32_t* offsets, void* dw, void* workspace, size_t workspace_bytes,
+                      void* stream) {
   if (!ctx) return HMM_ERR_ARG;
   const int rc = check_gmm(d);
   if (rc != HMM_OK) return rc;
@@ -1029,8 +1038,12 @@ int hmm_grouped_mm_dw(hmm_ctx* ctx, const hmm_gmm* d, const void* x, const void*
   if (!aligned16(dw)) return HMM_ERR_LAYOUT;
   if (d->R > 0) {
     if (!x || !dy || !offsets) return HMM_ERR_ARG;
-    if (!aligned16(x) || !aligned16(dy) || !aligned_to(offsets, HMM_DTYPE_F32))
+    if (!aligned16(x) || !aligned16(dy) || !aligned16(workspace) ||
+        !aligned_to(offsets, HMM_DTYPE_F32))
       return HMM_ERR_LAYOUT;
+    const size_t need = open_depth_workspace(d->K, d->N, d->R, d->E);
+    if (need > 0 && !workspace) return HMM_ERR_ARG;
+    if (workspace_bytes < need) return HMM_ERR_CAPACITY;
   }
   DeviceGuard g(ctx->device);
   if (!g.ok) return HMM_ERR_CUDA;
@@ -1040,9 +1053,9 @@ int hmm_grouped_mm_dw(hmm_ctx* ctx, const hmm_gmm* d, const void* x, const void*
   const bool f16 = d->dtype == HMM_DTYPE_F16;
   if (d->w_layout == HMM_W_KN)
     return launch_open_depth(open_env(ctx, stream), f16, x, d->ld_x, d->K, dy, d->ld_dy, d->N,
-                             d->R, d->E, offsets, dw);
+                             d->R, d->E, offsets, dw, workspace);
   return launch_open_depth(open_env(ctx, stream), f16, dy, d->ld_dy, d->N, x, d->ld_x, d->K, d->R,
-                           d->E, offsets, dw);
+                           d->E, offsets, dw, workspace);
 }
 
 int hmm_orthogonalize_workspace_size(const hmm_ortho* desc, size_t* workspace_bytes) {

@@ -524,8 +524,12 @@ int hmm_grouped_mm(hmm_ctx* ctx, const hmm_gmm* desc, const void* x, const void*
                    const int32_t* offsets, void* y, void* stream);
 int hmm_grouped_mm_dx(hmm_ctx* ctx, const hmm_gmm* desc, const void* dy, const void* w,
                       const int32_t* offsets, void* dx, void* stream);
+/* dw takes a workspace (16-byte aligned) where the rows of an expert are summed in
+ * pieces; the size may be 0, the pointer then NULL. */
+int hmm_grouped_mm_workspace_size(const hmm_gmm* desc, size_t* dw_workspace_bytes);
 int hmm_grouped_mm_dw(hmm_ctx* ctx, const hmm_gmm* desc, const void* x, const void* dy,
-                      const int32_t* offsets, void* dw, void* stream);
+                      const int32_t* offsets, void* dw, void* workspace, size_t workspace_bytes,
+                      void* stream);
 
 /* Orthogonalised update of a stack of matrices by Newton-Schulz products (the Muon
  * optimiser's step), each matrix G [M, N] by itself:

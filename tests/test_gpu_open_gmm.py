@@ -22,6 +22,11 @@ CASES = [
     ([700], 1408, 320),
     ([5000, 3, 0, 40], 320, 776),
     ([1] * 70 + [0] * 20 + [2] * 30, 512, 512),
+    # the rows of an expert in pieces: one hot expert between empty and small ones, whole
+    # pieces, one row more and less
+    ([0, 19000, 0, 5, 2049], 136, 264),
+    ([2048, 4096, 2049, 6143, 10241, 1], 64, 128),
+    ([20001], 72, 200),
 ]
 
 
@@ -190,6 +195,26 @@ def test_unordered_offsets_stay_inside(offsets):
     run(x, w, dy, o)
     assert hmm.hmm_status(h) == (0, 0)
     assert bool((guard[0] == 7).all()) and bool((guard[2] == 7).all())
+
+
+@pytest.mark.parametrize("offsets", [[0, 19000, 0, 19000, 0, 19000],
+                                     [19000, 0, 19000, 0, 19000, 10],
+                                     [-7, 8000, 3000, 40000, 6000, 19000]])
+def test_unordered_offsets_stay_in_the_workspace(offsets):
+    """The pieces of an expert's rows have places in the workspace that sums of rows
+    bound: with offsets out of order too."""
+    R, K, N, E = 19000, 64, 64, 5
+    x, _, dy, _ = problem([R, 0, 0, 0, 0], K, N, torch.bfloat16)
+    o = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    d = hmm.make_gmm(R, K, N, E)
+    size = hmm.hmm_grouped_mm_workspace_size(d)
+    assert size > 0
+    guard = torch.full((size + 65536,), 7, dtype=torch.uint8, device=DEV)
+    dw = torch.empty((E, K, N), dtype=torch.bfloat16, device=DEV)
+    h = hmm.Context.for_device(x.device).handle
+    hmm.hmm_grouped_mm_dw(h, d, x, dy, o, dw, guard[:size])
+    assert hmm.hmm_status(h) == (0, 0)
+    assert bool((guard[size:] == 7).all())
 
 
 def test_only_the_gradients_asked_for():
