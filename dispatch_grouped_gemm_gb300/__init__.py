@@ -1064,8 +1064,8 @@ def moe_route(topk_ids, num_experts):
     # one allocation: counts | offsets | slot2row | row2slot
     n = T * K
     buf = torch.empty(2 * E + 1 + 2 * n, dtype=torch.int32, device=dev)
-    counts, offsets = buf[:E], buf[E:2 * E + 1]
-    slot2row, row2slot = buf[2 * E + 1:2 * E + 1 + n].view(T, K), buf[2 * E + 1 + n:]
+    counts, offsets, slot2row, row2slot = buf.split((E, E + 1, n, n))
+    slot2row = slot2row.view(T, K)
     ws = torch.empty(size, dtype=torch.uint8, device=dev)
     rc = load_library().hmm_route(
         Context.for_device(dev).handle, ctypes.byref(shape), topk_ids.data_ptr(),
@@ -1351,10 +1351,10 @@ def orthogonalize(g, *, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, scale
         out_dtype = torch.float16 if g.dtype == torch.float16 else torch.bfloat16
     if out_dtype not in (torch.bfloat16, torch.float16):
         raise TypeError("out_dtype must be bfloat16 or float16 (the products take 16-bit operands)")
-    if not isinstance(coefficients[0], (tuple, list)):
+    if len(coefficients) > 0 and not isinstance(coefficients[0], (tuple, list)):
         coefficients = (tuple(coefficients),) * int(steps)
     coefficients = tuple(tuple(float(v) for v in c) for c in coefficients)
-    if len(coefficients) != steps or any(len(c) != 3 for c in coefficients):
+    if not coefficients or len(coefficients) != steps or any(len(c) != 3 for c in coefficients):
         raise ValueError("coefficients must be (a, b, c), or `steps` of them")
     if not g.is_cuda:
         raise ValueError("g must be a CUDA tensor")
