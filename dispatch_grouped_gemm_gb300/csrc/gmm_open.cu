@@ -90,7 +90,7 @@ struct OpenMaps {
 struct OpenTile {
   int z;       // expert or matrix
   int m0, n0;  // ROWS: n0 = first row of the block
-  int nv, nb;  // ROWS: rows of the block, MMA columns (a multiple of 16); else nb = 256,
+  int nv, nb;  // ROWS: rows of the block, MMA columns (a multiple of 16);
                // PIECES: nv = place in the workspace, -1: the expert's only piece
   int kb;      // K blocks
   int k0, k1;  // DEPTH: the expert's rows; CHAIN: product (3 per step) and its kind
@@ -234,6 +234,9 @@ __device__ __forceinline__ int open_div(int64_t u, int d, int& rest) {
   return q;
 }
 
+// MMA columns of the tile at n0: those that exist (a tile at the edge takes less time).
+__device__ __forceinline__ int open_width(int N, int n0) { return min(256, (N - n0 + 15) & ~15); }
+
 // The largest e <= hi with list[e] <= u.
 __device__ __forceinline__ int open_find(const int* list, int hi, int u) {
   int lo = 0;
@@ -289,7 +292,6 @@ __device__ __forceinline__ void chain_tile(const OpenParams& P, const OpenList& 
   t.z = 3 * k + g;
   t.k0 = lo - g;
   t.k1 = t.k0 % 3;
-  t.nv = t.nb = 256;
   const OpenPhase& ph = P.ph[t.k1];
   t.kb = ph.kb;
   open_place(r, ph.mt, ph.nt, ph.sym, t);
@@ -315,8 +317,8 @@ __device__ __forceinline__ bool open_tile(const OpenParams& P, const OpenList& l
     t.kb = P.kb;
   } else {
     const int i = open_div(u, P.tiles, r);
-    t.nv = t.nb = 256;
     open_place(r, P.mt, P.nt, false, t);
+    t.nb = open_width(P.N, t.n0);
     if constexpr (KIND == OPEN_PIECES) {
       // the whole pieces first, then the last ones from the longest to the shortest
       const int whole = l.full[P.Z];
@@ -508,8 +510,9 @@ __device__ __forceinline__ bool open_next(const OpenParams& P, const OpenList& l
     t.k1 = u.y % 3;
     t.m0 = u.z;
     t.n0 = u.w;
-    t.nv = t.nb = 256;
-    t.kb = P.ph[t.k1].kb;
+    const OpenPhase& ph = P.ph[t.k1];
+    t.nb = open_width(ph.N, t.n0);
+    t.kb = ph.kb;
     return true;
   }
 }
