@@ -62,6 +62,8 @@ constexpr int OA_BYTES = 2 * OCHUNK;     // this CTA's 128 rows of A
 constexpr int OB_BYTES = 2 * OCHUNK;     // this CTA's half of B's rows, at most 128
 constexpr int OSTAGE = OA_BYTES + OB_BYTES;
 constexpr int OBUF = 2048;             // a warp's staging of one 32 x 32 chunk of 16-bit results
+constexpr uint32_t IDESC_A_MN = idesc_bf16_f32(0, 0, 1, 0) ^ idesc_bf16_f32(0, 0, 0, 0);
+constexpr uint32_t IDESC_B_MN = idesc_bf16_f32(0, 0, 0, 1) ^ idesc_bf16_f32(0, 0, 0, 0);
 constexpr uint32_t O_TMEM_COLS = 512;  // two accumulators of 256 columns
 constexpr int O_SORT_MAX_E = 512;      // experts that DEPTH sorts by rows (E^2 / threads compares)
 constexpr int O_CUT_AHEAD = 1;         // blocks that a block to be cut is loaded early
@@ -613,6 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
     bool a_mn = DEPTH<KIND> || P.a_mn, b_mn = DEPTH<KIND>;
     const CUtensorMap* am = &maps.a;
     int depth = P.K;
+    int a_turn = 0, b_turn = 0;  // CHAIN: depths below are read from the other triangle
     for (; ok && more; t = next) {
       const int ma = t.m0 + 128 * static_cast<int>(rank);
       // B: this CTA's half of the columns, in boxes of a multiple of 16 rows
@@ -628,6 +631,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         b_mn = ph.b_mn;
         am = ph.a == 0 ? x : ph.a == 1 ? &maps.a : &maps.b;
         bm = ph.b == 0 ? x : ph.b == 1 ? &maps.a : &maps.b;
+        a_turn = ph.a == 0 ? 0 : t.m0;
+        b_turn = ph.b == 0 ? 0 : t.n0;
         depth = ph.K;
         // what this tile reads was written by other CTAs of this launch: the scheduler
         // acquired their counter; order that with the asynchronous copies
@@ -657,10 +662,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         // reaches it; MN-major ones in two boxes of 64 wide
         const bool deep = DEPTH<KIND> || k + 64 < depth;
         const bool cutting = tail && j == place;
+        const bool at = a_mn || (KIND == OPEN_CHAIN && k < a_turn);
+        const bool bt = b_mn || (KIND == OPEN_CHAIN && k < b_turn);
         uint8_t* sA = stages + stage * OSTAGE;
         uint8_t* sB = sA + OA_BYTES;
-        const uint32_t bytes =
-            (a_mn || deep ? OA_BYTES : OCHUNK) + (b_mn || deep ? 2 * b_box : b_box);
+        const uint32_t bytes = (at || deep ? OA_BYTES : OCHUNK) + (bt || deep ? 2 * b_box : b_box);
         if (elect_one()) {
           if (cutting) {
             // counted on this CTA's own barrier; `full` completes at once
@@ -677,14 +683,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
             const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
             // coordinates of an MN-major box: (m or n, c1, c2)
             const int c1 = DEPTH<KIND> ? t.k0 + k : k, c2 = DEPTH<KIND> ? 0 : t.z;
-            if (a_mn) {
+            if (at) {
               tma_load_3d_pair(sA, am, bar, ma, c1, c2);
               tma_load_3d_pair(sA + OCHUNK, am, bar, ma + 64, c1, c2);
             } else {
               tma_load_3d_pair(sA, am, bar, k, ma, t.z);
               if (deep) tma_load_3d_pair(sA + OCHUNK, am, bar, k + 64, ma, t.z);
             }
-            if (b_mn) {
+            if (bt) {
               tma_load_3d_pair(sB, bm, bar, nbase, c1, c2);
               tma_load_3d_pair(sB + OCHUNK, bm, bar, nbase + 64, c1, c2);
             } else {
@@ -726,6 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       const uint64_t a_k = smem_desc(smem_u32(stages), 16, 1024, LAYOUT_SW128);
       const uint64_t a_m = smem_desc(smem_u32(stages), OCHUNK, 1024, LAYOUT_SW128);
       bool a_mn = DEPTH<KIND> || P.a_mn, b_mn = DEPTH<KIND>;
+      int a_turn = 0, b_turn = 0;
       uint32_t stage = 0, sphase = 0, acc = 0, acc_phase = 0, cut_phase = 0;
       bool ok = true;
       OpenWalk walk;
@@ -734,15 +741,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       };
       OpenTile t, next;
       bool more = advance(t);
-      // the MMAs of the block in slot `at`, the first `steps` of them
-      const auto block = [&](uint32_t at, int steps, uint32_t d_tmem, uint32_t idesc, bool first) {
+      // the MMAs of the block in slot `at` from depth k on, the first `steps` of them
+      const auto block = [&](uint32_t at, int k, int steps, uint32_t d_tmem, uint32_t idesc,
+                             bool first) {
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t a_step = (a_mn ? 2048 : 32) / 16, b_step = (b_mn ? 2048 : 32) / 16;
-          const uint32_t a_jump = (a_mn ? 4 * 2048 : OCHUNK) / 16;
-          const uint32_t b_jump = (b_mn ? 4 * 2048 : OCHUNK) / 16;
-          const uint64_t ad = (a_mn ? a_m : a_k) + at * (OSTAGE / 16);
-          const uint64_t bd = (b_mn ? a_m : a_k) + at * (OSTAGE / 16) + OA_BYTES / 16;
+          const bool am = a_mn || (KIND == OPEN_CHAIN && k < a_turn);
+          const bool bm = b_mn || (KIND == OPEN_CHAIN && k < b_turn);
+          if constexpr (KIND == OPEN_CHAIN) idesc |= (am ? IDESC_A_MN : 0) | (bm ? IDESC_B_MN : 0);
+          const uint32_t a_step = (am ? 2048 : 32) / 16, b_step = (bm ? 2048 : 32) / 16;
+          const uint32_t a_jump = (am ? 4 * 2048 : OCHUNK) / 16;
+          const uint32_t b_jump = (bm ? 4 * 2048 : OCHUNK) / 16;
+          const uint64_t ad = (am ? a_m : a_k) + at * (OSTAGE / 16);
+          const uint64_t bd = (bm ? a_m : a_k) + at * (OSTAGE / 16) + OA_BYTES / 16;
           if (steps == OK_ / 16) {
 #pragma unroll
             for (int kk = 0; kk < OK_ / 16; ++kk)
@@ -771,7 +782,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           const OpenPhase& ph = P.ph[t.k1];
           a_mn = ph.a_mn;
           b_mn = ph.b_mn;
-          idesc |= ph.idesc;
+          a_turn = ph.a == 0 ? 0 : t.m0;
+          b_turn = ph.b == 0 ? 0 : t.n0;
           depth = ph.K;
         }
         ok = warp_all(mbar_wait(&tempty[acc], acc_phase ^ 1u, wc));
@@ -791,7 +803,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           } else {
             ok = warp_all(mbar_wait(&full[stage], sphase, wc));
             if (!ok) break;
-            block(stage, !tail && j == t.kb - 1 ? last_steps : OK_ / 16, d_tmem, idesc, first);
+            block(stage, j * OK_, !tail && j == t.kb - 1 ? last_steps : OK_ / 16, d_tmem, idesc,
+                  first);
             first = false;
           }
           if (++stage == ST) {
@@ -807,7 +820,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
                warp_all(mbar_wait<true>(&cut[held], cut_phase >> held & 1u, wc));
           if (!ok) break;
           cut_phase ^= 1u << held;
-          block(held, last_steps, d_tmem, idesc, first);
+          block(held, 0, last_steps, d_tmem, idesc, first);
         }
         if (elect_one()) umma_commit_pair(&tfull[acc], 0x3);
         __syncwarp();
@@ -1036,7 +1049,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         }
       } else {
         uint16_t* dst = reinterpret_cast<uint16_t*>(sum ? P.b_out : upd ? P.x_hi[from ^ 1] : P.a_out);
-        const bool mirror = !upd && t.n0 > t.m0, split = upd && !last && P.f[step + 1].low;
+        const bool split = upd && !last && P.f[step + 1].low;
 #pragma unroll 1
         for (int c = first; c < nch; c += SHARE) {
           uint32_t r[32];
@@ -1077,9 +1090,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           const int64_t at = in_at + 32 * c;
           const int cols = static_cast<int>(ld) - n;
           put_d(true, v, dst + at, ld, mrows, cols);
-          if (mirror)  // (the results are symmetric)
-            put_t(true, v, dst + (static_cast<int64_t>(t.z) * M + n) * ld + mw, ld, M - n,
-                  static_cast<int>(ld) - mw);
           if (split) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] -= half_round(v[j]);
@@ -1323,7 +1333,6 @@ int launch_open_chain(const GemmEnv& env, const OpenChain& s) {
     p.b = b;
     p.a_mn = a_mn;
     p.b_mn = b_mn;
-    p.idesc = open_idesc(true, a_mn, b_mn);
   };
   // A: the rows (wide) or columns of X against each other; B: A A; X: B X (X's rows are
   // the contraction) or X B

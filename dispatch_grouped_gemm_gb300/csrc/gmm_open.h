@@ -19,7 +19,8 @@ constexpr int OPEN_CHAIN = 2;
 //   1  B  = alpha_b A A + beta_b A + gamma_b I         symmetric
 //   2  v  = alpha_x B X + beta_x lo;  X <- hi = fp16(v), lo = fp16(v - hi), of the last
 //      step the caller's result (bf16 or fp16)
-// A symmetric result is computed for tiles on and above the diagonal and written twice.
+// Of a symmetric result only the tiles on and above the diagonal are computed and
+// written; as an operand its blocks below are read from the others, m / n contiguous.
 // The first X is stored without a factor `factor[z]` of its matrix.
 struct OpenFactors {
   float alpha_a, alpha_b, beta_b, gamma_b, alpha_x, beta_x;
@@ -32,7 +33,6 @@ struct OpenPhase {
   int sym;
   int a, b;           // operands: 0 X, 1 A, 2 B
   int a_mn, b_mn;     // ... with m / n contiguous
-  uint32_t idesc;
 };
 
 // [batch][rows][cols], rows ld and matrices stride elements apart (multiples of 8;
