@@ -1128,40 +1128,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
   }
 }
 
-// PIECES: the sums of the experts that have several, in order.  Blocks of 2048
-// elements, eight per thread, go round over the grid, expert after expert.
-__global__ void __launch_bounds__(256) open_join_kernel(const OpenParams P) {
+// PIECES: the sums of the experts that have several, in order.  Blocks of JOIN_CHUNK
+// elements, four per thread, go round over the grid, expert after expert.
+constexpr int JOIN_CHUNK = 4 * 128;
+__global__ void __launch_bounds__(128) open_join_kernel(const OpenParams P) {
   __shared__ int part[MAX_E + 1];
   grid_dep_wait();
   for (int e = threadIdx.x; e <= P.Z; e += blockDim.x) part[e] = P.part_at[e];
   __syncthreads();
   const int64_t size = static_cast<int64_t>(P.M) * P.N;
-  const int64_t chunks = (size + 2047) / 2048;
+  const int64_t chunks = (size + JOIN_CHUNK - 1) / JOIN_CHUNK;
   int64_t at = blockIdx.x;  // the next chunk of this block, counted from expert e's first
   for (int e = 0; e < P.Z; ++e) {
     const int first = part[e], pieces = part[e + 1] - first;
     if (pieces <= 0) continue;  // (written by its only tiles)
     for (; at < chunks; at += gridDim.x) {
-      const int64_t i = at * 2048 + threadIdx.x * 8;
+      const int64_t i = at * JOIN_CHUNK + threadIdx.x * 4;
       if (i >= size) continue;
       const float* src = P.parts + first * size + i;
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
-#pragma unroll 4
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
       for (int k = 0; k < pieces; ++k) {
-        const float4 a = *reinterpret_cast<const float4*>(src + k * size);
-        const float4 b = *reinterpret_cast<const float4*>(src + k * size + 4);
-        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(src + k * size));
+        v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
       }
-      uint32_t q[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        q[j] = P.out_f16 ? pack16<true>(v[2 * j], v[2 * j + 1])
-                         : pack16<false>(v[2 * j], v[2 * j + 1]);
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + e * size + i) =
-          make_uint4(q[0], q[1], q[2], q[3]);
+      const uint2 q = P.out_f16 ? make_uint2(pack16<true>(v.x, v.y), pack16<true>(v.z, v.w))
+                                : make_uint2(pack16<false>(v.x, v.y), pack16<false>(v.z, v.w));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + e * size + i) = q;
     }
     at -= chunks;
   }
@@ -1297,9 +1290,9 @@ int launch_open_depth(const GemmEnv& env, bool f16, const void* a, int64_t ld_a,
   if (!P.split) return launch_open<OPEN_DEPTH>(env, P, maps, most * P.tiles);
   rc = launch_open<OPEN_PIECES>(env, P, maps, most * P.tiles);
   if (rc != HMM_OK) return rc;
-  const int64_t chunks = R / P.split * ((M * N + 2047) / 2048);
-  const int blocks = static_cast<int>(std::min<int64_t>(8 * env.num_sms, chunks));
-  return launch_kernel(open_join_kernel, blocks, 256, 0, env.stream, env.pdl, 1, P) == cudaSuccess
+  const int64_t chunks = R / P.split * ((M * N + JOIN_CHUNK - 1) / JOIN_CHUNK);
+  const int blocks = static_cast<int>(std::min<int64_t>(16 * env.num_sms, chunks));
+  return launch_kernel(open_join_kernel, blocks, 128, 0, env.stream, env.pdl, 1, P) == cudaSuccess
              ? HMM_OK
              : HMM_ERR_CUDA;
 }

@@ -29,9 +29,8 @@
 // lo.
 //
 // What bounds it: 3 m^2 n + m^3 operations per step (A and A A are symmetric: one
-// triangle of tiles each) at the tensor rate; between them X moves four times
-// (hi, lo in and out), which the other products hide.  The norm and the first
-// conversion read G twice.
+// triangle of tiles each) at the tensor rate; X moves beside them (lo in, hi and lo
+// out, besides hi as the operand).  The norm and the first conversion read G twice.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,7 +46,10 @@ namespace {
 
 constexpr int ORTHO_THREADS = 256;
 constexpr int64_t ORTHO_PIECE = 8192;     // elements per block and matrix, at least
-constexpr int64_t ORTHO_BLOCKS = 152 * 8;  // blocks of the stack that fill the device
+// Blocks of the stack: those that run at once (each works out its matrix's factor first,
+// 5 us of latency that a second wave would pay again).
+constexpr int ORTHO_RESIDENT = 4;
+constexpr int64_t ORTHO_BLOCKS = 152 * ORTHO_RESIDENT;
 constexpr int ORTHO_MAX_PIECES = 256;
 
 // Sums of squares in three ranges, so that neither the squares of large elements
@@ -60,16 +62,28 @@ constexpr float SUM_BIG_SCALE = 0x1p-80f;
 constexpr float SUM_SMALL = 0x1p-50f;  // squares of smaller ones by 2^160
 constexpr float SUM_SMALL_SCALE = 0x1p80f;
 
-__device__ __forceinline__ void sum_add(Sums& s, float v) {
-  const float a = fabsf(v);
-  if (a > SUM_BIG) {
-    const float t = a * SUM_BIG_SCALE;
+// Eight elements.  Where their squares neither overflow nor add up to less than 2^-60,
+// those of elements below 2^-50 are below its rounding and one sum holds them all.
+__device__ __forceinline__ void sum_add(Sums& s, const float (&v)[8]) {
+  float most = 0.f, q = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    most = fmaxf(most, fabsf(v[j]));  // (leaves a NaN out; q does not)
+    q = fmaf(v[j], v[j], q);
+  }
+  if (most <= SUM_BIG && (q >= 0x1p-60f || most == 0.f)) {
+    s.mid += q;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float a = fabsf(v[j]);
+    const float t = a > SUM_BIG ? a * SUM_BIG_SCALE : 0.f;
+    const float u = a < SUM_SMALL ? a * SUM_SMALL_SCALE : 0.f;
+    const float m = a > SUM_BIG || a < SUM_SMALL ? 0.f : v[j];  // NaN too
     s.big = fmaf(t, t, s.big);
-  } else if (a < SUM_SMALL) {
-    const float t = a * SUM_SMALL_SCALE;
-    s.small = fmaf(t, t, s.small);
-  } else {
-    s.mid = fmaf(v, v, s.mid);  // NaN comes here
+    s.mid = fmaf(m, m, s.mid);
+    s.small = fmaf(u, u, s.small);
   }
 }
 
@@ -107,6 +121,7 @@ struct OrthoArgs {
   int64_t ld_x;
   float eps;
   float scale;  // 2^e of X
+  int aligned;  // every unit of eight elements is whole and on a 16-byte boundary
 };
 
 // Eight elements from any element address, the first `valid` of them (the others 0):
@@ -114,15 +129,6 @@ struct OrthoArgs {
 template <typename T>
 __device__ __forceinline__ void load8(const T* src, int valid, float (&v)[8]) {
   constexpr int B = sizeof(T), W = B == 4 ? 3 : 2;
-  if (valid == 8 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-    alignas(16) T e[8];
-#pragma unroll
-    for (int k = 0; k < B / 2; ++k)
-      reinterpret_cast<uint4*>(e)[k] = __ldg(reinterpret_cast<const uint4*>(src) + k);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = ortho_get(e[j]);
-    return;
-  }
   const uintptr_t at = reinterpret_cast<uintptr_t>(src);
   const int off = static_cast<int>(at & 15u);
   const uint4* p = reinterpret_cast<const uint4*>(at - off);
@@ -159,33 +165,54 @@ __device__ __forceinline__ void load8(const T* src, int valid, float (&v)[8]) {
   for (int j = 0; j < 8; ++j) v[j] = j < valid ? ortho_get(e[j]) : 0.f;
 }
 
-// The piece's rows in units of eight elements, four units of a thread in flight.
+// The piece's rows in units of eight elements, four units of a thread in flight (where
+// they are aligned: with load8's branches a thread waits for each of its loads, and the
+// norm of 46 M bf16 elements took 42 us, 2.2 TB/s).
 template <typename T, typename F>
 __device__ __forceinline__ void ortho_walk(const OrthoArgs& a, const F& f) {
-  constexpr int U = 4;
+  constexpr int U = 4, Q = sizeof(T) / 2;
   const int64_t r0 = blockIdx.x * a.rows_per_piece, r1 = min(a.M, r0 + a.rows_per_piece);
   const uint32_t per = static_cast<uint32_t>((a.N + 7) / 8);
   const uint32_t n = r1 > r0 ? static_cast<uint32_t>(r1 - r0) * per : 0;
   const T* g = static_cast<const T*>(a.g) + blockIdx.y * a.stride;
-  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += U * ORTHO_THREADS) {
-    float v[U][8];
-    int64_t r[U];
-    int c[U];
+  if (a.aligned) {
+    for (uint32_t i0 = threadIdx.x; i0 < n; i0 += U * ORTHO_THREADS) {
+      uint4 q[U][Q];
+      int64_t r[U];
+      int c[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t i = i0 + u * ORTHO_THREADS, q = i / per;
-      r[u] = r0 + q;
-      c[u] = static_cast<int>(i - q * per) * 8;
-      if (i < n) load8(g + r[u] * a.ld + c[u], static_cast<int>(min(int64_t(8), a.N - c[u])), v[u]);
+      for (int u = 0; u < U; ++u) {
+        const uint32_t i = min(i0 + u * ORTHO_THREADS, n - 1), row = i / per;
+        r[u] = r0 + row;
+        c[u] = static_cast<int>(i - row * per) * 8;
+        const uint4* src = reinterpret_cast<const uint4*>(g + r[u] * a.ld + c[u]);
+#pragma unroll
+        for (int k = 0; k < Q; ++k) q[u][k] = __ldg(src + k);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        alignas(16) T e[8];
+        memcpy(e, q[u], sizeof e);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = ortho_get(e[j]);
+        if (i0 + u * ORTHO_THREADS < n) f(r[u], c[u], v);
+      }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + u * ORTHO_THREADS < n) f(r[u], c[u], v[u]);
+    return;
+  }
+  for (uint32_t i = threadIdx.x; i < n; i += ORTHO_THREADS) {
+    const uint32_t row = i / per;
+    const int c = static_cast<int>(i - row * per) * 8;
+    float v[8];
+    load8(g + (r0 + row) * a.ld + c, static_cast<int>(min(int64_t(8), a.N - c)), v);
+    f(r0 + row, c, v);
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(ORTHO_THREADS) ortho_norm_kernel(const OrthoArgs a) {
+__global__ void __launch_bounds__(ORTHO_THREADS, ORTHO_RESIDENT)
+    ortho_norm_kernel(const OrthoArgs a) {
   __shared__ Sums part[ORTHO_THREADS / 32];
   grid_dep_wait();
   grid_dep_launch();
@@ -194,10 +221,7 @@ __global__ void __launch_bounds__(ORTHO_THREADS) ortho_norm_kernel(const OrthoAr
     if (blockIdx.y == 0) *a.ticket = 0;
   }
   Sums s{0.f, 0.f, 0.f};
-  ortho_walk<T>(a, [&](int64_t, int, const float (&v)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum_add(s, v[j]);
-  });
+  ortho_walk<T>(a, [&](int64_t, int, const float (&v)[8]) { sum_add(s, v); });
   sums_reduce(s, part);
   if (threadIdx.x == 0) a.sums[static_cast<int64_t>(blockIdx.y) * a.pieces + blockIdx.x] = s;
 }
@@ -235,7 +259,8 @@ __device__ float3 ortho_factor(const OrthoArgs& a) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(ORTHO_THREADS) ortho_first_kernel(const OrthoArgs a) {
+__global__ void __launch_bounds__(ORTHO_THREADS, ORTHO_RESIDENT)
+    ortho_first_kernel(const OrthoArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const float3 f = ortho_factor(a);
@@ -245,14 +270,14 @@ __global__ void __launch_bounds__(ORTHO_THREADS) ortho_first_kernel(const OrthoA
   ortho_walk<T>(a, [&](int64_t r, int c, const float (&v)[8]) {
     alignas(16) __half h[8], l[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = v[j] * f.x * f.y;
-      h[j] = __float2half_rn(x);
-      l[j] = __float2half_rn(x - __half2float(h[j]));
-    }
+    for (int j = 0; j < 8; ++j) h[j] = __float2half_rn(v[j] * f.x * f.y);
     // (rows of X are padded to eight elements)
     *reinterpret_cast<uint4*>(hi + r * a.ld_x + c) = *reinterpret_cast<const uint4*>(h);
-    if (lo) *reinterpret_cast<uint4*>(lo + r * a.ld_x + c) = *reinterpret_cast<const uint4*>(l);
+    if (lo) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) l[j] = __float2half_rn(v[j] * f.x * f.y - __half2float(h[j]));
+      *reinterpret_cast<uint4*>(lo + r * a.ld_x + c) = *reinterpret_cast<const uint4*>(l);
+    }
   });
 }
 
@@ -342,7 +367,7 @@ OrthoPlan ortho_plan(const hmm_ortho& d) {
   const int64_t n = d.M * round8(d.N);
   p.pieces = static_cast<int>(
       std::min<int64_t>({(n + ORTHO_PIECE - 1) / ORTHO_PIECE, ORTHO_MAX_PIECES, d.M,
-                         ORTHO_BLOCKS / std::max<int64_t>(d.batch, 1) + 1}));
+                         std::max<int64_t>(1, ORTHO_BLOCKS / std::max<int64_t>(d.batch, 1))}));
   p.rows_per_piece = (d.M + p.pieces - 1) / p.pieces;
   const size_t x = up256(static_cast<size_t>(d.batch) * d.M * p.ld_x * 2);
   const size_t a = up256(static_cast<size_t>(d.batch) * p.m * p.ld_a * 2);
@@ -371,6 +396,9 @@ int launch_ortho(const GemmEnv& env, const hmm_ortho& d, const OrthoPlan& p, con
   a.stride = d.stride;
   a.pieces = p.pieces;
   a.rows_per_piece = p.rows_per_piece;
+  const int64_t bytes = d.dtype == HMM_DTYPE_F32 ? 4 : 2;
+  a.aligned = d.N % 8 == 0 && (reinterpret_cast<uintptr_t>(g) & 15u) == 0 &&
+              (d.M == 1 || d.ld * bytes % 16 == 0) && (d.batch == 1 || d.stride * bytes % 16 == 0);
   a.sums = reinterpret_cast<Sums*>(ws);
   a.factor = reinterpret_cast<float*>(ws + p.off_factor);
   a.ticket = reinterpret_cast<int*>(ws + p.off_ticket);
