@@ -166,8 +166,8 @@ __device__ __forceinline__ void load8(const T* src, int valid, float (&v)[8]) {
 }
 
 // The piece's rows in units of eight elements, four units of a thread in flight (where
-// they are aligned: with load8's branches a thread waits for each of its loads, and the
-// norm of 46 M bf16 elements took 42 us, 2.2 TB/s).
+// they are aligned: with load8's branches a thread waits for each of its loads; 46 M
+// bf16 elements: norm 42 -> 20 us, first conversion 54 -> 29 us, 4.6 TB/s each).
 template <typename T, typename F>
 __device__ __forceinline__ void ortho_walk(const OrthoArgs& a, const F& f) {
   constexpr int U = 4, Q = sizeof(T) / 2;
