@@ -98,7 +98,9 @@ struct Cfg {
 
 struct OpenMaps {
   CUtensorMap a, b;      // CHAIN: A, B
-  CUtensorMap brows[8];  // ROWS: x in boxes of 16, 32 .. 128 rows; CHAIN: X of even, odd steps
+  // ROWS: x in boxes of 16, 32 .. 128 rows; CHAIN: X of even, odd steps, and with operands
+  // in two parts the second ones of X (two), A and B
+  CUtensorMap brows[8];
 };
 
 struct OpenTile {
@@ -625,8 +627,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
     OpenTile t, next;
     bool more = advance(t);
     bool a_mn = DEPTH<KIND> || P.a_mn, b_mn = DEPTH<KIND>;
-    const CUtensorMap* am = &maps.a;
+    const CUtensorMap *am = &maps.a, *am2 = am, *bm2 = am;
     int depth = P.K;
+    int pass_kb = 0;             // CHAIN: blocks of a pair of parts
     int a_turn = 0, b_turn = 0;  // CHAIN: depths below are read from the other triangle
     for (; ok && more; t = next) {
       const int ma = t.m0 + 128 * static_cast<int>(rank);
@@ -643,13 +646,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         b_mn = ph.b_mn;
         am = ph.a == 0 ? x : ph.a == 1 ? &maps.a : &maps.b;
         bm = ph.b == 0 ? x : ph.b == 1 ? &maps.a : &maps.b;
+        const CUtensorMap* x2 = &maps.brows[2 + (t.k0 / 3 & 1)];
+        am2 = ph.a == 0 ? x2 : &maps.brows[3 + ph.a];
+        bm2 = ph.b == 0 ? x2 : &maps.brows[3 + ph.b];
+        pass_kb = ph.pass_kb;
         a_turn = ph.a == 0 ? 0 : t.m0;
         b_turn = ph.b == 0 ? 0 : t.n0;
         depth = ph.K;
         // what this tile reads was written by other CTAs of this launch: the scheduler
         // acquired their counter; order that with the asynchronous copies
         fence_proxy_async_global();
-        if (t.k1 == 2 && P.f[t.k0 / 3].low) {  // what the epilogue adds, into L2 meanwhile
+        if (t.k1 == 2 && P.f[t.k0 / 3].low && !P.parts2) {  // what the epilogue adds, into L2 meanwhile
           const __half* lo = P.x_lo[t.k0 / 3 & 1];
           const int rows = min(128, ph.M - ma), lines = min(4, (ph.N - t.n0 + 63) >> 6);
           const int64_t at = (static_cast<int64_t>(t.z) * ph.M + ma) * P.ld_x + t.n0;
@@ -668,7 +675,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         ok = warp_all(mbar_wait(&empty[stage], sphase ^ 1u, wc));
         if (!ok) break;
         // block of the j-th load
-        const int kb = !tail || j < place ? j : (j == place ? t.kb - 1 : j - 1);
+        int kb = !tail || j < place ? j : (j == place ? t.kb - 1 : j - 1);
+        const CUtensorMap *pa = am, *pb = bm;
+        if constexpr (KIND == OPEN_CHAIN) {
+          // first times first parts, first times second, second times first
+          if (kb >= 2 * pass_kb) {
+            kb -= 2 * pass_kb;
+            pa = am2;
+          } else if (kb >= pass_kb) {
+            kb -= pass_kb;
+            pb = bm2;
+          }
+        }
         const int k = kb * OK_;
         // K-major operands come in two boxes of 64 deep, the second one only if K
         // reaches it; MN-major ones in two boxes of 64 wide
@@ -696,19 +714,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
             // coordinates of an MN-major box: (m or n, c1, c2)
             const int c1 = DEPTH<KIND> ? t.k0 + k : k, c2 = DEPTH<KIND> ? 0 : t.z;
             if (at) {
-              tma_load_3d_pair(sA, am, bar, ma, c1, c2);
-              tma_load_3d_pair(sA + OCHUNK, am, bar, ma + 64, c1, c2);
+              tma_load_3d_pair(sA, pa, bar, ma, c1, c2);
+              tma_load_3d_pair(sA + OCHUNK, pa, bar, ma + 64, c1, c2);
             } else {
-              tma_load_3d_pair(sA, am, bar, k, ma, t.z);
-              if (deep) tma_load_3d_pair(sA + OCHUNK, am, bar, k + 64, ma, t.z);
+              tma_load_3d_pair(sA, pa, bar, k, ma, t.z);
+              if (deep) tma_load_3d_pair(sA + OCHUNK, pa, bar, k + 64, ma, t.z);
             }
             if (bt) {
-              tma_load_3d_pair(sB, bm, bar, nbase, c1, c2);
-              tma_load_3d_pair(sB + OCHUNK, bm, bar, nbase + 64, c1, c2);
+              tma_load_3d_pair(sB, pb, bar, nbase, c1, c2);
+              tma_load_3d_pair(sB + OCHUNK, pb, bar, nbase + 64, c1, c2);
             } else {
               const int z = KIND == OPEN_ROWS ? 0 : t.z;
-              tma_load_3d_pair(sB, bm, bar, k, nbase, z);
-              if (deep) tma_load_3d_pair(sB + OCHUNK, bm, bar, k + 64, nbase, z);
+              tma_load_3d_pair(sB, pb, bar, k, nbase, z);
+              if (deep) tma_load_3d_pair(sB + OCHUNK, pb, bar, k + 64, nbase, z);
             }
           }
         }
@@ -805,7 +823,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         const bool tail = DEPTH<KIND> && open_tail(t) != 0;
         const int place = tail ? open_cut_place(t) : -1;
         // steps of the tile's last block
-        const int last_steps = (depth - (t.kb - 1) * OK_ + 15) >> 4;
+        const int pass_kb = KIND == OPEN_CHAIN ? P.ph[t.k1].pass_kb : t.kb;
+        const int last_steps = (depth - (pass_kb - 1) * OK_ + 15) >> 4;
+        int jp = 0;  // block of the pass
         uint32_t held = 0, held_phase = 0;
         bool first = true, known = false;
         for (int j = 0; j < t.kb; ++j) {
@@ -815,14 +835,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           } else {
             ok = warp_all(mbar_wait(&full[stage], sphase, wc));
             if (!ok) break;
-            block(stage, j * OK_, !tail && j == t.kb - 1 ? last_steps : OK_ / 16, d_tmem, idesc,
-                  first);
+            block(stage, jp * OK_, !tail && jp == pass_kb - 1 ? last_steps : OK_ / 16, d_tmem,
+                  idesc, first);
             first = false;
           }
           if (++stage == ST) {
             stage = 0;
             sphase ^= 1u;
           }
+          if (++jp == pass_kb) jp = 0;
           if (j == 0 && (known = open_known<KIND>(ring, leader, walk)))
             more = advance(next);  // beside the MMAs
         }
@@ -1016,7 +1037,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
       const int step = KIND == OPEN_CHAIN ? t.k0 / 3 : 0;
       const bool last = upd && step == P.steps - 1;       // ... the result
       const OpenFactors& fa = P.f[step];
-      const bool adds = sum || (upd && fa.low);
+      const bool adds = sum || (upd && fa.low && !P.parts2);
       const int64_t ld = KIND == OPEN_CHAIN ? (upd ? P.ld_x : P.ld_a) : N;
       const int64_t in_at = (static_cast<int64_t>(t.z) * M + mw) * ld + t.n0;
       const int from = step & 1;
@@ -1061,7 +1082,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
         }
       } else {
         uint16_t* dst = reinterpret_cast<uint16_t*>(sum ? P.b_out : upd ? P.x_hi[from ^ 1] : P.a_out);
-        const bool split = upd && !last && P.f[step + 1].low;
+        const bool split = P.parts2 ? !last : upd && !last && P.f[step + 1].low;
+        uint16_t* dst2 = reinterpret_cast<uint16_t*>(sum ? P.b_lo : upd ? P.x_lo[from ^ 1] : P.a_lo);
 #pragma unroll 1
         for (int c = first; c < nch; c += SHARE) {
           uint32_t r[32];
@@ -1074,6 +1096,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
             turn_in(sb, lane, q);
             if (c + SHARE < nch) fetch_in(c + SHARE);
             turn_out(sb, lane, [&](int j, float x) { v[j] = fmaf(beta, x, v[j]); });
+            if (sum && P.parts2) {  // A's second part
+              uint4 q2[4];
+              fetch(P.a_lo + in_at + 32 * c, lane, ld, mrows,
+                    static_cast<int>(ld) - t.n0 - 32 * c, q2);
+              turn_in(sb, lane, q2);
+              turn_out(sb, lane, [&](int j, float x) { v[j] = fmaf(beta, x, v[j]); });
+            }
           }
           const int n = t.n0 + 32 * c;
           if (sum && n == mw) {
@@ -1105,7 +1134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::THREADS, 
           if (split) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] -= half_round(v[j]);
-            put_d(true, v, reinterpret_cast<uint16_t*>(P.x_lo[from ^ 1]) + at, ld, mrows, cols);
+            put_d(true, v, dst2 + at, ld, mrows, cols);
           }
         }
       }
@@ -1329,7 +1358,8 @@ int launch_open_chain(const GemmEnv& env, const OpenChain& s) {
     p.M = static_cast<int>(M);
     p.N = static_cast<int>(N);
     p.K = static_cast<int>(K);
-    p.kb = static_cast<int>((K + OK_ - 1) / OK_);
+    p.pass_kb = static_cast<int>((K + OK_ - 1) / OK_);
+    p.kb = s.a_lo ? 3 * p.pass_kb : p.pass_kb;
     p.mt = static_cast<int>((M + 255) / 256);
     p.nt = static_cast<int>((N + 255) / 256);
     p.sym = sym;
@@ -1355,6 +1385,9 @@ int launch_open_chain(const GemmEnv& env, const OpenChain& s) {
   }
   P.a_out = s.a;
   P.b_out = s.b;
+  P.a_lo = s.a_lo;
+  P.b_lo = s.b_lo;
+  P.parts2 = s.a_lo != nullptr;
   P.factor = s.factor;
   P.ticket = s.ticket;
   P.done = s.done;
@@ -1367,6 +1400,15 @@ int launch_open_chain(const GemmEnv& env, const OpenChain& s) {
                          OpenOperand{s.x_hi[i], s.M, s.N, s.Z, s.ld_x, s.M * s.ld_x});
   rc |= encode_operand(env, &maps.a, true, OpenOperand{s.a, m, m, s.Z, s.ld_a, m * s.ld_a});
   rc |= encode_operand(env, &maps.b, true, OpenOperand{s.b, m, m, s.Z, s.ld_a, m * s.ld_a});
+  if (P.parts2) {
+    for (int i = 0; i < 2; ++i)
+      rc |= encode_operand(env, &maps.brows[2 + i], true,
+                           OpenOperand{s.x_lo[i], s.M, s.N, s.Z, s.ld_x, s.M * s.ld_x});
+    rc |= encode_operand(env, &maps.brows[4], true,
+                         OpenOperand{s.a_lo, m, m, s.Z, s.ld_a, m * s.ld_a});
+    rc |= encode_operand(env, &maps.brows[5], true,
+                         OpenOperand{s.b_lo, m, m, s.Z, s.ld_a, m * s.ld_a});
+  }
   if (rc != HMM_OK) return HMM_ERR_CUDA;
   // (a product of the whole stack at once is all that can run)
   const int64_t most = s.Z * std::max(P.ph[2].tiles, P.ph[0].tiles);

@@ -21,6 +21,9 @@ constexpr int OPEN_CHAIN = 2;
 //      step the caller's result (bf16 or fp16)
 // Of a symmetric result only the tiles on and above the diagonal are computed and
 // written; as an operand its blocks below are read from the others, m / n contiguous.
+// With operands in two parts X, A and B are all hi + lo, a product is the sum of hi hi,
+// hi lo and lo hi (the contraction three times as long), B adds beta_b (hi + lo) of A and
+// X no more than the product.
 // The first X is stored without a factor `factor[z]` of its matrix.
 struct OpenFactors {
   float alpha_a, alpha_b, beta_b, gamma_b, alpha_x, beta_x;
@@ -28,7 +31,8 @@ struct OpenFactors {
 };
 
 struct OpenPhase {
-  int M, N, K, kb;    // extents, depth in blocks
+  int M, N, K;        // extents
+  int kb, pass_kb;    // blocks of a tile; of a pair of operand parts
   int mt, nt, tiles;  // 256-tiles of m, of n, per matrix
   int sym;
   int a, b;           // operands: 0 X, 1 A, 2 B
@@ -61,7 +65,8 @@ struct OpenParams {
   OpenPhase ph[3];
   OpenFactors f[HMM_ORTHO_MAX_STEPS];
   int64_t ld_x, ld_a;
-  __half *x_hi[2], *x_lo[2], *a_out, *b_out;
+  __half *x_hi[2], *x_lo[2], *a_out, *b_out, *a_lo, *b_lo;
+  int parts2;              // operands in two parts
   const float* factor;     // [Z]
   int *ticket, *done;      // zero at launch; done [Z]
 };
@@ -72,6 +77,7 @@ struct OpenChain {
   const OpenFactors* f;
   __half *x_hi[2], *x_lo[2];  // [Z, M, ld_x], the first X in [0]
   __half *a, *b;              // [Z, m, ld_a]
+  __half *a_lo, *b_lo;        // ... null: operands in one part
   int64_t ld_x, ld_a;         // multiples of 8
   const float* factor;        // [Z]
   int *ticket, *done;         // device counters, zero

@@ -210,12 +210,13 @@ cudaError_t launch_rows_sum(const RowsArgs& a, int dtype, cudaStream_t st, bool 
 cudaError_t launch_rows_combine_grad(const RowsArgs& a, int dtype, cudaStream_t st, bool pdl);
 
 // The orthogonalised update (ortho.cu): workspace
-//   [sums of squares | factors | counters | X hi, lo | next X hi, lo | A | B]
+//   [sums of squares | factors | counters | X hi, lo | next X hi, lo | A | B | A lo | B lo]
 struct OrthoPlan {
   int64_t m, ld_x, ld_a;  // smaller side; padded rows of X and of A, B
   int pieces;             // blocks per matrix of the norm and the first conversion
   int64_t rows_per_piece;
-  size_t off_factor, off_ticket, off_x[4], off_a, off_b, bytes;
+  size_t off_factor, off_ticket, off_x[4], off_a, off_b, off_a_lo, off_b_lo, bytes;
+  bool parts2;  // operands in two fp16 parts (fp16 results)
 };
 struct GemmEnv;
 int check_ortho(const hmm_ortho* d);

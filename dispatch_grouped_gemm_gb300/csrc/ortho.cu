@@ -17,7 +17,10 @@
 // hi + lo, two fp16 (22 bits): the products read hi alone, with B' = B + a I, and the
 // epilogue adds a lo, which is X <- a X + B X but for B lo: 0.2 % off for every
 // spectrum, most of it the result's own rounding to bf16 (0.17 %).  (Where the steps
-// that are left multiply by at most 4, hi alone does, to the same 0.2 %.)  Three bits
+// that are left multiply by at most 4, hi alone does, to the same 0.2 %.)  A result in
+// fp16 rounds to 0.02 % only: for it A, B and X are operands in two parts, three products
+// for each one, and the result's rounding is all that shows (16 x 1408 x 2048 1055 ->
+// 2780 us; with operands in one part 0.11 - 0.18 % off).  Three bits
 // more than bf16 at the same rate are why it is fp16: its range is enough, because
 // every matrix here has a known bound.
 //   Bounds.  All singular values of X lie in [0, u] with u = 1 at first and then
@@ -380,7 +383,10 @@ OrthoPlan ortho_plan(const hmm_ortho& d) {
   }
   p.off_a = o;
   p.off_b = o + a;
-  p.bytes = o + 2 * a;
+  p.off_a_lo = o + 2 * a;
+  p.off_b_lo = o + 3 * a;
+  p.parts2 = d.out_dtype == HMM_DTYPE_F16;
+  p.bytes = o + (p.parts2 ? 4 : 2) * a;
   return p;
 }
 
@@ -404,7 +410,7 @@ int launch_ortho(const GemmEnv& env, const hmm_ortho& d, const OrthoPlan& p, con
   a.ticket = reinterpret_cast<int*>(ws + p.off_ticket);
   a.done = a.ticket + 1;
   a.hi = reinterpret_cast<__half*>(ws + p.off_x[0]);
-  a.lo = steps[0].low ? reinterpret_cast<__half*>(ws + p.off_x[1]) : nullptr;
+  a.lo = steps[0].low || p.parts2 ? reinterpret_cast<__half*>(ws + p.off_x[1]) : nullptr;
   a.ld_x = p.ld_x;
   a.eps = d.eps;
   a.scale = static_cast<float>(std::ldexp(1.0, scale_for(1.0)));
@@ -424,6 +430,8 @@ int launch_ortho(const GemmEnv& env, const hmm_ortho& d, const OrthoPlan& p, con
   }
   c.a = reinterpret_cast<__half*>(ws + p.off_a);
   c.b = reinterpret_cast<__half*>(ws + p.off_b);
+  c.a_lo = p.parts2 ? reinterpret_cast<__half*>(ws + p.off_a_lo) : nullptr;
+  c.b_lo = p.parts2 ? reinterpret_cast<__half*>(ws + p.off_b_lo) : nullptr;
   c.ld_x = p.ld_x;
   c.ld_a = p.ld_a;
   c.factor = a.factor;

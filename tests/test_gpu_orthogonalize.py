@@ -181,3 +181,24 @@ def test_refused_while_differentiating():
         hmm.orthogonalize(g)
     with torch.no_grad():
         hmm.orthogonalize(g)
+
+
+@pytest.mark.parametrize("spectrum", ["mixed", "low rank", "decaying"])
+@pytest.mark.parametrize("shape", [(4, 128, 250), (3, 300, 200), (2, 65, 1000), (1, 520, 768),
+                                   (40, 264, 270)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32], ids=str)
+def test_fp16_results_are_exact_to_their_rounding(shape, dtype, spectrum):
+    """Of a result in fp16 its own rounding shows, half a step, 2^-11 of each value at
+    most, or half of 2^-24, and the fp32 sums: an MMA adds to an accumulator that loses
+    2^-24 of the largest partial sum, 3 * 1000 / 16 of them in a sum at most, 2^-16, some
+    four times the result where terms cancel; fifteen products with a sensitivity of at
+    most 4 to the end add up to 2^-12 at most if all err alike.  (Operands in 11 bits
+    would be off by 2^-10.)"""
+    g = gradient(shape, spectrum).to(dtype)
+    got = hmm.orthogonalize(g, out_dtype=torch.float16)
+    want = ref.orthogonalize(g)
+    assert got.dtype == torch.float16
+    err = (got.double() - want).flatten(1).norm(dim=1)
+    least = 2.0 ** -25 * (shape[1] * shape[2]) ** 0.5
+    assert bool((err <= (2.0 ** -11 + 2.0 ** -12) * want.flatten(1).norm(dim=1) + least).all())
+    assert torch.equal(got, hmm.orthogonalize(g, out_dtype=torch.float16))
