@@ -30,7 +30,9 @@ constexpr int ROW_THREADS = 256;
 constexpr int ROW_WARPS = ROW_THREADS / 32;
 // Sums: blocks per SM that registers are held down to, so that the loads of 32 warps
 // are in flight.  (16384 tokens x 8 rows of 7168 bf16: all eight rows' vectors together
-// and 4 blocks 357 us, 5.9 TB/s; four rows of two vectors each 421 us.)
+// and 4 blocks 357 us, 5.9 TB/s; four rows of two vectors each 421 us.)  The combine's
+// gradient with two vectors of both rows at a time and 4 blocks 590 us, 6.8 TB/s, with
+// four vectors and 2 blocks 670 us (16383 tokens x 2 rows of 512 14.6 and 26 us).
 constexpr int ROW_SUM_BLOCKS = 4;
 // Dispatch: warps from which a lane takes four vectors instead of one (fewer warps than
 // this leave SMs without loads in flight).
@@ -174,11 +176,12 @@ __global__ void __launch_bounds__(ROW_THREADS, ROW_SUM_BLOCKS) rows_sum_kernel(c
 
 // A slot per warp, or per block (WPS warps) where there are few slots.
 template <typename T, int V, int WPS>
-__global__ void __launch_bounds__(ROW_THREADS) rows_combine_grad_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(ROW_THREADS, ROW_SUM_BLOCKS)
+    rows_combine_grad_kernel(const RowsArgs a) {
   __shared__ float part[ROW_WARPS];
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int U = 4;
+  constexpr int U = 2;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + wid;
   const int64_t s = warp / WPS, hv = a.H / V;
