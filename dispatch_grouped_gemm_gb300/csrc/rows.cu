@@ -28,12 +28,18 @@ namespace {
 
 constexpr int ROW_THREADS = 256;
 constexpr int ROW_WARPS = ROW_THREADS / 32;
-// Sums: blocks per SM that registers are held down to, so that the loads of 32 warps
-// are in flight.  (16384 tokens x 8 rows of 7168 bf16: all eight rows' vectors together
-// and 4 blocks 357 us, 5.9 TB/s; four rows of two vectors each 421 us.)  The combine's
-// gradient with two vectors of both rows at a time and 4 blocks 590 us, 6.8 TB/s, with
-// four vectors and 2 blocks 670 us (16383 tokens x 2 rows of 512 14.6 and 26 us).
-constexpr int ROW_SUM_BLOCKS = 4;
+// Blocks per SM that registers are held down to, so that enough loads are in flight.
+// The combine's gradient with two vectors of both rows at a time and 4 blocks moves
+// 16384 tokens x 8 rows of 7168 bf16 in 590 us, 6.8 TB/s; with four vectors and 2 blocks
+// 670 us (16383 tokens x 2 rows of 512 15 and 26 us).
+constexpr int ROW_BLOCKS = 4;
+// Sums, which lane loads what at a time (slots x vectors; us at the shapes of before, and
+// 16383 x 4 rows of 2048): more than four slots 4 x 1 and 6 blocks 337 (8 x 1 and 4 blocks
+// 357); three or four 4 x 2 55 (4 x 1 61); one or two 2 x 4 (65535 x 1 row of 1024 59, 2 x 2
+// 61), 2 x 2 for rows of up to 64 vectors, where half of the lanes' loads would be off
+// their end (8.2, 2 x 4 11.0).
+template <int U>
+constexpr int ROW_SUM_BLOCKS = U == 1 ? 6 : ROW_BLOCKS;
 // Dispatch: warps from which a lane takes four vectors instead of one (fewer warps than
 // this leave SMs without loads in flight).
 constexpr int64_t ROW_WIDE_WARPS = 152 * 16;
@@ -120,7 +126,8 @@ __global__ void __launch_bounds__(ROW_THREADS) rows_dispatch_kernel(const RowsAr
 // The same pieces summed over the slots of a token (w null: weights 1), KB slots at a
 // time with their loads together.
 template <typename T, int V, int U, int KB>
-__global__ void __launch_bounds__(ROW_THREADS, ROW_SUM_BLOCKS) rows_sum_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(ROW_THREADS, ROW_SUM_BLOCKS<U>)
+    rows_sum_kernel(const RowsArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
@@ -176,7 +183,7 @@ __global__ void __launch_bounds__(ROW_THREADS, ROW_SUM_BLOCKS) rows_sum_kernel(c
 
 // A slot per warp, or per block (WPS warps) where there are few slots.
 template <typename T, int V, int WPS>
-__global__ void __launch_bounds__(ROW_THREADS, ROW_SUM_BLOCKS)
+__global__ void __launch_bounds__(ROW_THREADS, ROW_BLOCKS)
     rows_combine_grad_kernel(const RowsArgs a) {
   __shared__ float part[ROW_WARPS];
   grid_dep_wait();
@@ -267,12 +274,15 @@ cudaError_t launch_rows_v(RowsOp op, const RowsArgs& a, cudaStream_t st, bool pd
     return launch_kernel(rows_combine_grad_kernel<T, V, 1>, blocks(slots), ROW_THREADS, 0, st, pdl,
                          1, a);
   }
-  const int u = op == ROWS_DISPATCH ? 4 : a.K > 4 ? 1 : a.K > 2 ? 2 : 4;
+  const int u = op == ROWS_DISPATCH ? 4 : a.K > 4 ? 1 : a.K > 2 || hv <= 64 ? 2 : 4;
   const int64_t wide = a.T * ((hv + 32 * u - 1) / (32 * u)), narrow = a.T * ((hv + 31) / 32);
   const bool several = op != ROWS_DISPATCH || wide >= ROW_WIDE_WARPS;
   auto kern = op == ROWS_DISPATCH
                   ? (several ? rows_dispatch_kernel<T, V, 4> : rows_dispatch_kernel<T, V, 1>)
-                  : (a.K > 4 ? rows_sum_kernel<T, V, 1, 8> : a.K > 2 ? rows_sum_kernel<T, V, 2, 4> : rows_sum_kernel<T, V, 4, 2>);
+              : a.K > 4  ? rows_sum_kernel<T, V, 1, 4>
+              : a.K > 2  ? rows_sum_kernel<T, V, 2, 4>
+              : u == 2   ? rows_sum_kernel<T, V, 2, 2>
+                         : rows_sum_kernel<T, V, 4, 2>;
   return launch_kernel(kern, blocks(several ? wide : narrow), ROW_THREADS, 0, st, pdl, 1, a);
 }
 
