@@ -216,7 +216,7 @@ struct OrthoPlan {
   int pieces;             // blocks per matrix of the norm and the first conversion
   int64_t rows_per_piece;
   size_t off_factor, off_ticket, off_x[4], off_a, off_b, off_a_lo, off_b_lo, bytes;
-  bool parts2;  // operands in two fp16 parts (fp16 results)
+  bool parts2;  // operands in two fp16 parts
 };
 struct GemmEnv;
 int check_ortho(const hmm_ortho* d);

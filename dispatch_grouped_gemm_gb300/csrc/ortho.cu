@@ -385,7 +385,13 @@ OrthoPlan ortho_plan(const hmm_ortho& d) {
   p.off_b = o + a;
   p.off_a_lo = o + 2 * a;
   p.off_b_lo = o + 3 * a;
-  p.parts2 = d.out_dtype == HMM_DTYPE_F16;
+  // Two parts for bf16 results as well where one leaves too little: few rows average the
+  // roundings of A, B and hi less, and each step adds its own (five steps of 128 x 250
+  // are 0.22 % off, of 1408 x 2048 0.19 %, 279 x 28 0.25 %; six of 513 x 600 0.25 %, of
+  // 1024 x 1500 0.23 %; 0.17 % with two parts).  Small products wait for each other more
+  // than for MMAs (4 x 128 x 250 137 us with one part, 157 us with two).
+  p.parts2 = d.out_dtype == HMM_DTYPE_F16 || p.m <= 64 || d.steps > 6 ||
+             (d.steps > 5 && p.m <= 1024);
   p.bytes = o + (p.parts2 ? 4 : 2) * a;
   return p;
 }

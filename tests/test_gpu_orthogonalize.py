@@ -202,3 +202,19 @@ def test_fp16_results_are_exact_to_their_rounding(shape, dtype, spectrum):
     least = 2.0 ** -25 * (shape[1] * shape[2]) ** 0.5
     assert bool((err <= (2.0 ** -11 + 2.0 ** -12) * want.flatten(1).norm(dim=1) + least).all())
     assert torch.equal(got, hmm.orthogonalize(g, out_dtype=torch.float16))
+
+
+@pytest.mark.parametrize("shape,steps", [((3, 279, 28), 4), ((36, 1000, 19), 5), ((2, 64, 300), 5),
+                                         ((5, 420, 387), 6), ((2, 512, 600), 8),
+                                         ((1, 600, 900), 6)], ids=str)
+def test_small_matrices_and_many_steps(shape, steps):
+    """bf16 results of small matrices, and of many steps, are exact to their rounding
+    too: half a step, 2^-8 of each value at most, and the fp32 sums' part of the test
+    above, 2^-12 times the steps over five."""
+    g = gradient(shape).to(torch.bfloat16)
+    got = hmm.orthogonalize(g, steps=steps).double()
+    want = ref.orthogonalize(g, steps=steps)
+    # (spread evenly, a rounding is half a step / sqrt(3) of values up to twice as large as
+    # their power of two: below 2^-8 / sqrt(3) over a whole matrix but for chance)
+    bound = 2.0 ** -8 / 3 ** 0.5 + 2.0 ** -12 * steps / 5
+    assert bool(((got - want).flatten(1).norm(dim=1) <= bound * want.flatten(1).norm(dim=1)).all())
